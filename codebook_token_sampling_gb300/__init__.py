@@ -7,12 +7,14 @@ only for device memory and streams.  The functions keep the C names:
     ts_create, ts_destroy, ts_max_top_k, ts_sample, ts_sample_debug,
     ts_sample_steps, ts_reserve, ts_sample_noalloc, ts_advance_steps,
     ts_read_status, ts_set_option, ts_plan, ts_status_string, ts_last_error,
-    ts_lm_head_logits, ts_lm_head_sample, ts_sample_host
+    ts_lm_head_logits, ts_lm_head_sample, ts_sample_host,
+    ts_reserve_kv, ts_kv_tables, ts_kv_append, ts_paged_attention
 
 ``Sampler`` wraps a handle; ``DeviceBatch`` holds one step's per-row arrays on
 the GPU with a prebuilt ``ts_batch`` so that repeated calls marshal nothing;
 ``LmHead`` holds a frame's hidden states and output heads with a prebuilt
-``ts_lm_head``.
+``ts_lm_head``; ``KvTables``, ``KvCache``, ``KvTokens`` and ``PagedQuery`` do the
+same for the paged key-value cache's calls.
 Importing this module loads the compiled library and raises if it is missing;
 there is no fallback.
 """
@@ -32,28 +34,36 @@ TS_ERR_CUDA = 3
 TS_ERR_NO_MEMORY = 4
 TS_DTYPE_F32 = 0
 TS_DTYPE_BF16 = 1
+TS_DTYPE_E4M3 = 2
 TS_ROW_BAD_SHAPE = 1
 TS_ROW_BAD_PARAM = 2
 TS_ROW_NONFINITE = 4
 TS_ROW_BAD_SLOT = 8
 TS_ROW_NOT_READY = 16
+TS_ROW_BAD_BLOCK = 32
+TS_ROW_NO_BLOCKS = 64
 TS_OPT_PATH = 1
 TS_OPT_CLUSTER = 2
 TS_OPT_PDL = 3
 TS_OPT_WIDE_EXACT = 4
 TS_OPT_WARPS_PER_ROW = 5
 TS_OPT_FAIL_LAUNCH = 6
+TS_OPT_KV_CTAS = 7
 TS_MAX_VOCAB_BF16 = 163840
 TS_MAX_VOCAB_F32 = 81920
 TS_NOALLOC_SCRATCH_BYTES = 4194304
 TS_NOALLOC_MAX_ROWS = 64
 TS_LM_HEAD_DIM_STEP = 64
 TS_LM_HEAD_MAX_DIM = 16384
+TS_KV_MAX_REQUESTS = 8192
+TS_KV_MAX_LEN = 2147482624
+TS_KV_MAX_HEAD_DIM = 256
 
 EXPORTED = ("ts_create", "ts_destroy", "ts_max_top_k", "ts_sample", "ts_sample_debug",
             "ts_sample_steps", "ts_reserve", "ts_sample_noalloc", "ts_advance_steps",
             "ts_read_status", "ts_set_option", "ts_plan", "ts_status_string", "ts_last_error",
-            "ts_lm_head_logits", "ts_lm_head_sample", "ts_sample_host")
+            "ts_lm_head_logits", "ts_lm_head_sample", "ts_sample_host",
+            "ts_reserve_kv", "ts_kv_tables", "ts_kv_append", "ts_paged_attention")
 
 
 class TsBatch(ctypes.Structure):
@@ -118,6 +128,92 @@ class TsLmHead(ctypes.Structure):
     ]
 
 
+class TsKvTables(ctypes.Structure):
+    """Mirror of ``ts_kv_tables_args``."""
+    _fields_ = [
+        ("n_requests", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("n_blocks", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32),
+        ("table_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("lens_out", ctypes.c_void_p),
+        ("n_new", ctypes.c_void_p),
+        ("finished", ctypes.c_void_p),
+        ("free_blocks", ctypes.c_void_p),
+        ("free_len", ctypes.c_int32),
+        ("n_free", ctypes.c_void_p),
+        ("n_free_out", ctypes.c_void_p),
+        ("max_tokens", ctypes.c_int32),
+        ("token_starts", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("requests", ctypes.c_void_p),
+    ]
+
+
+class TsKvCache(ctypes.Structure):
+    """Mirror of ``ts_kv_cache``."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("n_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("k_block_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_block_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class TsKvTokens(ctypes.Structure):
+    """Mirror of ``ts_kv_tokens``."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int32),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p),
+    ]
+
+
+class TsPagedQuery(ctypes.Structure):
+    """Mirror of ``ts_paged_query``."""
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("n_requests", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32),
+        ("q_request_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("out_request_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("lens", ctypes.c_void_p),
+        ("key_mask", ctypes.c_void_p),
+        ("mask_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("window", ctypes.c_int32),
+    ]
+
+
 class SamplerError(RuntimeError):
     def __init__(self, status: int, what: str):
         detail = _lib.ts_last_error().decode() if status == TS_ERR_CUDA else ""
@@ -150,6 +246,12 @@ def _load(path: str):
                               ctypes.c_int),
         "ts_lm_head_sample": ([vp, ctypes.POINTER(TsLmHead), ctypes.POINTER(TsBatch), vp],
                               ctypes.c_int),
+        "ts_reserve_kv": ([vp, i32], ctypes.c_int),
+        "ts_kv_tables": ([vp, ctypes.POINTER(TsKvTables), vp], ctypes.c_int),
+        "ts_kv_append": ([vp, ctypes.POINTER(TsKvCache), ctypes.POINTER(TsKvTokens), vp],
+                         ctypes.c_int),
+        "ts_paged_attention": ([vp, ctypes.POINTER(TsKvCache), ctypes.POINTER(TsPagedQuery), vp],
+                               ctypes.c_int),
         "ts_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "ts_last_error": ([], ctypes.c_char_p),
     }
@@ -278,6 +380,28 @@ def ts_lm_head_sample(handle: int, head: "LmHead", batch: "DeviceBatch", stream=
                                   _stream_ptr(stream)), "ts_lm_head_sample")
 
 
+def ts_reserve_kv(handle: int, max_requests: int) -> None:
+    """The workspace of the paged cache's calls: once, before any capture."""
+    _check(_lib.ts_reserve_kv(handle, max_requests), "ts_reserve_kv")
+
+
+def ts_kv_tables(handle: int, tables: "KvTables", stream=None) -> None:
+    """Block tables, lengths and slot maps of the next tokens (see the header)."""
+    _check(_lib.ts_kv_tables(handle, ctypes.byref(tables.c), _stream_ptr(stream)), "ts_kv_tables")
+
+
+def ts_kv_append(handle: int, cache: "KvCache", tokens: "KvTokens", stream=None) -> None:
+    """Writes the tokens' keys and values into the cache at their slots."""
+    _check(_lib.ts_kv_append(handle, ctypes.byref(cache.c), ctypes.byref(tokens.c),
+                             _stream_ptr(stream)), "ts_kv_append")
+
+
+def ts_paged_attention(handle: int, cache: "KvCache", query: "PagedQuery", stream=None) -> None:
+    """Attention of one query token per request over its cached tokens."""
+    _check(_lib.ts_paged_attention(handle, ctypes.byref(cache.c), ctypes.byref(query.c),
+                                   _stream_ptr(stream)), "ts_paged_attention")
+
+
 def ts_status_string(status: int) -> str:
     return _lib.ts_status_string(status).decode()
 
@@ -302,6 +426,9 @@ class Sampler:
 
     def sample(self, batch: "DeviceBatch", stream=None) -> None:
         ts_sample(self.handle, batch, stream)
+
+    def reserve_kv(self, max_requests: int) -> None:
+        ts_reserve_kv(self.handle, max_requests)
 
     def sample_debug(self, batch: "DeviceBatch", max_keep: int, stream=None) -> dict:
         import torch
@@ -505,3 +632,203 @@ class LmHead:
         self.weights = t
         self.c.weights = t.data_ptr()
         self.c.weights_len = t.numel()
+
+
+# --------------------------------------------------------------------------
+# The paged key-value cache
+# --------------------------------------------------------------------------
+def _kv_dtype(t) -> int:
+    import torch
+    kinds = {torch.float32: TS_DTYPE_F32, torch.bfloat16: TS_DTYPE_BF16,
+             torch.float8_e4m3fn: TS_DTYPE_E4M3}
+    if t.dtype not in kinds:
+        raise ValueError(f"no key-value type for {t.dtype}")
+    return kinds[t.dtype]
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _vector(t, n: int, dtype, device, what: str):
+    """``t``: a contiguous tensor of ``n`` entries or more of ``dtype`` on
+    ``device``; its address (0 for None)."""
+    if t is None:
+        return None
+    _need(t.dtype == dtype and t.is_contiguous() and t.numel() >= n and t.device == device, what)
+    return t.data_ptr()
+
+
+def _strides(t) -> list:
+    """Element strides of all but the last dimension, 0 for those of one entry."""
+    return [st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape[:-1])]
+
+
+class KvTables:
+    """Block tables, lengths, the stack of free blocks and the slot maps of one
+    cache, with a prebuilt ``ts_kv_tables_args``.
+
+    Starts with every request empty and every block free, or from the int32
+    device tensors given: ``lens`` [n], ``block_table`` [n, max_blocks] (rows
+    may be strided), ``free_blocks`` and ``n_free`` [1].  ``n_new`` (int32 [n];
+    None: one token each) and ``finished`` (uint8 [n], e.g. a ``DeviceBatch``'s
+    ``finish_reason``) are read by every call.  With ``double`` the new lengths
+    and the free count go to second arrays (``lens_out``, ``n_free_out``;
+    ``swap()`` exchanges them), otherwise they are updated in place.
+    """
+
+    def __init__(self, n_requests: int, max_blocks: int, n_blocks: int, block_size: int, *,
+                 max_tokens: int, lens=None, n_new=None, finished=None, block_table=None,
+                 free_blocks=None, n_free=None, double: bool = False, device="cuda"):
+        import torch
+        i32 = torch.int32
+        given = [t for t in (lens, block_table, free_blocks, n_free) if t is not None]
+        dev = given[0].device if given else torch.empty(0, device=device).device
+
+        def make(*shape, fill=0, dtype=i32):
+            return torch.full(shape, fill, dtype=dtype, device=dev)
+        self.lens = make(n_requests) if lens is None else lens
+        self.block_table = make(n_requests, max_blocks, fill=-1) if block_table is None else block_table
+        if free_blocks is None:
+            free_blocks = torch.arange(n_blocks - 1, -1, -1, dtype=i32, device=dev)
+        self.free_blocks = free_blocks
+        self.n_free = make(1, fill=n_blocks) if n_free is None else n_free
+        self.lens_out = torch.empty_like(self.lens) if double else self.lens
+        self.n_free_out = torch.empty_like(self.n_free) if double else self.n_free
+        self.n_new, self.finished = n_new, finished
+        self.token_starts = make(n_requests + 1)
+        self.slots = make(max_tokens, fill=-1, dtype=torch.int64)
+        self.positions = make(max_tokens, fill=-1)
+        self.requests = make(max_tokens, fill=-1)
+        t = self.block_table  # a strided row is as long as max_blocks at least
+        _need(t.dtype == i32 and t.device == dev and tuple(t.shape) == (n_requests, max_blocks)
+              and (max_blocks < 2 or t.stride(1) == 1), "block_table: int32 [n_requests, max_blocks]")
+        c = TsKvTables()
+        c.n_requests, c.block_size, c.n_blocks, c.max_blocks = n_requests, block_size, n_blocks, max_blocks
+        c.table_stride = max(t.stride(0), max_blocks)
+        c.block_table = t.data_ptr()
+        c.free_blocks = _vector(self.free_blocks, 1 if n_blocks else 0, i32, dev, "free_blocks: int32")
+        c.free_len = self.free_blocks.numel()
+        c.max_tokens = max_tokens
+        for name in ("token_starts", "slots", "positions", "requests"):
+            setattr(c, name, getattr(self, name).data_ptr())
+        self.c = c
+        self._n, self._dev = n_requests, dev
+        self._bind()
+        self.set_requests(n_new, finished)
+
+    def _bind(self) -> None:
+        import torch
+        for name, n in (("lens", self._n), ("lens_out", self._n), ("n_free", 1), ("n_free_out", 1)):
+            setattr(self.c, name, _vector(getattr(self, name), n, torch.int32, self._dev,
+                                          f"{name}: int32 [{n}]"))
+
+    def set_requests(self, n_new=None, finished=None) -> None:
+        """Other arrays of new tokens and ended requests for the next calls."""
+        import torch
+        self.n_new, self.finished = n_new, finished
+        self.c.n_new = _vector(n_new, self._n, torch.int32, self._dev, "n_new: int32 [n_requests]")
+        self.c.finished = _vector(finished, self._n, torch.uint8, self._dev,
+                                  "finished: uint8 [n_requests]")
+
+    def swap(self) -> None:
+        """With ``double``: what the last call wrote becomes what the next one
+        reads (host-side pointer swap; capture it between calls)."""
+        self.lens, self.lens_out = self.lens_out, self.lens
+        self.n_free, self.n_free_out = self.n_free_out, self.n_free
+        self._bind()
+
+
+class KvCache:
+    """A paged cache with a prebuilt ``ts_kv_cache``: ``k`` and ``v`` are device
+    tensors seen as [n_blocks, block_size, n_kv_heads, head_dim], in whatever
+    order they lie in memory (permute a [block, head, token, dim] tensor), of
+    type float32, bfloat16 or float8_e4m3fn; the 8-bit type may have float32
+    scales, one per key head."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device,
+              "k and v: [n_blocks, block_size, n_kv_heads, head_dim] of one type")
+        _need(k.stride(3) == 1 and v.stride(3) == 1, "k and v: head_dim is contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        c = TsKvCache()
+        c.k, c.v = k.data_ptr(), v.data_ptr()
+        c.dtype = _kv_dtype(k)
+        c.n_blocks, c.block_size, c.n_kv_heads, c.head_dim = k.shape
+        c.k_block_stride, c.k_token_stride, c.k_head_stride = _strides(k)
+        c.v_block_stride, c.v_token_stride, c.v_head_stride = _strides(v)
+        c.k_scale = _vector(k_scale, k.shape[2], torch.float32, k.device, "k_scale: float32 [n_kv_heads]")
+        c.v_scale = _vector(v_scale, k.shape[2], torch.float32, k.device, "v_scale: float32 [n_kv_heads]")
+        self.c = c
+
+
+class KvTokens:
+    """New tokens' keys and values [n_tokens, n_kv_heads, head_dim] (any strides
+    with head_dim contiguous) and their slots, with a prebuilt ``ts_kv_tokens``."""
+
+    def __init__(self, k, v, slots):
+        import torch
+        _need(k.dim() == 3 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device,
+              "k and v: [n_tokens, n_kv_heads, head_dim] of one type")
+        _need(k.stride(2) == 1 and v.stride(2) == 1, "k and v: head_dim is contiguous")
+        self.k, self.v, self.slots = k, v, slots
+        c = TsKvTokens()
+        c.k, c.v = k.data_ptr(), v.data_ptr()
+        c.dtype = _kv_dtype(k)
+        c.n_tokens = k.shape[0]
+        c.k_token_stride, c.k_head_stride = _strides(k)
+        c.v_token_stride, c.v_head_stride = _strides(v)
+        c.slots = _vector(slots, k.shape[0], torch.int64, k.device, "slots: int64 [n_tokens]")
+        self.c = c
+
+
+class PagedQuery:
+    """One query token per request [n_requests, n_heads, head_dim], its output
+    and what it attends to, with a prebuilt ``ts_paged_query``.  ``scale``
+    defaults to head_dim ** -0.5; ``lse`` (float32 [n_requests, n_heads]),
+    ``key_mask`` (uint8 [n_requests, max_blocks * block_size or more]),
+    ``window`` and ``softcap`` are optional."""
+
+    def __init__(self, q, out, block_table, lens, *, scale=None, lse=None, key_mask=None,
+                 window: int = 0, softcap: float = 0.0):
+        import torch
+        n, heads, dim = q.shape
+        _need(q.shape == out.shape and q.dtype == out.dtype and q.device == out.device,
+              "q and out: [n_requests, n_heads, head_dim] of one type")
+        _need(q.stride(2) == 1 and out.stride(2) == 1, "q and out: head_dim is contiguous")
+        _need(block_table.dtype == torch.int32 and block_table.dim() == 2
+              and block_table.shape[0] == n and block_table.device == q.device
+              and (block_table.shape[1] < 2 or block_table.stride(1) == 1),
+              "block_table: int32 [n_requests, max_blocks]")
+        self.q, self.out, self.block_table, self.lens = q, out, block_table, lens
+        self.lse, self.key_mask = lse, key_mask
+        c = TsPagedQuery()
+        c.q, c.out = q.data_ptr(), out.data_ptr()
+        c.lse = _vector(lse, n * heads, torch.float32, q.device, "lse: float32 [n_requests, n_heads]")
+        c.dtype = _kv_dtype(q)
+        c.n_requests, c.n_heads, c.max_blocks = n, heads, block_table.shape[1]
+        c.q_request_stride, c.q_head_stride = _strides(q)
+        c.out_request_stride, c.out_head_stride = _strides(out)
+        c.block_table = block_table.data_ptr()
+        c.table_stride = max(block_table.stride(0), block_table.shape[1])
+        c.lens = _vector(lens, n, torch.int32, q.device, "lens: int32 [n_requests]")
+        c.key_mask = None
+        if key_mask is not None:
+            _need(key_mask.dtype == torch.uint8 and key_mask.dim() == 2 and key_mask.shape[0] == n
+                  and key_mask.device == q.device
+                  and (key_mask.shape[1] < 2 or key_mask.stride(1) == 1), "key_mask: uint8 [n_requests, tokens]")
+            c.key_mask = key_mask.data_ptr()
+            # a row holds this many entries; one request's stride says nothing
+            c.mask_stride = key_mask.stride(0) if n > 1 else key_mask.shape[1]
+        c.scale = dim ** -0.5 if scale is None else scale
+        c.softcap, c.window = softcap, window
+        self.c = c
+
+    def set_lens(self, lens) -> None:
+        """Another array of lengths (e.g. after ``KvTables.swap``)."""
+        import torch
+        self.lens = lens
+        self.c.lens = _vector(lens, self.c.n_requests, torch.int32, self.q.device,
+                              "lens: int32 [n_requests]")

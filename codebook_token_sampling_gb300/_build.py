@@ -14,6 +14,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+                  + glob.glob(os.path.join(CSRC, "*.h"))
                   + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
@@ -32,15 +33,26 @@ def nvcc() -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/ts_sampler.cu (one translation unit) into libts_sampler.so."""
+    """Compile csrc/*.cu (in parallel, one object each) into libts_sampler.so."""
     if not force and up_to_date():
         return LIB_PATH
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "-I", INCLUDE, "-o", tmp, os.path.join(CSRC, "ts_sampler.cu")]
+    flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
+        flags.append("-Xptxas=-v")
+    objects, running = [], []
+    for src in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
+        objects.append(f"{tmp}.{os.path.basename(src)}.o")
+        running.append(subprocess.Popen([nvcc(), *flags, "-c", src, "-o", objects[-1]]))
+    try:
+        for status, proc in [(p.wait(), p) for p in running]:
+            if status:
+                raise subprocess.CalledProcessError(status, proc.args)
+        subprocess.check_call([nvcc(), *ARCH, "-shared", "-o", tmp, *objects])
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -1,0 +1,419 @@
+// ts_kv.cuh -- the paged key-value cache's bookkeeping and writes: block
+// tables and slot maps built from request lengths (kv_tables_kernel), and the
+// write of new tokens' keys and values at their slots (kv_append_kernel).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "ts_device.cuh"
+
+namespace ts {
+
+constexpr uint32_t kRowBadBlock = 32u;
+constexpr uint32_t kRowNoBlocks = 64u;
+
+// n / d for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 d) and
+// mul = floor(2^(31 + l) / d) + 1, n * mul / 2^(31 + l) exceeds n / d by less
+// than 2^-l <= 1 / d, so its floor is the quotient.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __host__ static FastDiv of(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    FastDiv f;
+    f.d = d;
+    f.mul = static_cast<uint32_t>((1ull << (31 + l)) / d + 1);
+    f.shift = 31 + l;
+    return f;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(n) * mul) >> shift);
+  }
+};
+
+// --------------------------------------------------------------------------
+// Block tables and slot maps
+// --------------------------------------------------------------------------
+constexpr int kTablesMaxThreads = 1024;
+constexpr int kTablesMaxRequests = 8192;
+constexpr int kTablesPerThread = kTablesMaxRequests / kTablesMaxThreads;
+
+struct KvTablesParams {
+  int32_t n_requests, block_size, n_blocks, max_blocks, max_tokens, free_len;
+  int64_t table_stride;
+  int32_t *block_table;
+  const int32_t *lens;
+  const int32_t *n_new;      // null: one token each
+  const uint8_t *finished;   // null: none
+  int32_t *free_blocks;
+  const int32_t *n_free;
+  int32_t *lens_out;         // where this launch leaves them (a scratch array when
+  int32_t *n_free_out;       // several blocks work in place)
+  int32_t *token_starts;
+  int64_t *slots;
+  int32_t *positions;        // may be null
+  int32_t *requests;         // may be null
+  uint32_t *status;
+  FastDiv by_block;
+};
+
+__host__ __device__ constexpr uint32_t kv_tables_smem(int n_requests) {
+  return static_cast<uint32_t>(4 * (n_requests + 1)) * 4u;
+}
+
+// Exclusive prefix sums of K 64-bit values per thread over the block; total[]
+// gets the sums.  `part` holds K * 32 values.  Ends with the block in step.
+template <int K>
+__device__ __forceinline__ void block_scan(const int64_t (&x)[K], int64_t (&before)[K],
+                                           int64_t (&total)[K], int64_t *part) {
+  const int lane = static_cast<int>(lane_id());
+  const int warp = static_cast<int>(threadIdx.x) >> 5;
+  const int warps = static_cast<int>(blockDim.x) >> 5;
+  int64_t in[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    int64_t v = x[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    in[k] = v;
+    if (lane == 31) part[k * 32 + warp] = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    int64_t v = lane < warps ? part[k * 32 + lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    total[k] = __shfl_sync(0xFFFFFFFFu, v, 31);
+    const int64_t w = __shfl_sync(0xFFFFFFFFu, v, warp > 0 ? warp - 1 : 0);
+    before[k] = in[k] - x[k] + (warp > 0 ? w : 0);
+  }
+  __syncthreads();
+}
+
+// The last i in [0, n) with start[i] <= x, for ascending starts and start[0] <= x.
+__device__ __forceinline__ int last_start(const int32_t *start, int n, int32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Every block scans all requests (12 bytes each, from L2) into its shared
+// memory and then fills its share of the three lists that the scans lay out:
+// released blocks, handed-out blocks and new tokens, each entry finding its
+// request by bisection.  One launch therefore serves from one request to
+// thousands with hundreds of thousands of tokens: scanning again in every
+// block costs about as much as one block boundary's worth of latency, a second
+// launch that read the scans back would cost more.
+__global__ void __launch_bounds__(kTablesMaxThreads) kv_tables_kernel(const KvTablesParams p) {
+  extern __shared__ int32_t kv_smem[];
+  __shared__ int64_t part[3 * 32];
+  const int n = p.n_requests;
+  int32_t *tok_start = kv_smem;              // [n + 1] first token of a request
+  int32_t *blk_start = tok_start + (n + 1);  // [n + 1] blocks handed out before it
+  int32_t *rel_start = blk_start + (n + 1);  // [n + 1] blocks released before it
+  int32_t *len_of = rel_start + (n + 1);     // [n] length before the call
+  const int t = static_cast<int>(threadIdx.x), nt = static_cast<int>(blockDim.x);
+  const int per = (n + nt - 1) / nt;
+  const int i0 = t * per;
+  const bool first_block = blockIdx.x == 0;
+  pdl_wait_and_release();
+
+  uint32_t bits = 0;
+  const int32_t free_in = *p.n_free;
+  const int32_t free0 = min(max(free_in, 0), p.free_len);
+  if (free0 != free_in) bits |= kRowBadShape;
+  const int64_t room = static_cast<int64_t>(p.max_blocks) * p.block_size;
+
+  int32_t want[kTablesPerThread], need[kTablesPerThread], out_len[kTablesPerThread];
+  uint32_t gone = 0;  // requests that end here (bit j)
+  int64_t sum[3] = {0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < kTablesPerThread; ++j) {
+    want[j] = need[j] = out_len[j] = 0;
+    const int i = i0 + j;
+    if (j < per && i < n) {
+      const int32_t len = p.lens[i];
+      const int32_t a = p.n_new ? p.n_new[i] : 1;
+      const bool fin = p.finished && p.finished[i];
+      const bool bad = len < 0 || len > room || (!fin && (a < 0 || len + static_cast<int64_t>(a) > room));
+      out_len[j] = len;
+      len_of[i] = bad ? 0 : len;
+      int32_t held = 0;
+      if (bad) {
+        bits |= kRowBadShape;
+      } else {
+        held = static_cast<int32_t>(p.by_block.div(static_cast<uint32_t>(len)));
+        if (held * static_cast<int64_t>(p.block_size) < len) ++held;
+        if (fin) {
+          gone |= 1u << j;
+          sum[2] += held;
+          need[j] = held;
+        } else {
+          want[j] = a;
+          const int32_t end = len + a;
+          int32_t all = static_cast<int32_t>(p.by_block.div(static_cast<uint32_t>(end)));
+          if (all * static_cast<int64_t>(p.block_size) < end) ++all;
+          need[j] = all - held;
+          sum[0] += need[j];
+          sum[1] += a;
+        }
+      }
+    }
+  }
+  int64_t before[3], total[3];
+  block_scan<3>(sum, before, total, part);
+
+  // the stack with the released blocks on it; entries past its end are dropped
+  const int64_t top64 = free0 + total[2];
+  const int32_t top = static_cast<int32_t>(min(top64, static_cast<int64_t>(p.free_len)));
+  if (top < top64) bits |= kRowBadShape;
+  const int32_t released = top - free0;
+
+  int64_t blocks = before[0], tokens = before[1], rel = before[2];
+  int64_t got[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < kTablesPerThread; ++j) {
+    const int i = i0 + j;
+    if (j < per && i < n) {
+      rel_start[i] = static_cast<int32_t>(min(rel, static_cast<int64_t>(released)));
+      if ((gone >> j) & 1u) {
+        rel += need[j];
+        need[j] = 0;
+        out_len[j] = 0;
+      } else {
+        blocks += need[j];
+        tokens += want[j];
+        const bool given = want[j] == 0 || ((need[j] == 0 || blocks <= top) && tokens <= p.max_tokens);
+        if (!given) {
+          want[j] = need[j] = 0;
+          bits |= kRowNoBlocks;
+        }
+        got[0] += want[j];
+        got[1] += need[j];
+      }
+    }
+  }
+  int64_t at[2], all[2];
+  block_scan<2>(got, at, all, part);
+  const int32_t n_tokens = static_cast<int32_t>(all[0]), n_given = static_cast<int32_t>(all[1]);
+  int32_t tok = static_cast<int32_t>(at[0]), blk = static_cast<int32_t>(at[1]);
+#pragma unroll
+  for (int j = 0; j < kTablesPerThread; ++j) {
+    const int i = i0 + j;
+    if (j < per && i < n) {
+      tok_start[i] = tok;
+      blk_start[i] = blk;
+      if (first_block) {
+        p.token_starts[i] = tok;
+        p.lens_out[i] = out_len[j] + want[j];
+      }
+      tok += want[j];
+      blk += need[j];
+    }
+  }
+  if (t == 0) {
+    tok_start[n] = n_tokens;
+    blk_start[n] = n_given;
+    rel_start[n] = released;
+    if (first_block) {
+      p.token_starts[n] = n_tokens;
+      *p.n_free_out = top - n_given;
+    }
+  }
+  if (!first_block) bits = 0;  // one report per call
+  __syncthreads();
+
+  // entry x of the blocks that the call releases
+  const auto released_block = [&](int32_t x) {
+    const int r = last_start(rel_start, n, x);
+    return p.block_table[r * p.table_stride + (x - rel_start[r])];
+  };
+  // entry x of the stack as the releases leave it (read from the tables, so
+  // that no thread waits for the stores of another)
+  const auto stack_at = [&](int32_t x) {
+    return x < free0 ? p.free_blocks[x] : released_block(x - free0);
+  };
+  const auto held_of = [&](int32_t len) {
+    const int32_t b = static_cast<int32_t>(p.by_block.div(static_cast<uint32_t>(len)));
+    return b * static_cast<int64_t>(p.block_size) < len ? b + 1 : b;
+  };
+
+  const int32_t step = static_cast<int32_t>(gridDim.x) * nt;
+  const int32_t g0 = static_cast<int32_t>(blockIdx.x) * nt + t;
+  for (int64_t x = g0; x < released; x += step)
+    p.free_blocks[free0 + x] = released_block(static_cast<int32_t>(x));
+  for (int64_t x = g0; x < n_given; x += step) {
+    const int r = last_start(blk_start, n, static_cast<int32_t>(x));
+    const int32_t j = held_of(len_of[r]) + (static_cast<int32_t>(x) - blk_start[r]);
+    p.block_table[r * p.table_stride + j] = stack_at(top - 1 - static_cast<int32_t>(x));
+  }
+  for (int64_t x = g0; x < p.max_tokens; x += step) {
+    int64_t slot = -1;
+    int32_t pos = -1, r = -1;
+    if (x < n_tokens) {
+      r = last_start(tok_start, n, static_cast<int32_t>(x));
+      const int32_t len = len_of[r];
+      pos = len + (static_cast<int32_t>(x) - tok_start[r]);
+      const int32_t b = static_cast<int32_t>(p.by_block.div(static_cast<uint32_t>(pos)));
+      const int32_t held = held_of(len);
+      const int32_t id = b < held ? p.block_table[r * p.table_stride + b]
+                                  : stack_at(top - 1 - (blk_start[r] + b - held));
+      if (id >= 0 && id < p.n_blocks)
+        slot = static_cast<int64_t>(id) * p.block_size + (pos - b * p.block_size);
+      else
+        bits |= kRowBadBlock;
+    }
+    p.slots[x] = slot;
+    if (p.positions) p.positions[x] = pos;
+    if (p.requests) p.requests[x] = r;
+  }
+  if (bits) atomicOr(p.status, bits);
+}
+
+// The end of an update in place by several blocks: the new lengths and the
+// free count go from the scratch array to their places.
+__global__ void kv_tables_store_kernel(const int32_t *lens_new, int32_t *lens, int32_t n,
+                                       const int32_t *free_new, int32_t *n_free) {
+  pdl_wait_and_release();
+  const int i = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);
+  if (lens && i < n) lens[i] = lens_new[i];
+  if (n_free && i == 0) *n_free = *free_new;
+}
+
+// --------------------------------------------------------------------------
+// Writing new tokens' keys and values
+// --------------------------------------------------------------------------
+constexpr int kAppendThreads = 256;
+constexpr int kAppendUnroll = 4;
+
+struct KvAppendParams {
+  const void *src[2];               // K and V of the new tokens
+  int64_t src_token[2], src_head[2];  // strides in elements
+  void *dst[2];
+  int64_t dst_block[2], dst_token[2], dst_head[2];
+  const float *scale[2];            // one per key head, null: 1 (e4m3 only)
+  const int64_t *slots;
+  int64_t n_slots;                  // n_blocks * block_size
+  int64_t block_size;
+  int32_t n_tokens;
+  int32_t heads;
+  int32_t tokens_per_block;         // CTA
+  FastDiv by_token, by_head;        // units of VEC elements per token, per head
+  uint32_t *status;
+};
+
+// Eight or sixteen elements as they are stored.
+template <class Src, class Dst, int VEC, bool WIDE>
+struct AppendUnit {
+  static constexpr int kWords = VEC * static_cast<int>(sizeof(Src)) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const Src *p) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    } else {
+      // element by element
+      Src e[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = p[i];
+      memcpy(w, e, sizeof w);
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(Src) == 2)
+      return __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+    else
+      return __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ void store(Dst *p, float scale) const {
+    if constexpr (sizeof(Src) == sizeof(Dst)) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i)
+        reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+      // x / scale in 32 bits, then the nearest e4m3 value (ties to even, at
+      // most 448 in size): the only rounding to 8 bits
+      static_assert(VEC == 16, "sixteen 8-bit values per 16-byte store");
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+            make_float2(__fdiv_rn(at(4 * i), scale), __fdiv_rn(at(4 * i + 1), scale)), __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+            make_float2(__fdiv_rn(at(4 * i + 2), scale), __fdiv_rn(at(4 * i + 3), scale)), __NV_SATFINITE, __NV_E4M3);
+        o[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+      }
+      *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+};
+
+// A thread moves kAppendUnroll units of VEC elements, each of K and of V, so
+// that eight 16-byte loads are in flight; a CTA takes whole tokens.  A skipped
+// token's rows are not read.  Bound by DRAM: each element is read once and
+// written once.
+template <class Src, class Dst, int VEC, bool WIDE>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppendParams p) {
+  pdl_wait_and_release();
+  const int32_t t0 = static_cast<int32_t>(blockIdx.x) * p.tokens_per_block;
+  const int32_t nt = min(p.tokens_per_block, p.n_tokens - t0);
+  const uint32_t units = static_cast<uint32_t>(nt) * p.by_token.d;
+  uint32_t bits = 0;
+  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kAppendThreads * kAppendUnroll) {
+    AppendUnit<Src, Dst, VEC, WIDE> k[kAppendUnroll], v[kAppendUnroll];
+    int64_t slot[kAppendUnroll];
+#pragma unroll
+    for (int j = 0; j < kAppendUnroll; ++j) {
+      const uint32_t u = u0 + j * kAppendThreads;
+      slot[j] = u < units ? p.slots[t0 + p.by_token.div(u)] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kAppendUnroll; ++j) {
+      if (slot[j] >= p.n_slots) {
+        bits |= kRowBadSlot;
+        slot[j] = -1;
+      }
+      if (slot[j] >= 0) {
+        const uint32_t u = u0 + j * kAppendThreads;
+        const uint32_t t = p.by_token.div(u), in = u - t * p.by_token.d;
+        const uint32_t h = p.by_head.div(in), e = (in - h * p.by_head.d) * VEC;
+        const int64_t token = t0 + static_cast<int64_t>(t);
+        k[j].load(static_cast<const Src *>(p.src[0]) + token * p.src_token[0] + h * p.src_head[0] + e);
+        v[j].load(static_cast<const Src *>(p.src[1]) + token * p.src_token[1] + h * p.src_head[1] + e);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAppendUnroll; ++j) {
+      if (slot[j] >= 0) {
+        const uint32_t u = u0 + j * kAppendThreads;
+        const uint32_t in = u - p.by_token.div(u) * p.by_token.d;
+        const uint32_t h = p.by_head.div(in), e = (in - h * p.by_head.d) * VEC;
+        const int64_t blk = slot[j] / p.block_size, off = slot[j] - blk * p.block_size;
+        Dst *kd = static_cast<Dst *>(p.dst[0]) + blk * p.dst_block[0] + off * p.dst_token[0] + h * p.dst_head[0] + e;
+        Dst *vd = static_cast<Dst *>(p.dst[1]) + blk * p.dst_block[1] + off * p.dst_token[1] + h * p.dst_head[1] + e;
+        k[j].store(kd, p.scale[0] ? p.scale[0][h] : 1.0f);
+        v[j].store(vd, p.scale[1] ? p.scale[1][h] : 1.0f);
+      }
+    }
+  }
+  if (bits) atomicOr(p.status, bits);
+}
+
+}  // namespace ts

@@ -14,32 +14,11 @@
 #include "../../include/ts_sampler.h"
 #include "ts_cluster.cuh"
 #include "ts_device.cuh"
+#include "ts_host.h"
 #include "ts_lmhead.cuh"
 #include "ts_split.cuh"
 #include "ts_warp.cuh"
 #include "ts_wide.cuh"
-
-struct ts_sampler {
-  int device;
-  int cap;
-  int num_sms;
-  int force_path;     // 0 auto, 1 warps per row, 2 CTA/cluster per row, 3 wide cluster, 4 split
-  int force_cluster;  // 0 auto, else CTAs per row
-  int pdl;            // launch with programmatic stream serialization
-  int wide_exact;     // wide path: always take the exact path (testing)
-  int force_wpr;      // warp-per-row path: 0 auto, else warps per row (1, 2, 4)
-  int fail_launch;    // tests: the split path's launch of this index (2 or 3) fails once
-  uint32_t *status;   // device word (first of two: the status word, then the ticket)
-  uint32_t *ticket;   // the warp path's fused step advance: blocks done so far
-  int occ_warp[2][5][3];  // resident blocks per SM of each warp-path variant
-  int occ_seg[2];         // of the segmented 16-column, one-warp-per-row variant
-  int occ_seg32;          // of the fp32 32-column variant (16 columns staged at a time)
-  void *ws;           // split wide path workspace (ts_reserve), or null
-  size_t ws_bytes;
-  int ws_rows;        // row records it holds
-  int ws_units;       // unit records it holds
-  int ws_vocab;       // widest row it was sized for
-};
 
 // Scratch of ts_sample_noalloc, for callers that cannot allocate device
 // memory: the split path's workspace, after a 256-byte slot that takes the row
@@ -48,14 +27,16 @@ struct ts_sampler {
 // the array; its device address comes from cudaGetSymbolAddress.
 static __device__ __align__(256) unsigned char g_noalloc_scratch[TS_NOALLOC_SCRATCH_BYTES];
 
-namespace {
+static thread_local char g_last_error[256] = "";
 
-thread_local char g_last_error[256] = "";
-
-ts_status cuda_fail(cudaError_t e, const char *what) {
+ts_status ts_host::cuda_fail(cudaError_t e, const char *what) {
   std::snprintf(g_last_error, sizeof g_last_error, "%s: %s", what, cudaGetErrorString(e));
   return TS_ERR_CUDA;
 }
+
+namespace {
+
+using ts_host::cuda_fail;
 
 int cap_of(int requested) {
   if (requested == 0) return 64;
@@ -687,6 +668,8 @@ ts_status ts_create(int device, int max_top_k, ts_sampler **out) {
   s->ws_rows = 0;
   s->ws_units = 0;
   s->ws_vocab = 0;
+  s->kv = nullptr;
+  s->kv_ctas = 0;
   ts_status rc = TS_OK;
   e = cudaDeviceGetAttribute(&s->num_sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) rc = cuda_fail(e, "cudaDeviceGetAttribute");
@@ -722,6 +705,8 @@ ts_status ts_destroy(ts_sampler *s) {
     const cudaError_t e2 = cudaFree(s->ws);
     if (e == cudaSuccess) e = e2;
   }
+  const cudaError_t e3 = ts_host::kv_free(s);
+  if (e == cudaSuccess) e = e3;
   cudaSetDevice(prev);
   delete s;
   return e == cudaSuccess ? TS_OK : cuda_fail(e, "cudaFree");
@@ -963,6 +948,11 @@ ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value) {
   if (option == TS_OPT_WARPS_PER_ROW) {
     if (value != 0 && value != 1 && value != 2 && value != 4) return TS_ERR_INVALID_ARG;
     s->force_wpr = value;
+    return TS_OK;
+  }
+  if (option == TS_OPT_KV_CTAS) {
+    if (value < 0) return TS_ERR_INVALID_ARG;
+    s->kv_ctas = value;
     return TS_OK;
   }
   if (option == TS_OPT_FAIL_LAUNCH) {

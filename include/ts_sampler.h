@@ -63,7 +63,8 @@ typedef enum {
   TS_ERR_NO_MEMORY = 4     /* host or device allocation failed in ts_create */
 } ts_status;
 
-typedef enum { TS_DTYPE_F32 = 0, TS_DTYPE_BF16 = 1 } ts_dtype;
+/* TS_DTYPE_E4M3 (8 bits, no infinities, at most 448): key-value caches only. */
+typedef enum { TS_DTYPE_F32 = 0, TS_DTYPE_BF16 = 1, TS_DTYPE_E4M3 = 2 } ts_dtype;
 
 /* Per-row error bits.  A row with an error gets out_ids = -1, out_eos = 0
  * and no write-back; the bit is ORed into the sampler's device status word
@@ -72,7 +73,7 @@ typedef enum { TS_DTYPE_F32 = 0, TS_DTYPE_BF16 = 1 } ts_dtype;
                                or row_stream outside [0, n_streams) */
 #define TS_ROW_BAD_PARAM 2u /* temperature NaN or +-inf, or top_p NaN */
 #define TS_ROW_NONFINITE 4u /* a NaN or +inf logit, or no finite logit */
-#define TS_ROW_BAD_SLOT 8u  /* feedback_slot >= feedback_len */
+#define TS_ROW_BAD_SLOT 8u  /* feedback_slot >= feedback_len, or a cache slot past the cache */
 
 /* Largest row width each dtype supports (TS_ERR_UNSUPPORTED above it). */
 #define TS_MAX_VOCAB_BF16 163840
@@ -382,6 +383,175 @@ ts_status ts_lm_head_logits(ts_sampler *s, const ts_lm_head *h, const ts_batch *
  * host-side refusal of the sampler is returned before the head launches. */
 ts_status ts_lm_head_sample(ts_sampler *s, const ts_lm_head *h, const ts_batch *b, void *stream);
 
+/* --------------------------------------------------------------------------
+ * The paged key-value cache in front of the LM head.
+ *
+ * The Drama 3 article ("两阶段共享一张卡") runs its codebook tower on paged
+ * attention that shares the backbone's block table; the calls below are that
+ * table, the cache's writes and the attention of a decode step:
+ *   ts_kv_tables        block tables and slot maps, built on the GPU from the
+ *                       requests' lengths,
+ *   ts_kv_append        new tokens' keys and values written at their slots,
+ *   ts_paged_attention  one new token per request against the whole cache.
+ * Like ts_sample they read no device memory on the host, never synchronise
+ * and never allocate, so that a step can be captured in a CUDA graph: tables
+ * once per step, then append and attention once per layer, then the LM head
+ * and the sampler, whose finish_reason array is the next step's `finished`.
+ * Row errors set bits of the sampler's status word and never trap. */
+
+/* Allocates the workspace of the calls below: the pieces that
+ * ts_paged_attention joins (about 40 MB) and, for ts_kv_tables calls that
+ * update in place, 4 bytes per request.  Call it before any stream capture and
+ * not concurrently with work on the sampler; a smaller request than the
+ * current size keeps it, 0 frees it.  ts_paged_attention and ts_kv_tables return
+ * TS_ERR_INVALID_ARG without it.  Calls share it: two calls on one sampler must
+ * not overlap on the GPU (order them on one stream or with events). */
+ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests);
+
+/* Block tables and slot maps.  The cache is n_blocks blocks of block_size
+ * tokens; request i's token at position t lies in block
+ * block_table[i * table_stride + t / block_size] at t mod block_size, and its
+ * slot is block * block_size + t mod block_size.  Unused blocks are a stack:
+ * free_blocks[0 .. *n_free), the top last.  With len_i = lens[i], a_i = n_new[i]
+ * (1 where n_new is NULL) and ceil(x) = blocks that x tokens take:
+ *   - a request with finished[i] != 0 ends: its ceil(len_i) blocks go on the
+ *     stack (requests in order, each request's in table order), its new length
+ *     is 0, n_new[i] is not looked at, and its table row is left as it is;
+ *   - another one gets need_i = ceil(len_i + a_i) - ceil(len_i) blocks, taken off
+ *     the top of the stack as the releases left it, requests in order, and its
+ *     new length is len_i + a_i;
+ *   - but nothing (and the status bit TS_ROW_NO_BLOCKS) where a_i > 0 and either
+ *     need_i > 0 and the needs of requests 0 .. i add up to more than the stack
+ *     holds, or a_0 + .. + a_i exceeds max_tokens (finished requests count 0).
+ * The new tokens are packed in request order: request i's start at
+ * token_starts[i], token_starts[n_requests] is their number, and token x has
+ * slots[x], positions[x] and requests[x]; entries from that number to max_tokens
+ * are -1, so that a captured ts_kv_append of max_tokens tokens skips them.
+ *
+ * Errors.  Host side: TS_ERR_INVALID_ARG for a NULL pointer (n_new, finished,
+ * lens_out, n_free_out, positions and requests may be NULL), a negative size, a
+ * table_stride below max_blocks, or output arrays that overlap their inputs in
+ * part; TS_ERR_UNSUPPORTED for more than TS_KV_MAX_REQUESTS requests,
+ * block_size above 65536, or max_blocks * block_size above TS_KV_MAX_LEN.  Per
+ * request: a negative length or a_i, or a length beyond max_blocks blocks, sets
+ * TS_ROW_BAD_SHAPE and leaves the request as it is without new tokens; a table
+ * or stack entry outside [0, n_blocks) gives its tokens slot -1 and
+ * TS_ROW_BAD_BLOCK.  *n_free outside [0, free_len] is clamped and releases past
+ * free_len are dropped, both with TS_ROW_BAD_SHAPE. */
+#define TS_KV_MAX_REQUESTS 8192
+#define TS_KV_MAX_LEN 2147482624
+#define TS_ROW_BAD_BLOCK 32u
+#define TS_ROW_NO_BLOCKS 64u
+typedef struct {
+  int32_t n_requests;        /* 0 is allowed: nothing runs */
+  int32_t block_size;        /* tokens per block */
+  int32_t n_blocks;          /* blocks in the cache */
+  int32_t max_blocks;        /* table entries per request */
+  int64_t table_stride;      /* entries from one request's table to the next */
+  int32_t *block_table;      /* updated in place */
+  const int32_t *lens;       /* [n_requests] tokens in the cache before the call */
+  int32_t *lens_out;         /* [n_requests] after it; NULL or lens: in place */
+  const int32_t *n_new;      /* [n_requests] or NULL: one each */
+  const uint8_t *finished;   /* [n_requests] or NULL: none (ts_batch.finish_reason) */
+  int32_t *free_blocks;      /* [free_len] the stack, updated in place */
+  int32_t free_len;
+  const int32_t *n_free;     /* [1] */
+  int32_t *n_free_out;       /* [1] NULL or n_free: in place */
+  int32_t max_tokens;        /* entries of the maps below */
+  int32_t *token_starts;     /* [n_requests + 1] */
+  int64_t *slots;            /* [max_tokens] */
+  int32_t *positions;        /* [max_tokens] or NULL */
+  int32_t *requests;         /* [max_tokens] or NULL */
+} ts_kv_tables_args;
+ts_status ts_kv_tables(ts_sampler *s, const ts_kv_tables_args *t, void *stream);
+
+/* A cache in device memory.  Element d of key head h of the token at `off` in
+ * block b is k[b * k_block_stride + off * k_token_stride + h * k_head_stride +
+ * d] (strides in elements; v alike), so that blocks may hold tokens before
+ * heads or heads before tokens.  k and v and every stride in bytes are
+ * multiples of 16, as is head_dim in bytes; head_dim is at most
+ * TS_KV_MAX_HEAD_DIM.  An e4m3 cache holds value / scale: k_scale and v_scale
+ * have one fp32 scale per key head (NULL: 1); the other types take none. */
+#define TS_KV_MAX_HEAD_DIM 256
+typedef struct {
+  void *k;
+  void *v;
+  int32_t dtype;             /* TS_DTYPE_F32, TS_DTYPE_BF16 or TS_DTYPE_E4M3 */
+  int32_t n_blocks;
+  int32_t block_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int64_t k_block_stride, k_token_stride, k_head_stride;
+  int64_t v_block_stride, v_token_stride, v_head_stride;
+  const float *k_scale;      /* [n_kv_heads] or NULL */
+  const float *v_scale;
+} ts_kv_cache;
+
+/* Writes token x's keys and values (k[x * k_token_stride + h * k_head_stride +
+ * d], strides in elements, any alignment) into the cache at slots[x]; a negative
+ * slot skips the token, whose rows are then not read.  The tokens have the
+ * cache's type, or for an e4m3 cache bf16 or fp32: x / scale is computed in fp32
+ * and rounded to the nearest e4m3 value (ties to even, values beyond 448 to
+ * 448 with their sign, NaN kept).  Tokens of one call have slots of their own.
+ * A slot past the cache sets TS_ROW_BAD_SLOT and is skipped.
+ * TS_ERR_INVALID_ARG for a NULL pointer, a negative size or a cache outside the
+ * rules above; TS_ERR_UNSUPPORTED for another pair of types. */
+typedef struct {
+  const void *k;
+  const void *v;
+  int32_t dtype;             /* TS_DTYPE_F32 or TS_DTYPE_BF16 */
+  int32_t n_tokens;          /* 0 is allowed: nothing runs */
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  const int64_t *slots;      /* [n_tokens] */
+} ts_kv_tokens;
+ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *t, void *stream);
+
+/* Attention of one query token per request over its lens[r] cached tokens (its
+ * own among them).  Query head h uses key head h / (n_heads / n_kv_heads).
+ * Token t of request r is attended if t < lens[r], t >= lens[r] - window (window
+ * 0: all) and key_mask[r * mask_stride + t] != 0 (NULL: all); what the cache
+ * holds in other places is not read.  With s_t = scale * q . k_t, then
+ * softcap * tanh(s_t / softcap) where softcap > 0:
+ *   out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),   m = max_t s_t,
+ *   lse = m + ln sum_t exp(s_t - m)   (natural logarithm; lse may be NULL).
+ * A head that attends to nothing gets out = 0 and lse = -inf.  Scores, maxima,
+ * sums and the outputs' sums are fp32; the output is rounded once to the
+ * queries' type.  Results depend on the lengths (how the work is cut and
+ * joined) but are the same in every run.
+ *
+ * Types: bf16 queries on a bf16 or e4m3 cache, fp32 queries on an fp32 cache
+ * (else TS_ERR_UNSUPPORTED).  q and out, and their strides in bytes, are
+ * multiples of 16; out may not overlap q.  TS_ERR_INVALID_ARG for a NULL
+ * pointer, a negative size or stride, n_heads not a multiple of n_kv_heads, a
+ * scale or softcap that is not finite, a negative softcap or window, a mask row
+ * shorter than max_blocks * block_size, or no workspace (ts_reserve_kv).
+ * TS_ERR_UNSUPPORTED for max_blocks * block_size above TS_KV_MAX_LEN.  Per
+ * request: a negative length or one beyond max_blocks blocks sets
+ * TS_ROW_BAD_SHAPE, an attended token's block outside [0, n_blocks) sets
+ * TS_ROW_BAD_BLOCK; the heads concerned get NaN. */
+typedef struct {
+  const void *q;             /* [n_requests][n_heads][head_dim] by strides */
+  void *out;                 /* the same */
+  float *lse;                /* [n_requests][n_heads] contiguous, or NULL */
+  int32_t dtype;             /* of q and out */
+  int32_t n_requests;        /* 0 is allowed: nothing runs */
+  int32_t n_heads;
+  int32_t max_blocks;        /* table entries per request */
+  int64_t q_request_stride, q_head_stride;      /* elements */
+  int64_t out_request_stride, out_head_stride;
+  const int32_t *block_table;
+  int64_t table_stride;
+  const int32_t *lens;       /* [n_requests] */
+  const uint8_t *key_mask;   /* or NULL */
+  int64_t mask_stride;
+  float scale;
+  float softcap;             /* 0: none */
+  int32_t window;            /* 0: none */
+} ts_paged_query;
+ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged_query *q,
+                             void *stream);
+
 /* step[i] += 1 for i < n_streams, on the device (graph-capturable).  Call it
  * after the step's ts_sample so that sibling rows of one stream share a step
  * (or set ts_batch.advance_steps, which does the same inside the call). */
@@ -422,6 +592,9 @@ ts_status ts_read_status(ts_sampler *s, uint32_t *bits, void *stream);
  * was queued, the call zeroes the rows' workspace records on the stream
  * before it returns, so the next call starts from clean counters. */
 #define TS_OPT_FAIL_LAUNCH 6
+/* TS_OPT_KV_CTAS: the number of CTAs that ts_paged_attention deals its work to
+ * (0 = automatic: what the GPU holds at once; more than that is cut to it). */
+#define TS_OPT_KV_CTAS 7
 ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value);
 
 /* Describes the kernel that ts_sample would launch for `b` (path 1 .. 4,

@@ -1,0 +1,62 @@
+"""The paged cache's C structs and their Python mirrors, and the plain 64-bit
+versions' own pins (no GPU)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import kv as okv
+from test_abi import _c_layout
+
+
+def test_structs_match_the_header(tmp_path):
+    import codebook_token_sampling_gb300 as ts
+    for struct, mirror in (("ts_kv_tables_args", ts.TsKvTables), ("ts_kv_cache", ts.TsKvCache),
+                           ("ts_kv_tokens", ts.TsKvTokens), ("ts_paged_query", ts.TsPagedQuery)):
+        fields = [name for name, _ in mirror._fields_]
+        want = [getattr(mirror, f).offset for f in fields] + [ctypes.sizeof(mirror)]
+        assert _c_layout(tmp_path, struct, fields) == want, struct
+
+
+def test_e4m3_codes():
+    values = okv.e4m3_values()
+    assert values[0] == 0 and values[1] == 2.0 ** -9 and values[8] == 2.0 ** -6 and values[126] == 448
+    assert np.all(np.diff(values) > 0)
+    codes = np.arange(127, dtype=np.uint8)
+    assert np.array_equal(okv.to_e4m3(values), codes)
+    assert np.array_equal(okv.from_e4m3(codes), values)
+    assert okv.to_e4m3([1e9, -1e9, 1.0625, 1.1875]).tolist() == [126, 254, 56, 58]  # ties to even codes
+    torch = pytest.importorskip("torch")
+    x = np.random.default_rng(0).normal(0, 50, 5000).astype(np.float32)
+    want = torch.from_numpy(x).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(okv.to_e4m3(x), want)
+
+
+def test_tables_by_hand():
+    """Three requests of 2-token blocks: one ends (its block 5 goes on the
+    stack), one crosses a block, one stays inside its block."""
+    got = okv.tables([[4, -1], [5, -1], [6, -1]], [2, 2, 1], None, [0, 1, 0], [7, 8, -1, -1], 2, block_size=2, n_blocks=9,
+                     max_tokens=4)
+    assert got["block_table"].tolist() == [[4, 5], [5, -1], [6, -1]]
+    assert got["free_blocks"].tolist() == [7, 8, 5, -1] and got["n_free"] == 2
+    assert got["lens"].tolist() == [3, 0, 2] and got["token_starts"].tolist() == [0, 1, 1, 2]
+    assert got["slots"].tolist() == [10, 13, -1, -1] and got["positions"].tolist() == [2, 1, -1, -1]
+    assert got["requests"].tolist() == [0, 2, -1, -1] and got["status"] == 0
+
+
+def test_tables_without_blocks():
+    got = okv.tables([[-1], [0]], [0, 1], None, None, [], 0, block_size=2, n_blocks=1, max_tokens=2)
+    assert got["lens"].tolist() == [0, 2] and got["status"] == okv.NO_BLOCKS and got["slots"].tolist() == [1, -1]
+
+
+def test_attention_by_hand():
+    """Two keys with scores 0 and ln 3: weights 1/4 and 3/4."""
+    k = np.zeros((1, 2, 1, 1))
+    k[0, 1, 0, 0] = np.log(3)
+    v = np.array([8.0, 4.0]).reshape(1, 2, 1, 1)
+    got = okv.attention(np.ones((1, 1, 1)), k, v, np.array([[0]]), [2], scale=1.0, n_blocks=1)
+    assert np.isclose(got["out"][0, 0, 0], 5.0) and np.isclose(got["lse"][0, 0], np.log(4))
+    none = okv.attention(np.ones((1, 1, 1)), k, v, np.array([[0]]), [2], scale=1.0, n_blocks=1, key_mask=[[0, 0]])
+    assert none["out"][0, 0, 0] == 0 and none["lse"][0, 0] == -np.inf
+    last = okv.attention(np.ones((1, 1, 1)), k, v, np.array([[0]]), [2], scale=1.0, n_blocks=1, window=1)
+    assert last["out"][0, 0, 0] == 4.0
