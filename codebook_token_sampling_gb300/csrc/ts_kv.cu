@@ -55,13 +55,6 @@ bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) %
 // --------------------------------------------------------------------------
 // Paged attention's kernels
 // --------------------------------------------------------------------------
-// Stages per warp: three or four stages keep 100 KB and more of loads in
-// flight per SM at the CTAs that fit beside each other.
-template <class Core>
-constexpr int stages_of() {
-  return Core::kRowBytes * Core::kTok >= 4096 ? 3 : 4;
-}
-
 struct PagedKernel {
   const void *fn;
   uint32_t smem;
@@ -70,24 +63,28 @@ struct PagedKernel {
 
 template <class Core>
 PagedKernel paged_kernel(bool page16) {
-  constexpr int ns = stages_of<Core>();
+  constexpr int ns = 3;  // stages per warp
   static_assert(ts::PagedShape<Core, ns>::kSmem <= 226 * 1024, "shared memory of a CTA");
   return {page16 ? reinterpret_cast<const void *>(ts::paged_attention_kernel<Core, ns, true>)
                  : reinterpret_cast<const void *>(ts::paged_attention_kernel<Core, ns, false>),
           ts::PagedShape<Core, ns>::kSmem, 0};
 }
 
-// kind 0: bf16 cache, 1: e4m3, 2 .. 5: f32 with 1, 2, 4 or 8 rows; width 0, 1,
-// 2: 64, 128 or 256 elements per row.
-constexpr int kPagedKinds = 6;
+// kind 0, 1: bf16 cache with up to 8 or 16 query heads per item, 2, 3: e4m3, 4
+// .. 7: f32 with up to 1, 2, 4 or 8; width 0, 1, 2: up to 64, 128 or 256
+// elements per row.  A step takes 4 KB of keys where that is 16 or 32 tokens.
+constexpr int kPagedKinds = 8;
 template <int DP>
 PagedKernel paged_kernel_of(int kind, bool page16) {
+  constexpr int kt = DP <= 64 ? 2 : 1;
   switch (kind) {
-    case 0: return paged_kernel<ts::MmaCore<false, DP>>(page16);
-    case 1: return paged_kernel<ts::MmaCore<true, DP>>(page16);
-    case 2: return paged_kernel<ts::FmaCore<1, DP>>(page16);
-    case 3: return paged_kernel<ts::FmaCore<2, DP>>(page16);
-    case 4: return paged_kernel<ts::FmaCore<4, DP>>(page16);
+    case 0: return paged_kernel<ts::MmaCore<false, DP, 1, kt>>(page16);
+    case 1: return paged_kernel<ts::MmaCore<false, DP, 2, kt>>(page16);
+    case 2: return paged_kernel<ts::MmaCore<true, DP, 1, 2>>(page16);
+    case 3: return paged_kernel<ts::MmaCore<true, DP, 2, 2>>(page16);
+    case 4: return paged_kernel<ts::FmaCore<1, DP>>(page16);
+    case 5: return paged_kernel<ts::FmaCore<2, DP>>(page16);
+    case 6: return paged_kernel<ts::FmaCore<4, DP>>(page16);
     default: return paged_kernel<ts::FmaCore<8, DP>>(page16);
   }
 }
@@ -380,11 +377,12 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   const int group = q->n_heads / c->n_kv_heads;
   int kind, rows;
   if (!f32) {
-    kind = c->dtype == TS_DTYPE_E4M3 ? 1 : 0;
-    rows = ts::kPagedRows;
+    rows = group <= 8 ? 8 : 16;
+    kind = (c->dtype == TS_DTYPE_E4M3 ? 2 : 0) + (rows == 16 ? 1 : 0);
   } else {
-    kind = group == 1 ? 2 : group == 2 ? 3 : group <= 4 ? 4 : 5;
-    rows = 1 << (kind - 2);
+    const int size = group == 1 ? 0 : group == 2 ? 1 : group <= 4 ? 2 : 3;
+    rows = 1 << size;
+    kind = 4 + size;
   }
   const int width = c->head_dim <= 64 ? 0 : c->head_dim <= 128 ? 1 : 2;
   const PagedKernel &k = g_paged[s->device].kernel[kind][width][c->block_size % ts::kPagedPage == 0];

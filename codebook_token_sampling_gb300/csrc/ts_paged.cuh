@@ -36,9 +36,9 @@ constexpr int kPagedRows = 16;                       // most query heads per ite
 constexpr int kPagedMaxDim = 256;
 
 // A piece of an item in the workspace: kPagedRows rows of kPagedMaxDim sums,
-// and each row's maximum and sum.
+// each row's maximum and sum, and which item it is.
 struct PagedDesc {
-  int32_t request, head, parts, pad;  // parts > 1: the item starts in this CTA
+  int32_t request, head, piece, parts;  // parts > 1: the item starts in this CTA
 };
 constexpr size_t kPagedAccBytes = sizeof(float) * kPagedRows * kPagedMaxDim;
 constexpr size_t paged_workspace_bytes(int ctas) {
@@ -108,6 +108,12 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// an 8 x 8 piece of 16-bit values, transposed
+__device__ __forceinline__ uint32_t transposed_8x8(uint32_t x) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
 // two e4m3 values as two f16 values (exact)
 __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t x) {
   uint32_t d;
@@ -126,280 +132,340 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   return d;
 }
 
-// A stage row's 16-byte chunk c sits at chunk c ^ (a function of the row), so
-// that the eight rows of a matrix load (or the lanes of a vector load) fall on
-// different banks.
-// LANES: lanes that read one row side by side (0: matrix loads).
+// A stage row's 16-byte chunk c sits at chunk c ^ stage_xor(row), so that the
+// eight rows of a matrix load (or the lanes of a vector load) fall on different
+// banks.  stage_xor(a + b) = stage_xor(a) ^ stage_xor(b) where a and b share no
+// bits.  LANES: lanes that read one row side by side (0: matrix loads).
+template <int ROW_BYTES, int LANES>
+__host__ __device__ __forceinline__ constexpr int stage_xor(int row) {
+  if constexpr (LANES > 0) return LANES * (row & (8 / LANES - 1));
+  else return ROW_BYTES >= 128 ? row & 7 : (row >> 1) & 3;
+}
 template <int ROW_BYTES, int LANES>
 __device__ __forceinline__ uint32_t stage_at(int row, int chunk) {
-  constexpr int kChunks = ROW_BYTES / 16;
-  int c;
-  if constexpr (LANES > 0) c = chunk ^ (LANES * (row & (8 / LANES - 1)));
-  else if constexpr (kChunks >= 8) c = chunk ^ (row & 7);
-  else c = chunk ^ ((row >> 1) & 3);
-  return static_cast<uint32_t>(row * ROW_BYTES + c * 16);
+  return static_cast<uint32_t>(row * ROW_BYTES + ((chunk ^ stage_xor<ROW_BYTES, LANES>(row)) << 4));
 }
 
 // --------------------------------------------------------------------------
-// One warp's arithmetic on the tensor cores (bf16 and e4m3 caches): 16 query
-// heads x 16 tokens x DP elements.  Rows past the item's heads are zero.
+// One warp's arithmetic on the tensor cores (bf16 and e4m3 caches).  Tokens
+// are the products' rows and query heads their columns, eight at a time (NT
+// groups of eight): S^T = K Q^T, then O^T = V^T P^T, so that up to eight query
+// heads per key head cost one product each and few registers.  A step takes 16
+// KT tokens.  Columns past the item's heads are zero.
 // --------------------------------------------------------------------------
-template <bool E4M3, int DP>
+template <bool E4M3, int DP, int NT, int KT>
 struct MmaCore {
-  static constexpr int kRows = 16;
-  static constexpr int kTok = 16;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kTok = 16 * KT;
   static constexpr int kPer = 0;
   static constexpr bool kFma = false;
   static constexpr int kElemBytes = E4M3 ? 1 : 2;
   static constexpr int kRowBytes = DP * kElemBytes;
-  static constexpr uint32_t kQBytes = 0;     // shared memory of the CTA's queries
-  static constexpr uint32_t kWarpBytes = 0;  // of a warp's own
-  static constexpr int kKSteps = DP / 16;
+  static constexpr int kDim = DP;
+  static constexpr int kSteps = DP / 16;
+  // wide rows leave no registers for the queries: one copy in shared memory
+  static constexpr bool kSharedQ = DP > 128;
+  static constexpr uint32_t kQBytes = kSharedQ ? NT * kSteps * 32 * 8 : 0;
+  static constexpr uint32_t kWarpBytes = 0;  // shared memory of a warp's own
 
-  uint32_t qf[kKSteps][4];
-  float o[DP / 8][4];
-  float m[2], l[2];  // rows g and g + 8; l: this lane's tokens only
-  float sc[2];       // score factor of the rows
+  // lane = 4 g + tg
+  uint32_t qf[NT][kSharedQ ? 1 : kSteps][2];  // head 8 n + g
+  uint32_t q_at;                   // of this lane's share of the shared copy
+  float o[NT][kSteps][4];          // heads 8 n + 2 tg + (0, 1)
+  float m[NT][2], l[NT][2], sc[NT][2];  // of those heads; l: this lane's tokens only
+
+  // The queries' words of group n, step kk.
+  __device__ __forceinline__ void query(int n, int kk, uint32_t (&x)[2]) const {
+    if constexpr (kSharedQ)
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                   : "=r"(x[0]), "=r"(x[1]) : "r"(q_at + (n * kSteps + kk) * 256) : "memory");
+    else
+      x[0] = qf[n][kk][0], x[1] = qf[n][kk][1];
+  }
 
   __device__ __forceinline__ void begin(const PagedParams &p, const uint16_t *q, int rows,
-                                        float k_scale, void *) {
+                                        float k_scale, void *shared) {
     const int lane = static_cast<int>(lane_id()), g = lane >> 2, tg = lane & 3;
+    const int warp = static_cast<int>(threadIdx.x) >> 5;
     const float unit = p.softcap > 0.0f ? p.scale * k_scale : p.scale * k_scale * kLog2e;
-    const uint16_t *row[2] = {q + g * p.q_head, q + (g + 8) * p.q_head};
-    const bool real[2] = {g < rows, g + 8 < rows};
-    if constexpr (!E4M3) {
+    if constexpr (kSharedQ)
+      q_at = static_cast<uint32_t>(__cvta_generic_to_shared(shared)) + lane * 8;
 #pragma unroll
-      for (int kk = 0; kk < kKSteps; ++kk) {
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const int c = kk * 16 + 2 * tg + (a >> 1) * 8;
-          qf[kk][a] = real[a & 1] && c < p.dim
-                          ? *reinterpret_cast<const uint32_t *>(row[a & 1] + c) : 0u;
+    for (int n = 0; n < NT; ++n) {
+      const uint16_t *row = q + (8 * n + g) * p.q_head;
+      const bool real = 8 * n + g < rows;
+      const auto keep = [&](int kk, uint32_t x, uint32_t y) {
+        if constexpr (kSharedQ) {
+          if ((kk & 3) == warp)
+            *reinterpret_cast<uint2 *>(static_cast<char *>(shared) + (n * kSteps + kk) * 256 + lane * 8) =
+                make_uint2(x, y);
+        } else {
+          qf[n][kk][0] = x;
+          qf[n][kk][1] = y;
         }
-      }
-      sc[0] = sc[1] = unit;
-    } else {
-      // The cache's values are exact in f16, a bf16 query is not in f16's
-      // range: each row is divided by a power of two that brings its largest
-      // element into [1, 2).  What f16 then drops is below 2^-25 of that.
-      // Elements 4 tg .. 4 tg + 3 of a 16-element step stand in the places
-      // 2 tg, 2 tg + 1, 2 tg + 8, 2 tg + 9, as the keys' bytes do.
+      };
+      if constexpr (!E4M3) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint2 raw[kKSteps];
+        for (int kk = 0; kk < kSteps; ++kk) {
+          const int c = kk * 16 + 2 * tg;
+          keep(kk, real && c < p.dim ? *reinterpret_cast<const uint32_t *>(row + c) : 0u,
+               real && c + 8 < p.dim ? *reinterpret_cast<const uint32_t *>(row + c + 8) : 0u);
+        }
+        sc[n][0] = sc[n][1] = unit;
+      } else {
+        // The cache's values are exact in f16, a bf16 query is not in f16's
+        // range: each row is divided by a power of two that brings its largest
+        // element into [1, 2).  What f16 then drops is below 2^-25 of that.
+        // Elements 4 tg .. 4 tg + 3 of a 16-element step stand in the places
+        // 2 tg, 2 tg + 1, 2 tg + 8, 2 tg + 9, as the keys' bytes do.
+        const auto raw_at = [&](int kk) {
+          const int c = kk * 16 + 4 * tg;
+          return real && c < p.dim ? *reinterpret_cast<const uint2 *>(row + c) : make_uint2(0u, 0u);
+        };
+        const auto low = [](uint32_t w) { return __uint_as_float(w << 16); };
+        const auto high = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
         float big = 0.0f;
 #pragma unroll
-        for (int kk = 0; kk < kKSteps; ++kk) {
-          const int c = kk * 16 + 4 * tg;
-          raw[kk] = real[h] && c < p.dim ? *reinterpret_cast<const uint2 *>(row[h] + c)
-                                         : make_uint2(0u, 0u);
-          big = fmaxf(big, fmaxf(fmaxf(fabsf(__uint_as_float(raw[kk].x << 16)),
-                                       fabsf(__uint_as_float(raw[kk].x & 0xFFFF0000u))),
-                                 fmaxf(fabsf(__uint_as_float(raw[kk].y << 16)),
-                                       fabsf(__uint_as_float(raw[kk].y & 0xFFFF0000u)))));
+        for (int kk = 0; kk < kSteps; ++kk) {
+          const uint2 raw = raw_at(kk);
+          big = fmaxf(big, fmaxf(fmaxf(fabsf(low(raw.x)), fabsf(high(raw.x))),
+                                 fmaxf(fabsf(low(raw.y)), fabsf(high(raw.y)))));
         }
         big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
         const int e = big > 0.0f && big < INFINITY ? ilogbf(big) : 0;
-        const auto half_of = [&](uint32_t w) {
-          return f16x2_of(scalbnf(__uint_as_float(w << 16), -e),
-                          scalbnf(__uint_as_float(w & 0xFFFF0000u), -e));
-        };
 #pragma unroll
-        for (int kk = 0; kk < kKSteps; ++kk) {
-          qf[kk][h] = half_of(raw[kk].x);
-          qf[kk][2 + h] = half_of(raw[kk].y);
+        for (int kk = 0; kk < kSteps; ++kk) {
+          const uint2 raw = raw_at(kk);
+          keep(kk, f16x2_of(scalbnf(low(raw.x), -e), scalbnf(high(raw.x), -e)),
+               f16x2_of(scalbnf(low(raw.y), -e), scalbnf(high(raw.y), -e)));
         }
-        sc[h] = scalbnf(unit, e);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          sc[n][h] = scalbnf(unit, __shfl_sync(0xFFFFFFFFu, e, 4 * (2 * tg + h)));
       }
+#pragma unroll
+      for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][d][e] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
     }
-#pragma unroll
-    for (int n = 0; n < DP / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.0f;
+    if constexpr (kSharedQ) __syncthreads();
   }
 
-  __device__ __forceinline__ void poison() { l[0] = l[1] = __int_as_float(0x7FC00000); }
+  __device__ __forceinline__ void poison() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) l[n][0] = l[n][1] = __int_as_float(0x7FC00000);
+  }
 
-  // 16 tokens: K rows at shared address ks, V rows at vs, bit t of `valid` set
+  // kTok tokens: K rows at shared address ks, V rows at vs, bit t of `valid` set
   // where token t is attended (the others' rows are zero)
   __device__ __forceinline__ void step(const PagedParams &p, uint32_t ks, uint32_t vs,
                                        uint32_t valid, void *) {
-    const int lane = static_cast<int>(lane_id()), tg = lane & 3;
-    float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-    if constexpr (!E4M3) {
-      const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+    const int lane = static_cast<int>(lane_id()), g = lane >> 2;
+    // rows 0-7 | 8-15 by lane bit 3, chunk by bit 4
+    const int row = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+    float s[KT][NT][4];
+    // one chain of products would be as long as the row: two halves of it side
+    // by side where there is nothing else to interleave
+    constexpr int kChains = KT * NT == 1 ? 2 : 1;
+    float s2[NT][4];
 #pragma unroll
-      for (int kk = 0; kk < kKSteps; ++kk) {
-        uint32_t b[4];
-        ldmatrix_x4_at(b, ks + stage_at<kRowBytes, 0>(row, 2 * kk + half));
-        mma_bf16_16816(s[0], qf[kk], b[0], b[1]);
-        mma_bf16_16816(s[1], qf[kk], b[2], b[3]);
-      }
-    } else {
-      const int row = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int k2 = 0; k2 < kKSteps / 2; ++k2) {
-        uint32_t b[4];
-        ldmatrix_x4_at(b, ks + stage_at<kRowBytes, 0>(row, 2 * k2 + half));
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma_f16_16816(s[e & 1], qf[2 * k2 + (e >> 1)], f16x2_of_e4m3x2(b[e]),
-                        f16x2_of_e4m3x2(b[e] >> 16));
-      }
-    }
-    // scores in units of ln 2, unattended ones at -inf
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = s[n][e] * sc[e >> 1];
-        if (p.softcap > 0.0f) x = p.softcap * tanhf(x / p.softcap) * kLog2e;
-        s[n][e] = x;
-      }
-    if (valid != 0xFFFFu) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!((valid >> (n * 8 + 2 * tg + (e & 1))) & 1u)) s[n][e] = -INFINITY;
-    }
-    float base[2];
-    bool moved = false;
-    float drop[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float x = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-      x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-      x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-      const float top = fmaxf(m[h], x);
-      base[h] = top == -INFINITY ? 0.0f : top;  // a row with nothing yet
-      drop[h] = exp2_from(m[h], base[h]);
-      moved |= top != m[h];
-      m[h] = top;
-    }
-    if (__any_sync(0xFFFFFFFFu, moved)) {
-#pragma unroll
-      for (int n = 0; n < DP / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] *= drop[e >> 1];
-      l[0] *= drop[0];
-      l[1] *= drop[1];
-    }
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[n][e] = exp2f(s[n][e] - base[e >> 1]);
-        l[e >> 1] += s[n][e];
-      }
-    // The weights as the products' left side.  bf16 values carry V: a weight
-    // goes in as the sum of two bf16 numbers, its upper half and what is left,
-    // so that less than 2^-16 of it is lost and the output's own rounding stays
-    // the largest error.  The second number is kept above zero (by 2^-20 of the
-    // weight): an attended infinity in V then comes out as one, not as the NaN
-    // of 0 times it.  An f16 weight (e4m3 values) keeps 11 bits, enough for the
-    // same, and e4m3 has no infinities.
-    uint32_t a[4], a2[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = s[i >> 1][2 * (i & 1)], y = s[i >> 1][2 * (i & 1) + 1];
-      if constexpr (E4M3) {
-        a[i] = f16x2_of(x, y);
-      } else {
-        const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
-        a[i] = __byte_perm(ux, uy, 0x7632);
-        a2[i] = bf16x2_of(fmaf(x, 0x1p-20f, x - __uint_as_float(ux & 0xFFFF0000u)),
-                          fmaf(y, 0x1p-20f, y - __uint_as_float(uy & 0xFFFF0000u)));
-      }
-    }
-    const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vhalf = lane >> 4;
+        for (int e = 0; e < 4; ++e) s[t][n][e] = s2[n][e] = 0.0f;
     if constexpr (!E4M3) {
 #pragma unroll
-      for (int d = 0; d < DP / 16; ++d) {
-        uint32_t b[4];
-        ldmatrix_x4_trans_at(b, vs + stage_at<kRowBytes, 0>(vrow, 2 * d + vhalf));
-        mma_bf16_16816(o[2 * d], a, b[0], b[1]);
-        mma_bf16_16816(o[2 * d + 1], a, b[2], b[3]);
-        mma_bf16_16816(o[2 * d], a2, b[0], b[1]);
-        mma_bf16_16816(o[2 * d + 1], a2, b[2], b[3]);
+      for (int kk = 0; kk < kSteps; ++kk) {
+        uint32_t x[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) query(n, kk, x[n]);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          uint32_t a[4];
+          ldmatrix_x4_at(a, ks + stage_at<kRowBytes, 0>(16 * t + row, 2 * kk + half));
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma_bf16_16816(kChains == 2 && (kk & 1) ? s2[n] : s[t][n], a, x[n][0], x[n][1]);
+        }
       }
     } else {
-      // A transposed load of 16-bit units hands a lane elements 2 g, 2 g + 1
-      // of tokens 2 tg, 2 tg + 1: the even elements make one product's column
-      // g, the odd ones another's.
 #pragma unroll
-      for (int d2 = 0; d2 < DP / 32; ++d2) {
-        uint32_t b[4];
-        ldmatrix_x4_trans_at(b, vs + stage_at<kRowBytes, 0>(vrow, 2 * d2 + vhalf));
+      for (int k2 = 0; k2 < kSteps / 2; ++k2) {
+        uint32_t x[2][NT][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i], 0u, 0x3120);
+        for (int n = 0; n < NT; ++n) query(n, 2 * k2, x[0][n]), query(n, 2 * k2 + 1, x[1][n]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mma_f16_16816(o[4 * d2 + 2 * h], a, f16x2_of_e4m3x2(b[2 * h]), f16x2_of_e4m3x2(b[2 * h + 1]));
-          mma_f16_16816(o[4 * d2 + 2 * h + 1], a, f16x2_of_e4m3x2(b[2 * h] >> 16),
-                        f16x2_of_e4m3x2(b[2 * h + 1] >> 16));
+        for (int t = 0; t < KT; ++t) {
+          uint32_t b[4];
+          ldmatrix_x4_at(b, ks + stage_at<kRowBytes, 0>(16 * t + row, 2 * k2 + half));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {f16x2_of_e4m3x2(b[2 * h]), f16x2_of_e4m3x2(b[2 * h + 1]),
+                                   f16x2_of_e4m3x2(b[2 * h] >> 16), f16x2_of_e4m3x2(b[2 * h + 1] >> 16)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma_f16_16816(kChains == 2 && h ? s2[n] : s[t][n], a, x[h][n][0], x[h][n][1]);
+          }
         }
       }
     }
-  }
-
-  // Each row's maximum and sum to the warp's places.
-  __device__ __forceinline__ void give_ml(float *sm, float *sl) {
-    const int lane = static_cast<int>(lane_id()), g = lane >> 2, tg = lane & 3;
+    if constexpr (kChains == 2) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float x = l[h];
-      x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-      x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-      if (tg == 0) {
-        sm[g + 8 * h] = m[h];
-        sl[g + 8 * h] = x;
+      for (int e = 0; e < 4; ++e) s[0][0][e] += s2[0][e];
+    }
+    // scores in units of ln 2, unattended ones at -inf
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][n][e] *= sc[n][e & 1];
+    if (p.softcap > 0.0f) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[t][n][e] = p.softcap * tanhf(s[t][n][e] / p.softcap) * kLog2e;
+    }
+    constexpr uint32_t kAll = kTok == 32 ? 0xFFFFFFFFu : (1u << (kTok & 31)) - 1;
+    if (valid != kAll) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!((valid >> (16 * t + g + 8 * (e >> 1))) & 1u)) s[t][n][e] = -INFINITY;
+    }
+    float base[NT][2], drop[NT][2];
+    bool moved = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = fmaxf(s[0][n][h], s[0][n][2 + h]);
+#pragma unroll
+        for (int t = 1; t < KT; ++t) x = fmaxf(x, fmaxf(s[t][n][h], s[t][n][2 + h]));
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+        const float top = fmaxf(m[n][h], x);
+        base[n][h] = top == -INFINITY ? 0.0f : top;  // a head with nothing yet
+        drop[n][h] = exp2_from(m[n][h], base[n][h]);
+        moved |= top != m[n][h];
+        m[n][h] = top;
       }
+    if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][d][e] *= drop[n][e & 1];
+        l[n][0] *= drop[n][0];
+        l[n][1] *= drop[n][1];
+      }
+    }
+    // The weights as the second products' right side, transposed in 8 x 8
+    // pieces.  bf16 values carry V: a weight goes in as the sum of two bf16
+    // numbers, its upper half and what is left, so that less than 2^-16 of it
+    // is lost and the output's own rounding stays the largest error.  The
+    // second number is kept above zero (by 2^-20 of the weight): an attended
+    // infinity in V then comes out as one, not as the NaN of 0 times it.  An
+    // f16 weight (e4m3 values) keeps 11 bits, enough for the same, and e4m3 has
+    // no infinities.
+    uint32_t hi[KT][NT][2], lo[KT][NT][2];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float x = exp2f(s[t][n][2 * r] - base[n][0]), y = exp2f(s[t][n][2 * r + 1] - base[n][1]);
+          l[n][0] += x;
+          l[n][1] += y;
+          if constexpr (E4M3) {
+            hi[t][n][r] = transposed_8x8(f16x2_of(x, y));
+          } else {
+            const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+            hi[t][n][r] = transposed_8x8(__byte_perm(ux, uy, 0x7632));
+            lo[t][n][r] = transposed_8x8(
+                bf16x2_of(fmaf(x, 0x1p-20f, x - __uint_as_float(ux & 0xFFFF0000u)),
+                          fmaf(y, 0x1p-20f, y - __uint_as_float(uy & 0xFFFF0000u))));
+          }
+        }
+    if constexpr (!E4M3) {
+      // rows 0-7 | 8-15 by lane bit 4, chunk by bit 3
+      const int vrow = (lane & 7) + ((lane >> 4) << 3), vhalf = (lane >> 3) & 1;
+#pragma unroll
+      for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          uint32_t a[4];
+          ldmatrix_x4_trans_at(a, vs + stage_at<kRowBytes, 0>(16 * t + vrow, 2 * d + vhalf));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_bf16_16816(o[n][d], a, hi[t][n][0], hi[t][n][1]);
+            mma_bf16_16816(o[n][d], a, lo[t][n][0], lo[t][n][1]);
+          }
+        }
+    } else {
+      // A transposed load of 16-bit units hands a lane elements 2 g, 2 g + 1
+      // of tokens 2 tg, 2 tg + 1: the even elements make a product's rows 0-7,
+      // the odd ones its rows 8-15.
+#pragma unroll
+      for (int d2 = 0; d2 < kSteps / 2; ++d2)
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          uint32_t b[4];
+          ldmatrix_x4_trans_at(b, vs + stage_at<kRowBytes, 0>(16 * t + row, 2 * d2 + half));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i], 0u, 0x3120);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {f16x2_of_e4m3x2(b[2 * h]), f16x2_of_e4m3x2(b[2 * h] >> 16),
+                                   f16x2_of_e4m3x2(b[2 * h + 1]), f16x2_of_e4m3x2(b[2 * h + 1] >> 16)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16_16816(o[n][2 * d2 + h], a, hi[t][n][0], hi[t][n][1]);
+          }
+        }
     }
   }
 
-  // Adds the warp's scaled sums to the buffer (rows of DP + 8 floats).  In
-  // round i the warps work on different quarters of the columns, each quarter
-  // being begun by one warp and added to by the others in a fixed order.
-  static constexpr int kPitch = DP + 8;
-  __device__ __forceinline__ void add_round(float *buf, int round, int warp, const float *top,
-                                            int rows) {
+  // Where column c of head h's sums lies in a warp's buffer: heads 2 tg of one
+  // column on different banks, four columns from a multiple of four together.
+  static __device__ __forceinline__ int at(int h, int c) { return h * DP + (c ^ (((h >> 1) & 3) << 3)); }
+
+  // The warp's maxima, sums and weighted sums of V.
+  __device__ __forceinline__ void give(float *buf, float *sm, float *sl) {
     const int lane = static_cast<int>(lane_id()), g = lane >> 2, tg = lane & 3;
-    const int mine = (warp + round) & 3;
-    const float f[2] = {exp2_from(m[0], top[g]), exp2_from(m[1], top[g + 8])};
 #pragma unroll
-    for (int qd = 0; qd < 4; ++qd) {
-      if (qd != mine) continue;
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int n = qd * DP / 32; n < (qd + 1) * DP / 32; ++n) {
+      for (int h = 0; h < 2; ++h) {
+        float x = l[n][h];
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
+        const int head = 8 * n + 2 * tg + h;
+        if (g == 0) {
+          sm[head] = m[n][h];
+          sl[head] = x;
+        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (g + 8 * h >= rows) continue;
-          float *b = buf + (g + 8 * h) * kPitch;
-          if constexpr (!E4M3) {
-            float2 *at = reinterpret_cast<float2 *>(b + n * 8 + 2 * tg);
-            float2 x = make_float2(o[n][2 * h] * f[h], o[n][2 * h + 1] * f[h]);
-            if (round) {
-              const float2 y = *at;
-              x.x += y.x;
-              x.y += y.y;
-            }
-            *at = x;
-          } else if ((n & 1) == 0) {
-            float4 *at = reinterpret_cast<float4 *>(b + n * 8 + 4 * tg);
-            float4 x = make_float4(o[n][2 * h] * f[h], o[n + 1][2 * h] * f[h],
-                                   o[n][2 * h + 1] * f[h], o[n + 1][2 * h + 1] * f[h]);
-            if (round) {
-              const float4 y = *at;
-              x.x += y.x;
-              x.y += y.y;
-              x.z += y.z;
-              x.w += y.w;
-            }
-            *at = x;
+        for (int d = 0; d < kSteps; ++d) {
+          if constexpr (E4M3) {
+            *reinterpret_cast<float2 *>(buf + at(head, 16 * d + 2 * g)) =
+                make_float2(o[n][d][h], o[n][d][2 + h]);
+          } else {
+            buf[at(head, 16 * d + g)] = o[n][d][h];
+            buf[at(head, 16 * d + 8 + g)] = o[n][d][2 + h];
           }
         }
       }
@@ -416,7 +482,7 @@ struct MmaCore {
 template <int GR, int DP>
 struct FmaCore {
   static constexpr int kRows = GR;
-  static constexpr int kTok = DP > 128 ? 8 : 16;  // three stages fit beside each other
+  static constexpr int kTok = DP > 64 ? 8 : 16;
   static constexpr int kPer = 32 / kTok;
   static constexpr bool kFma = true;
   static constexpr int kElemBytes = 4;
@@ -426,7 +492,7 @@ struct FmaCore {
   static constexpr int kLanes = DP / 4 < 32 ? DP / 4 : 32;  // lanes across a row
   static constexpr int kSplit = 32 / kLanes;                // tokens side by side
   static constexpr int kCols = DP / 128 > 0 ? DP / 128 : 1; // chunks per lane
-  static constexpr int kPitch = DP;
+  static constexpr int kDim = DP;
 
   float o[GR][kCols * 4];
   float m[GR], l[GR];
@@ -543,8 +609,10 @@ struct FmaCore {
     __syncwarp();  // the weights are read before the next step writes them
   }
 
-  __device__ __forceinline__ void give_ml(float *sm, float *sl) {
-    const int lane = static_cast<int>(lane_id());
+  static __device__ __forceinline__ int at(int h, int c) { return h * DP + c; }
+
+  __device__ __forceinline__ void give(float *buf, float *sm, float *sl) {
+    const int lane = static_cast<int>(lane_id()), col = lane % kLanes;
 #pragma unroll
     for (int g = 0; g < GR; ++g) {
       float x = l[g];
@@ -554,36 +622,16 @@ struct FmaCore {
         sm[g] = m[g];
         sl[g] = x;
       }
-    }
-  }
-
-  // In round i warp i adds.
-  __device__ __forceinline__ void add_round(float *buf, int round, int warp, const float *top, int) {
-    const int lane = static_cast<int>(lane_id()), col = lane % kLanes;
-    if (round != warp) return;
-#pragma unroll
-    for (int g = 0; g < GR; ++g) {
-      const float f = exp2_from(m[g], top[g]);
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        float x[4];
+        float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[e] = o[g][4 * c + e] * f;
-          if constexpr (kSplit == 2) x[e] += __shfl_xor_sync(0xFFFFFFFFu, x[e], 16);
+          y[e] = o[g][4 * c + e];
+          if constexpr (kSplit == 2) y[e] += __shfl_xor_sync(0xFFFFFFFFu, y[e], 16);
         }
-        if (lane < kLanes) {
-          float4 *at = reinterpret_cast<float4 *>(buf + g * kPitch + 4 * (col + c * 32));
-          float4 y = make_float4(x[0], x[1], x[2], x[3]);
-          if (round) {
-            const float4 z = *at;
-            y.x += z.x;
-            y.y += z.y;
-            y.z += z.z;
-            y.w += z.w;
-          }
-          *at = y;
-        }
+        if (lane < kLanes)
+          *reinterpret_cast<float4 *>(buf + at(g, 4 * (col + c * 32))) = make_float4(y[0], y[1], y[2], y[3]);
       }
     }
   }
@@ -597,9 +645,9 @@ struct PagedShape {
   static constexpr int kTile = Core::kTok * kPagedWarps;  // tokens
   static constexpr uint32_t kHalf = Core::kTok * Core::kRowBytes;  // K or V of a stage
   static constexpr uint32_t kRing = NS * 2 * kHalf;               // of a warp
-  static constexpr uint32_t kBuf = Core::kRows * Core::kPitch * 4;
-  static constexpr uint32_t kSmem =
-      kPagedWarps * (kRing + Core::kWarpBytes) + Core::kQBytes + kBuf;
+  // an item's end puts the warp's sums where its last stage was
+  static_assert(Core::kRows * Core::kDim * 4 <= 2 * kHalf, "a stage holds the sums");
+  static constexpr uint32_t kSmem = kPagedWarps * (kRing + Core::kWarpBytes) + Core::kQBytes;
 };
 
 // Tiles of request r's items, 0 where nothing is attended; `bad`: its length
@@ -627,17 +675,20 @@ __device__ __forceinline__ void paged_store4(const PagedParams &p, int64_t at, f
   }
 }
 
-// PAGE16: the block size is a multiple of 16, so that a stage's tokens lie in
-// one block and one table entry is looked up per stage instead of one per
-// token.
+__device__ __forceinline__ float paged_lse(float top, float sum) {
+  return top == -INFINITY && sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// PAGE16: the block size is a multiple of 16, so that every 16 tokens of a
+// stage lie in one block, whose rows follow one another: one table entry per
+// 16 tokens and addresses by addition, instead of both per token.
 template <class Core, int NS, bool PAGE16>
 __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const PagedParams p) {
   using Shape = PagedShape<Core, NS>;
   using Elem = std::conditional_t<Core::kFma, float, uint16_t>;  // of the queries
   extern __shared__ __align__(128) unsigned char paged_smem[];
-  __shared__ uint32_t valid_ring[kPagedWarps][NS];
+  __shared__ uint32_t valid_ring[kPagedWarps][NS], lost_ring[kPagedWarps][NS];
   __shared__ float sm[kPagedWarps][kPagedRows], sl[kPagedWarps][kPagedRows];
-  __shared__ float s_top[kPagedRows], s_sum[kPagedRows];
   __shared__ int64_t s_part[kPagedWarps];
   __shared__ int64_t s_before;
   __shared__ int32_t s_request;
@@ -647,7 +698,6 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   unsigned char *own = paged_smem + kPagedWarps * Shape::kRing + warp * Core::kWarpBytes;
   unsigned char *sq = paged_smem + kPagedWarps * (Shape::kRing + Core::kWarpBytes);
-  float *buf = reinterpret_cast<float *>(sq + Core::kQBytes);
   pdl_wait_and_release();
 
   // ---- this CTA's run of tiles ----
@@ -716,17 +766,21 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
     if (seen > u0) break;
   }
 
-  // ---- cursors over the run ----
+  // ---- cursors over the run: requests, their key heads, pieces of the query
+  // heads, tiles ----
   struct Cursor {
-    int64_t left;     // tiles of the run, this one included
-    int32_t request, head, tile;  // head: key head * pieces + piece
+    int64_t left;  // tiles of the run, this one included
+    int32_t request, head, piece, tile;
     PagedSpan span;
   };
+  // steps to the next tile; true where that is another item's first
   const auto next = [&](Cursor &c) {
     --c.left;
-    if (++c.tile == c.span.tiles) {
-      c.tile = 0;
-      if (++c.head == per_request) {
+    if (++c.tile < c.span.tiles) return false;
+    c.tile = 0;
+    if (++c.piece == p.pieces) {
+      c.piece = 0;
+      if (++c.head == p.kv_heads) {
         c.head = 0;
         if (c.left > 0) {
           bool bad;
@@ -735,6 +789,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
         }
       }
     }
+    return true;
   };
   Cursor use;
   use.left = u1 - u0;
@@ -743,13 +798,32 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
     bool bad;
     use.span = paged_span<Shape::kTile>(p, p.lens[use.request], bad);
     const int64_t in = u0 - s_before;
-    use.head = static_cast<int32_t>(in / use.span.tiles);
-    use.tile = static_cast<int32_t>(in - static_cast<int64_t>(use.head) * use.span.tiles);
+    const int32_t item = static_cast<int32_t>(in / use.span.tiles);
+    use.tile = static_cast<int32_t>(in - static_cast<int64_t>(item) * use.span.tiles);
+    use.head = item / p.pieces;
+    use.piece = item - use.head * p.pieces;
   }
   Cursor get = use;
 
   // ---- loading: a stage's table entry and mask byte are fetched one stage
   // before its rows ----
+  constexpr int kChunks = Core::kRowBytes / 16;              // of a row
+  constexpr int kRowsAt = kChunks <= 32 ? 32 / kChunks : 1;  // rows that the lanes copy at once
+  constexpr int kParts = kChunks <= 32 ? 1 : kChunks / 32;   // copies of a row by all lanes
+  constexpr uint32_t kAll = Core::kTok == 32 ? 0xFFFFFFFFu : (1u << (Core::kTok & 31)) - 1;
+  const int my_row = kChunks <= 32 ? lane / kChunks : 0, my_chunk = lane % kChunks;
+  const int chunks = p.dim * Core::kElemBytes / 16;
+  const uint32_t my_at = ring_at + stage_at<Core::kRowBytes, Core::kPer>(my_row, my_chunk);
+  const int32_t *table = nullptr;
+  const uint8_t *mask = nullptr;
+  const char *kh = nullptr, *vh = nullptr;  // the item's rows, for this lane's first chunk
+  const auto aim = [&]() {
+    table = p.table + get.request * p.table_stride;
+    if (p.mask) mask = p.mask + get.request * p.mask_stride;
+    kh = static_cast<const char *>(p.k) + get.head * p.k_head;
+    vh = static_cast<const char *>(p.v) + get.head * p.v_head;
+  };
+  aim();
   int32_t entry = -1;
   bool keep = false;
   const auto look_up = [&]() {
@@ -758,55 +832,71 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
     const int32_t t = base + lane % Core::kTok;
     keep = t >= get.span.first && t < get.span.len;
     entry = -1;
-    if (PAGE16 ? base < get.span.len : keep)
-      entry = p.table[get.request * p.table_stride +
-                      p.by_block.div(static_cast<uint32_t>(PAGE16 ? base : t))];
-    if (keep && p.mask) keep = p.mask[get.request * p.mask_stride + t] != 0;
+    if constexpr (PAGE16) {
+      // a lane's entry is that of its token's 16
+      const int32_t at = Core::kTok <= kPagedPage ? base : base + (lane & kPagedPage);
+      if (at < get.span.len) entry = table[p.by_block.div(static_cast<uint32_t>(at))];
+    } else if (keep) {
+      entry = table[p.by_block.div(static_cast<uint32_t>(t))];
+    }
+    if (keep && mask) keep = mask[t] != 0;
   };
   const auto fetch = [&](int stage) {
     const int32_t base = get.span.t0 + get.tile * Shape::kTile + warp * Core::kTok;
     const bool inside = entry >= 0 && entry < p.n_blocks;
-    constexpr uint32_t kAll = (1u << Core::kTok) - 1;
     const uint32_t want = __ballot_sync(0xFFFFFFFFu, keep) & kAll;
     const uint32_t valid = __ballot_sync(0xFFFFFFFFu, keep && inside) & kAll;
-    // bit 31: a wanted token's block is outside the cache
-    if (lane == 0) valid_ring[warp][stage] = valid | (want != valid ? 0x80000000u : 0u);
-    const uint32_t ks = ring_at + stage * 2 * Shape::kHalf, vs = ks + Shape::kHalf;
-    const int32_t kvh = get.head / p.pieces;
-    const char *kb = static_cast<const char *>(p.k) + kvh * p.k_head;
-    const char *vb = static_cast<const char *>(p.v) + kvh * p.v_head;
-    constexpr int kChunks = Core::kRowBytes / 16;
-    const int chunks = p.dim * Core::kElemBytes / 16;
-    if constexpr (PAGE16) {
-      const int32_t b = static_cast<int32_t>(p.by_block.div(static_cast<uint32_t>(base)));
-      const int32_t off = base - b * p.block_size;
-      const int64_t e = inside ? entry : 0;
-      kb += e * p.k_block + off * p.k_token;
-      vb += e * p.v_block + off * p.v_token;
+    if (lane == 0) {
+      valid_ring[warp][stage] = valid;
+      // a wanted token's block is outside the cache
+      lost_ring[warp][stage] = want != valid;
     }
+    const uint32_t to = my_at + stage * 2 * Shape::kHalf;
+    // copies rows r0 .. r0 + n - 1 of the stage from rows that lie a token
+    // stride apart, the first at ka and va (this lane's row and chunk)
+    const auto copy = [&](int r0, int n, const char *ka, const char *va) {
 #pragma unroll
-    for (int i = 0; i < Core::kTok * kChunks / 32; ++i) {
-      const int c = lane + 32 * i, row = c / kChunks, ch = c % kChunks;
-      const bool real = ((valid >> row) & 1u) && ch < chunks;
-      const char *ka = kb, *va = vb;
-      if constexpr (PAGE16) {
-        if (real) {
-          ka += row * p.k_token + ch * 16;
-          va += row * p.v_token + ch * 16;
+      for (int i = 0; i < n / kRowsAt; ++i) {
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          const int r = r0 + i * kRowsAt;
+          const bool real = ((valid >> (r + my_row)) & 1u) && my_chunk + 32 * part < chunks;
+          const uint32_t at = (to ^ (stage_xor<Core::kRowBytes, Core::kPer>(r) << 4)) +
+                              r * Core::kRowBytes + 512 * part;
+          const int skip = my_chunk + 32 * part < chunks ? 16 * (my_chunk + 32 * part) : 0;
+          cp_async16_or_zero(at, ka + skip, real);
+          cp_async16_or_zero(at + Shape::kHalf, va + skip, real);
         }
-      } else {
-        const int64_t e = __shfl_sync(0xFFFFFFFFu, entry, row);
-        if (real) {
-          const uint32_t t = static_cast<uint32_t>(base + row);
-          const int64_t off = t - p.by_block.div(t) * p.by_block.d;
-          ka += e * p.k_block + off * p.k_token + ch * 16;
-          va += e * p.v_block + off * p.v_token + ch * 16;
-        }
+        ka += kRowsAt * p.k_token;
+        va += kRowsAt * p.v_token;
       }
-      const uint32_t at = stage_at<Core::kRowBytes, Core::kPer>(row, ch);
-      cp_async16_or_zero(ks + at, ka, real);
-      cp_async16_or_zero(vs + at, va, real);
+    };
+    if constexpr (PAGE16) {
+      // a block holds whole groups of 16 tokens, all of them inside the cache
+      constexpr int kGroup = Core::kTok <= kPagedPage ? Core::kTok : kPagedPage;
+#pragma unroll
+      for (int r0 = 0; r0 < Core::kTok; r0 += kGroup) {
+        const int32_t e = Core::kTok <= kPagedPage ? entry : __shfl_sync(0xFFFFFFFFu, entry, r0);
+        const uint32_t t = static_cast<uint32_t>(base + r0);
+        const int64_t b = e >= 0 && e < p.n_blocks ? e : 0;
+        const int64_t off = t - p.by_block.div(t) * p.by_block.d + my_row;
+        copy(r0, kGroup, kh + b * p.k_block + off * p.k_token, vh + b * p.v_block + off * p.v_token);
+      }
+    } else {
+      // the lane of a row knows where it lies
+      const uint32_t t = static_cast<uint32_t>(base + lane % Core::kTok);
+      const int64_t b = keep && inside ? entry : 0;
+      const int64_t off = keep && inside ? t - p.by_block.div(t) * p.by_block.d : 0;
+      const int64_t ko = b * p.k_block + off * p.k_token, vo = b * p.v_block + off * p.v_token;
+#pragma unroll
+      for (int r = 0; r < Core::kTok; r += kRowsAt)
+        copy(r, kRowsAt, kh + __shfl_sync(0xFFFFFFFFu, ko, r + my_row),
+             vh + __shfl_sync(0xFFFFFFFFu, vo, r + my_row));
     }
+  };
+  const auto advance = [&]() {
+    if (next(get) && get.left > 0) aim();
+    look_up();
   };
 
   look_up();
@@ -814,8 +904,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   for (int s = 0; s < NS - 1; ++s) {
     if (get.left > 0) {
       fetch(s);
-      next(get);
-      look_up();
+      advance();
     }
     cp_async_commit();
   }
@@ -823,15 +912,13 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   // ---- the run ----
   Core core;
   int stage = 0, fill = NS - 1;
-  bool fresh = true;      // the item's queries are not loaded yet
-  bool from_start = true; // the run holds the item's first tile
+  bool fresh = true;       // the item's queries are not loaded yet
+  bool from_start = true;  // the run holds the item's first tile
   while (use.left > 0) {
-    const int32_t kvh = use.head / p.pieces, h0 = (use.head - kvh * p.pieces) * p.rows;
-    const int rows = min(p.rows, p.group - h0);
     if (fresh) {
-      const Elem *q = static_cast<const Elem *>(p.q) + use.request * p.q_req +
-                      (static_cast<int64_t>(kvh) * p.group + h0) * p.q_head;
-      core.begin(p, q, rows, p.k_scale ? p.k_scale[kvh] : 1.0f, sq);
+      const int64_t head = static_cast<int64_t>(use.head) * p.group + use.piece * p.rows;
+      core.begin(p, static_cast<const Elem *>(p.q) + use.request * p.q_req + head * p.q_head,
+                 min(p.rows, p.group - use.piece * p.rows), p.k_scale ? p.k_scale[use.head] : 1.0f, sq);
       from_start = use.tile == 0;
       fresh = false;
     }
@@ -839,83 +926,75 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
     __syncwarp();  // the stage is in, and the one before it is no longer read
     if (get.left > 0) {
       fetch(fill);
-      next(get);
-      look_up();
+      advance();
     }
     cp_async_commit();
     const uint32_t valid = valid_ring[warp][stage];
     const uint32_t ks = ring_at + stage * 2 * Shape::kHalf;
-    if (valid & 0xFFFFu) core.step(p, ks, ks + Shape::kHalf, valid & 0xFFFFu, own);
-    if (valid >> 31) {
+    if (valid) core.step(p, ks, ks + Shape::kHalf, valid, own);
+    if (lost_ring[warp][stage]) {
       core.poison();
       bits |= kRowBadBlock;
     }
-    stage = stage + 1 == NS ? 0 : stage + 1;
-    fill = fill + 1 == NS ? 0 : fill + 1;
 
     const bool item_end = use.tile == use.span.tiles - 1;
     if (item_end || use.left == 1) {
-      // ---- the four warps' parts as one ----
-      core.give_ml(sm[warp], sl[warp]);
+      // ---- the four warps' parts as one: each puts its sums where its stage
+      // was ----
+      __syncwarp();
+      core.give(reinterpret_cast<float *>(ring + stage * 2 * Shape::kHalf), sm[warp], sl[warp]);
       __syncthreads();
-      if (tid < Core::kRows) {
-        float top = sm[0][tid];
+      const int rows = min(p.rows, p.group - use.piece * p.rows), quads = p.dim / 4;
+      const int64_t head = static_cast<int64_t>(use.head) * p.group + use.piece * p.rows;
+      const bool whole = from_start && item_end;
+      // a piece: the item's first one goes to slot 1, the others are the first
+      // thing in their CTA's run and go to slot 0
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0);
+      const float vscale = p.v_scale ? p.v_scale[use.head] : 1.0f;
+      for (int i = tid; i < rows * quads; i += kPagedThreads) {
+        const int r = i / quads, c = 4 * (i - r * quads);
+        float top = sm[0][r];
 #pragma unroll
-        for (int w = 1; w < kPagedWarps; ++w) top = fmaxf(top, sm[w][tid]);
+        for (int w = 1; w < kPagedWarps; ++w) top = fmaxf(top, sm[w][r]);
         float sum = 0.0f;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kPagedWarps; ++w) sum += exp2_from(sm[w][tid], top) * sl[w][tid];
-        s_top[tid] = top;
-        s_sum[tid] = sum;
-      }
-      __syncthreads();
-#pragma unroll 1
-      for (int i = 0; i < kPagedWarps; ++i) {
-        core.add_round(buf, i, warp, s_top, rows);
-        __syncthreads();
-      }
-      const int quads = p.dim / 4;
-      if (from_start && item_end) {
-        const float vscale = p.v_scale ? p.v_scale[kvh] : 1.0f;
-        const int64_t head = static_cast<int64_t>(kvh) * p.group + h0;
-        for (int i = tid; i < rows * quads; i += kPagedThreads) {
-          const int r = i / quads, c = 4 * (i - r * quads);
-          const float sum = s_sum[r], f = sum == 0.0f ? 0.0f : vscale / sum;
-          float4 x = *reinterpret_cast<const float4 *>(buf + r * Core::kPitch + c);
-          x.x *= f;
-          x.y *= f;
-          x.z *= f;
-          x.w *= f;
-          paged_store4(p, use.request * p.o_req + (head + r) * p.o_head + c, x);
+        for (int w = 0; w < kPagedWarps; ++w) {
+          const float f = exp2_from(sm[w][r], top);
+          const float4 y = *reinterpret_cast<const float4 *>(
+              reinterpret_cast<const float *>(paged_smem + w * Shape::kRing + stage * 2 * Shape::kHalf) +
+              Core::at(r, c));
+          sum = fmaf(f, sl[w][r], sum);
+          x.x = fmaf(f, y.x, x.x);
+          x.y = fmaf(f, y.y, x.y);
+          x.z = fmaf(f, y.z, x.z);
+          x.w = fmaf(f, y.w, x.w);
         }
-        if (p.lse && tid < rows)
-          p.lse[static_cast<int64_t>(use.request) * n_heads + head + tid] =
-              s_top[tid] == -INFINITY && s_sum[tid] == 0.0f
-                  ? -INFINITY : (s_top[tid] + log2f(s_sum[tid])) * kLn2;
-      } else {
-        // a piece: the item's first one goes to slot 1, the others are the
-        // first thing in their CTA's run and go to slot 0
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0);
-        float *acc = p.acc + slot * kPagedRows * kPagedMaxDim;
-        for (int i = tid; i < rows * quads; i += kPagedThreads) {
-          const int r = i / quads, c = 4 * (i - r * quads);
-          *reinterpret_cast<float4 *>(acc + r * kPagedMaxDim + c) =
-              *reinterpret_cast<const float4 *>(buf + r * Core::kPitch + c);
-        }
-        if (tid < rows) p.ml[slot * kPagedRows + tid] = make_float2(s_top[tid], s_sum[tid]);
-        if (from_start && tid == 0) {
-          const int64_t more = use.span.tiles - 1 - use.tile;  // tiles in the CTAs after this one
-          PagedDesc d;
-          d.request = use.request;
-          d.head = use.head;
-          d.parts = static_cast<int32_t>(1 + (more + run - 1) / run);
-          d.pad = 0;
-          p.desc[blockIdx.x] = d;
+        if (whole) {
+          const float f = sum == 0.0f ? 0.0f : vscale / sum;
+          paged_store4(p, use.request * p.o_req + (head + r) * p.o_head + c,
+                       make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
+          if (c == 0 && p.lse)
+            p.lse[static_cast<int64_t>(use.request) * n_heads + head + r] = paged_lse(top, sum);
+        } else {
+          *reinterpret_cast<float4 *>(p.acc + (slot * kPagedRows + r) * kPagedMaxDim + c) = x;
+          if (c == 0) p.ml[slot * kPagedRows + r] = make_float2(top, sum);
         }
       }
-      __syncthreads();  // the buffers are read before the next item's end writes them
+      if (!whole && from_start && tid == 0) {
+        const int64_t more = use.span.tiles - 1 - use.tile;  // tiles in the CTAs after this one
+        PagedDesc d;
+        d.request = use.request;
+        d.head = use.head;
+        d.piece = use.piece;
+        d.parts = static_cast<int32_t>(1 + (more + run - 1) / run);
+        p.desc[blockIdx.x] = d;
+      }
+      __syncthreads();  // the sums are read before the stage is filled again
       fresh = true;
     }
+    stage = stage + 1 == NS ? 0 : stage + 1;
+    fill = fill + 1 == NS ? 0 : fill + 1;
     next(use);
   }
   cp_async_wait_group<0>();
@@ -932,7 +1011,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_join_kernel(const PagedPa
   const int c = static_cast<int>(blockIdx.x), row = static_cast<int>(blockIdx.y);
   const PagedDesc d = p.desc[c];
   if (d.parts < 2) return;
-  const int32_t kvh = d.head / p.pieces, h0 = (d.head - kvh * p.pieces) * p.rows;
+  const int32_t kvh = d.head, h0 = d.piece * p.rows;
   if (row >= min(p.rows, p.group - h0)) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const auto slot_of = [&](int j) { return 2 * static_cast<int64_t>(c + j) + (j == 0 ? 1 : 0); };
@@ -989,7 +1068,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_join_kernel(const PagedPa
   }
   if (p.lse && tid == 0)
     p.lse[static_cast<int64_t>(d.request) * p.kv_heads * p.group + head] =
-        top == -INFINITY && sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        paged_lse(top, sum);
 }
 
 }  // namespace ts
