@@ -22,7 +22,7 @@ struct ts_kv_state {
   void *mem;
   int ctas;          // pieces for this many CTAs
   int max_requests;
-  ts::PagedDesc *desc;
+  ts::PagedPart *parts;
   float *acc;
   float2 *ml;
   int32_t *lens, *n_free;
@@ -203,7 +203,7 @@ ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests) {
         at += 2 * static_cast<size_t>(ctas) * ts::kPagedAccBytes;
         kv->ml = reinterpret_cast<float2 *>(at);
         at += 2 * static_cast<size_t>(ctas) * ts::kPagedRows * sizeof(float2);
-        kv->desc = reinterpret_cast<ts::PagedDesc *>(at);
+        kv->parts = reinterpret_cast<ts::PagedPart *>(at);
         kv->n_free = reinterpret_cast<int32_t *>(static_cast<char *>(kv->mem) + pieces);
         kv->lens = kv->n_free + 1;
         s->kv = kv;
@@ -334,9 +334,10 @@ ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *
   const int64_t per_head = c->head_dim / vec, per_token = per_head * c->n_kv_heads;
   if (per_token > (1 << 20)) return TS_ERR_UNSUPPORTED;
   // whole tokens, about four units per thread, fewer while SMs would idle
-  const int64_t fill = ts::kAppendThreads * ts::kAppendUnroll;
+  const int64_t fill = ts::kAppendThreads * 4;
   p.tokens_per_block = static_cast<int32_t>(std::max<int64_t>(
       1, std::min<int64_t>(fill / per_token, (t->n_tokens + s->num_sms - 1) / s->num_sms)));
+  p.by_block = ts::FastDiv::of(static_cast<uint32_t>(c->block_size));
   p.by_token = ts::FastDiv::of(static_cast<uint32_t>(per_token));
   p.by_head = ts::FastDiv::of(static_cast<uint32_t>(per_head));
   p.status = s->status;
@@ -426,7 +427,7 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.softcap = q->softcap;
   p.window = q->window;
   p.by_block = ts::FastDiv::of(static_cast<uint32_t>(c->block_size));
-  p.desc = s->kv->desc;
+  p.parts = s->kv->parts;
   p.acc = s->kv->acc;
   p.ml = s->kv->ml;
   p.ctas = k.occupancy * s->num_sms;
@@ -439,8 +440,7 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
                          s->pdl != 0, st, args);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   e = launch(reinterpret_cast<const void *>(ts::paged_join_kernel),
-             dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>(std::min(rows, group))),
-             ts::kPagedThreads, 0, s->pdl != 0, st, args);
+             dim3(static_cast<unsigned>(p.ctas)), ts::kJoinThreads, 0, s->pdl != 0, st, args);
   return e == cudaSuccess ? TS_OK : cuda_fail(e, "paged attention join launch");
 }
 

@@ -295,7 +295,10 @@ __global__ void kv_tables_store_kernel(const int32_t *lens_new, int32_t *lens, i
 // Writing new tokens' keys and values
 // --------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
-constexpr int kAppendUnroll = 4;
+// Units per thread and round: 4 of 16 bytes, fewer of the 32 or 64 bytes that
+// make 16 e4m3 values.
+template <class Src, int VEC>
+constexpr int kAppendUnroll = sizeof(Src) * VEC == 16 ? 4 : sizeof(Src) * VEC == 32 ? 2 : 1;
 
 struct KvAppendParams {
   const void *src[2];               // K and V of the new tokens
@@ -309,9 +312,26 @@ struct KvAppendParams {
   int32_t n_tokens;
   int32_t heads;
   int32_t tokens_per_block;         // CTA
-  FastDiv by_token, by_head;        // units of VEC elements per token, per head
+  FastDiv by_block, by_token, by_head;        // units of VEC elements per token, per head
   uint32_t *status;
 };
+
+// x / scale correctly rounded, given inv = 1 / scale correctly rounded: Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor"
+// (1990): with q within a unit of the quotient, q + (x - q scale) inv rounds to
+// it where nothing over- or underflows.  The scales that this is used for lie
+// within 2^-90 .. 2^90 (quotient_inverse), a quotient beyond 2^20 is as good as
+// any other beyond 448 (infinite and NaN ones among them), and where x - q scale
+// underflows the quotient rounds to an e4m3 zero.
+__device__ __forceinline__ float quotient(float x, float scale, float inv) {
+  const float q = x * inv;
+  const float y = fmaf(fmaf(-q, scale, x), inv, q);
+  return fabsf(q) < 0x1p20f && q != 0.0f ? y : q;  // a zero keeps its sign
+}
+__device__ __forceinline__ float quotient_inverse(float scale) {
+  const float a = fabsf(scale);
+  return a >= 0x1p-90f && a <= 0x1p90f ? __fdiv_rn(1.0f, scale) : 0.0f;
+}
 
 // Eight or sixteen elements as they are stored.
 template <class Src, class Dst, int VEC, bool WIDE>
@@ -342,7 +362,8 @@ struct AppendUnit {
     else
       return __uint_as_float(w[i]);
   }
-  __device__ __forceinline__ void store(Dst *p, float scale) const {
+  // `inv`: 1 / scale, or 0 where it does not serve (see quotient)
+  __device__ __forceinline__ void store(Dst *p, float scale, float inv) const {
     if constexpr (sizeof(Src) == sizeof(Dst)) {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i)
@@ -354,10 +375,12 @@ struct AppendUnit {
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(at(4 * i), scale), __fdiv_rn(at(4 * i + 1), scale)), __NV_SATFINITE, __NV_E4M3);
-        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(at(4 * i + 2), scale), __fdiv_rn(at(4 * i + 3), scale)), __NV_SATFINITE, __NV_E4M3);
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          y[j] = inv != 0.0f ? quotient(at(4 * i + j), scale, inv) : __fdiv_rn(at(4 * i + j), scale);
+        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
         o[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
       }
       *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -365,27 +388,28 @@ struct AppendUnit {
   }
 };
 
-// A thread moves kAppendUnroll units of VEC elements, each of K and of V, so
-// that eight 16-byte loads are in flight; a CTA takes whole tokens.  A skipped
+// A thread moves a few units of VEC elements, each of K and of V, so that eight
+// 16-byte loads are in flight; a CTA takes whole tokens.  A skipped
 // token's rows are not read.  Bound by DRAM: each element is read once and
 // written once.
 template <class Src, class Dst, int VEC, bool WIDE>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppendParams p) {
+  constexpr int kUnroll = kAppendUnroll<Src, VEC>;
   pdl_wait_and_release();
   const int32_t t0 = static_cast<int32_t>(blockIdx.x) * p.tokens_per_block;
   const int32_t nt = min(p.tokens_per_block, p.n_tokens - t0);
   const uint32_t units = static_cast<uint32_t>(nt) * p.by_token.d;
   uint32_t bits = 0;
-  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kAppendThreads * kAppendUnroll) {
-    AppendUnit<Src, Dst, VEC, WIDE> k[kAppendUnroll], v[kAppendUnroll];
-    int64_t slot[kAppendUnroll];
+  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kAppendThreads * kUnroll) {
+    AppendUnit<Src, Dst, VEC, WIDE> k[kUnroll], v[kUnroll];
+    int64_t slot[kUnroll];
 #pragma unroll
-    for (int j = 0; j < kAppendUnroll; ++j) {
+    for (int j = 0; j < kUnroll; ++j) {
       const uint32_t u = u0 + j * kAppendThreads;
       slot[j] = u < units ? p.slots[t0 + p.by_token.div(u)] : -1;
     }
 #pragma unroll
-    for (int j = 0; j < kAppendUnroll; ++j) {
+    for (int j = 0; j < kUnroll; ++j) {
       if (slot[j] >= p.n_slots) {
         bits |= kRowBadSlot;
         slot[j] = -1;
@@ -400,16 +424,29 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppen
       }
     }
 #pragma unroll
-    for (int j = 0; j < kAppendUnroll; ++j) {
+    for (int j = 0; j < kUnroll; ++j) {
       if (slot[j] >= 0) {
         const uint32_t u = u0 + j * kAppendThreads;
         const uint32_t in = u - p.by_token.div(u) * p.by_token.d;
         const uint32_t h = p.by_head.div(in), e = (in - h * p.by_head.d) * VEC;
-        const int64_t blk = slot[j] / p.block_size, off = slot[j] - blk * p.block_size;
+        // a cache of 2^31 slots and more takes the 64-bit division
+        const int64_t blk = p.n_slots <= 0x7FFFFFFF
+                                ? static_cast<int64_t>(p.by_block.div(static_cast<uint32_t>(slot[j])))
+                                : slot[j] / p.block_size;
+        const int64_t off = slot[j] - blk * p.block_size;
         Dst *kd = static_cast<Dst *>(p.dst[0]) + blk * p.dst_block[0] + off * p.dst_token[0] + h * p.dst_head[0] + e;
         Dst *vd = static_cast<Dst *>(p.dst[1]) + blk * p.dst_block[1] + off * p.dst_token[1] + h * p.dst_head[1] + e;
-        k[j].store(kd, p.scale[0] ? p.scale[0][h] : 1.0f);
-        v[j].store(vd, p.scale[1] ? p.scale[1][h] : 1.0f);
+        float scale[2] = {1.0f, 1.0f}, inv[2] = {1.0f, 1.0f};
+        if constexpr (sizeof(Dst) == 1) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (p.scale[s]) {
+              scale[s] = p.scale[s][h];
+              inv[s] = quotient_inverse(scale[s]);
+            }
+        }
+        k[j].store(kd, scale[0], inv[0]);
+        v[j].store(vd, scale[1], inv[1]);
       }
     }
   }

@@ -35,15 +35,18 @@ constexpr int kPagedPage = 16;                       // a stage's tokens divide 
 constexpr int kPagedRows = 16;                       // most query heads per item
 constexpr int kPagedMaxDim = 256;
 
-// A piece of an item in the workspace: kPagedRows rows of kPagedMaxDim sums,
-// each row's maximum and sum, and which item it is.
-struct PagedDesc {
-  int32_t request, head, piece, parts;  // parts > 1: the item starts in this CTA
+// A part of an item in the workspace: kPagedRows rows of kPagedMaxDim sums,
+// each row's maximum and sum, and what it is a part of.  A CTA's first part (of
+// an item that began in an earlier CTA) is its part 0, the item that it begins
+// and does not end its part 1.
+struct PagedPart {
+  int32_t request, head, piece;
+  int32_t first, parts;  // the CTA of the item's first part, their number (0: none here)
 };
 constexpr size_t kPagedAccBytes = sizeof(float) * kPagedRows * kPagedMaxDim;
 constexpr size_t paged_workspace_bytes(int ctas) {
   return static_cast<size_t>(ctas) *
-         (sizeof(PagedDesc) + 2 * (kPagedAccBytes + sizeof(float2) * kPagedRows));
+         (2 * (sizeof(PagedPart) + kPagedAccBytes + sizeof(float2) * kPagedRows));
 }
 
 struct PagedParams {
@@ -70,7 +73,7 @@ struct PagedParams {
   float scale, softcap;
   int32_t window;           // 0: none
   FastDiv by_block;
-  PagedDesc *desc;
+  PagedPart *parts;         // [2 ctas]
   float *acc;               // [2 ctas][kPagedRows][kPagedMaxDim]
   float2 *ml;               // [2 ctas][kPagedRows]
   int32_t ctas;             // of the main launch
@@ -120,6 +123,28 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t x) {
   const uint16_t h = static_cast<uint16_t>(x);
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(h));
   return d;
+}
+// two fp32 values side by side
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_of(float x) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ float low_of(uint64_t x) {
+  return __uint_as_float(static_cast<uint32_t>(x));
+}
+__device__ __forceinline__ float high_of(uint64_t x) {
+  return __uint_as_float(static_cast<uint32_t>(x >> 32));
 }
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   uint32_t d;
@@ -494,15 +519,15 @@ struct FmaCore {
   static constexpr int kCols = DP / 128 > 0 ? DP / 128 : 1; // chunks per lane
   static constexpr int kDim = DP;
 
-  float o[GR][kCols * 4];
+  uint64_t o[GR][kCols * 2];  // pairs of columns
   float m[GR], l[GR];
   float sc;
-  const float *q;
+  uint32_t q_at;
 
   __device__ __forceinline__ void begin(const PagedParams &p, const float *src, int rows,
                                         float k_scale, void *shared) {
     float *sq = static_cast<float *>(shared);
-    q = sq;
+    q_at = static_cast<uint32_t>(__cvta_generic_to_shared(sq));
     sc = p.softcap > 0.0f ? p.scale * k_scale : p.scale * k_scale * kLog2e;
     for (int i = static_cast<int>(threadIdx.x); i < GR * DP / 4; i += kPagedThreads) {
       const int r = i / (DP / 4), c = 4 * (i % (DP / 4));
@@ -516,7 +541,7 @@ struct FmaCore {
       m[g] = -INFINITY;
       l[g] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < kCols * 4; ++c) o[g][c] = 0.0f;
+      for (int c = 0; c < kCols * 2; ++c) o[g][c] = 0;
     }
   }
 
@@ -525,32 +550,32 @@ struct FmaCore {
     for (int g = 0; g < GR; ++g) l[g] = __int_as_float(0x7FC00000);
   }
 
-  static __device__ __forceinline__ float4 lds4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
+  static __device__ __forceinline__ void lds_pairs(uint64_t (&v)[2], uint32_t a) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(a) : "memory");
   }
 
   __device__ __forceinline__ void step(const PagedParams &p, uint32_t ks, uint32_t vs,
                                        uint32_t valid, void *own) {
     const int lane = static_cast<int>(lane_id()), t = lane / kPer, part = lane % kPer;
     float *sp = static_cast<float *>(own);  // [kTok][GR] weights
-    float s[GR];
+    uint64_t pair[GR];  // two running sums per head
 #pragma unroll
-    for (int g = 0; g < GR; ++g) s[g] = 0.0f;
+    for (int g = 0; g < GR; ++g) pair[g] = 0;
 #pragma unroll 4
     for (int c = part; c < DP / 4; c += kPer) {
-      const float4 k = lds4(ks + stage_at<kRowBytes, kPer>(t, c));
+      uint64_t k[2];
+      lds_pairs(k, ks + stage_at<kRowBytes, kPer>(t, c));
 #pragma unroll
       for (int g = 0; g < GR; ++g) {
-        const float4 x = reinterpret_cast<const float4 *>(q)[g * (DP / 4) + c];
-        s[g] = fmaf(x.x, k.x, s[g]);
-        s[g] = fmaf(x.y, k.y, s[g]);
-        s[g] = fmaf(x.z, k.z, s[g]);
-        s[g] = fmaf(x.w, k.w, s[g]);
+        uint64_t x[2];
+        lds_pairs(x, q_at + g * DP * 4 + c * 16);
+        pair[g] = fma_pair(x[0], k[0], pair[g]);
+        pair[g] = fma_pair(x[1], k[1], pair[g]);
       }
     }
+    float s[GR];
+#pragma unroll
+    for (int g = 0; g < GR; ++g) s[g] = low_of(pair[g]) + high_of(pair[g]);
     const bool on = (valid >> t) & 1u;
     bool moved = false;
     float drop[GR];
@@ -577,7 +602,7 @@ struct FmaCore {
       for (int g = 0; g < GR; ++g) {
         l[g] *= drop[g];
 #pragma unroll
-        for (int c = 0; c < kCols * 4; ++c) o[g][c] *= drop[g];
+        for (int c = 0; c < kCols * 2; ++c) o[g][c] = mul_pair(o[g][c], pair_of(drop[g]));
       }
     }
 #pragma unroll
@@ -596,13 +621,12 @@ struct FmaCore {
       for (int g = 0; g < GR; ++g) w[g] = sp[u * GR + g];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        const float4 v = lds4(vs + stage_at<kRowBytes, kPer>(u, col + c * 32));
+        uint64_t v[2];
+        lds_pairs(v, vs + stage_at<kRowBytes, kPer>(u, col + c * 32));
 #pragma unroll
         for (int g = 0; g < GR; ++g) {
-          o[g][4 * c] = fmaf(w[g], v.x, o[g][4 * c]);
-          o[g][4 * c + 1] = fmaf(w[g], v.y, o[g][4 * c + 1]);
-          o[g][4 * c + 2] = fmaf(w[g], v.z, o[g][4 * c + 2]);
-          o[g][4 * c + 3] = fmaf(w[g], v.w, o[g][4 * c + 3]);
+          o[g][2 * c] = fma_pair(pair_of(w[g]), v[0], o[g][2 * c]);
+          o[g][2 * c + 1] = fma_pair(pair_of(w[g]), v[1], o[g][2 * c + 1]);
         }
       }
     }
@@ -627,7 +651,7 @@ struct FmaCore {
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          y[e] = o[g][4 * c + e];
+          y[e] = e & 1 ? high_of(o[g][2 * c + e / 2]) : low_of(o[g][2 * c + e / 2]);
           if constexpr (kSplit == 2) y[e] += __shfl_xor_sync(0xFFFFFFFFu, y[e], 16);
         }
         if (lane < kLanes)
@@ -689,7 +713,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   extern __shared__ __align__(128) unsigned char paged_smem[];
   __shared__ uint32_t valid_ring[kPagedWarps][NS], lost_ring[kPagedWarps][NS];
   __shared__ float sm[kPagedWarps][kPagedRows], sl[kPagedWarps][kPagedRows];
-  __shared__ int64_t s_part[kPagedWarps];
+  __shared__ int64_t s_part[kPagedWarps], s_rest[kPagedWarps];
   __shared__ int64_t s_before;
   __shared__ int32_t s_request;
 
@@ -700,70 +724,88 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   unsigned char *sq = paged_smem + kPagedWarps * (Shape::kRing + Core::kWarpBytes);
   pdl_wait_and_release();
 
-  // ---- this CTA's run of tiles ----
+  // ---- this CTA's run of tiles: the first 128 requests' tiles are summed and
+  // searched with one load each, more requests in further rounds ----
   const int per_request = p.kv_heads * p.pieces;
   const int n_heads = p.kv_heads * p.group;
   uint32_t bits = 0;
-  int64_t total = 0;
-  for (int r = tid; r < p.n_requests; r += kPagedThreads) {
+  const auto tiles_of = [&](int64_t r) {
     bool bad;
-    total += static_cast<int64_t>(paged_span<Shape::kTile>(p, p.lens[r], bad).tiles) * per_request;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-  if (lane == 0) s_part[warp] = total;
-  __syncthreads();
-  total = s_part[0] + s_part[1] + s_part[2] + s_part[3];
-  const int64_t run = (total + p.ctas - 1) / p.ctas;
-  const int64_t u0 = run * blockIdx.x;
-  const int64_t u1 = min(u0 + run, total);
-  __syncthreads();
-
-  // requests with nothing to attend to are answered here
-  for (int r = static_cast<int>(blockIdx.x); r < p.n_requests; r += p.ctas) {
-    bool bad;
-    const PagedSpan s = paged_span<Shape::kTile>(p, p.lens[r], bad);
-    if (s.tiles > 0) continue;
-    if (bad) bits |= kRowBadShape;
-    const float x = bad ? __int_as_float(0x7FC00000) : 0.0f;
-    for (int i = tid; i < n_heads * (p.dim / 4); i += kPagedThreads) {
-      const int h = i / (p.dim / 4), c = 4 * (i - h * (p.dim / 4));
-      paged_store4(p, r * p.o_req + h * p.o_head + c, make_float4(x, x, x, x));
-    }
-    if (p.lse)
-      for (int h = tid; h < n_heads; h += kPagedThreads)
-        p.lse[static_cast<int64_t>(r) * n_heads + h] = bad ? x : -INFINITY;
-  }
-  if (tid == 0) p.desc[blockIdx.x].parts = 0;
-  if (u0 >= u1) {
-    if (bits && tid == 0) atomicOr(p.status, bits);
-    return;
-  }
-
-  // the request that holds tile u0
-  for (int64_t seen = 0, r0 = 0; r0 < p.n_requests; r0 += kPagedThreads) {
-    const int64_t r = r0 + tid;
-    bool bad;
-    int64_t mine = 0;
-    if (r < p.n_requests)
-      mine = static_cast<int64_t>(paged_span<Shape::kTile>(p, p.lens[r], bad).tiles) * per_request;
-    int64_t in = mine;
+    return r < p.n_requests
+               ? static_cast<int64_t>(paged_span<Shape::kTile>(p, p.lens[r], bad).tiles) * per_request
+               : 0;
+  };
+  int64_t mine = tiles_of(tid), rest = 0;
+  for (int64_t r = tid + kPagedThreads; r < p.n_requests; r += kPagedThreads) rest += tiles_of(r);
+  // leaves in `in` the sum of the threads' values up to this one's, in the
+  // warps' places their totals
+  int64_t in;
+  const auto scan = [&]() {
+    in = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xFFFFFFFFu, in, o);
       if (lane >= o) in += x;
     }
     if (lane == 31) s_part[warp] = in;
-    __syncthreads();
-    int64_t before = seen + in - mine;
-    for (int w = 0; w < warp; ++w) before += s_part[w];
-    if (before <= u0 && u0 < before + mine) {
-      s_request = static_cast<int32_t>(r);
-      s_before = before;
+  };
+  scan();
+  if (p.n_requests > kPagedThreads) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+  }
+  if (lane == 0) s_rest[warp] = rest;
+  __syncthreads();
+  int64_t seen = s_part[0] + s_part[1] + s_part[2] + s_part[3];
+  const int64_t total = seen + s_rest[0] + s_rest[1] + s_rest[2] + s_rest[3];
+  const int64_t run = (total + p.ctas - 1) / p.ctas;
+  const int64_t u0 = run * blockIdx.x;
+  const int64_t u1 = min(u0 + run, total);
+
+  // requests with nothing to attend to
+  const auto answer_empty = [&]() {
+    for (int r = static_cast<int>(blockIdx.x); r < p.n_requests; r += p.ctas) {
+      bool bad;
+      const PagedSpan s = paged_span<Shape::kTile>(p, p.lens[r], bad);
+      if (s.tiles > 0) continue;
+      if (bad) bits |= kRowBadShape;
+      const float x = bad ? __int_as_float(0x7FC00000) : 0.0f;
+      for (int i = tid; i < n_heads * (p.dim / 4); i += kPagedThreads) {
+        const int h = i / (p.dim / 4), c = 4 * (i - h * (p.dim / 4));
+        paged_store4(p, r * p.o_req + h * p.o_head + c, make_float4(x, x, x, x));
+      }
+      if (p.lse)
+        for (int h = tid; h < n_heads; h += kPagedThreads)
+          p.lse[static_cast<int64_t>(r) * n_heads + h] = bad ? x : -INFINITY;
     }
-    seen += s_part[0] + s_part[1] + s_part[2] + s_part[3];
-    __syncthreads();
-    if (seen > u0) break;
+  };
+  PagedPart *parts = p.parts + 2 * static_cast<int64_t>(blockIdx.x);
+  if (tid < 2) parts[tid].parts = 0;
+  if (u0 >= u1) {
+    answer_empty();
+    if (bits && tid == 0) atomicOr(p.status, bits);
+    return;
+  }
+
+  // the request that holds tile u0
+  {
+    int64_t r = tid, before = in - mine;
+    for (int w = 0; w < warp; ++w) before += s_part[w];
+    while (true) {
+      if (before <= u0 && u0 < before + mine) {
+        s_request = static_cast<int32_t>(r);
+        s_before = before;
+      }
+      __syncthreads();
+      if (seen > u0) break;
+      r += kPagedThreads;
+      mine = tiles_of(r);
+      scan();
+      __syncthreads();
+      before = seen + in - mine;
+      for (int w = 0; w < warp; ++w) before += s_part[w];
+      seen += s_part[0] + s_part[1] + s_part[2] + s_part[3];
+    }
   }
 
   // ---- cursors over the run: requests, their key heads, pieces of the query
@@ -797,9 +839,9 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   {
     bool bad;
     use.span = paged_span<Shape::kTile>(p, p.lens[use.request], bad);
-    const int64_t in = u0 - s_before;
-    const int32_t item = static_cast<int32_t>(in / use.span.tiles);
-    use.tile = static_cast<int32_t>(in - static_cast<int64_t>(item) * use.span.tiles);
+    const int64_t at = u0 - s_before;
+    const int32_t item = static_cast<int32_t>(at / use.span.tiles);
+    use.tile = static_cast<int32_t>(at - static_cast<int64_t>(item) * use.span.tiles);
     use.head = item / p.pieces;
     use.piece = item - use.head * p.pieces;
   }
@@ -895,7 +937,17 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
     }
   };
   const auto advance = [&]() {
-    if (next(get) && get.left > 0) aim();
+    if (next(get) && get.left > 0) {
+      aim();
+      // the item's queries towards L1, a line per lane
+      const char *q = reinterpret_cast<const char *>(
+          static_cast<const Elem *>(p.q) + get.request * p.q_req +
+          (static_cast<int64_t>(get.head) * p.group + get.piece * p.rows) * p.q_head);
+      const int rows = min(p.rows, p.group - get.piece * p.rows);
+      for (int r = warp; r < rows; r += kPagedWarps)
+        if (lane * 128 < p.dim * static_cast<int>(sizeof(Elem)))
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(q + r * p.q_head * sizeof(Elem) + lane * 128));
+    }
     look_up();
   };
 
@@ -908,6 +960,8 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
     }
     cp_async_commit();
   }
+
+  answer_empty();
 
   // ---- the run ----
   Core core;
@@ -981,14 +1035,16 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
           if (c == 0) p.ml[slot * kPagedRows + r] = make_float2(top, sum);
         }
       }
-      if (!whole && from_start && tid == 0) {
-        const int64_t more = use.span.tiles - 1 - use.tile;  // tiles in the CTAs after this one
-        PagedDesc d;
+      if (!whole && tid == 0) {
+        PagedPart d;
         d.request = use.request;
         d.head = use.head;
         d.piece = use.piece;
-        d.parts = static_cast<int32_t>(1 + (more + run - 1) / run);
-        p.desc[blockIdx.x] = d;
+        // the item's tiles in the whole order: from its first to its last
+        const int64_t here = u1 - use.left, begin = here - use.tile;
+        d.first = static_cast<int32_t>(begin / run);
+        d.parts = static_cast<int32_t>((begin + use.span.tiles - 1) / run) - d.first + 1;
+        parts[from_start ? 1 : 0] = d;
       }
       __syncthreads();  // the sums are read before the stage is filled again
       fresh = true;
@@ -1001,74 +1057,140 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   if (bits && lane == 0) atomicOr(p.status, bits);
 }
 
-// Joins the items that are spread over several CTAs: block (c, h) takes row h
-// of the item whose first piece is CTA c's last.  Each warp sums every fourth
-// part, then the four are added up.
-__global__ void __launch_bounds__(kPagedThreads) paged_join_kernel(const PagedParams p) {
-  __shared__ float s_acc[kPagedWarps][kPagedMaxDim];
-  __shared__ float s_top[kPagedWarps], s_sum[kPagedWarps];
-  pdl_wait_and_release();
-  const int c = static_cast<int>(blockIdx.x), row = static_cast<int>(blockIdx.y);
-  const PagedDesc d = p.desc[c];
-  if (d.parts < 2) return;
-  const int32_t kvh = d.head, h0 = d.piece * p.rows;
-  if (row >= min(p.rows, p.group - h0)) return;
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  const auto slot_of = [&](int j) { return 2 * static_cast<int64_t>(c + j) + (j == 0 ? 1 : 0); };
+// Joins the items that are spread over several CTAs.  Of an item's rows, block
+// first + j takes rows j, j + parts, ..: a row per warp where there are few
+// parts, all warps on a row where there are many.  Bound by the latency of two
+// dependent reads (which parts, then their sums), so the sums of up to eight
+// parts are asked for at once.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinAhead = 8;
 
-  float top = -INFINITY;
-  for (int j = tid; j < d.parts; j += kPagedThreads)
-    top = fmaxf(top, p.ml[slot_of(j) * kPagedRows + row].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+struct JoinRow {
+  float4 x[2];
+  float top, sum;
+};
 
-  float4 x[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
-  float sum = 0.0f;
-#pragma unroll 4
-  for (int j = warp; j < d.parts; j += kPagedWarps) {
-    const int64_t s = slot_of(j);
-    const float2 ml = p.ml[s * kPagedRows + row];
-    const float f = exp2_from(ml.x, top);
-    sum += f * ml.y;
-    const float *a = p.acc + (s * kPagedRows + row) * kPagedMaxDim;
+// Parts j0, j0 + step, .. of row `row`, by one warp.
+__device__ __forceinline__ JoinRow join_parts(const PagedParams &p, const PagedPart &d, int row,
+                                              int j0, int step) {
+  const int lane = static_cast<int>(lane_id());
+  JoinRow y;
+  y.x[0] = y.x[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  y.top = -INFINITY;
+  y.sum = 0.0f;
+  for (int j = j0; j < d.parts; j += step * kJoinAhead) {
+    float2 ml[kJoinAhead];
+    float4 a[kJoinAhead][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int col = 4 * lane + 128 * i;
-      if (col < p.dim) {
-        const float4 y = *reinterpret_cast<const float4 *>(a + col);
-        x[i].x = fmaf(f, y.x, x[i].x);
-        x[i].y = fmaf(f, y.y, x[i].y);
-        x[i].z = fmaf(f, y.z, x[i].z);
-        x[i].w = fmaf(f, y.w, x[i].w);
+    for (int i = 0; i < kJoinAhead; ++i) {
+      const int k = j + i * step;
+      ml[i] = make_float2(-INFINITY, 0.0f);
+      a[i][0] = a[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k < d.parts) {
+        // the item's first part is its CTA's part 1, the others are part 0
+        const int64_t s = 2 * (static_cast<int64_t>(d.first) + k) + (k == 0 ? 1 : 0);
+        ml[i] = p.ml[s * kPagedRows + row];
+        const float *from = p.acc + (s * kPagedRows + row) * kPagedMaxDim + 4 * lane;
+        if (4 * lane < p.dim) a[i][0] = *reinterpret_cast<const float4 *>(from);
+        if (4 * lane + 128 < p.dim) a[i][1] = *reinterpret_cast<const float4 *>(from + 128);
       }
     }
-  }
+    float top = y.top;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    *reinterpret_cast<float4 *>(&s_acc[warp][4 * lane + 128 * i]) = x[i];
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  sum = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-  const int64_t head = static_cast<int64_t>(kvh) * p.group + h0 + row;
-  const float f = sum == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[kvh] : 1.0f) / sum;
-  for (int col = 4 * tid; col < p.dim; col += 4 * kPagedThreads) {
-    float4 y = make_float4(0, 0, 0, 0);
+    for (int i = 0; i < kJoinAhead; ++i) top = fmaxf(top, ml[i].x);
+    const float drop = exp2_from(y.top, top);
+    y.sum *= drop;
 #pragma unroll
-    for (int w = 0; w < kPagedWarps; ++w) {
-      y.x += s_acc[w][col];
-      y.y += s_acc[w][col + 1];
-      y.z += s_acc[w][col + 2];
-      y.w += s_acc[w][col + 3];
+    for (int c = 0; c < 2; ++c) {
+      y.x[c].x *= drop;
+      y.x[c].y *= drop;
+      y.x[c].z *= drop;
+      y.x[c].w *= drop;
     }
-    paged_store4(p, d.request * p.o_req + head * p.o_head + col,
-                 make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) {
+      const float f = exp2_from(ml[i].x, top);
+      y.sum = fmaf(f, ml[i].y, y.sum);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        y.x[c].x = fmaf(f, a[i][c].x, y.x[c].x);
+        y.x[c].y = fmaf(f, a[i][c].y, y.x[c].y);
+        y.x[c].z = fmaf(f, a[i][c].z, y.x[c].z);
+        y.x[c].w = fmaf(f, a[i][c].w, y.x[c].w);
+      }
+    }
+    y.top = top;
   }
-  if (p.lse && tid == 0)
-    p.lse[static_cast<int64_t>(d.request) * p.kv_heads * p.group + head] =
-        paged_lse(top, sum);
+  return y;
+}
+
+__device__ __forceinline__ void join_store(const PagedParams &p, const PagedPart &d, int row,
+                                           const JoinRow &y) {
+  const int lane = static_cast<int>(lane_id());
+  const int64_t head = static_cast<int64_t>(d.head) * p.group + d.piece * p.rows + row;
+  const float f = y.sum == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[d.head] : 1.0f) / y.sum;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int col = 4 * lane + 128 * c;
+    if (col < p.dim)
+      paged_store4(p, d.request * p.o_req + head * p.o_head + col,
+                   make_float4(y.x[c].x * f, y.x[c].y * f, y.x[c].z * f, y.x[c].w * f));
+  }
+  if (p.lse && lane == 0)
+    p.lse[static_cast<int64_t>(d.request) * p.kv_heads * p.group + head] = paged_lse(y.top, y.sum);
+}
+
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p) {
+  __shared__ float4 s_x[kJoinWarps][2][32];
+  __shared__ float s_top[kJoinWarps], s_sum[kJoinWarps];
+  const int c = static_cast<int>(blockIdx.x);
+  const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x) >> 5;
+  pdl_wait_and_release();
+  PagedPart d[2] = {p.parts[2 * static_cast<int64_t>(c)], p.parts[2 * static_cast<int64_t>(c) + 1]};
+  int turn = 0;  // of the warps, over both items' rows
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (d[k].parts < 2) continue;
+    const int rows = min(p.rows, p.group - d[k].piece * p.rows);
+    for (int row = c - d[k].first; row < rows; row += d[k].parts) {
+      if (d[k].parts <= kJoinAhead) {
+        if (turn++ % kJoinWarps == warp) join_store(p, d[k], row, join_parts(p, d[k], row, 0, 1));
+        continue;
+      }
+      JoinRow y = join_parts(p, d[k], row, warp, kJoinWarps);
+      s_x[warp][0][lane] = y.x[0];
+      s_x[warp][1][lane] = y.x[1];
+      if (lane == 0) {
+        s_top[warp] = y.top;
+        s_sum[warp] = y.sum;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        float top = s_top[0];
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
+        y.x[0] = y.x[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        y.sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+          const float f = exp2_from(s_top[w], top);
+          y.sum = fmaf(f, s_sum[w], y.sum);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 v = s_x[w][h][lane];
+            y.x[h].x = fmaf(f, v.x, y.x[h].x);
+            y.x[h].y = fmaf(f, v.y, y.x[h].y);
+            y.x[h].z = fmaf(f, v.z, y.x[h].z);
+            y.x[h].w = fmaf(f, v.w, y.x[h].w);
+          }
+        }
+        y.top = top;
+        join_store(p, d[k], row, y);
+      }
+      __syncthreads();
+    }
+  }
 }
 
 }  // namespace ts

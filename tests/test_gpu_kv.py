@@ -271,6 +271,30 @@ def test_append_e4m3_rounding(ts, sampler):
     assert np.array_equal(raw(torch, v).reshape(-1), got)
 
 
+@pytest.mark.parametrize("scale", [0.03, 1.0 / 3.0, 7.3e-5, 448.0, 1e-30, 3e30, 2.0 ** -100])
+def test_append_e4m3_scales(ts, sampler, scale):
+    """Values around every tie times the scale, at scales from tiny to huge: the
+    fp32 quotient, rounded once more."""
+    import torch
+    scale = np.float32(scale)
+    vals = okv.e4m3_values()
+    mid = np.concatenate([(vals[1:] + vals[:-1]) / 2, vals])
+    rng = np.random.default_rng(3)
+    with np.errstate(over="ignore"):
+        at = (mid * float(scale)).astype(np.float32)
+        x = np.concatenate([at] + [np.nextafter(at, np.float32(s), dtype=np.float32) for s in (0, 3e38)]
+                           + [(rng.normal(0, 100, 20000) * float(scale)).astype(np.float32)])
+        x = np.concatenate([x, -x, np.array([np.inf, -np.inf, 3e38, -3e38, 0.0, -0.0], np.float32)])
+        x = np.concatenate([x, np.zeros(-x.size % 16, np.float32)])
+        want = okv.to_e4m3(x / scale)
+    k, v = cache_pair(torch, x.size // 16, 1, 1, 16, torch.float8_e4m3fn, "nhd")
+    new = torch.from_numpy(x).cuda().view(-1, 1, 16)
+    sc = torch.tensor([float(scale)], device="cuda")
+    ts.ts_kv_append(sampler.handle, ts.KvCache(k, v, sc, sc), ts.KvTokens(new, new, torch.arange(new.shape[0], device="cuda")))
+    assert np.array_equal(raw(torch, k).reshape(-1), want)
+    assert np.array_equal(raw(torch, v).reshape(-1), want)
+
+
 def test_append_refusals(ts, sampler):
     import torch
     k, v = cache_pair(torch, 4, 16, 2, 64, torch.bfloat16, "nhd")
