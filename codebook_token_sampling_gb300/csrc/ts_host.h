@@ -29,6 +29,7 @@ struct ts_sampler {
   int ws_vocab;       // widest row it was sized for
   struct ts_kv_state *kv;  // the paged cache's workspace (ts_reserve_kv), or null
   int kv_ctas;        // paged attention: 0 auto, else its number of CTAs (testing)
+  int kv_join;        // 0 auto, 1 joins by a launch of their own, 2 by the last CTA (testing)
 };
 
 namespace ts_host {

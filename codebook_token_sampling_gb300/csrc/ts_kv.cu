@@ -22,7 +22,8 @@ struct ts_kv_state {
   void *mem;
   int ctas;          // pieces for this many CTAs
   int max_requests;
-  ts::PagedPart *parts;
+  ts::PagedParts *parts;
+  uint32_t *arrived;
   float *acc;
   float2 *ml;
   int32_t *lens, *n_free;
@@ -58,6 +59,7 @@ bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) %
 struct PagedKernel {
   const void *fn;
   uint32_t smem;
+  int tile;       // tokens
   int occupancy;  // CTAs per SM
 };
 
@@ -67,7 +69,7 @@ PagedKernel paged_kernel(bool page16) {
   static_assert(ts::PagedShape<Core, ns>::kSmem <= 226 * 1024, "shared memory of a CTA");
   return {page16 ? reinterpret_cast<const void *>(ts::paged_attention_kernel<Core, ns, true>)
                  : reinterpret_cast<const void *>(ts::paged_attention_kernel<Core, ns, false>),
-          ts::PagedShape<Core, ns>::kSmem, 0};
+          ts::PagedShape<Core, ns>::kSmem, ts::PagedShape<Core, ns>::kTile, 0};
 }
 
 // kind 0, 1: bf16 cache with up to 8 or 16 query heads per item, 2, 3: e4m3, 4
@@ -92,6 +94,10 @@ PagedKernel paged_kernel_for(int kind, int width, bool page16) {
   return width == 0 ? paged_kernel_of<64>(kind, page16)
        : width == 1 ? paged_kernel_of<128>(kind, page16) : paged_kernel_of<256>(kind, page16);
 }
+
+// Items of up to about this many parts are joined by the last CTA to come,
+// those of more by a launch of their own.
+constexpr int kJoinHere = 10;
 
 // Per device, once: the kernels' shared-memory limits and occupancies.
 constexpr int kMaxDevices = 64;
@@ -195,6 +201,11 @@ ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests) {
       if (e != cudaSuccess) {
         delete kv;
         rc = e == cudaErrorMemoryAllocation ? TS_ERR_NO_MEMORY : cuda_fail(e, "cudaMalloc");
+      } else if ((e = cudaMemset(kv->mem, 0, bytes)) != cudaSuccess ||  // the counters start at zero,
+                 (e = cudaStreamSynchronize(nullptr)) != cudaSuccess) {  // for calls on any stream
+        cudaFree(kv->mem);
+        delete kv;
+        rc = cuda_fail(e, "cudaMemset");
       } else {
         kv->ctas = ctas;
         kv->max_requests = max_requests;
@@ -203,7 +214,9 @@ ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests) {
         at += 2 * static_cast<size_t>(ctas) * ts::kPagedAccBytes;
         kv->ml = reinterpret_cast<float2 *>(at);
         at += 2 * static_cast<size_t>(ctas) * ts::kPagedRows * sizeof(float2);
-        kv->parts = reinterpret_cast<ts::PagedPart *>(at);
+        kv->parts = reinterpret_cast<ts::PagedParts *>(at);
+        at += 2 * static_cast<size_t>(ctas) * sizeof(ts::PagedParts);
+        kv->arrived = reinterpret_cast<uint32_t *>(at);
         kv->n_free = reinterpret_cast<int32_t *>(static_cast<char *>(kv->mem) + pieces);
         kv->lens = kv->n_free + 1;
         s->kv = kv;
@@ -402,7 +415,7 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.mask_stride = q->mask_stride;
   p.table = q->block_table;
   p.table_stride = q->table_stride;
-  p.max_blocks = q->max_blocks;
+  p.room = q->max_blocks * c->block_size;
   p.lens = q->lens;
   p.n_requests = q->n_requests;
   p.k = c->k;
@@ -428,10 +441,19 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.window = q->window;
   p.by_block = ts::FastDiv::of(static_cast<uint32_t>(c->block_size));
   p.parts = s->kv->parts;
+  p.arrived = s->kv->arrived;
   p.acc = s->kv->acc;
   p.ml = s->kv->ml;
   p.ctas = k.occupancy * s->num_sms;
   if (s->kv_ctas) p.ctas = std::min(p.ctas, s->kv_ctas);
+  p.by_ctas = ts::FastDiv::of(static_cast<uint32_t>(p.ctas));
+  // a request's tiles of 32 tokens or more, rounded up twice
+  const double tiles = (p.room / 32 + 2.0) * p.pieces * p.kv_heads * q->n_requests;
+  p.tiles_fit = tiles < 2.0e9 ? 1 : 0;
+  // Parts of an item, about: the CTAs that share it, no more than its tiles.
+  const int64_t items = static_cast<int64_t>(p.pieces) * p.kv_heads * q->n_requests;
+  const int64_t parts = std::min<int64_t>(p.ctas / items + 2, (p.room + k.tile - 1) / k.tile);
+  p.join_here = s->kv_join ? s->kv_join - 1 : parts <= kJoinHere ? 1 : 0;
   p.out_f32 = f32 ? 1 : 0;
   p.status = s->status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -439,6 +461,7 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   cudaError_t e = launch(k.fn, dim3(static_cast<unsigned>(p.ctas)), ts::kPagedThreads, k.smem,
                          s->pdl != 0, st, args);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  if (p.join_here) return TS_OK;
   e = launch(reinterpret_cast<const void *>(ts::paged_join_kernel),
              dim3(static_cast<unsigned>(p.ctas)), ts::kJoinThreads, 0, s->pdl != 0, st, args);
   return e == cudaSuccess ? TS_OK : cuda_fail(e, "paged attention join launch");

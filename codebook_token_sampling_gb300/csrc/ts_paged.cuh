@@ -12,8 +12,10 @@
 // laid end to end, are dealt to the CTAs in equal runs.  Every CTA finds its
 // run by summing the lengths itself, so ragged batches balance with nothing
 // planned on the host and no launch before this one.  A run holds whole items
-// and at most two pieces of items, which go to a workspace and are joined by
-// paged_join_kernel.
+// and at most two parts of items that other runs share: those go to a
+// workspace, and the CTA that brings an item's last part joins them; where
+// items have many parts, paged_join_kernel does.  The parts' order in the sums
+// is always the same.
 //
 // A CTA is four warps; warp w takes the w-th quarter of a tile's tokens with a
 // running maximum and sum of its own and a private ring of cp.async stages (a
@@ -35,18 +37,19 @@ constexpr int kPagedPage = 16;                       // a stage's tokens divide 
 constexpr int kPagedRows = 16;                       // most query heads per item
 constexpr int kPagedMaxDim = 256;
 
-// A part of an item in the workspace: kPagedRows rows of kPagedMaxDim sums,
-// each row's maximum and sum, and what it is a part of.  A CTA's first part (of
-// an item that began in an earlier CTA) is its part 0, the item that it begins
-// and does not end its part 1.
-struct PagedPart {
+// The workspace: two places per CTA for parts of items (place 0 for an item
+// that began in an earlier CTA, place 1 for one that it begins and does not
+// end), each of kPagedRows rows of kPagedMaxDim sums, the rows' maxima and sums
+// and what it is a part of; and a counter per CTA of the parts that have come
+// of the item that it begins.  Counters are zero between calls.
+struct PagedParts {
+  int32_t first, parts;  // the CTA of the item's first part; their number, 0: nothing here
   int32_t request, head, piece;
-  int32_t first, parts;  // the CTA of the item's first part, their number (0: none here)
 };
 constexpr size_t kPagedAccBytes = sizeof(float) * kPagedRows * kPagedMaxDim;
 constexpr size_t paged_workspace_bytes(int ctas) {
   return static_cast<size_t>(ctas) *
-         (2 * (sizeof(PagedPart) + kPagedAccBytes + sizeof(float2) * kPagedRows));
+         (2 * (kPagedAccBytes + sizeof(float2) * kPagedRows + sizeof(PagedParts)) + sizeof(uint32_t));
 }
 
 struct PagedParams {
@@ -59,7 +62,7 @@ struct PagedParams {
   int64_t mask_stride;
   const int32_t *table;
   int64_t table_stride;
-  int32_t max_blocks;
+  int32_t room;             // tokens of a table row
   const int32_t *lens;
   int32_t n_requests;
   const void *k, *v;
@@ -73,10 +76,14 @@ struct PagedParams {
   float scale, softcap;
   int32_t window;           // 0: none
   FastDiv by_block;
-  PagedPart *parts;         // [2 ctas]
+  PagedParts *parts;        // [2 ctas]
+  uint32_t *arrived;        // [ctas]
   float *acc;               // [2 ctas][kPagedRows][kPagedMaxDim]
   float2 *ml;               // [2 ctas][kPagedRows]
   int32_t ctas;             // of the main launch
+  int32_t join_here;        // 1: the last CTA to come joins, 0: paged_join_kernel does
+  FastDiv by_ctas;
+  int32_t tiles_fit;        // all tiles, and what a search adds to them, stay below 2^31
   int32_t out_f32;
   uint32_t *status;
 };
@@ -89,9 +96,11 @@ __device__ __forceinline__ float exp2_from(float m, float top) {
   return m == -INFINITY ? 0.0f : exp2f(m - top);
 }
 
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gmem, bool real) {
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gmem, bool real,
+                                                   uint64_t policy) {
   const int n = real ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(n)
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(smem),
+               "l"(gmem), "r"(n), "l"(policy)
                : "memory");
 }
 
@@ -672,6 +681,9 @@ struct PagedShape {
   // an item's end puts the warp's sums where its last stage was
   static_assert(Core::kRows * Core::kDim * 4 <= 2 * kHalf, "a stage holds the sums");
   static constexpr uint32_t kSmem = kPagedWarps * (kRing + Core::kWarpBytes) + Core::kQBytes;
+  // CTAs per SM that the registers have to allow
+  static constexpr int kFit = static_cast<int>(226 * 1024 / (kSmem + 2048));
+  static constexpr int kPerSm = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
 };
 
 // Tiles of request r's items, 0 where nothing is attended; `bad`: its length
@@ -682,12 +694,109 @@ struct PagedSpan {
 template <int TILE>
 __device__ __forceinline__ PagedSpan paged_span(const PagedParams &p, int32_t len, bool &bad) {
   PagedSpan s;
-  bad = len < 0 || len > static_cast<int64_t>(p.max_blocks) * p.block_size;
+  bad = len < 0 || len > p.room;
   s.len = bad ? 0 : len;
   s.first = p.window > 0 && s.len > p.window ? s.len - p.window : 0;
   s.t0 = s.first & ~(kPagedPage - 1);
   s.tiles = (s.len - s.t0 + TILE - 1) / TILE;
   return s;
+}
+
+// A CTA's run of tiles [u0, u1) of all, and where tile u0 is.
+struct PagedRun {
+  int64_t run, u0, u1;  // run: tiles of a full run
+  int32_t request, len, head, piece, tile;
+};
+
+// Every warp finds it for itself, so that none waits: a lane takes four
+// requests of 128 at a time, one round of loads and one warp scan where that
+// is all of them.  It stands before a call's first load of the cache, and with
+// few requests most of what it takes is the latency of its instructions: 32-bit
+// sums and a multiplication for the division where the tiles allow.
+template <class Int, int TILE>
+__device__ __forceinline__ PagedRun paged_run(const PagedParams &p) {
+  const int lane = static_cast<int>(lane_id());
+  const Int per_request = static_cast<Int>(p.kv_heads * p.pieces);
+  int32_t len[4];
+  Int mine[4], sum, in;
+  const auto load = [&](int64_t r0) {  // a round's requests: four per lane
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = r0 + 4 * lane + i;
+      len[i] = r < p.n_requests ? p.lens[r] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      bool bad;
+      mine[i] = static_cast<Int>(paged_span<TILE>(p, len[i], bad).tiles) * per_request;
+      sum += mine[i];
+    }
+  };
+  const auto scan = [&]() {
+    in = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Int x = __shfl_up_sync(0xFFFFFFFFu, in, o);
+      if (lane >= o) in += x;
+    }
+  };
+  Int total = 0;
+  for (int64_t r0 = 128; r0 < p.n_requests; r0 += 128) {
+    load(r0);
+    total += sum;
+  }
+  if (p.n_requests > 128) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  }
+  load(0);
+  scan();
+  Int seen = __shfl_sync(0xFFFFFFFFu, in, 31);
+  total += seen;
+
+  PagedRun y;
+  Int run;
+  if constexpr (sizeof(Int) == 4) run = p.by_ctas.div(total + p.ctas - 1);
+  else run = (total + p.ctas - 1) / p.ctas;
+  const Int u0 = run * static_cast<Int>(blockIdx.x);
+  y.run = run;
+  y.u0 = u0;
+  y.u1 = min(u0 + run, total);
+  y.request = y.len = y.head = y.piece = y.tile = 0;
+  if (u0 >= total) return y;
+  for (int64_t r0 = 0;;) {
+    if (u0 < seen) {
+      const Int before = seen - __shfl_sync(0xFFFFFFFFu, in, 31) + in - sum;
+      const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, u0 < before + sum)) - 1;
+      int which = 0;
+      Int skip = before;
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (which == i && u0 >= skip + mine[i]) {
+          skip += mine[i];
+          which = i + 1;
+        }
+      int32_t l = len[0];
+#pragma unroll
+      for (int i = 1; i < 4; ++i)
+        if (which == i) l = len[i];
+      y.request = __shfl_sync(0xFFFFFFFFu, static_cast<int32_t>(r0) + 4 * lane + which, owner);
+      y.len = __shfl_sync(0xFFFFFFFFu, l, owner);
+      const Int off = u0 - __shfl_sync(0xFFFFFFFFu, skip, owner);
+      bool bad;
+      const Int tiles = static_cast<Int>(paged_span<TILE>(p, y.len, bad).tiles);
+      const int32_t item = static_cast<int32_t>(off / tiles);
+      y.tile = static_cast<int32_t>(off - item * tiles);
+      y.head = p.pieces == 1 ? item : item / p.pieces;
+      y.piece = item - y.head * p.pieces;
+      return y;
+    }
+    r0 += 128;
+    load(r0);
+    scan();
+    seen += __shfl_sync(0xFFFFFFFFu, in, 31);
+  }
 }
 
 __device__ __forceinline__ void paged_store4(const PagedParams &p, int64_t at, float4 x) {
@@ -703,19 +812,96 @@ __device__ __forceinline__ float paged_lse(float top, float sum) {
   return top == -INFINITY && sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
+// The place of an item's part k: its first part is its CTA's place 1.
+__device__ __forceinline__ int64_t place_of(int first, int k) {
+  return 2 * (static_cast<int64_t>(first) + k) + (k == 0 ? 1 : 0);
+}
+
+// Four columns of a row of one or several parts.
+struct PagedSum {
+  float4 x;
+  float top, sum;
+};
+
+__device__ __forceinline__ uint32_t counted(const uint32_t *p) {
+  uint32_t x;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
+
+__device__ __forceinline__ void take_in(PagedSum &y, float f, const float4 &x, float sum) {
+  y.sum = fmaf(f, sum, y.sum);
+  y.x.x = fmaf(f, x.x, y.x.x);
+  y.x.y = fmaf(f, x.y, y.x.y);
+  y.x.z = fmaf(f, x.z, y.x.z);
+  y.x.w = fmaf(f, x.w, y.x.w);
+}
+
+// Parts k0, k0 + step, .. below k1, AHEAD of them asked for at once, from L2
+// (other SMs wrote them).  Part `mine` is not read: it is `own`.
+template <int AHEAD>
+__device__ __forceinline__ PagedSum join_parts(const PagedParams &p, int first, int row, int col,
+                                               int k0, int k1, int step, int mine,
+                                               const PagedSum &own) {
+  PagedSum y;
+  y.x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  y.top = -INFINITY;
+  y.sum = 0.0f;
+#pragma unroll 1
+  for (int k = k0; k < k1; k += step * AHEAD) {
+    PagedSum a[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int part = k + i * step;
+      a[i].x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      a[i].top = -INFINITY;
+      a[i].sum = 0.0f;
+      if (part == mine) {
+        a[i] = own;
+      } else if (part < k1) {
+        const int64_t at = place_of(first, part) * kPagedRows + row;
+        const float2 ml = __ldcg(p.ml + at);
+        a[i].top = ml.x;
+        a[i].sum = ml.y;
+        a[i].x = __ldcg(reinterpret_cast<const float4 *>(p.acc + at * kPagedMaxDim + col));
+      }
+    }
+    float top = y.top;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) top = fmaxf(top, a[i].top);
+    const PagedSum was = y;
+    y.x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    y.sum = 0.0f;
+    y.top = top;
+    take_in(y, exp2_from(was.top, top), was.x, was.sum);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) take_in(y, exp2_from(a[i].top, top), a[i].x, a[i].sum);
+  }
+  return y;
+}
+
+// Four columns of a head's output, and with the first of them its lse.
+__device__ __forceinline__ void paged_answer(const PagedParams &p, int request, int kv_head,
+                                             int64_t head, int col, const PagedSum &y) {
+  const float f = y.sum == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[kv_head] : 1.0f) / y.sum;
+  paged_store4(p, request * p.o_req + head * p.o_head + col,
+               make_float4(y.x.x * f, y.x.y * f, y.x.z * f, y.x.w * f));
+  if (col == 0 && p.lse)
+    p.lse[static_cast<int64_t>(request) * p.kv_heads * p.group + head] = paged_lse(y.top, y.sum);
+}
+
 // PAGE16: the block size is a multiple of 16, so that every 16 tokens of a
 // stage lie in one block, whose rows follow one another: one table entry per
 // 16 tokens and addresses by addition, instead of both per token.
 template <class Core, int NS, bool PAGE16>
-__global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kPagedThreads, PagedShape<Core, NS>::kPerSm)
+    paged_attention_kernel(const PagedParams p) {
   using Shape = PagedShape<Core, NS>;
   using Elem = std::conditional_t<Core::kFma, float, uint16_t>;  // of the queries
   extern __shared__ __align__(128) unsigned char paged_smem[];
   __shared__ uint32_t valid_ring[kPagedWarps][NS], lost_ring[kPagedWarps][NS];
   __shared__ float sm[kPagedWarps][kPagedRows], sl[kPagedWarps][kPagedRows];
-  __shared__ int64_t s_part[kPagedWarps], s_rest[kPagedWarps];
-  __shared__ int64_t s_before;
-  __shared__ int32_t s_request;
+  __shared__ int s_come;
 
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   unsigned char *ring = paged_smem + warp * Shape::kRing;
@@ -724,43 +910,15 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   unsigned char *sq = paged_smem + kPagedWarps * (Shape::kRing + Core::kWarpBytes);
   pdl_wait_and_release();
 
-  // ---- this CTA's run of tiles: the first 128 requests' tiles are summed and
-  // searched with one load each, more requests in further rounds ----
-  const int per_request = p.kv_heads * p.pieces;
+  // ---- this CTA's run of tiles ----
   const int n_heads = p.kv_heads * p.group;
   uint32_t bits = 0;
-  const auto tiles_of = [&](int64_t r) {
-    bool bad;
-    return r < p.n_requests
-               ? static_cast<int64_t>(paged_span<Shape::kTile>(p, p.lens[r], bad).tiles) * per_request
-               : 0;
-  };
-  int64_t mine = tiles_of(tid), rest = 0;
-  for (int64_t r = tid + kPagedThreads; r < p.n_requests; r += kPagedThreads) rest += tiles_of(r);
-  // leaves in `in` the sum of the threads' values up to this one's, in the
-  // warps' places their totals
-  int64_t in;
-  const auto scan = [&]() {
-    in = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, in, o);
-      if (lane >= o) in += x;
-    }
-    if (lane == 31) s_part[warp] = in;
-  };
-  scan();
-  if (p.n_requests > kPagedThreads) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
-  }
-  if (lane == 0) s_rest[warp] = rest;
-  __syncthreads();
-  int64_t seen = s_part[0] + s_part[1] + s_part[2] + s_part[3];
-  const int64_t total = seen + s_rest[0] + s_rest[1] + s_rest[2] + s_rest[3];
-  const int64_t run = (total + p.ctas - 1) / p.ctas;
-  const int64_t u0 = run * blockIdx.x;
-  const int64_t u1 = min(u0 + run, total);
+  PagedRun at;
+  if (p.tiles_fit)
+    at = paged_run<uint32_t, Shape::kTile>(p);
+  else
+    at = paged_run<int64_t, Shape::kTile>(p);
+  const int64_t run = at.run, u0 = at.u0, u1 = at.u1;
 
   // requests with nothing to attend to
   const auto answer_empty = [&]() {
@@ -779,33 +937,11 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
           p.lse[static_cast<int64_t>(r) * n_heads + h] = bad ? x : -INFINITY;
     }
   };
-  PagedPart *parts = p.parts + 2 * static_cast<int64_t>(blockIdx.x);
-  if (tid < 2) parts[tid].parts = 0;
+  if (!p.join_here && tid < 2) p.parts[2 * static_cast<int64_t>(blockIdx.x) + tid].parts = 0;
   if (u0 >= u1) {
     answer_empty();
     if (bits && tid == 0) atomicOr(p.status, bits);
     return;
-  }
-
-  // the request that holds tile u0
-  {
-    int64_t r = tid, before = in - mine;
-    for (int w = 0; w < warp; ++w) before += s_part[w];
-    while (true) {
-      if (before <= u0 && u0 < before + mine) {
-        s_request = static_cast<int32_t>(r);
-        s_before = before;
-      }
-      __syncthreads();
-      if (seen > u0) break;
-      r += kPagedThreads;
-      mine = tiles_of(r);
-      scan();
-      __syncthreads();
-      before = seen + in - mine;
-      for (int w = 0; w < warp; ++w) before += s_part[w];
-      seen += s_part[0] + s_part[1] + s_part[2] + s_part[3];
-    }
   }
 
   // ---- cursors over the run: requests, their key heads, pieces of the query
@@ -835,15 +971,13 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   };
   Cursor use;
   use.left = u1 - u0;
-  use.request = s_request;
+  use.request = at.request;
+  use.head = at.head;
+  use.piece = at.piece;
+  use.tile = at.tile;
   {
     bool bad;
-    use.span = paged_span<Shape::kTile>(p, p.lens[use.request], bad);
-    const int64_t at = u0 - s_before;
-    const int32_t item = static_cast<int32_t>(at / use.span.tiles);
-    use.tile = static_cast<int32_t>(at - static_cast<int64_t>(item) * use.span.tiles);
-    use.head = item / p.pieces;
-    use.piece = item - use.head * p.pieces;
+    use.span = paged_span<Shape::kTile>(p, at.len, bad);
   }
   Cursor get = use;
 
@@ -856,6 +990,9 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   const int my_row = kChunks <= 32 ? lane / kChunks : 0, my_chunk = lane % kChunks;
   const int chunks = p.dim * Core::kElemBytes / 16;
   const uint32_t my_at = ring_at + stage_at<Core::kRowBytes, Core::kPer>(my_row, my_chunk);
+  // the rows are read once per step: in L2 they make way for what every layer
+  // and CTA reads again (tables, lengths, queries, parts)
+  const uint64_t policy = l2_evict_first();
   const int32_t *table = nullptr;
   const uint8_t *mask = nullptr;
   const char *kh = nullptr, *vh = nullptr;  // the item's rows, for this lane's first chunk
@@ -906,8 +1043,8 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
           const uint32_t at = (to ^ (stage_xor<Core::kRowBytes, Core::kPer>(r) << 4)) +
                               r * Core::kRowBytes + 512 * part;
           const int skip = my_chunk + 32 * part < chunks ? 16 * (my_chunk + 32 * part) : 0;
-          cp_async16_or_zero(at, ka + skip, real);
-          cp_async16_or_zero(at + Shape::kHalf, va + skip, real);
+          cp_async16_or_zero(at, ka + skip, real, policy);
+          cp_async16_or_zero(at + Shape::kHalf, va + skip, real, policy);
         }
         ka += kRowsAt * p.k_token;
         va += kRowsAt * p.v_token;
@@ -996,55 +1133,76 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
       // ---- the four warps' parts as one: each puts its sums where its stage
       // was ----
       __syncwarp();
+      const bool whole = from_start && item_end;
+      PagedParts d;
+      if (!whole) {
+        // the item's tiles in the order of all: from its first to its last
+        const int64_t begin = u1 - use.left - use.tile, last = begin + use.span.tiles - 1;
+        if (p.tiles_fit) {
+          d.first = static_cast<uint32_t>(begin) / static_cast<uint32_t>(run);
+          d.parts = static_cast<uint32_t>(last) / static_cast<uint32_t>(run) - d.first + 1;
+        } else {
+          d.first = static_cast<int32_t>(begin / run);
+          d.parts = static_cast<int32_t>(last / run) - d.first + 1;
+        }
+        d.request = use.request;
+        d.head = use.head;
+        d.piece = use.piece;
+        // whether the others are there is asked before they are needed
+        if (tid == 0) s_come = p.join_here ? static_cast<int>(counted(p.arrived + d.first)) : -1;
+      }
       core.give(reinterpret_cast<float *>(ring + stage * 2 * Shape::kHalf), sm[warp], sl[warp]);
       __syncthreads();
       const int rows = min(p.rows, p.group - use.piece * p.rows), quads = p.dim / 4;
       const int64_t head = static_cast<int64_t>(use.head) * p.group + use.piece * p.rows;
-      const bool whole = from_start && item_end;
-      // a piece: the item's first one goes to slot 1, the others are the first
-      // thing in their CTA's run and go to slot 0
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0);
-      const float vscale = p.v_scale ? p.v_scale[use.head] : 1.0f;
-      for (int i = tid; i < rows * quads; i += kPagedThreads) {
-        const int r = i / quads, c = 4 * (i - r * quads);
-        float top = sm[0][r];
+      const int64_t place = 2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0);
+      const int mine = whole ? 0 : static_cast<int>(blockIdx.x) - d.first;
+      bool join = !whole && s_come == d.parts - 1;
+      const auto each = [&](bool publish, bool joined) {
+        for (int i = tid; i < rows * quads; i += kPagedThreads) {
+          const int r = i / quads, c = 4 * (i - r * quads);
+          PagedSum y;
+          y.top = sm[0][r];
 #pragma unroll
-        for (int w = 1; w < kPagedWarps; ++w) top = fmaxf(top, sm[w][r]);
-        float sum = 0.0f;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int w = 1; w < kPagedWarps; ++w) y.top = fmaxf(y.top, sm[w][r]);
+          y.sum = 0.0f;
+          y.x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kPagedWarps; ++w) {
-          const float f = exp2_from(sm[w][r], top);
-          const float4 y = *reinterpret_cast<const float4 *>(
-              reinterpret_cast<const float *>(paged_smem + w * Shape::kRing + stage * 2 * Shape::kHalf) +
-              Core::at(r, c));
-          sum = fmaf(f, sl[w][r], sum);
-          x.x = fmaf(f, y.x, x.x);
-          x.y = fmaf(f, y.y, x.y);
-          x.z = fmaf(f, y.z, x.z);
-          x.w = fmaf(f, y.w, x.w);
+          for (int w = 0; w < kPagedWarps; ++w)
+            take_in(y, exp2_from(sm[w][r], y.top),
+                    *reinterpret_cast<const float4 *>(
+                        reinterpret_cast<const float *>(paged_smem + w * Shape::kRing +
+                                                        stage * 2 * Shape::kHalf) + Core::at(r, c)),
+                    sl[w][r]);
+          if (publish) {
+            *reinterpret_cast<float4 *>(p.acc + (place * kPagedRows + r) * kPagedMaxDim + c) = y.x;
+            if (c == 0) p.ml[place * kPagedRows + r] = make_float2(y.top, y.sum);
+          } else {
+            if (joined) y = join_parts<4>(p, d.first, r, c, 0, d.parts, 1, mine, y);
+            paged_answer(p, use.request, use.head, head + r, c, y);
+          }
         }
-        if (whole) {
-          const float f = sum == 0.0f ? 0.0f : vscale / sum;
-          paged_store4(p, use.request * p.o_req + (head + r) * p.o_head + c,
-                       make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
-          if (c == 0 && p.lse)
-            p.lse[static_cast<int64_t>(use.request) * n_heads + head + r] = paged_lse(top, sum);
-        } else {
-          *reinterpret_cast<float4 *>(p.acc + (slot * kPagedRows + r) * kPagedMaxDim + c) = x;
-          if (c == 0) p.ml[slot * kPagedRows + r] = make_float2(top, sum);
+      };
+      if (whole || join) {
+        each(false, join);
+        if (join && tid == 0) p.arrived[d.first] = 0;
+      } else {
+        each(true, false);
+        if (p.join_here) {
+          __syncthreads();  // the part is written
+          if (tid == 0) {
+            __threadfence();
+            s_come = static_cast<int>(atomicAdd(p.arrived + d.first, 1u));
+            __threadfence();
+          }
+          __syncthreads();
+          if (s_come == d.parts - 1) {  // the others came meanwhile
+            each(false, true);
+            if (tid == 0) p.arrived[d.first] = 0;
+          }
+        } else if (tid == 0) {
+          p.parts[place] = d;
         }
-      }
-      if (!whole && tid == 0) {
-        PagedPart d;
-        d.request = use.request;
-        d.head = use.head;
-        d.piece = use.piece;
-        // the item's tiles in the whole order: from its first to its last
-        const int64_t here = u1 - use.left, begin = here - use.tile;
-        d.first = static_cast<int32_t>(begin / run);
-        d.parts = static_cast<int32_t>((begin + use.span.tiles - 1) / run) - d.first + 1;
-        parts[from_start ? 1 : 0] = d;
       }
       __syncthreads();  // the sums are read before the stage is filled again
       fresh = true;
@@ -1057,136 +1215,43 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_kernel(const Pa
   if (bits && lane == 0) atomicOr(p.status, bits);
 }
 
-// Joins the items that are spread over several CTAs.  Of an item's rows, block
-// first + j takes rows j, j + parts, ..: a row per warp where there are few
-// parts, all warps on a row where there are many.  Bound by the latency of two
-// dependent reads (which parts, then their sums), so the sums of up to eight
-// parts are asked for at once.
+// Joins the items that are spread over many CTAs.  Of an item's rows, block
+// first + j takes rows j, j + parts, ..: its eight warps share the parts, a
+// lane four or eight columns of them, and are added up in shared memory.  Its
+// launch waits for all CTAs, which with few parts costs more than the last CTA
+// needs to join them (measured: see join_here in ts_kv.cu).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinAhead = 8;
-
-struct JoinRow {
-  float4 x[2];
-  float top, sum;
-};
-
-// Parts j0, j0 + step, .. of row `row`, by one warp.
-__device__ __forceinline__ JoinRow join_parts(const PagedParams &p, const PagedPart &d, int row,
-                                              int j0, int step) {
-  const int lane = static_cast<int>(lane_id());
-  JoinRow y;
-  y.x[0] = y.x[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  y.top = -INFINITY;
-  y.sum = 0.0f;
-  for (int j = j0; j < d.parts; j += step * kJoinAhead) {
-    float2 ml[kJoinAhead];
-    float4 a[kJoinAhead][2];
-#pragma unroll
-    for (int i = 0; i < kJoinAhead; ++i) {
-      const int k = j + i * step;
-      ml[i] = make_float2(-INFINITY, 0.0f);
-      a[i][0] = a[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (k < d.parts) {
-        // the item's first part is its CTA's part 1, the others are part 0
-        const int64_t s = 2 * (static_cast<int64_t>(d.first) + k) + (k == 0 ? 1 : 0);
-        ml[i] = p.ml[s * kPagedRows + row];
-        const float *from = p.acc + (s * kPagedRows + row) * kPagedMaxDim + 4 * lane;
-        if (4 * lane < p.dim) a[i][0] = *reinterpret_cast<const float4 *>(from);
-        if (4 * lane + 128 < p.dim) a[i][1] = *reinterpret_cast<const float4 *>(from + 128);
-      }
-    }
-    float top = y.top;
-#pragma unroll
-    for (int i = 0; i < kJoinAhead; ++i) top = fmaxf(top, ml[i].x);
-    const float drop = exp2_from(y.top, top);
-    y.sum *= drop;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      y.x[c].x *= drop;
-      y.x[c].y *= drop;
-      y.x[c].z *= drop;
-      y.x[c].w *= drop;
-    }
-#pragma unroll
-    for (int i = 0; i < kJoinAhead; ++i) {
-      const float f = exp2_from(ml[i].x, top);
-      y.sum = fmaf(f, ml[i].y, y.sum);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        y.x[c].x = fmaf(f, a[i][c].x, y.x[c].x);
-        y.x[c].y = fmaf(f, a[i][c].y, y.x[c].y);
-        y.x[c].z = fmaf(f, a[i][c].z, y.x[c].z);
-        y.x[c].w = fmaf(f, a[i][c].w, y.x[c].w);
-      }
-    }
-    y.top = top;
-  }
-  return y;
-}
-
-__device__ __forceinline__ void join_store(const PagedParams &p, const PagedPart &d, int row,
-                                           const JoinRow &y) {
-  const int lane = static_cast<int>(lane_id());
-  const int64_t head = static_cast<int64_t>(d.head) * p.group + d.piece * p.rows + row;
-  const float f = y.sum == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[d.head] : 1.0f) / y.sum;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int col = 4 * lane + 128 * c;
-    if (col < p.dim)
-      paged_store4(p, d.request * p.o_req + head * p.o_head + col,
-                   make_float4(y.x[c].x * f, y.x[c].y * f, y.x[c].z * f, y.x[c].w * f));
-  }
-  if (p.lse && lane == 0)
-    p.lse[static_cast<int64_t>(d.request) * p.kv_heads * p.group + head] = paged_lse(y.top, y.sum);
-}
 
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p) {
-  __shared__ float4 s_x[kJoinWarps][2][32];
-  __shared__ float s_top[kJoinWarps], s_sum[kJoinWarps];
+  __shared__ PagedSum s_sum[kJoinWarps][2][32];
   const int c = static_cast<int>(blockIdx.x);
   const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x) >> 5;
   pdl_wait_and_release();
-  PagedPart d[2] = {p.parts[2 * static_cast<int64_t>(c)], p.parts[2 * static_cast<int64_t>(c) + 1]};
-  int turn = 0;  // of the warps, over both items' rows
-#pragma unroll
+  const PagedParts d[2] = {p.parts[2 * static_cast<int64_t>(c)], p.parts[2 * static_cast<int64_t>(c) + 1]};
+#pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     if (d[k].parts < 2) continue;
     const int rows = min(p.rows, p.group - d[k].piece * p.rows);
+    const int64_t head = static_cast<int64_t>(d[k].head) * p.group + d[k].piece * p.rows;
     for (int row = c - d[k].first; row < rows; row += d[k].parts) {
-      if (d[k].parts <= kJoinAhead) {
-        if (turn++ % kJoinWarps == warp) join_store(p, d[k], row, join_parts(p, d[k], row, 0, 1));
-        continue;
-      }
-      JoinRow y = join_parts(p, d[k], row, warp, kJoinWarps);
-      s_x[warp][0][lane] = y.x[0];
-      s_x[warp][1][lane] = y.x[1];
-      if (lane == 0) {
-        s_top[warp] = y.top;
-        s_sum[warp] = y.sum;
-      }
+      for (int h = 0; 4 * lane + 128 * h < p.dim && h < 2; ++h)
+        s_sum[warp][h][lane] = join_parts<8>(p, d[k].first, row, 4 * lane + 128 * h, warp, d[k].parts,
+                                             kJoinWarps, -1, PagedSum());
       __syncthreads();
-      if (warp == 0) {
-        float top = s_top[0];
+      if (warp < 2 && 4 * lane + 128 * warp < p.dim) {
+        PagedSum y;
+        y.top = s_sum[0][warp][lane].top;
 #pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
-        y.x[0] = y.x[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = 1; w < kJoinWarps; ++w) y.top = fmaxf(y.top, s_sum[w][warp][lane].top);
+        y.x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         y.sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) {
-          const float f = exp2_from(s_top[w], top);
-          y.sum = fmaf(f, s_sum[w], y.sum);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 v = s_x[w][h][lane];
-            y.x[h].x = fmaf(f, v.x, y.x[h].x);
-            y.x[h].y = fmaf(f, v.y, y.x[h].y);
-            y.x[h].z = fmaf(f, v.z, y.x[h].z);
-            y.x[h].w = fmaf(f, v.w, y.x[h].w);
-          }
+          const PagedSum &z = s_sum[w][warp][lane];
+          take_in(y, exp2_from(z.top, y.top), z.x, z.sum);
         }
-        y.top = top;
-        join_store(p, d[k], row, y);
+        paged_answer(p, d[k].request, d[k].head, head + row, 4 * lane + 128 * warp, y);
       }
       __syncthreads();
     }

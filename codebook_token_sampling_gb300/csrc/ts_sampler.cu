@@ -670,6 +670,7 @@ ts_status ts_create(int device, int max_top_k, ts_sampler **out) {
   s->ws_vocab = 0;
   s->kv = nullptr;
   s->kv_ctas = 0;
+  s->kv_join = 0;
   ts_status rc = TS_OK;
   e = cudaDeviceGetAttribute(&s->num_sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) rc = cuda_fail(e, "cudaDeviceGetAttribute");
@@ -953,6 +954,11 @@ ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value) {
   if (option == TS_OPT_KV_CTAS) {
     if (value < 0) return TS_ERR_INVALID_ARG;
     s->kv_ctas = value;
+    return TS_OK;
+  }
+  if (option == TS_OPT_KV_JOIN) {
+    if (value < 0 || value > 2) return TS_ERR_INVALID_ARG;
+    s->kv_join = value;
     return TS_OK;
   }
   if (option == TS_OPT_FAIL_LAUNCH) {

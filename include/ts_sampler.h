@@ -595,6 +595,9 @@ ts_status ts_read_status(ts_sampler *s, uint32_t *bits, void *stream);
 /* TS_OPT_KV_CTAS: the number of CTAs that ts_paged_attention deals its work to
  * (0 = automatic: what the GPU holds at once; more than that is cut to it). */
 #define TS_OPT_KV_CTAS 7
+/* TS_OPT_KV_JOIN: how ts_paged_attention joins the parts of its work (0 =
+ * automatic, 1 = by a launch of their own, 2 = by the last CTA to come). */
+#define TS_OPT_KV_JOIN 8
 ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value);
 
 /* Describes the kernel that ts_sample would launch for `b` (path 1 .. 4,

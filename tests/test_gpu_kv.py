@@ -474,17 +474,20 @@ def test_attention_masks(ts, sampler, kind, window, softcap, masked, block):
 
 
 @pytest.mark.parametrize("kind,group", [("bf16", 4), ("e4m3", 8), ("f32", 2), ("f32", 11)])
+@pytest.mark.parametrize("join", [1, 2])
 @pytest.mark.parametrize("ctas", [1, 2, 3, 7, 40, 0])
-def test_attention_cuts(ts, sampler, kind, group, ctas):
+def test_attention_cuts(ts, sampler, kind, group, ctas, join):
     """The same answers however the tiles are dealt to the CTAs."""
     import torch
     c = attention_case(torch, 11, [1000, 3, 0, 700, 64, 1, 2000], heads=2, group=group, dim=128, block=16, layout="hnd",
                        kind=kind)
     sampler.set_option(ts.TS_OPT_KV_CTAS, ctas)
+    sampler.set_option(ts.TS_OPT_KV_JOIN, join)
     try:
         one = check_attention(ts, sampler, c)
         two = run_attention(ts, sampler, c)
     finally:
+        sampler.set_option(ts.TS_OPT_KV_JOIN, 0)
         sampler.set_option(ts.TS_OPT_KV_CTAS, 0)
     assert np.array_equal(one[0], two[0]) and np.array_equal(one[1], two[1])  # the same in every run
 
@@ -501,13 +504,18 @@ def test_attention_many_requests(ts, sampler):
     assert not got.any() and np.isneginf(lse).all() and status == 0
 
 
+@pytest.mark.parametrize("join", [0, 2])
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
-def test_attention_long(ts, sampler, kind):
+def test_attention_long(ts, sampler, kind, join):
     """One long context, peaked scores (the running maximum moves late)."""
     import torch
     c = attention_case(torch, 13, [20011], heads=1, group=8, dim=128, block=32, layout="hnd", kind=kind, spread=6.0)
     c["k"].view(torch.uint8)[0] = c["k"].view(torch.uint8)[1]
-    check_attention(ts, sampler, c)
+    sampler.set_option(ts.TS_OPT_KV_JOIN, join)
+    try:
+        check_attention(ts, sampler, c)
+    finally:
+        sampler.set_option(ts.TS_OPT_KV_JOIN, 0)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
