@@ -59,17 +59,30 @@ bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) %
 struct PagedKernel {
   const void *fn;
   uint32_t smem;
+  int threads;
   int tile;       // tokens
   int occupancy;  // CTAs per SM
 };
 
+// Stages per warp.  Two, and twelve warps per SM, beat three and eight wherever
+// the registers allow (128 requests of up to 8000 tokens, bf16, 8 x 4 heads of
+// 128: 305 against 317 us; 24 of up to 3001, fp32, 8 x 8 heads: 86 against 102).
+// The 8 KB K rows of wide bf16 and e4m3 heads, and 16 query heads, leave room
+// for fewer warps anyway: three.
+template <class Core>
+constexpr int stages_of() {
+  if (Core::kFma) return 2;
+  if (Core::kTok * Core::kRowBytes > 4096) return 3;
+  return Core::kRows > 8 && Core::kDim > 64 ? 3 : 2;
+}
+
 template <class Core>
 PagedKernel paged_kernel(bool page16) {
-  constexpr int ns = 3;  // stages per warp
+  constexpr int ns = stages_of<Core>();
   static_assert(ts::PagedShape<Core, ns>::kSmem <= 226 * 1024, "shared memory of a CTA");
   return {page16 ? reinterpret_cast<const void *>(ts::paged_attention_kernel<Core, ns, true>)
                  : reinterpret_cast<const void *>(ts::paged_attention_kernel<Core, ns, false>),
-          ts::PagedShape<Core, ns>::kSmem, ts::PagedShape<Core, ns>::kTile, 0};
+          ts::PagedShape<Core, ns>::kSmem, ts::PagedShape<Core, ns>::kThreads, ts::PagedShape<Core, ns>::kTile, 0};
 }
 
 // kind 0, 1: bf16 cache with up to 8 or 16 query heads per item, 2, 3: e4m3, 4
@@ -82,7 +95,7 @@ PagedKernel paged_kernel_of(int kind, bool page16) {
   switch (kind) {
     case 0: return paged_kernel<ts::MmaCore<false, DP, 1, kt>>(page16);
     case 1: return paged_kernel<ts::MmaCore<false, DP, 2, kt>>(page16);
-    case 2: return paged_kernel<ts::MmaCore<true, DP, 1, 2>>(page16);
+    case 2: return paged_kernel<ts::MmaCore<true, DP, 1, DP <= 128 ? 2 : 1>>(page16);
     case 3: return paged_kernel<ts::MmaCore<true, DP, 2, 2>>(page16);
     case 4: return paged_kernel<ts::FmaCore<1, DP>>(page16);
     case 5: return paged_kernel<ts::FmaCore<2, DP>>(page16);
@@ -119,7 +132,7 @@ ts_status paged_setup(int device) {
         cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(k.smem));
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k.occupancy, k.fn, ts::kPagedThreads,
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k.occupancy, k.fn, k.threads,
                                                           k.smem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
         if (k.occupancy < 1) return TS_ERR_UNSUPPORTED;
@@ -447,8 +460,8 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.ctas = k.occupancy * s->num_sms;
   if (s->kv_ctas) p.ctas = std::min(p.ctas, s->kv_ctas);
   p.by_ctas = ts::FastDiv::of(static_cast<uint32_t>(p.ctas));
-  // a request's tiles of 32 tokens or more, rounded up twice
-  const double tiles = (p.room / 32 + 2.0) * p.pieces * p.kv_heads * q->n_requests;
+  // a request's tiles, rounded up at both ends
+  const double tiles = (p.room / k.tile + 2.0) * p.pieces * p.kv_heads * q->n_requests;
   p.tiles_fit = tiles < 2.0e9 ? 1 : 0;
   // Parts of an item, about: the CTAs that share it, no more than its tiles.
   const int64_t items = static_cast<int64_t>(p.pieces) * p.kv_heads * q->n_requests;
@@ -458,7 +471,7 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.status = s->status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   void *args[] = {&p};
-  cudaError_t e = launch(k.fn, dim3(static_cast<unsigned>(p.ctas)), ts::kPagedThreads, k.smem,
+  cudaError_t e = launch(k.fn, dim3(static_cast<unsigned>(p.ctas)), k.threads, k.smem,
                          s->pdl != 0, st, args);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   if (p.join_here) return TS_OK;

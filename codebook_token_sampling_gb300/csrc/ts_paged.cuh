@@ -17,9 +17,10 @@
 // items have many parts, paged_join_kernel does.  The parts' order in the sums
 // is always the same.
 //
-// A CTA is four warps; warp w takes the w-th quarter of a tile's tokens with a
-// running maximum and sum of its own and a private ring of cp.async stages (a
-// quarter's K and V each), so no warp waits for another inside an item.
+// A CTA is four warps (two where fp32 rows are wide); each takes its share of a
+// tile's tokens with a running maximum and sum of its own and a private ring of
+// cp.async stages (a share's K and V each), so no warp waits for another inside
+// an item.
 // The ring runs on across items.  At an item's end the four warps' results
 // are joined in shared memory.
 #pragma once
@@ -31,8 +32,6 @@
 
 namespace ts {
 
-constexpr int kPagedThreads = 128;
-constexpr int kPagedWarps = 4;
 constexpr int kPagedPage = 16;                       // a stage's tokens divide this
 constexpr int kPagedRows = 16;                       // most query heads per item
 constexpr int kPagedMaxDim = 256;
@@ -196,6 +195,7 @@ struct MmaCore {
   static constexpr int kElemBytes = E4M3 ? 1 : 2;
   static constexpr int kRowBytes = DP * kElemBytes;
   static constexpr int kDim = DP;
+  static constexpr int kWarps = 4;
   static constexpr int kSteps = DP / 16;
   // wide rows leave no registers for the queries: one copy in shared memory
   static constexpr bool kSharedQ = DP > 128;
@@ -230,7 +230,7 @@ struct MmaCore {
       const bool real = 8 * n + g < rows;
       const auto keep = [&](int kk, uint32_t x, uint32_t y) {
         if constexpr (kSharedQ) {
-          if ((kk & 3) == warp)
+          if (kk % kWarps == warp)
             *reinterpret_cast<uint2 *>(static_cast<char *>(shared) + (n * kSteps + kk) * 256 + lane * 8) =
                 make_uint2(x, y);
         } else {
@@ -527,6 +527,9 @@ struct FmaCore {
   static constexpr int kSplit = 32 / kLanes;                // tokens side by side
   static constexpr int kCols = DP / 128 > 0 ? DP / 128 : 1; // chunks per lane
   static constexpr int kDim = DP;
+  // stages of 16 KB: six warps per SM as three CTAs of two (62 us), not four as
+  // one (73 us: 24 requests of up to 3001 tokens, 4 x 4 heads of 256)
+  static constexpr int kWarps = DP > 128 ? 2 : 4;
 
   uint64_t o[GR][kCols * 2];  // pairs of columns
   float m[GR], l[GR];
@@ -538,7 +541,7 @@ struct FmaCore {
     float *sq = static_cast<float *>(shared);
     q_at = static_cast<uint32_t>(__cvta_generic_to_shared(sq));
     sc = p.softcap > 0.0f ? p.scale * k_scale : p.scale * k_scale * kLog2e;
-    for (int i = static_cast<int>(threadIdx.x); i < GR * DP / 4; i += kPagedThreads) {
+    for (int i = static_cast<int>(threadIdx.x); i < GR * DP / 4; i += 32 * kWarps) {
       const int r = i / (DP / 4), c = 4 * (i % (DP / 4));
       reinterpret_cast<float4 *>(sq)[i] = r < rows && c < p.dim
           ? *reinterpret_cast<const float4 *>(src + r * p.q_head + c)
@@ -675,15 +678,19 @@ struct FmaCore {
 // --------------------------------------------------------------------------
 template <class Core, int NS>
 struct PagedShape {
-  static constexpr int kTile = Core::kTok * kPagedWarps;  // tokens
+  static constexpr int kTile = Core::kTok * Core::kWarps;  // tokens
   static constexpr uint32_t kHalf = Core::kTok * Core::kRowBytes;  // K or V of a stage
   static constexpr uint32_t kRing = NS * 2 * kHalf;               // of a warp
   // an item's end puts the warp's sums where its last stage was
   static_assert(Core::kRows * Core::kDim * 4 <= 2 * kHalf, "a stage holds the sums");
-  static constexpr uint32_t kSmem = kPagedWarps * (kRing + Core::kWarpBytes) + Core::kQBytes;
+  static constexpr int kThreads = 32 * Core::kWarps;
+  static constexpr uint32_t kSmem = Core::kWarps * (kRing + Core::kWarpBytes) + Core::kQBytes;
   // CTAs per SM that the registers have to allow
   static constexpr int kFit = static_cast<int>(226 * 1024 / (kSmem + 2048));
-  static constexpr int kPerSm = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
+  static constexpr int kMost = (Core::kFma || Core::kRows <= 8 ? 4 : Core::kDim > 64 ? 2 : 3) * 4 / Core::kWarps;
+  static constexpr int kRegs = Core::kDim > 128 ? 65536 / (256 * 32 * Core::kWarps) : kMost;
+  static constexpr int kMin = kFit > kMost ? kMost : kFit;
+  static constexpr int kPerSm = kMin > kRegs ? kRegs : kMin;
 };
 
 // Tiles of request r's items, 0 where nothing is attended; `bad`: its length
@@ -894,10 +901,11 @@ __device__ __forceinline__ void paged_answer(const PagedParams &p, int request, 
 // stage lie in one block, whose rows follow one another: one table entry per
 // 16 tokens and addresses by addition, instead of both per token.
 template <class Core, int NS, bool PAGE16>
-__global__ void __launch_bounds__(kPagedThreads, PagedShape<Core, NS>::kPerSm)
+__global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Core, NS>::kPerSm)
     paged_attention_kernel(const PagedParams p) {
   using Shape = PagedShape<Core, NS>;
   using Elem = std::conditional_t<Core::kFma, float, uint16_t>;  // of the queries
+  constexpr int kPagedWarps = Core::kWarps, kPagedThreads = Shape::kThreads;
   extern __shared__ __align__(128) unsigned char paged_smem[];
   __shared__ uint32_t valid_ring[kPagedWarps][NS], lost_ring[kPagedWarps][NS];
   __shared__ float sm[kPagedWarps][kPagedRows], sl[kPagedWarps][kPagedRows];
