@@ -63,14 +63,15 @@ def split_kernels(plan, num_sms: int, n_rows: int) -> int:
 
 
 def kernel_source_hash(src: str | None = None) -> str:
-    """Hash of the CUDA sources with comments and whitespace removed, to tell
-    whether recorded ncu counters still describe the kernels that run."""
+    """Hash of the sampler's CUDA sources with comments and whitespace removed,
+    to tell whether recorded ncu counters still describe the kernels that run
+    (the paged cache's own sources hold none of them)."""
     import hashlib
     import re
     h = hashlib.sha256()
     src = src or os.path.join(ROOT, "codebook_token_sampling_gb300", "csrc")
     for name in sorted(os.listdir(src)):
-        if name.endswith((".cu", ".cuh")):
+        if name.endswith((".cu", ".cuh")) and not name.startswith(("ts_kv", "ts_paged")):
             with open(os.path.join(src, name), encoding="utf-8") as f:
                 text = f.read()
             text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)

@@ -187,6 +187,8 @@ class TsKvTokens(ctypes.Structure):
         ("v_token_stride", ctypes.c_int64),
         ("v_head_stride", ctypes.c_int64),
         ("slots", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int32),
     ]
 
 
@@ -766,22 +768,25 @@ class KvCache:
 
 
 class KvTokens:
-    """New tokens' keys and values [n_tokens, n_kv_heads, head_dim] (any strides
-    with head_dim contiguous) and their slots, with a prebuilt ``ts_kv_tokens``."""
+    """New tokens' keys and values [n_rows, n_kv_heads, head_dim] (any strides
+    with head_dim contiguous) and their slots, with a prebuilt ``ts_kv_tokens``.
+    Token x is row x, or with ``rows`` (int32, one per slot) row ``rows[x]``."""
 
-    def __init__(self, k, v, slots):
+    def __init__(self, k, v, slots, rows=None):
         import torch
         _need(k.dim() == 3 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device,
               "k and v: [n_tokens, n_kv_heads, head_dim] of one type")
         _need(k.stride(2) == 1 and v.stride(2) == 1, "k and v: head_dim is contiguous")
-        self.k, self.v, self.slots = k, v, slots
+        self.k, self.v, self.slots, self.rows = k, v, slots, rows
         c = TsKvTokens()
         c.k, c.v = k.data_ptr(), v.data_ptr()
         c.dtype = _kv_dtype(k)
-        c.n_tokens = k.shape[0]
+        c.n_rows = k.shape[0]
+        c.n_tokens = k.shape[0] if rows is None else rows.numel()
         c.k_token_stride, c.k_head_stride = _strides(k)
         c.v_token_stride, c.v_head_stride = _strides(v)
-        c.slots = _vector(slots, k.shape[0], torch.int64, k.device, "slots: int64 [n_tokens]")
+        c.slots = _vector(slots, c.n_tokens, torch.int64, k.device, "slots: int64 [n_tokens]")
+        c.rows = _vector(rows, c.n_tokens, torch.int32, k.device, "rows: int32 [n_tokens]")
         self.c = c
 
 

@@ -66,14 +66,11 @@ struct PagedKernel {
 
 // Stages per warp.  Two, and twelve warps per SM, beat three and eight wherever
 // the registers allow (128 requests of up to 8000 tokens, bf16, 8 x 4 heads of
-// 128: 305 against 317 us; 24 of up to 3001, fp32, 8 x 8 heads: 86 against 102).
-// The 8 KB K rows of wide bf16 and e4m3 heads, and 16 query heads, leave room
-// for fewer warps anyway: three.
+// 128: 310 against 321 us; 24 of up to 3001, fp32, 8 x 8 heads: 86 against 102).
+// Sixteen query heads of 128 leave room for eight warps: three.
 template <class Core>
 constexpr int stages_of() {
-  if (Core::kFma) return 2;
-  if (Core::kTok * Core::kRowBytes > 4096) return 3;
-  return Core::kRows > 8 && Core::kDim > 64 ? 3 : 2;
+  return !Core::kFma && Core::kRows > 8 && Core::kDim == 128 ? 3 : 2;
 }
 
 template <class Core>
@@ -120,6 +117,11 @@ struct PagedDevice {
   PagedKernel kernel[kPagedKinds][3][2];
 } g_paged[kMaxDevices];
 
+const void *tables_kernel(bool wide) {
+  return wide ? reinterpret_cast<const void *>(ts::kv_tables_kernel<int64_t>)
+              : reinterpret_cast<const void *>(ts::kv_tables_kernel<int32_t>);
+}
+
 ts_status paged_setup(int device) {
   if (device < 0 || device >= kMaxDevices) return TS_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lock(g_paged_mu);
@@ -138,11 +140,12 @@ ts_status paged_setup(int device) {
         if (k.occupancy < 1) return TS_ERR_UNSUPPORTED;
         d.kernel[kind][width][page] = k;
       }
-  const cudaError_t e =
-      cudaFuncSetAttribute(reinterpret_cast<const void *>(ts::kv_tables_kernel),
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(ts::kv_tables_smem(ts::kTablesMaxRequests)));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  for (int wide = 0; wide < 2; ++wide) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        tables_kernel(wide != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
+        static_cast<int>(ts::kv_tables_smem(ts::kTablesMaxRequests)));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  }
   d.ready = true;
   return TS_OK;
 }
@@ -280,11 +283,13 @@ ts_status ts_kv_tables(ts_sampler *s, const ts_kv_tables_args *t, void *stream) 
   p.requests = t->requests;
   p.status = s->status;
   p.by_block = ts::FastDiv::of(static_cast<uint32_t>(t->block_size));
+  p.per_lane = t->max_tokens > 32768 ? 4 : 1;
+  p.wide_maps = aligned(t->slots, 16) && aligned(t->positions, 16) && aligned(t->requests, 16);
 
-  // one block for a frame's few tokens; for prompts a block per 4096 map
-  // entries, as far as the GPU holds them
-  const bool small = t->n_requests <= 256 && t->max_tokens <= 1024;
-  const int threads = small ? 256 : ts::kTablesMaxThreads;
+  // one block for a frame's few tokens (of 512 threads: 4.8 us for 128 requests,
+  // 5.1 with 256 or 1024); for prompts a block per 4096 map entries, as far as
+  // the GPU holds them
+  const int threads = t->n_requests <= 1024 && t->max_tokens <= 4096 ? 512 : ts::kTablesMaxThreads;
   const int grid = std::max(1, std::min(s->num_sms, (t->max_tokens + 4095) / 4096));
   // blocks that still read the old values may run beside block 0: in place,
   // the new ones go through the workspace
@@ -293,8 +298,8 @@ ts_status ts_kv_tables(ts_sampler *s, const ts_kv_tables_args *t, void *stream) 
   if (staged_free) p.n_free_out = s->kv->n_free;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   void *args[] = {&p};
-  cudaError_t e = launch(reinterpret_cast<const void *>(ts::kv_tables_kernel),
-                         dim3(static_cast<unsigned>(grid)), threads,
+  const bool wide = static_cast<int64_t>(t->n_requests) * t->max_blocks * t->block_size > INT32_MAX;
+  cudaError_t e = launch(tables_kernel(wide), dim3(static_cast<unsigned>(grid)), threads,
                          ts::kv_tables_smem(t->n_requests), s->pdl != 0, st, args);
   if (e != cudaSuccess) return cuda_fail(e, "block tables launch");
   if (staged_lens || staged_free) {
@@ -314,7 +319,7 @@ ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *
   if (!s || !t) return TS_ERR_INVALID_ARG;
   const ts_status rc = check_cache(c);
   if (rc != TS_OK) return rc;
-  if (t->n_tokens < 0 || (t->dtype != TS_DTYPE_F32 && t->dtype != TS_DTYPE_BF16))
+  if (t->n_tokens < 0 || (t->rows && t->n_rows < 0) || (t->dtype != TS_DTYPE_F32 && t->dtype != TS_DTYPE_BF16))
     return TS_ERR_INVALID_ARG;
   if (t->k_token_stride < 0 || t->k_head_stride < 0 || t->v_token_stride < 0 || t->v_head_stride < 0)
     return TS_ERR_INVALID_ARG;
@@ -353,6 +358,8 @@ ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *
   p.scale[0] = c->k_scale;
   p.scale[1] = c->v_scale;
   p.slots = t->slots;
+  p.rows = t->rows;
+  p.n_rows = t->n_rows;
   p.block_size = c->block_size;
   p.n_slots = static_cast<int64_t>(c->n_blocks) * c->block_size;
   p.n_tokens = t->n_tokens;

@@ -17,7 +17,7 @@
 // items have many parts, paged_join_kernel does.  The parts' order in the sums
 // is always the same.
 //
-// A CTA is four warps (two where fp32 rows are wide); each takes its share of a
+// A CTA is four warps (six or two where rows are wide); each takes its share of a
 // tile's tokens with a running maximum and sum of its own and a private ring of
 // cp.async stages (a share's K and V each), so no warp waits for another inside
 // an item.
@@ -195,7 +195,9 @@ struct MmaCore {
   static constexpr int kElemBytes = E4M3 ? 1 : 2;
   static constexpr int kRowBytes = DP * kElemBytes;
   static constexpr int kDim = DP;
-  static constexpr int kWarps = 4;
+  // stages of 16 KB: six warps with two stages each (56 us), not four with
+  // three (59 us: 48 requests of up to 6000 tokens, 2 x 8 bf16 heads of 256)
+  static constexpr int kWarps = kTok * kRowBytes > 4096 ? 6 : 4;
   static constexpr int kSteps = DP / 16;
   // wide rows leave no registers for the queries: one copy in shared memory
   static constexpr bool kSharedQ = DP > 128;
@@ -688,7 +690,8 @@ struct PagedShape {
   // CTAs per SM that the registers have to allow
   static constexpr int kFit = static_cast<int>(226 * 1024 / (kSmem + 2048));
   static constexpr int kMost = (Core::kFma || Core::kRows <= 8 ? 4 : Core::kDim > 64 ? 2 : 3) * 4 / Core::kWarps;
-  static constexpr int kRegs = Core::kDim > 128 ? 65536 / (256 * 32 * Core::kWarps) : kMost;
+  static constexpr int kRegs = Core::kDim <= 128 || (Core::kElemBytes == 1 && Core::kRows <= 8)
+                                   ? kMost : 65536 / (256 * 32 * Core::kWarps);
   static constexpr int kMin = kFit > kMost ? kMost : kFit;
   static constexpr int kPerSm = kMin > kRegs ? kRegs : kMin;
 };

@@ -487,13 +487,17 @@ typedef struct {
   const float *v_scale;
 } ts_kv_cache;
 
-/* Writes token x's keys and values (k[x * k_token_stride + h * k_head_stride +
- * d], strides in elements, any alignment) into the cache at slots[x]; a negative
- * slot skips the token, whose rows are then not read.  The tokens have the
+/* Writes token x's keys and values (k[r * k_token_stride + h * k_head_stride +
+ * d] with r = rows[x], or x where rows is NULL; strides in elements, any
+ * alignment) into the cache at slots[x]; a negative slot skips the token, whose
+ * rows are then not read.  rows serves a decode step that keeps a row per
+ * request while ts_kv_tables packs the tokens of those that go on: its
+ * `requests` map is this one's rows.  The tokens have the
  * cache's type, or for an e4m3 cache bf16 or fp32: x / scale is computed in fp32
  * and rounded to the nearest e4m3 value (ties to even, values beyond 448 to
  * 448 with their sign, NaN kept).  Tokens of one call have slots of their own.
- * A slot past the cache sets TS_ROW_BAD_SLOT and is skipped.
+ * A slot past the cache, or a row outside [0, n_rows), sets TS_ROW_BAD_SLOT and
+ * is skipped.
  * TS_ERR_INVALID_ARG for a NULL pointer, a negative size or a cache outside the
  * rules above; TS_ERR_UNSUPPORTED for another pair of types. */
 typedef struct {
@@ -504,6 +508,8 @@ typedef struct {
   int64_t k_token_stride, k_head_stride;
   int64_t v_token_stride, v_head_stride;
   const int64_t *slots;      /* [n_tokens] */
+  const int32_t *rows;       /* [n_tokens] or NULL */
+  int32_t n_rows;            /* rows of k and v; looked at with rows only */
 } ts_kv_tokens;
 ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *t, void *stream);
 

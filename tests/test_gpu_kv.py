@@ -86,6 +86,7 @@ def check_tables(ts, sampler, st, **how):
     (1, 16, 0, 1, 0.0, 0), (1, 1, 3, 2, 0.0, 0), (5, 16, 40, 1, 0.3, 0), (37, 7, 100, 30, 0.2, 0),
     (128, 16, 2000, 1, 0.1, 0), (257, 24, 50, 9, 0.3, 40), (1000, 16, 0, 60, 0.0, 90),
     (1025, 128, 300, 3, 0.5, 3), (64, 16, 64, 300, 0.1, 25), (3000, 8, 20, 12, 0.1, 0),
+    (150, 16, 30, 700, 0.1, 60), (40, 6, 30, 2500, 0.0, 7),
     (8192, 16, 40, 2, 0.2, 11)])
 def test_tables(ts, sampler, n, block_size, len_hi, new_hi, finished, short, double):
     rng = np.random.default_rng([n, block_size, len_hi, new_hi, short])
@@ -269,6 +270,29 @@ def test_append_e4m3_rounding(ts, sampler):
     assert np.array_equal(got[~nan], want[~nan])
     assert np.all(got[nan] & 0x7F == 0x7F)
     assert np.array_equal(raw(torch, v).reshape(-1), got)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_append_rows(ts, sampler, cache):
+    """Tokens in other rows than their own: a row twice, rows out of range (bit
+    set, skipped), a skipped token's row not looked at."""
+    import torch
+    types = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
+    k, v = cache_pair(torch, 3, 8, 2, 64, types[cache], "nhd")
+    before = raw(torch, k).copy()
+    new = torch.randn((5, 2, 2, 64), device="cuda").bfloat16()
+    rows = torch.tensor([4, 0, 4, 2, 9, -1, 5, 1], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([3, 20, 7, -1, -1, 11, 12, 23], device="cuda")
+    sampler.read_status()
+    ts.ts_kv_append(sampler.handle, ts.KvCache(k, v), ts.KvTokens(new[:, 0], new[:, 1], slots, rows))
+    torch.cuda.synchronize()
+    assert sampler.read_status() == ts.TS_ROW_BAD_SLOT
+    for x, i in ((k, 0), (v, 1)):
+        want = before.copy()
+        for s, r in ((3, 4), (20, 0), (7, 4), (23, 1)):
+            y = new[r, i]
+            want[s // 8, s % 8] = okv.to_e4m3(y.float().cpu().numpy()) if cache == "e4m3" else raw(torch, y)
+        assert np.array_equal(raw(torch, x), want)
 
 
 @pytest.mark.parametrize("scale", [0.03, 1.0 / 3.0, 7.3e-5, 448.0, 1e-30, 3e30, 2.0 ** -100])
