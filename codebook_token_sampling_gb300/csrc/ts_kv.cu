@@ -92,7 +92,7 @@ PagedKernel paged_kernel_of(int kind, bool page16) {
   switch (kind) {
     case 0: return paged_kernel<ts::MmaCore<false, DP, 1, kt>>(page16);
     case 1: return paged_kernel<ts::MmaCore<false, DP, 2, kt>>(page16);
-    case 2: return paged_kernel<ts::MmaCore<true, DP, 1, DP <= 128 ? 2 : 1>>(page16);
+        case 2: return paged_kernel<ts::MmaCore<true, DP, 1, DP <= 128 ? 2 : 1>>(page16);
     case 3: return paged_kernel<ts::MmaCore<true, DP, 2, 2>>(page16);
     case 4: return paged_kernel<ts::FmaCore<1, DP>>(page16);
     case 5: return paged_kernel<ts::FmaCore<2, DP>>(page16);
@@ -165,6 +165,8 @@ ts_status check_cache(const ts_kv_cache *c) {
     if (x < 0 || x * es % 16) return TS_ERR_INVALID_ARG;
   if (c->dtype != TS_DTYPE_E4M3 && (c->k_scale || c->v_scale)) return TS_ERR_INVALID_ARG;
   if (c->head_dim > TS_KV_MAX_HEAD_DIM || c->block_size > 65536) return TS_ERR_UNSUPPORTED;
+  for (int64_t x : {c->k_block_stride, c->k_token_stride, c->v_block_stride, c->v_token_stride})
+    if (x > INT32_MAX / es) return TS_ERR_UNSUPPORTED;
   return TS_OK;
 }
 
@@ -174,9 +176,12 @@ bool overlap_in_part(const int32_t *a, const int32_t *b, int64_t n) {
 }
 
 template <class Src, class Dst, int VEC>
-const void *append_kernel(bool wide) {
-  return wide ? reinterpret_cast<const void *>(ts::kv_append_kernel<Src, Dst, VEC, true>)
-              : reinterpret_cast<const void *>(ts::kv_append_kernel<Src, Dst, VEC, false>);
+const void *append_kernel(bool wide, bool rows) {
+  if (rows)
+    return wide ? reinterpret_cast<const void *>(ts::kv_append_kernel<Src, Dst, VEC, true, true>)
+                : reinterpret_cast<const void *>(ts::kv_append_kernel<Src, Dst, VEC, false, true>);
+  return wide ? reinterpret_cast<const void *>(ts::kv_append_kernel<Src, Dst, VEC, true, false>)
+              : reinterpret_cast<const void *>(ts::kv_append_kernel<Src, Dst, VEC, false, false>);
 }
 
 }  // namespace
@@ -333,12 +338,12 @@ ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *
   const bool wide = aligned(t->k, 16) && aligned(t->v, 16) && t->k_token_stride * es % 16 == 0 &&
                     t->k_head_stride * es % 16 == 0 && t->v_token_stride * es % 16 == 0 &&
                     t->v_head_stride * es % 16 == 0;
-  const bool bf16 = t->dtype == TS_DTYPE_BF16;
+  const bool bf16 = t->dtype == TS_DTYPE_BF16, rows = t->rows != nullptr;
   const void *fn = c->dtype == TS_DTYPE_E4M3
-                       ? (bf16 ? append_kernel<uint16_t, uint8_t, 16>(wide)
-                               : append_kernel<float, uint8_t, 16>(wide))
-                       : (bf16 ? append_kernel<uint16_t, uint16_t, 8>(wide)
-                               : append_kernel<float, float, 4>(wide));
+                       ? (bf16 ? append_kernel<uint16_t, uint8_t, 16>(wide, rows)
+                               : append_kernel<float, uint8_t, 16>(wide, rows))
+                       : (bf16 ? append_kernel<uint16_t, uint16_t, 8>(wide, rows)
+                               : append_kernel<float, float, 4>(wide, rows));
   ts::KvAppendParams p;
   std::memset(&p, 0, sizeof p);
   p.src[0] = t->k;
@@ -440,11 +445,11 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.n_requests = q->n_requests;
   p.k = c->k;
   p.v = c->v;
-  p.k_block = c->k_block_stride * ces;
-  p.k_token = c->k_token_stride * ces;
+  p.k_block = static_cast<int32_t>(c->k_block_stride * ces);
+  p.k_token = static_cast<int32_t>(c->k_token_stride * ces);
   p.k_head = c->k_head_stride * ces;
-  p.v_block = c->v_block_stride * ces;
-  p.v_token = c->v_token_stride * ces;
+  p.v_block = static_cast<int32_t>(c->v_block_stride * ces);
+  p.v_token = static_cast<int32_t>(c->v_token_stride * ces);
   p.v_head = c->v_head_stride * ces;
   p.k_scale = c->k_scale;
   p.v_scale = c->v_scale;

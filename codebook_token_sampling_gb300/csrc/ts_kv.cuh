@@ -386,7 +386,8 @@ __global__ void kv_tables_store_kernel(const int32_t *lens_new, int32_t *lens, i
 constexpr int kAppendThreads = 256;
 // Units per thread and round: 4 of 16 bytes, one of the 32 or 64 bytes that make
 // 16 e4m3 values (five CTAs per SM then hide what their arithmetic takes: 65 us
-// for 65,536 tokens of 8 x 128 bf16, against 80 with two units and two CTAs).
+// for 65,536 tokens of 8 x 128 bf16, against 80 with two units and two CTAs;
+// three CTAs for the others: 41 us for 32,768 tokens, 46 with two or five).
 template <class Src, int VEC>
 constexpr int kAppendUnroll = sizeof(Src) * VEC == 16 ? 4 : 1;
 
@@ -397,7 +398,7 @@ struct KvAppendParams {
   int64_t dst_block[2], dst_token[2], dst_head[2];
   const float *scale[2];            // one per key head, null: 1 (e4m3 only)
   const int64_t *slots;
-  const int32_t *rows;              // or null: token x is row x
+  const int32_t *rows;              // ROWS kernels only
   int32_t n_rows;
   int64_t n_slots;                  // n_blocks * block_size
   int64_t block_size;
@@ -507,8 +508,10 @@ struct AppendUnit {
 // eight 16-byte loads are in flight; a CTA takes whole tokens.  A skipped
 // token's rows are not read.  Bound by DRAM: each element is read once and
 // written once.
-template <class Src, class Dst, int VEC, bool WIDE>
-__global__ void __launch_bounds__(kAppendThreads, sizeof(Dst) == 1 ? 5 : 1) kv_append_kernel(const KvAppendParams p) {
+// ROWS: token x is row rows[x] (its own kernel: the look-up would slow the
+// other by a tenth).
+template <class Src, class Dst, int VEC, bool WIDE, bool ROWS>
+__global__ void __launch_bounds__(kAppendThreads, sizeof(Dst) == 1 ? 5 : 3) kv_append_kernel(const KvAppendParams p) {
   constexpr int kUnroll = kAppendUnroll<Src, VEC>;
   pdl_wait_and_release();
   const int32_t t0 = static_cast<int32_t>(blockIdx.x) * p.tokens_per_block;
@@ -518,25 +521,28 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(Dst) == 1 ? 5 : 1) kv_a
   for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kAppendThreads * kUnroll) {
     AppendUnit<Src, Dst, VEC, WIDE> k[kUnroll], v[kUnroll];
     int64_t slot[kUnroll];
-    int32_t from[kUnroll];
+    int32_t from[ROWS ? kUnroll : 1];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       const uint32_t u = u0 + j * kAppendThreads;
-      const int32_t x = t0 + static_cast<int32_t>(p.by_token.div(u));
+      const uint32_t x = t0 + p.by_token.div(u);
       slot[j] = u < units ? p.slots[x] : -1;
-      from[j] = u < units && p.rows ? p.rows[x] : x;
+      if constexpr (ROWS) from[j] = u < units ? p.rows[x] : 0;
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      if (slot[j] >= p.n_slots || (p.rows && slot[j] >= 0 && (from[j] < 0 || from[j] >= p.n_rows))) {
+      bool bad = slot[j] >= p.n_slots;
+      if constexpr (ROWS) bad |= slot[j] >= 0 && (from[j] < 0 || from[j] >= p.n_rows);
+      if (bad) {
         bits |= kRowBadSlot;
         slot[j] = -1;
       }
       if (slot[j] >= 0) {
         const uint32_t u = u0 + j * kAppendThreads;
-        const uint32_t in = u - p.by_token.div(u) * p.by_token.d;
+        const uint32_t t = p.by_token.div(u), in = u - t * p.by_token.d;
         const uint32_t h = p.by_head.div(in), e = (in - h * p.by_head.d) * VEC;
-        const int64_t token = from[j];
+        int64_t token = t0 + static_cast<int64_t>(t);
+        if constexpr (ROWS) token = from[j];
         k[j].load(static_cast<const Src *>(p.src[0]) + token * p.src_token[0] + h * p.src_head[0] + e);
         v[j].load(static_cast<const Src *>(p.src[1]) + token * p.src_token[1] + h * p.src_head[1] + e);
       }

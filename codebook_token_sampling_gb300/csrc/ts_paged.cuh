@@ -65,8 +65,8 @@ struct PagedParams {
   const int32_t *lens;
   int32_t n_requests;
   const void *k, *v;
-  int64_t k_block, k_token, k_head;  // bytes
-  int64_t v_block, v_token, v_head;
+  int64_t k_head, v_head;   // bytes
+  int32_t k_block, k_token, v_block, v_token;  // bytes, below 2^31: products of 32 bits
   const float *k_scale, *v_scale;
   int32_t n_blocks, block_size, kv_heads, dim;
   int32_t group;            // query heads per key head
@@ -89,6 +89,10 @@ struct PagedParams {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ int64_t wide_product(int32_t a, int32_t b) {
+  return static_cast<int64_t>(a) * b;
+}
 
 // 2^(m - top), 0 for an empty part
 __device__ __forceinline__ float exp2_from(float m, float top) {
@@ -125,12 +129,11 @@ __device__ __forceinline__ uint32_t transposed_8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
   return d;
 }
-// two e4m3 values as two f16 values (exact)
-__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t x) {
-  uint32_t d;
-  const uint16_t h = static_cast<uint16_t>(x);
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(h));
-  return d;
+// four e4m3 values as f16 values (exact): the lower two and the upper two
+__device__ __forceinline__ void f16_of_e4m3x4(uint32_t x, uint32_t &lower, uint32_t &upper) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lower), "=r"(upper) : "r"(x));
 }
 // two fp32 values side by side
 __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
@@ -340,8 +343,9 @@ struct MmaCore {
           ldmatrix_x4_at(b, ks + stage_at<kRowBytes, 0>(16 * t + row, 2 * k2 + half));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t a[4] = {f16x2_of_e4m3x2(b[2 * h]), f16x2_of_e4m3x2(b[2 * h + 1]),
-                                   f16x2_of_e4m3x2(b[2 * h] >> 16), f16x2_of_e4m3x2(b[2 * h + 1] >> 16)};
+            uint32_t a[4];
+            f16_of_e4m3x4(b[2 * h], a[0], a[2]);
+            f16_of_e4m3x4(b[2 * h + 1], a[1], a[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
               mma_f16_16816(kChains == 2 && h ? s2[n] : s[t][n], a, x[h][n][0], x[h][n][1]);
@@ -465,8 +469,9 @@ struct MmaCore {
           for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i], 0u, 0x3120);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t a[4] = {f16x2_of_e4m3x2(b[2 * h]), f16x2_of_e4m3x2(b[2 * h] >> 16),
-                                   f16x2_of_e4m3x2(b[2 * h + 1]), f16x2_of_e4m3x2(b[2 * h + 1] >> 16)};
+            uint32_t a[4];
+            f16_of_e4m3x4(b[2 * h], a[0], a[1]);
+            f16_of_e4m3x4(b[2 * h + 1], a[2], a[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma_f16_16816(o[n][2 * d2 + h], a, hi[t][n][0], hi[t][n][1]);
           }
@@ -1057,8 +1062,8 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
           cp_async16_or_zero(at, ka + skip, real, policy);
           cp_async16_or_zero(at + Shape::kHalf, va + skip, real, policy);
         }
-        ka += kRowsAt * p.k_token;
-        va += kRowsAt * p.v_token;
+        ka += static_cast<int64_t>(kRowsAt) * p.k_token;
+        va += static_cast<int64_t>(kRowsAt) * p.v_token;
       }
     };
     if constexpr (PAGE16) {
@@ -1068,16 +1073,18 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
       for (int r0 = 0; r0 < Core::kTok; r0 += kGroup) {
         const int32_t e = Core::kTok <= kPagedPage ? entry : __shfl_sync(0xFFFFFFFFu, entry, r0);
         const uint32_t t = static_cast<uint32_t>(base + r0);
-        const int64_t b = e >= 0 && e < p.n_blocks ? e : 0;
-        const int64_t off = t - p.by_block.div(t) * p.by_block.d + my_row;
-        copy(r0, kGroup, kh + b * p.k_block + off * p.k_token, vh + b * p.v_block + off * p.v_token);
+        const int32_t b = e >= 0 && e < p.n_blocks ? e : 0;
+        const int32_t off = static_cast<int32_t>(t - p.by_block.div(t) * p.by_block.d) + my_row;
+        copy(r0, kGroup, kh + wide_product(b, p.k_block) + wide_product(off, p.k_token),
+             vh + wide_product(b, p.v_block) + wide_product(off, p.v_token));
       }
     } else {
       // the lane of a row knows where it lies
       const uint32_t t = static_cast<uint32_t>(base + lane % Core::kTok);
-      const int64_t b = keep && inside ? entry : 0;
-      const int64_t off = keep && inside ? t - p.by_block.div(t) * p.by_block.d : 0;
-      const int64_t ko = b * p.k_block + off * p.k_token, vo = b * p.v_block + off * p.v_token;
+      const int32_t b = keep && inside ? entry : 0;
+      const int32_t off = keep && inside ? static_cast<int32_t>(t - p.by_block.div(t) * p.by_block.d) : 0;
+      const int64_t ko = wide_product(b, p.k_block) + wide_product(off, p.k_token);
+      const int64_t vo = wide_product(b, p.v_block) + wide_product(off, p.v_token);
 #pragma unroll
       for (int r = 0; r < Core::kTok; r += kRowsAt)
         copy(r, kRowsAt, kh + __shfl_sync(0xFFFFFFFFu, ko, r + my_row),

@@ -469,8 +469,9 @@ ts_status ts_kv_tables(ts_sampler *s, const ts_kv_tables_args *t, void *stream);
  * block b is k[b * k_block_stride + off * k_token_stride + h * k_head_stride +
  * d] (strides in elements; v alike), so that blocks may hold tokens before
  * heads or heads before tokens.  k and v and every stride in bytes are
- * multiples of 16, as is head_dim in bytes; head_dim is at most
- * TS_KV_MAX_HEAD_DIM.  An e4m3 cache holds value / scale: k_scale and v_scale
+ * multiples of 16, as is head_dim in bytes (else TS_ERR_INVALID_ARG); head_dim
+ * is at most TS_KV_MAX_HEAD_DIM, block_size 65536, and a block or token stride
+ * below 2 GB (else TS_ERR_UNSUPPORTED).  An e4m3 cache holds value / scale: k_scale and v_scale
  * have one fp32 scale per key head (NULL: 1); the other types take none. */
 #define TS_KV_MAX_HEAD_DIM 256
 typedef struct {

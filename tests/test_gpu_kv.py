@@ -340,7 +340,8 @@ def test_append_refusals(ts, sampler):
     assert go(cfield="head_dim", cvalue=60) == inv and go(cfield="head_dim", cvalue=264) == uns
     assert go(cfield="k", cvalue=k.data_ptr() + 2) == inv and go(cfield="v_head_stride", cvalue=63) == inv
     assert go(cfield="k_scale", cvalue=slots.data_ptr()) == inv and go(cfield="n_blocks", cvalue=0) == inv
-    assert go(cfield="dtype", cvalue=7) == inv
+    assert go(cfield="dtype", cvalue=7) == inv and go(cfield="v_block_stride", cvalue=1 << 30) == uns
+    assert go(cfield="block_size", cvalue=65537) == uns
     assert go(tokens=new.float()) == uns  # fp32 tokens for a bf16 cache
     with pytest.raises(ValueError):
         ts.KvTokens(new, new, slots.int())
