@@ -472,8 +472,8 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.ctas = k.occupancy * s->num_sms;
   if (s->kv_ctas) p.ctas = std::min(p.ctas, s->kv_ctas);
   p.by_ctas = ts::FastDiv::of(static_cast<uint32_t>(p.ctas));
-  // a request's tiles, rounded up at both ends
-  const double tiles = (p.room / k.tile + 2.0) * p.pieces * p.kv_heads * q->n_requests;
+  // a request's units of work, rounded up
+  const double tiles = (p.room / k.tile + 4.0) * p.pieces * p.kv_heads * q->n_requests;
   p.tiles_fit = tiles < 2.0e9 ? 1 : 0;
   // Parts of an item, about: the CTAs that share it, no more than its tiles.
   const int64_t items = static_cast<int64_t>(p.pieces) * p.kv_heads * q->n_requests;
