@@ -41,7 +41,8 @@
  * Every pointer in ts_batch is a DEVICE pointer owned by the caller and must
  * stay valid until the work queued on `stream` has run.  The library never
  * allocates, frees or synchronises inside ts_sample / ts_sample_debug /
- * ts_sample_steps / ts_advance_steps, so those calls may be captured into a
+ * ts_sample_steps / ts_advance_steps / ts_lm_head_* / ts_kv_tables /
+ * ts_kv_append / ts_paged_attention, so those calls may be captured into a
  * CUDA graph.  They
  * run on the device that is current when they are called, which must be the
  * device the sampler was created on.
@@ -173,13 +174,14 @@ typedef struct {
 /* Creates a sampler on CUDA device `device`.  max_top_k: 0 selects the
  * default cap 64; otherwise a power of two in [32, 4096] (else
  * TS_ERR_INVALID_ARG).  Allocates a 4-byte device status word (besides the
- * workspace of ts_reserve, the only allocation the library makes).  Call it
+ * workspaces of ts_reserve and ts_reserve_kv, the only allocation the library
+ * makes).  Call it
  * before any stream capture. */
 ts_status ts_create(int device, int max_top_k, ts_sampler **out);
 /* (The status word shares its 8-byte allocation with the ticket counter that
  * the warp path's fused step advance uses; both start at zero.) */
 
-/* Frees the sampler and its status word.  NULL is accepted. */
+/* Frees the sampler, its status word and its workspaces.  NULL is accepted. */
 ts_status ts_destroy(ts_sampler *s);
 
 /* Effective top-k cap of the sampler (or -1 for NULL). */
