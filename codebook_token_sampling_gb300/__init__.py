@@ -59,6 +59,7 @@ TS_LM_HEAD_MAX_DIM = 16384
 TS_KV_MAX_REQUESTS = 8192
 TS_KV_MAX_LEN = 2147482624
 TS_KV_MAX_HEAD_DIM = 256
+TS_KV_MAX_HEADS = 65536
 
 EXPORTED = ("ts_create", "ts_destroy", "ts_max_top_k", "ts_sample", "ts_sample_debug",
             "ts_sample_steps", "ts_reserve", "ts_sample_noalloc", "ts_advance_steps",

@@ -399,7 +399,8 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
     return TS_ERR_INVALID_ARG;
   const bool f32 = q->dtype == TS_DTYPE_F32;
   if (f32 != (c->dtype == TS_DTYPE_F32)) return TS_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(q->max_blocks) * c->block_size > TS_KV_MAX_LEN) return TS_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(q->max_blocks) * c->block_size > TS_KV_MAX_LEN || q->n_heads > TS_KV_MAX_HEADS)
+    return TS_ERR_UNSUPPORTED;
   if (q->n_requests == 0) return TS_OK;
   const int es = f32 ? 4 : 2;
   if (!q->q || !q->out || !q->lens || (!q->block_table && q->max_blocks > 0) ||
@@ -460,7 +461,6 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.group = group;
   p.rows = rows;
   p.pieces = (group + rows - 1) / rows;
-  if (static_cast<int64_t>(p.pieces) * p.kv_heads > (1 << 24)) return TS_ERR_UNSUPPORTED;
   p.scale = q->scale;
   p.softcap = q->softcap;
   p.window = q->window;
@@ -469,6 +469,8 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.arrived = s->kv->arrived;
   p.acc = s->kv->acc;
   p.ml = s->kv->ml;
+  const int64_t items = static_cast<int64_t>(p.pieces) * p.kv_heads * q->n_requests;
+  const int64_t item_tiles = std::max<int64_t>(1, (p.room + k.tile - 1) / k.tile);
   p.ctas = k.occupancy * s->num_sms;
   if (s->kv_ctas) p.ctas = std::min(p.ctas, s->kv_ctas);
   p.by_ctas = ts::FastDiv::of(static_cast<uint32_t>(p.ctas));
@@ -476,8 +478,7 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   const double tiles = (p.room / k.tile + 4.0) * p.pieces * p.kv_heads * q->n_requests;
   p.tiles_fit = tiles < 2.0e9 ? 1 : 0;
   // Parts of an item, about: the CTAs that share it, no more than its tiles.
-  const int64_t items = static_cast<int64_t>(p.pieces) * p.kv_heads * q->n_requests;
-  const int64_t parts = std::min<int64_t>(p.ctas / items + 2, (p.room + k.tile - 1) / k.tile);
+  const int64_t parts = std::min<int64_t>(p.ctas / items + 2, item_tiles);
   p.join_here = s->kv_join ? s->kv_join - 1 : parts <= kJoinHere ? 1 : 0;
   p.out_f32 = f32 ? 1 : 0;
   p.status = s->status;

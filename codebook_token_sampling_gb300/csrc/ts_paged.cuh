@@ -8,21 +8,22 @@
 // share it: 4 G flops per 2-byte element, so the bound is DRAM.
 //
 // Work.  An item is one (request, key head, piece of at most kRows query
-// heads); its tokens are cut into tiles of 64 (32 for fp32 rows of 1 KB), and the tiles of all items,
-// laid end to end, are dealt to the CTAs in equal runs.  Every CTA finds its
-// run by summing the lengths itself, so ragged batches balance with nothing
-// planned on the host and no launch before this one.  A run holds whole items
+// heads); its tokens are cut into tiles of 16 to 128 (a step of every warp), and
+// the tiles of all items, laid end to end, are dealt to the CTAs in runs of equal
+// cost.  Every CTA finds its run by summing the lengths itself, so ragged batches
+// balance with nothing planned on the host and no launch before this one.  (The
+// lengths stay as they are while the call runs; should they change, its loops
+// still end inside the arrays.)  A run holds whole items
 // and at most two parts of items that other runs share: those go to a
 // workspace, and the CTA that brings an item's last part joins them; where
 // items have many parts, paged_join_kernel does.  The parts' order in the sums
 // is always the same.
 //
-// A CTA is four warps (six or two where rows are wide); each takes its share of a
-// tile's tokens with a running maximum and sum of its own and a private ring of
-// cp.async stages (a share's K and V each), so no warp waits for another inside
-// an item.
-// The ring runs on across items.  At an item's end the four warps' results
-// are joined in shared memory.
+// A CTA is four warps (six or two where rows are wide); each takes its share of
+// a tile's tokens with a running maximum and sum of its own and a private ring
+// of cp.async stages (a share's K and V each), so no warp waits for another
+// inside an item.  The ring runs on across items.  At an item's end the warps'
+// results are joined in shared memory.
 #pragma once
 
 #include <type_traits>
@@ -828,6 +829,10 @@ __device__ __forceinline__ PagedRun paged_run(const PagedParams &p) {
       return y;
     }
     r0 += 128;
+    if (r0 >= p.n_requests) {  // only if the lengths changed meanwhile
+      y.u1 = y.u0;
+      return y;
+    }
     load(r0);
     scan();
     seen += __shfl_sync(0xFFFFFFFFu, in, 31);
@@ -999,8 +1004,13 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
         c.head = 0;
         if (c.left > 0) {
           bool bad;
-          do c.span = paged_span<Shape::kTile>(p, p.lens[++c.request], bad);
-          while (c.span.tiles == 0);
+          do {
+            if (++c.request >= p.n_requests) {
+              c.left = 0;
+              break;
+            }
+            c.span = paged_span<Shape::kTile>(p, p.lens[c.request], bad);
+          } while (c.span.tiles == 0);
         }
       }
     }
@@ -1179,7 +1189,7 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
 
     const bool item_end = use.tile == use.span.tiles - 1;
     if (item_end || use.left == 1) {
-      // ---- the four warps' parts as one: each puts its sums where its stage
+      // ---- the warps' parts as one: each puts its sums where its stage
       // was ----
       __syncwarp();
       const bool whole = from_start && item_end;

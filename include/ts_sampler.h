@@ -476,6 +476,7 @@ ts_status ts_kv_tables(ts_sampler *s, const ts_kv_tables_args *t, void *stream);
  * below 2 GB (else TS_ERR_UNSUPPORTED).  An e4m3 cache holds value / scale: k_scale and v_scale
  * have one fp32 scale per key head (NULL: 1); the other types take none. */
 #define TS_KV_MAX_HEAD_DIM 256
+#define TS_KV_MAX_HEADS 65536
 typedef struct {
   void *k;
   void *v;
@@ -535,10 +536,10 @@ ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *
  * pointer, a negative size or stride, n_heads not a multiple of n_kv_heads, a
  * scale or softcap that is not finite, a negative softcap or window, a mask row
  * shorter than max_blocks * block_size, or no workspace (ts_reserve_kv).
- * TS_ERR_UNSUPPORTED for max_blocks * block_size above TS_KV_MAX_LEN.  Per
- * request: a negative length or one beyond max_blocks blocks sets
- * TS_ROW_BAD_SHAPE, an attended token's block outside [0, n_blocks) sets
- * TS_ROW_BAD_BLOCK; the heads concerned get NaN. */
+ * TS_ERR_UNSUPPORTED for max_blocks * block_size above TS_KV_MAX_LEN or more than
+ * TS_KV_MAX_HEADS query heads.  Per request: a negative length or one beyond
+ * max_blocks blocks sets TS_ROW_BAD_SHAPE, an attended token's block outside [0,
+ * n_blocks) sets TS_ROW_BAD_BLOCK; the heads concerned get NaN. */
 typedef struct {
   const void *q;             /* [n_requests][n_heads][head_dim] by strides */
   void *out;                 /* the same */

@@ -671,6 +671,7 @@ def test_attention_refusals(ts, sampler):
     assert go("q", c["q"].data_ptr() + 2) == inv and go("q_head_stride", 63) == inv
     assert go("out_request_stride", -64) == inv and go("dtype", 2) == inv and go("dtype", 0) == uns
     assert go("max_blocks", 1 << 28) == inv  # the stride is below it
+    assert go("n_heads", 1 << 17) == uns
     assert go(cfield="dtype", cvalue=0) == uns and go(cfield="block_size", cvalue=0) == inv
     assert go(cfield="head_dim", cvalue=264) == uns and go(cfield="v", cvalue=None) == inv
     fresh = ts.Sampler(0)
