@@ -105,8 +105,9 @@ PagedKernel paged_kernel_for(int kind, int width, bool page16) {
        : width == 1 ? paged_kernel_of<128>(kind, page16) : paged_kernel_of<256>(kind, page16);
 }
 
-// Items of up to about this many parts are joined by the last CTA to come,
-// those of more by a launch of their own.
+// Items of up to about this many parts are joined by the last CTA to come (32
+// streams of up to 1500 tokens: 25.2 us, 27.9 with the launch), those of more by
+// a launch of their own (one request of 131,071: 50 us, 70 by the last CTA).
 constexpr int kJoinHere = 10;
 
 // Per device, once: the kernels' shared-memory limits and occupancies.

@@ -275,17 +275,22 @@ struct MmaCore {
 #pragma unroll
         for (int kk = 0; kk < kSteps; ++kk) {
           const uint2 raw = raw_at(kk);
+          if constexpr (!kSharedQ) keep(kk, raw.x, raw.y);
           big = fmaxf(big, fmaxf(fmaxf(fabsf(low(raw.x)), fabsf(high(raw.x))),
                                  fmaxf(fabsf(low(raw.y)), fabsf(high(raw.y)))));
         }
         big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
         const int e = big > 0.0f && big < INFINITY ? ilogbf(big) : 0;
+        // 2^-e in two factors: e goes down to that of the smallest bf16 number
+        const float f0 = scalbnf(1.0f, -(e / 2)), f1 = scalbnf(1.0f, -(e - e / 2));
 #pragma unroll
         for (int kk = 0; kk < kSteps; ++kk) {
-          const uint2 raw = raw_at(kk);
-          keep(kk, f16x2_of(scalbnf(low(raw.x), -e), scalbnf(high(raw.x), -e)),
-               f16x2_of(scalbnf(low(raw.y), -e), scalbnf(high(raw.y), -e)));
+          uint2 raw;
+          if constexpr (kSharedQ) raw = raw_at(kk);
+          else raw = make_uint2(qf[n][kk][0], qf[n][kk][1]);
+          keep(kk, f16x2_of(low(raw.x) * f0 * f1, high(raw.x) * f0 * f1),
+               f16x2_of(low(raw.y) * f0 * f1, high(raw.y) * f0 * f1));
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -865,7 +870,7 @@ struct PagedSum {
 
 __device__ __forceinline__ uint32_t counted(const uint32_t *p) {
   uint32_t x;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
   return x;
 }
 
@@ -1207,10 +1212,15 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
         d.request = use.request;
         d.head = use.head;
         d.piece = use.piece;
-        // whether the others are there is asked before they are needed
-        if (tid == 0) s_come = p.join_here ? static_cast<int>(counted(p.arrived + d.first)) : -1;
       }
+      // whether the others are there is asked before the sums are written
+      int come = -1;
+      if (!whole && tid == 0 && p.join_here) come = static_cast<int>(counted(p.arrived + d.first));
       core.give(reinterpret_cast<float *>(ring + stage * 2 * Shape::kHalf), sm[warp], sl[warp]);
+      if (!whole && tid == 0) {
+        if (come == d.parts - 1) __threadfence();
+        s_come = come;
+      }
       __syncthreads();
       const int rows = min(p.rows, p.group - use.piece * p.rows), quads = p.dim / 4;
       const int64_t head = static_cast<int64_t>(use.head) * p.group + use.piece * p.rows;
