@@ -9,7 +9,8 @@
 
 #include "ts_host.h"
 #include "ts_kv.cuh"
-#include "ts_paged.cuh"
+#include "ts_paged_join.cuh"
+#include "ts_paged_kernels.h"
 
 static_assert(ts::kRowBadBlock == TS_ROW_BAD_BLOCK && ts::kRowNoBlocks == TS_ROW_NO_BLOCKS,
               "status bits");
@@ -32,6 +33,10 @@ struct ts_kv_state {
 namespace {
 
 using ts_host::cuda_fail;
+using ts_host::PagedKernel;
+using ts_host::paged_kernel_bf16;
+using ts_host::paged_kernel_e4m3;
+using ts_host::paged_kernel_f32;
 
 cudaError_t launch(const void *fn, dim3 grid, int threads, size_t smem, bool pdl, cudaStream_t st,
                    void **args) {
@@ -56,53 +61,10 @@ bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) %
 // --------------------------------------------------------------------------
 // Paged attention's kernels
 // --------------------------------------------------------------------------
-struct PagedKernel {
-  const void *fn;
-  uint32_t smem;
-  int threads;
-  int tile;       // tokens
-  int occupancy;  // CTAs per SM
-};
-
-// Stages per warp.  Two, and twelve warps per SM, beat three and eight wherever
-// the registers allow (128 requests of up to 8000 tokens, bf16, 8 x 4 heads of
-// 128: 310 against 321 us; 24 of up to 3001, fp32, 8 x 8 heads: 86 against 102).
-// Sixteen query heads of 128 leave room for eight warps: three.
-template <class Core>
-constexpr int stages_of() {
-  return !Core::kFma && Core::kRows > 8 && Core::kDim == 128 ? 3 : 2;
-}
-
-template <class Core>
-PagedKernel paged_kernel(bool page16) {
-  constexpr int ns = stages_of<Core>();
-  static_assert(ts::PagedShape<Core, ns>::kSmem <= 226 * 1024, "shared memory of a CTA");
-  return {page16 ? reinterpret_cast<const void *>(ts::paged_attention_kernel<Core, ns, true>)
-                 : reinterpret_cast<const void *>(ts::paged_attention_kernel<Core, ns, false>),
-          ts::PagedShape<Core, ns>::kSmem, ts::PagedShape<Core, ns>::kThreads, ts::PagedShape<Core, ns>::kTile, 0};
-}
-
-// kind 0, 1: bf16 cache with up to 8 or 16 query heads per item, 2, 3: e4m3, 4
-// .. 7: f32 with up to 1, 2, 4 or 8; width 0, 1, 2: up to 64, 128 or 256
-// elements per row.  A step takes 4 KB of keys where that is 16 or 32 tokens.
-constexpr int kPagedKinds = 8;
-template <int DP>
-PagedKernel paged_kernel_of(int kind, bool page16) {
-  constexpr int kt = DP <= 64 ? 2 : 1;
-  switch (kind) {
-    case 0: return paged_kernel<ts::MmaCore<false, DP, 1, kt>>(page16);
-    case 1: return paged_kernel<ts::MmaCore<false, DP, 2, kt>>(page16);
-        case 2: return paged_kernel<ts::MmaCore<true, DP, 1, DP <= 128 ? 2 : 1>>(page16);
-    case 3: return paged_kernel<ts::MmaCore<true, DP, 2, 2>>(page16);
-    case 4: return paged_kernel<ts::FmaCore<1, DP>>(page16);
-    case 5: return paged_kernel<ts::FmaCore<2, DP>>(page16);
-    case 6: return paged_kernel<ts::FmaCore<4, DP>>(page16);
-    default: return paged_kernel<ts::FmaCore<8, DP>>(page16);
-  }
-}
+constexpr int kPagedKinds = 8, kPagedWidths = 5;
 PagedKernel paged_kernel_for(int kind, int width, bool page16) {
-  return width == 0 ? paged_kernel_of<64>(kind, page16)
-       : width == 1 ? paged_kernel_of<128>(kind, page16) : paged_kernel_of<256>(kind, page16);
+  return kind < 2 ? paged_kernel_bf16(kind, width, page16)
+       : kind < 4 ? paged_kernel_e4m3(kind, width, page16) : paged_kernel_f32(kind, width, page16);
 }
 
 // Items of up to about this many parts are joined by the last CTA to come (32
@@ -115,7 +77,7 @@ constexpr int kMaxDevices = 64;
 std::mutex g_paged_mu;
 struct PagedDevice {
   bool ready;
-  PagedKernel kernel[kPagedKinds][3][2];
+  PagedKernel kernel[kPagedKinds][kPagedWidths][2];
 } g_paged[kMaxDevices];
 
 const void *tables_kernel(bool wide) {
@@ -129,7 +91,7 @@ ts_status paged_setup(int device) {
   PagedDevice &d = g_paged[device];
   if (d.ready) return TS_OK;
   for (int kind = 0; kind < kPagedKinds; ++kind)
-    for (int width = 0; width < 3; ++width)
+    for (int width = 0; width < kPagedWidths; ++width)
       for (int page = 0; page < 2; ++page) {
         PagedKernel k = paged_kernel_for(kind, width, page != 0);
         cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -425,7 +387,8 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
     rows = 1 << size;
     kind = 4 + size;
   }
-  const int width = c->head_dim <= 64 ? 0 : c->head_dim <= 128 ? 1 : 2;
+  const int width = c->head_dim <= 64 ? 0 : c->head_dim <= 96 ? 1 : c->head_dim <= 128 ? 2
+                  : c->head_dim <= 192 ? 3 : 4;
   const PagedKernel &k = g_paged[s->device].kernel[kind][width][c->block_size % ts::kPagedPage == 0];
 
   ts::PagedParams p;

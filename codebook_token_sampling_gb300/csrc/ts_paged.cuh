@@ -28,7 +28,7 @@
 
 #include <type_traits>
 
-#include "ts_kv.cuh"
+#include "ts_kv_common.cuh"
 #include "ts_lmhead.cuh"
 
 namespace ts {
@@ -183,7 +183,9 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
 template <int ROW_BYTES, int LANES>
 __host__ __device__ __forceinline__ constexpr int stage_xor(int row) {
   if constexpr (LANES > 0) return LANES * (row & (8 / LANES - 1));
-  else return ROW_BYTES >= 128 ? row & 7 : (row >> 1) & 3;
+  else if constexpr (ROW_BYTES % 128 == 0) return row & 7;
+  else if constexpr (ROW_BYTES % 64 == 0) return (row >> 1) & 3;  // two rows share a 128-byte line's phase
+  else return (row >> 2) & 1;                                     // rows of 96 bytes
 }
 template <int ROW_BYTES, int LANES>
 __device__ __forceinline__ uint32_t stage_at(int row, int chunk) {
@@ -208,7 +210,7 @@ struct MmaCore {
   static constexpr int kDim = DP;
   // stages of 16 KB: six warps with two stages each (56 us), not four with
   // three (59 us: 48 requests of up to 6000 tokens, 2 x 8 bf16 heads of 256)
-  static constexpr int kWarps = kTok * kRowBytes > 4096 ? 6 : 4;
+  static constexpr int kWarps = kTok * kRowBytes > 6144 ? 6 : 4;
   static constexpr int kSteps = DP / 16;
   // wide rows leave no registers for the queries: one copy in shared memory
   static constexpr bool kSharedQ = DP > 128;
@@ -545,7 +547,8 @@ struct FmaCore {
   static constexpr uint32_t kWarpBytes = kTok * GR * 4;
   static constexpr int kLanes = DP / 4 < 32 ? DP / 4 : 32;  // lanes across a row
   static constexpr int kSplit = 32 / kLanes;                // tokens side by side
-  static constexpr int kCols = DP / 128 > 0 ? DP / 128 : 1; // chunks per lane
+  static constexpr int kCols = (DP + 127) / 128;            // chunks per lane
+  static constexpr int kQuads = DP / 4;
   static constexpr int kDim = DP;
   // stages of 16 KB: six warps per SM as three CTAs of two (62 us), not four as
   // one (73 us: 24 requests of up to 3001 tokens, 4 x 4 heads of 256)
@@ -645,7 +648,7 @@ struct FmaCore {
       }
     }
     __syncwarp();
-    const int col = lane % kLanes, sub = lane / kLanes;
+    const int col = lane % kLanes, sub = kSplit == 1 ? 0 : lane / kLanes;
 #pragma unroll 4
     for (int u = sub; u < kTok; u += kSplit) {
       float w[GR];
@@ -653,6 +656,7 @@ struct FmaCore {
       for (int g = 0; g < GR; ++g) w[g] = sp[u * GR + g];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
+        if (kQuads % kLanes && col + c * 32 >= kQuads) continue;
         uint64_t v[2];
         lds_pairs(v, vs + stage_at<kRowBytes, kPer>(u, col + c * 32));
 #pragma unroll
@@ -686,7 +690,7 @@ struct FmaCore {
           y[e] = e & 1 ? high_of(o[g][2 * c + e / 2]) : low_of(o[g][2 * c + e / 2]);
           if constexpr (kSplit == 2) y[e] += __shfl_xor_sync(0xFFFFFFFFu, y[e], 16);
         }
-        if (lane < kLanes)
+        if (lane < kLanes && col + c * 32 < kQuads)
           *reinterpret_cast<float4 *>(buf + at(g, 4 * (col + c * 32))) = make_float4(y[0], y[1], y[2], y[3]);
       }
     }
@@ -708,9 +712,11 @@ struct PagedShape {
   static constexpr uint32_t kSmem = Core::kWarps * (kRing + Core::kWarpBytes) + Core::kQBytes;
   // CTAs per SM that the registers have to allow
   static constexpr int kFit = static_cast<int>(226 * 1024 / (kSmem + 2048));
-  static constexpr int kMost = (Core::kFma || Core::kRows <= 8 ? 4 : Core::kDim > 64 ? 2 : 3) * 4 / Core::kWarps;
-  static constexpr int kRegs = Core::kDim <= 128 || (Core::kElemBytes == 1 && Core::kRows <= 8)
-                                   ? kMost : 65536 / (256 * 32 * Core::kWarps);
+    static constexpr int kFour = Core::kDim == 96 && (!Core::kFma || Core::kRows > 4) ? 3 : 4;
+  static constexpr int kMost = (Core::kFma || Core::kRows <= 8 ? kFour : Core::kDim > 64 ? 2 : 3) * 4 / Core::kWarps;
+  static constexpr int kRegs = Core::kDim <= 128 ? kMost
+                               : Core::kElemBytes == 1 && Core::kRows <= 8 ? 3
+                               : 65536 / (256 * 32 * Core::kWarps);
   static constexpr int kMin = kFit > kMost ? kMost : kFit;
   static constexpr int kPerSm = kMin > kRegs ? kRegs : kMin;
 };
@@ -1046,10 +1052,12 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
   // ---- loading: a stage's table entry and mask byte are fetched one stage
   // before its rows ----
   constexpr int kChunks = Core::kRowBytes / 16;              // of a row
-  constexpr int kRowsAt = kChunks <= 32 ? 32 / kChunks : 1;  // rows that the lanes copy at once
-  constexpr int kParts = kChunks <= 32 ? 1 : kChunks / 32;   // copies of a row by all lanes
+  // rows that the lanes copy at once (a power of two), copies of a row by all lanes
+  constexpr int kRowsAt = kChunks <= 4 ? 8 : kChunks <= 8 ? 4 : kChunks <= 16 ? 2 : 1;
+  constexpr int kParts = (kChunks + 31) / 32;
   constexpr uint32_t kAll = Core::kTok == 32 ? 0xFFFFFFFFu : (1u << (Core::kTok & 31)) - 1;
-  const int my_row = kChunks <= 32 ? lane / kChunks : 0, my_chunk = lane % kChunks;
+  const int my_row = kChunks <= 32 ? min(lane / kChunks, kRowsAt - 1) : 0;
+  const int my_chunk = kChunks <= 32 ? lane - my_row * kChunks : lane;  // kChunks and more: none
   const int chunks = p.dim * Core::kElemBytes / 16;
   const uint32_t my_at = ring_at + stage_at<Core::kRowBytes, Core::kPer>(my_row, my_chunk);
   // the rows are read once per step: in L2 they make way for what every layer
@@ -1092,7 +1100,8 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
       // a wanted token's block is outside the cache
       lost_ring[warp][stage] = want != valid;
     }
-    const uint32_t to = my_at + stage * 2 * Shape::kHalf;
+    const uint32_t to = (Core::kRowBytes % 128 ? ring_at + my_row * Core::kRowBytes : my_at) + stage * 2 * Shape::kHalf;
+    const int my_place = my_chunk ^ stage_xor<Core::kRowBytes, Core::kPer>(my_row);
     // copies rows r0 .. r0 + n - 1 of the stage from rows that lie a token
     // stride apart, the first at ka and va (this lane's row and chunk)
     const auto copy = [&](int r0, int n, const char *ka, const char *va) {
@@ -1101,9 +1110,12 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
           const int r = r0 + i * kRowsAt;
+          if ((kRowsAt * kChunks) % 32 && my_chunk + 32 * part >= kChunks) continue;
           const bool real = ((valid >> (r + my_row)) & 1u) && my_chunk + 32 * part < chunks;
-          const uint32_t at = (to ^ (stage_xor<Core::kRowBytes, Core::kPer>(r) << 4)) +
-                              r * Core::kRowBytes + 512 * part;
+          constexpr bool kLines = Core::kRowBytes % 128 == 0;  // a row's address has its chunk's bits
+          const uint32_t at =
+              kLines ? (to ^ (stage_xor<Core::kRowBytes, Core::kPer>(r) << 4)) + r * Core::kRowBytes + 512 * part
+                     : to + r * Core::kRowBytes + ((my_place ^ stage_xor<Core::kRowBytes, Core::kPer>(r)) << 4);
           const int skip = my_chunk + 32 * part < chunks ? 16 * (my_chunk + 32 * part) : 0;
           cp_async16_or_zero(at, ka + skip, real, policy);
           cp_async16_or_zero(at + Shape::kHalf, va + skip, real, policy);
@@ -1282,49 +1294,6 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
   }
   cp_async_wait_group<0>();
   if (bits && lane == 0) atomicOr(p.status, bits);
-}
-
-// Joins the items that are spread over many CTAs.  Of an item's rows, block
-// first + j takes rows j, j + parts, ..: its eight warps share the parts, a
-// lane four or eight columns of them, and are added up in shared memory.  Its
-// launch waits for all CTAs, which with few parts costs more than the last CTA
-// needs to join them (measured: see join_here in ts_kv.cu).
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
-
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p) {
-  __shared__ PagedSum s_sum[kJoinWarps][2][32];
-  const int c = static_cast<int>(blockIdx.x);
-  const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x) >> 5;
-  pdl_wait_and_release();
-  const PagedParts d[2] = {p.parts[2 * static_cast<int64_t>(c)], p.parts[2 * static_cast<int64_t>(c) + 1]};
-#pragma unroll 1
-  for (int k = 0; k < 2; ++k) {
-    if (d[k].parts < 2) continue;
-    const int rows = min(p.rows, p.group - d[k].piece * p.rows);
-    const int64_t head = static_cast<int64_t>(d[k].head) * p.group + d[k].piece * p.rows;
-    for (int row = c - d[k].first; row < rows; row += d[k].parts) {
-      for (int h = 0; 4 * lane + 128 * h < p.dim && h < 2; ++h)
-        s_sum[warp][h][lane] = join_parts<8>(p, d[k].first, row, 4 * lane + 128 * h, warp, d[k].parts,
-                                             kJoinWarps, -1, PagedSum());
-      __syncthreads();
-      if (warp < 2 && 4 * lane + 128 * warp < p.dim) {
-        PagedSum y;
-        y.top = s_sum[0][warp][lane].top;
-#pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) y.top = fmaxf(y.top, s_sum[w][warp][lane].top);
-        y.x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        y.sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-          const PagedSum &z = s_sum[w][warp][lane];
-          take_in(y, exp2_from(z.top, y.top), z.x, z.sum);
-        }
-        paged_answer(p, d[k].request, d[k].head, head + row, 4 * lane + 128 * warp, y);
-      }
-      __syncthreads();
-    }
-  }
 }
 
 }  // namespace ts

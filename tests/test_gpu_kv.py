@@ -473,7 +473,7 @@ EDGES = [0, 1, 15, 16, 17, 63, 64, 65, 0, 128, 200, 255, 257, 511]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
-@pytest.mark.parametrize("dim", [16, 64, 80, 128, 144, 256])
+@pytest.mark.parametrize("dim", [16, 64, 80, 96, 128, 144, 192, 256])
 @pytest.mark.parametrize("group,block,layout", [(1, 16, "nhd"), (2, 24, "hnd"), (5, 7, "nhd"), (16, 64, "hnd"),
                                                 (20, 1, "nhd")])
 def test_attention_shapes(ts, sampler, kind, dim, group, block, layout):
