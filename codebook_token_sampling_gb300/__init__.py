@@ -281,11 +281,21 @@ def _check(status: int, what: str):
         raise SamplerError(status, what)
 
 
+_current_stream = None  # () -> the current stream's address
+
+
 def _stream_ptr(stream) -> int:
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return int(stream.cuda_stream)
+    global _current_stream
+    if stream is not None:
+        return int(stream.cuda_stream)
+    if _current_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:  # without a Stream object per call
+            _current_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
+        else:
+            _current_stream = lambda: int(torch.cuda.current_stream().cuda_stream)  # noqa: E731
+    return _current_stream()
 
 
 # --------------------------------------------------------------------------
