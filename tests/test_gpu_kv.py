@@ -99,6 +99,14 @@ def test_tables(ts, sampler, n, block_size, len_hi, new_hi, finished, short, dou
     assert bool(want["status"] & okv.NO_BLOCKS) == bool(need > st["n_free"] + held[ends].sum())
 
 
+def test_tables_sums_past_32_bits(ts, sampler):
+    """Table rows that could hold more than 2^31 tokens together (64-bit sums)."""
+    rng = np.random.default_rng(9)
+    st = tables_state(rng, 40, block_size=65536, len_hi=300000, new_hi=4000, finished=0.2, wide=1024)
+    for double in (False, True):
+        check_tables(ts, sampler, st, double=double)
+
+
 def test_tables_one_token_each_and_a_short_map(ts, sampler):
     rng = np.random.default_rng(5)
     st = tables_state(rng, 60, block_size=16, len_hi=100, new_hi=1)
@@ -515,6 +523,34 @@ def test_attention_cuts(ts, sampler, kind, group, ctas, join):
         sampler.set_option(ts.TS_OPT_KV_JOIN, 0)
         sampler.set_option(ts.TS_OPT_KV_CTAS, 0)
     assert np.array_equal(one[0], two[0]) and np.array_equal(one[1], two[1])  # the same in every run
+
+
+def test_attention_sums_past_32_bits(ts, sampler):
+    """Table rows that could hold more than 2^31 tiles of work together, and a
+    context that crosses one of its 65,536-token blocks."""
+    import torch
+    c = attention_case(torch, 20, [100, 0, 65540], heads=32, group=1, dim=16, block=65536, layout="nhd", kind="bf16",
+                       stale=False)
+    wide = np.random.default_rng(0).integers(-2**31, 2**31, (3, 32000)).astype(np.int32)
+    wide[:, :2] = c["table"][:, :2]
+    c["table"] = wide
+    check_attention(ts, sampler, c)
+
+
+def test_attention_nothing_to_do(ts, sampler):
+    """No requests, and requests whose tables have no entries."""
+    import torch
+    c = attention_case(torch, 21, [0, 0], heads=1, group=2, dim=64, block=16, layout="nhd", kind="bf16", stale=False)
+    c["table"] = c["table"][:, :0]
+    got, lse, status = run_attention(ts, sampler, c)
+    assert not got.any() and np.isneginf(lse).all() and status == 0
+    c["lens"] = np.array([0, 1], np.int32)  # longer than its table
+    got, lse, status = run_attention(ts, sampler, c)
+    assert not got[0].any() and np.isnan(got[1]).all() and np.isnan(lse[1]).all() and status == okv.BAD_SHAPE
+    q = c["q"][:0]
+    query = ts.PagedQuery(q, torch.empty_like(q), torch.zeros((0, 4), dtype=torch.int32, device="cuda"),
+                          torch.zeros(0, dtype=torch.int32, device="cuda"))
+    ts.ts_paged_attention(sampler.handle, ts.KvCache(c["k"], c["v"]), query)
 
 
 def test_attention_many_requests(ts, sampler):
