@@ -207,6 +207,7 @@ struct MmaCore {
   static constexpr int kTok = 16 * KT;
   static constexpr int kPer = 0;
   static constexpr bool kFma = false;
+  static constexpr float kLift = E4M3 ? 15.0f : 0.0f;  // weights count from 2^kLift (see step)
   static constexpr int kElemBytes = E4M3 ? 1 : 2;
   static constexpr int kRowBytes = DP * kElemBytes;
   static constexpr int kDim = DP;
@@ -223,7 +224,8 @@ struct MmaCore {
   uint32_t qf[NT][kSharedQ ? 1 : kSteps][2];  // head 8 n + g
   uint32_t q_at;                   // of this lane's share of the shared copy
   float o[NT][kSteps][4];          // heads 8 n + 2 tg + (0, 1)
-  float m[NT][2], l[NT][2], sc[NT][2];  // of those heads; l: this lane's tokens only
+  // of those heads; l: this lane's tokens only; o and l hold 2^kLift times theirs
+  float m[NT][2], l[NT][2], sc[NT][2];
 
   // The queries' words of group n, step kk.
   __device__ __forceinline__ void query(int n, int kk, uint32_t (&x)[2]) const {
@@ -313,6 +315,11 @@ struct MmaCore {
   __device__ __forceinline__ void poison() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) l[n][0] = l[n][1] = __int_as_float(0x7FC00000);
+  }
+
+  static __device__ __forceinline__ float weight(float s, float base) {
+    if constexpr (kLift != 0.0f) return exp2_of(s - base + kLift);
+    else return exp2_of(s - base);
   }
 
   // kTok tokens: K rows at shared address ks, V rows at vs, bit t of `valid` set
@@ -435,8 +442,11 @@ struct MmaCore {
     // is lost and the output's own rounding stays the largest error.  The
     // second number is kept above zero (by 2^-20 of the weight): an attended
     // infinity in V then comes out as one, not as the NaN of 0 times it.  An
-    // f16 weight (e4m3 values) keeps 11 bits, enough for the same, and e4m3 has
-    // no infinities.
+    // f16 weight (e4m3 values, which have no infinities) keeps 11 bits.  f16's
+    // range is short, and many small weights may make up the output beside a
+    // large one whose value is zero: so the largest is 2^kLift, at the range's
+    // upper end, and 2^-29 of it keeps 11 bits still, 2^-39 is not lost.  (Counted
+    // from 1, all below 2^-25 were lost from the output, not from the sums.)
     uint32_t hi[KT][NT][2], lo[KT][NT][2];
 #pragma unroll
     for (int t = 0; t < KT; ++t)
@@ -444,7 +454,7 @@ struct MmaCore {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float x = exp2_of(s[t][n][2 * r] - base[n][0]), y = exp2_of(s[t][n][2 * r + 1] - base[n][1]);
+          const float x = weight(s[t][n][2 * r], base[n][0]), y = weight(s[t][n][2 * r + 1], base[n][1]);
           l[n][0] += x;
           l[n][1] += y;
           if constexpr (E4M3) {
@@ -500,8 +510,10 @@ struct MmaCore {
   // column on different banks, four columns from a multiple of four together.
   static __device__ __forceinline__ int at(int h, int c) { return h * DP + (c ^ (((h >> 1) & 3) << 3)); }
 
-  // The warp's maxima, sums and weighted sums of V.
+  // The warp's maxima, sums and weighted sums of V (the lift's power of two goes
+  // off without a rounding).
   __device__ __forceinline__ void give(float *buf, float *sm, float *sl) {
+    constexpr float kLower = E4M3 ? 0x1p-15f : 1.0f;  // 2^-kLift
     const int lane = static_cast<int>(lane_id()), g = lane >> 2, tg = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -514,13 +526,13 @@ struct MmaCore {
         const int head = 8 * n + 2 * tg + h;
         if (g == 0) {
           sm[head] = m[n][h];
-          sl[head] = x;
+          sl[head] = x * kLower;
         }
 #pragma unroll
         for (int d = 0; d < kSteps; ++d) {
           if constexpr (E4M3) {
             *reinterpret_cast<float2 *>(buf + at(head, 16 * d + 2 * g)) =
-                make_float2(o[n][d][h], o[n][d][2 + h]);
+                make_float2(o[n][d][h] * kLower, o[n][d][2 + h] * kLower);
           } else {
             buf[at(head, 16 * d + g)] = o[n][d][h];
             buf[at(head, 16 * d + 8 + g)] = o[n][d][2 + h];

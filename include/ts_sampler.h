@@ -527,7 +527,10 @@ ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *
  *   lse = m + ln sum_t exp(s_t - m)   (natural logarithm; lse may be NULL).
  * A head that attends to nothing gets out = 0 and lse = -inf.  Scores, maxima,
  * sums and the outputs' sums are fp32; the output is rounded once to the
- * queries' type.  Results depend on the lengths (how the work is cut and
+ * queries' type.  On its way into a product a weight beside bf16 values keeps 16
+ * bits, one beside e4m3 values 11 (fewer below 2^-29 of the head's largest,
+ * nothing below 2^-39), a query beside e4m3 keys 2^-25 of its row's largest
+ * element.  Results depend on the lengths (how the work is cut and
  * joined) but are the same in every run.
  *
  * Types: bf16 queries on a bf16 or e4m3 cache, fp32 queries on an fp32 cache

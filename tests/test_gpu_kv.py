@@ -601,6 +601,41 @@ def test_attention_values(ts, sampler, kind):
     assert np.isposinf(got[3, :, 7]).all() and np.isfinite(np.delete(got[3], 7, 1)).all()
 
 
+@pytest.mark.parametrize("gap", [12.0, 16.0, 18.0, 20.0, 24.0])
+@pytest.mark.parametrize("n,group,dim,ctas", [(1500, 2, 64, 0), (1500, 16, 128, 1), (16000, 8, 128, 1), (16000, 1, 256, 0),
+                                              (16000, 3, 192, 40)])
+def test_attention_small_weights_on_e4m3(ts, sampler, gap, n, group, dim, ctas):
+    """One key far above all others in score, with a value of zeros: what comes
+    out is the others', whose weights are 2^-17 to 2^-35 of the largest.  Bounds
+    as in assert_attention, but a weight in f16 counts from 2^15, so what it
+    loses at least is 2^-40 of the largest weight."""
+    import torch
+    c = attention_case(torch, 22, [n, 300], heads=1, group=group, dim=dim, block=16, layout="nhd", kind="e4m3", stale=False)
+    c.update(k_scale=None, v_scale=None, scale=1.0)
+    c["q"][:] = 0
+    c["q"][:, :, 0] = 1
+    c["k"].view(torch.uint8)[:] = 0
+    c["v"].copy_(c["v"].float().abs().to(c["v"].dtype))
+    for r, t in ((0, n // 3), (1, 299)):
+        at = int(c["table"][r, t // 16]), t % 16
+        c["k"].view(torch.uint8)[at[0], at[1], 0, 0] = int(okv.to_e4m3([gap])[0])
+        c["v"].view(torch.uint8)[at] = 0
+    want = want_attention(torch, c)
+    assert np.allclose(want["lse"][0], np.logaddexp(gap, np.log(n - 1)), rtol=1e-12)
+    sampler.set_option(ts.TS_OPT_KV_CTAS, ctas)
+    try:
+        got, lse, status = run_attention(ts, sampler, c)
+    finally:
+        sampler.set_option(ts.TS_OPT_KV_CTAS, 0)
+    assert status == 0
+    keys = want["keys"][:, None]
+    err = dim * 2.0 ** -22 * want["dot"] + 2.0 ** -21 * (np.abs(want["lse"]) + want["dot"])
+    bound = want["abs_v"] * (4 * err + keys * 2.0 ** -23 + 2.0 ** -10)[..., None] + 2.0 ** -8 * want["out"]
+    bound = bound + (keys * 2.0 ** -40 * want["max_v"])[..., None]
+    assert np.all(np.abs(got - want["out"]) <= bound), np.max((np.abs(got - want["out"]) / want["out"]))
+    assert np.all(np.abs(lse - want["lse"]) <= 2 * err + keys * 2.0 ** -23 + 2.0 ** -20)
+
+
 def test_attention_large_queries_on_e4m3(ts, sampler):
     """Query rows far outside f16's range, and one of zeros."""
     import torch
