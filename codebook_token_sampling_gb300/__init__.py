@@ -679,6 +679,16 @@ def _strides(t) -> list:
     return [st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape[:-1])]
 
 
+def _table_stride(t) -> int:
+    """The stride of a block table's rows, which are contiguous and do not overlap
+    (a row that several requests share, e.g. an expanded one, is refused); a single
+    row's says nothing."""
+    n, wide = t.shape
+    _need((wide < 2 or t.stride(1) == 1) and (n < 2 or t.stride(0) >= wide),
+          "block_table: contiguous rows of their own")
+    return t.stride(0) if n > 1 else wide
+
+
 class KvTables:
     """Block tables, lengths, the stack of free blocks and the slot maps of one
     cache, with a prebuilt ``ts_kv_tables_args``.
@@ -715,12 +725,12 @@ class KvTables:
         self.slots = make(max_tokens, fill=-1, dtype=torch.int64)
         self.positions = make(max_tokens, fill=-1)
         self.requests = make(max_tokens, fill=-1)
-        t = self.block_table  # a strided row is as long as max_blocks at least
-        _need(t.dtype == i32 and t.device == dev and tuple(t.shape) == (n_requests, max_blocks)
-              and (max_blocks < 2 or t.stride(1) == 1), "block_table: int32 [n_requests, max_blocks]")
+        t = self.block_table
+        _need(t.dtype == i32 and t.device == dev and tuple(t.shape) == (n_requests, max_blocks),
+              "block_table: int32 [n_requests, max_blocks]")
         c = TsKvTables()
         c.n_requests, c.block_size, c.n_blocks, c.max_blocks = n_requests, block_size, n_blocks, max_blocks
-        c.table_stride = max(t.stride(0), max_blocks)
+        c.table_stride = _table_stride(t)
         c.block_table = t.data_ptr()
         c.free_blocks = _vector(self.free_blocks, 1 if n_blocks else 0, i32, dev, "free_blocks: int32")
         c.free_len = self.free_blocks.numel()
@@ -816,8 +826,7 @@ class PagedQuery:
               "q and out: [n_requests, n_heads, head_dim] of one type")
         _need(q.stride(2) == 1 and out.stride(2) == 1, "q and out: head_dim is contiguous")
         _need(block_table.dtype == torch.int32 and block_table.dim() == 2
-              and block_table.shape[0] == n and block_table.device == q.device
-              and (block_table.shape[1] < 2 or block_table.stride(1) == 1),
+              and block_table.shape[0] == n and block_table.device == q.device,
               "block_table: int32 [n_requests, max_blocks]")
         self.q, self.out, self.block_table, self.lens = q, out, block_table, lens
         self.lse, self.key_mask = lse, key_mask
@@ -829,7 +838,7 @@ class PagedQuery:
         c.q_request_stride, c.q_head_stride = _strides(q)
         c.out_request_stride, c.out_head_stride = _strides(out)
         c.block_table = block_table.data_ptr()
-        c.table_stride = max(block_table.stride(0), block_table.shape[1])
+        c.table_stride = _table_stride(block_table)
         c.lens = _vector(lens, n, torch.int32, q.device, "lens: int32 [n_requests]")
         c.key_mask = None
         if key_mask is not None:

@@ -60,3 +60,30 @@ def test_attention_by_hand():
     assert none["out"][0, 0, 0] == 0 and none["lse"][0, 0] == -np.inf
     last = okv.attention(np.ones((1, 1, 1)), k, v, np.array([[0]]), [2], scale=1.0, n_blocks=1, window=1)
     assert last["out"][0, 0, 0] == 4.0
+
+
+def test_table_rows_are_rows_of_their_own():
+    """A table whose rows overlap in memory (one row expanded to all requests) is
+    refused; strided rows and a single row keep their meaning."""
+    import torch
+    import codebook_token_sampling_gb300 as ts
+    i32 = torch.int32
+
+    def query(table):
+        n = table.shape[0]
+        q = torch.zeros((n, 2, 64), dtype=torch.bfloat16)
+        return ts.PagedQuery(q, torch.empty_like(q), table, torch.zeros(n, dtype=i32))
+
+    def tables(table):
+        return ts.KvTables(*table.shape, 100, 16, max_tokens=4, block_table=table, device="cpu")
+    row = torch.arange(8, dtype=i32)
+    wide = torch.zeros((4, 20), dtype=i32)
+    for make in (query, tables):
+        for bad in (row.expand(4, -1), row.as_strided((3, 6), (1, 1)), wide[:, ::2], wide.t()[:8]):
+            with pytest.raises(ValueError):
+                make(bad)
+        assert make(wide).c.table_stride == 20 and make(wide[:, 3:11]).c.table_stride == 20
+        assert make(wide[::2]).c.table_stride == 40
+        for one in (row.expand(1, -1), wide[1:2, :8], row.as_strided((1, 8), (0, 1))):
+            made = make(one)
+            assert made.c.table_stride >= 8 and made.c.max_blocks == 8
