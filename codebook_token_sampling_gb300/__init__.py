@@ -405,13 +405,19 @@ def ts_kv_tables(handle: int, tables: "KvTables", stream=None) -> None:
 
 
 def ts_kv_append(handle: int, cache: "KvCache", tokens: "KvTokens", stream=None) -> None:
-    """Writes the tokens' keys and values into the cache at their slots."""
+    """Writes the tokens' keys and values into the cache at their slots; they have
+    its heads, row width and device (ValueError)."""
+    if tokens.rows_of != cache.rows_of:
+        raise ValueError(f"tokens of {tokens.rows_of} for a cache of {cache.rows_of}")
     _check(_lib.ts_kv_append(handle, ctypes.byref(cache.c), ctypes.byref(tokens.c),
                              _stream_ptr(stream)), "ts_kv_append")
 
 
 def ts_paged_attention(handle: int, cache: "KvCache", query: "PagedQuery", stream=None) -> None:
-    """Attention of one query token per request over its cached tokens."""
+    """Attention of one query token per request over its cached tokens; queries
+    have the cache's row width and device (ValueError)."""
+    if query.rows_of != cache.rows_of[1:]:
+        raise ValueError(f"queries of {query.rows_of} for a cache of {cache.rows_of[1:]}")
     _check(_lib.ts_paged_attention(handle, ctypes.byref(cache.c), ctypes.byref(query.c),
                                    _stream_ptr(stream)), "ts_paged_attention")
 
@@ -777,6 +783,8 @@ class KvCache:
               "k and v: [n_blocks, block_size, n_kv_heads, head_dim] of one type")
         _need(k.stride(3) == 1 and v.stride(3) == 1, "k and v: head_dim is contiguous")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        # what tokens and queries have to match: key heads, head_dim, device
+        self.rows_of = (k.shape[2], k.shape[3], k.device)
         c = TsKvCache()
         c.k, c.v = k.data_ptr(), v.data_ptr()
         c.dtype = _kv_dtype(k)
@@ -799,6 +807,7 @@ class KvTokens:
               "k and v: [n_tokens, n_kv_heads, head_dim] of one type")
         _need(k.stride(2) == 1 and v.stride(2) == 1, "k and v: head_dim is contiguous")
         self.k, self.v, self.slots, self.rows = k, v, slots, rows
+        self.rows_of = (k.shape[1], k.shape[2], k.device)
         c = TsKvTokens()
         c.k, c.v = k.data_ptr(), v.data_ptr()
         c.dtype = _kv_dtype(k)
@@ -830,6 +839,7 @@ class PagedQuery:
               "block_table: int32 [n_requests, max_blocks]")
         self.q, self.out, self.block_table, self.lens = q, out, block_table, lens
         self.lse, self.key_mask = lse, key_mask
+        self.rows_of = (dim, q.device)
         c = TsPagedQuery()
         c.q, c.out = q.data_ptr(), out.data_ptr()
         c.lse = _vector(lse, n * heads, torch.float32, q.device, "lse: float32 [n_requests, n_heads]")

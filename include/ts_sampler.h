@@ -496,7 +496,8 @@ typedef struct {
  * alignment) into the cache at slots[x]; a negative slot skips the token, whose
  * rows are then not read.  rows serves a decode step that keeps a row per
  * request while ts_kv_tables packs the tokens of those that go on: its
- * `requests` map is this one's rows.  The tokens have the
+ * `requests` map is this one's rows.  A row has the cache's n_kv_heads heads of
+ * head_dim elements (the call cannot check this).  The tokens have the
  * cache's type, or for an e4m3 cache bf16 or fp32: x / scale is computed in fp32
  * and rounded to the nearest e4m3 value (ties to even, values beyond 448 to
  * 448 with their sign, NaN kept).  Tokens of one call have slots of their own.
@@ -525,7 +526,8 @@ ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *
  * softcap * tanh(s_t / softcap) where softcap > 0:
  *   out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),   m = max_t s_t,
  *   lse = m + ln sum_t exp(s_t - m)   (natural logarithm; lse may be NULL).
- * A head that attends to nothing gets out = 0 and lse = -inf.  Scores, maxima,
+ * Rows of q and out have the cache's head_dim elements (the call cannot check
+ * this).  A head that attends to nothing gets out = 0 and lse = -inf.  Scores, maxima,
  * sums and the outputs' sums are fp32; the output is rounded once to the
  * queries' type.  On its way into a product a weight beside bf16 values keeps 16
  * bits, one beside e4m3 values 11 (fewer below 2^-29 of the head's largest,

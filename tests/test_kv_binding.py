@@ -87,3 +87,37 @@ def test_table_rows_are_rows_of_their_own():
         for one in (row.expand(1, -1), wide[1:2, :8], row.as_strided((1, 8), (0, 1))):
             made = make(one)
             assert made.c.table_stride >= 8 and made.c.max_blocks == 8
+
+
+class _Stream:
+    cuda_stream = 0
+
+
+def test_tokens_and_queries_fit_the_cache():
+    """Heads, row widths and devices are compared before a call reaches the
+    library (which here refuses the NULL handle of those that fit)."""
+    import torch
+    import codebook_token_sampling_gb300 as ts
+
+    def cache(heads, dim):
+        k = torch.zeros((2, 16, heads, dim), dtype=torch.bfloat16)
+        return ts.KvCache(k, torch.zeros_like(k))
+
+    def tokens(heads, dim, device="cpu"):
+        k = torch.zeros((3, heads, dim), dtype=torch.bfloat16, device=device)
+        return ts.KvTokens(k, k, torch.zeros(3, dtype=torch.int64, device=device))
+
+    def query(heads, dim, device="cpu"):
+        q = torch.zeros((3, heads, dim), dtype=torch.bfloat16, device=device)
+        i32 = {"dtype": torch.int32, "device": device}
+        return ts.PagedQuery(q, torch.empty_like(q), torch.zeros((3, 2), **i32), torch.zeros(3, **i32))
+    for call, make in ((ts.ts_kv_append, tokens), (ts.ts_paged_attention, query)):
+        with pytest.raises(ts.SamplerError) as e:
+            call(None, cache(4, 64), make(4, 64), _Stream)
+        assert e.value.status == ts.TS_ERR_INVALID_ARG
+        for other in (make(4, 128), make(4, 32), make(4, 64, "meta")):
+            with pytest.raises(ValueError):
+                call(None, cache(4, 64), other, _Stream)
+    for heads in (2, 8):
+        with pytest.raises(ValueError):
+            ts.ts_kv_append(None, cache(4, 64), tokens(heads, 64), _Stream)
