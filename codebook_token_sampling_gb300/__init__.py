@@ -415,9 +415,14 @@ def ts_kv_append(handle: int, cache: "KvCache", tokens: "KvTokens", stream=None)
 
 def ts_paged_attention(handle: int, cache: "KvCache", query: "PagedQuery", stream=None) -> None:
     """Attention of one query token per request over its cached tokens; queries
-    have the cache's row width and device (ValueError)."""
+    have the cache's row width and device, a key mask a column for each token of a
+    table row (ValueError)."""
     if query.rows_of != cache.rows_of[1:]:
         raise ValueError(f"queries of {query.rows_of} for a cache of {cache.rows_of[1:]}")
+    if query.key_mask is not None:
+        tokens = query.block_table.shape[1] * cache.k.shape[1]
+        if query.key_mask.shape[1] < tokens:
+            raise ValueError(f"key_mask: {query.key_mask.shape[1]} columns for tables of {tokens} tokens")
     _check(_lib.ts_paged_attention(handle, ctypes.byref(cache.c), ctypes.byref(query.c),
                                    _stream_ptr(stream)), "ts_paged_attention")
 

@@ -121,3 +121,24 @@ def test_tokens_and_queries_fit_the_cache():
     for heads in (2, 8):
         with pytest.raises(ValueError):
             ts.ts_kv_append(None, cache(4, 64), tokens(heads, 64), _Stream)
+
+
+def test_key_masks_are_as_wide_as_the_tables():
+    """A mask's columns count, not the stride of the rows that they are taken from."""
+    import torch
+    import codebook_token_sampling_gb300 as ts
+    q = torch.zeros((3, 4, 64), dtype=torch.bfloat16)
+    k = torch.zeros((2, 16, 4, 64), dtype=torch.bfloat16)
+    cache = ts.KvCache(k, torch.zeros_like(k))
+    i32 = {"dtype": torch.int32}
+    wide = torch.ones((3, 1000), dtype=torch.uint8)
+
+    def call(mask):
+        ts.ts_paged_attention(None, cache, ts.PagedQuery(q, torch.empty_like(q), torch.zeros((3, 2), **i32),
+                                                         torch.zeros(3, **i32), key_mask=mask), _Stream)
+    for enough in (wide, wide[:, :32], wide[:, 7:39], None):
+        with pytest.raises(ts.SamplerError):  # the NULL handle
+            call(enough)
+    for narrow in (wide[:, :31], wide[:, :10], wide[:, 999:]):
+        with pytest.raises(ValueError):
+            call(narrow)
