@@ -258,7 +258,8 @@ ts_status ts_kv_tables(ts_sampler *s, const ts_kv_tables_args *t, void *stream) 
   // 5.1 with 256 or 1024); for prompts a block per 4096 map entries, as far as
   // the GPU holds them
   const int threads = t->n_requests <= 1024 && t->max_tokens <= 4096 ? 512 : ts::kTablesMaxThreads;
-  const int grid = std::max(1, std::min(s->num_sms, (t->max_tokens + 4095) / 4096));
+  const int grid = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>(s->num_sms, (static_cast<int64_t>(t->max_tokens) + 4095) / 4096)));
   // blocks that still read the old values may run beside block 0: in place,
   // the new ones go through the workspace
   const bool staged_lens = grid > 1 && lens_in_place, staged_free = grid > 1 && free_in_place;
@@ -335,14 +336,14 @@ ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *
   const int64_t per_head = c->head_dim / vec, per_token = per_head * c->n_kv_heads;
   if (per_token > (1 << 20)) return TS_ERR_UNSUPPORTED;
   // whole tokens, about four units per thread, fewer while SMs would idle
-  const int64_t fill = ts::kAppendThreads * 4;
+  const int64_t fill = ts::kAppendThreads * 4, n_tokens = t->n_tokens;
   p.tokens_per_block = static_cast<int32_t>(std::max<int64_t>(
-      1, std::min<int64_t>(fill / per_token, (t->n_tokens + s->num_sms - 1) / s->num_sms)));
+      1, std::min<int64_t>(fill / per_token, (n_tokens + s->num_sms - 1) / s->num_sms)));
   p.by_block = ts::FastDiv::of(static_cast<uint32_t>(c->block_size));
   p.by_token = ts::FastDiv::of(static_cast<uint32_t>(per_token));
   p.by_head = ts::FastDiv::of(static_cast<uint32_t>(per_head));
   p.status = s->status;
-  const int grid = (t->n_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
+  const int64_t grid = (n_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
   void *args[] = {&p};
   const cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), ts::kAppendThreads, 0,
                                s->pdl != 0, static_cast<cudaStream_t>(stream), args);

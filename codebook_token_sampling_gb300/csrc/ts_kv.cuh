@@ -315,10 +315,10 @@ __global__ void __launch_bounds__(kTablesMaxThreads) kv_tables_kernel(const KvTa
       continue;
     }
     r0 = y0 < n_tokens ? last_start(tok_start, n, y0) : n - 1;
-    const int32_t p0 = len_of[r0] + (y0 - tok_start[r0]);
-    const int32_t b0 = static_cast<int32_t>(p.by_block.div(static_cast<uint32_t>(max(p0, 0))));
+    const int32_t p0 = y0 < n_tokens ? len_of[r0] + (y0 - tok_start[r0]) : 0;
+    const int32_t b0 = static_cast<int32_t>(p.by_block.div(static_cast<uint32_t>(p0)));
     const int32_t off0 = p0 - b0 * p.block_size;
-    if (y0 + 4 <= tok_start[r0 + 1] && off0 + 4 <= p.block_size) {  // four tokens of one block
+    if (tok_start[r0 + 1] - y0 >= 4 && off0 + 4 <= p.block_size) {  // four tokens of one block
       const int64_t s = slot_of(*block_at(r0, b0, held_of(len_of[r0])), off0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
 
   // requests with nothing to attend to
   const auto answer_empty = [&]() {
-    for (int r = static_cast<int>(blockIdx.x); r < p.n_requests; r += p.ctas) {
+    for (int64_t r = blockIdx.x; r < p.n_requests; r += p.ctas) {
       bool bad;
       const PagedSpan s = paged_span<Shape::kTile>(p, p.lens[r], bad);
       if (s.tiles > 0) continue;
@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(PagedShape<Core, NS>::kThreads, PagedShape<Cor
       }
       if (p.lse)
         for (int h = tid; h < n_heads; h += kPagedThreads)
-          p.lse[static_cast<int64_t>(r) * n_heads + h] = bad ? x : -INFINITY;
+          p.lse[r * n_heads + h] = bad ? x : -INFINITY;
     }
   };
   if (!p.join_here && tid < 2) p.parts[2 * static_cast<int64_t>(blockIdx.x) + tid].parts = 0;

@@ -155,6 +155,42 @@ def test_tables_errors(ts, sampler):
         assert check_tables(ts, sampler, st, double=False)["status"] & okv.BAD_SHAPE
 
 
+def test_the_longest_token_maps(ts, sampler):
+    """Maps of 2^31 - 1 entries: the tokens there are in front, then -1; and a cache
+    write of as many tokens, all but those skipped."""
+    import torch
+    most, block = 2 ** 31 - 1, 6
+    st = tables_state(np.random.default_rng(11), 50, block_size=block, len_hi=40, new_hi=90)
+    want = okv.tables(st["block_table"], st["lens"], st["n_new"], None, st["free_blocks"], st["n_free"],
+                      block_size=block, n_blocks=st["n_blocks"], max_tokens=st["max_tokens"])
+    put = {k: torch.from_numpy(st[k]).cuda() for k in ("lens", "n_new", "block_table", "free_blocks")}
+    slots = torch.zeros(most, dtype=torch.int64, device="cuda")
+    t = ts.KvTables(50, st["block_table"].shape[1], st["n_blocks"], block, max_tokens=1, double=True,
+                    n_free=torch.tensor([st["n_free"]], dtype=torch.int32, device="cuda"), **put)
+    t.c.max_tokens, t.c.slots, t.c.positions, t.c.requests = most, slots.data_ptr(), None, None
+    sampler.read_status()
+    ts.ts_kv_tables(sampler.handle, t)
+    n = int(want["token_starts"][-1])
+    assert 1000 < n < st["max_tokens"]
+    assert np.array_equal(slots[:n].cpu().numpy(), want["slots"][:n])
+    assert int(slots[n:].max()) == int(slots[n:].min()) == -1
+    assert np.array_equal(t.token_starts.cpu().numpy(), want["token_starts"])
+    assert np.array_equal(t.lens_out.cpu().numpy(), want["lens"]) and int(t.n_free_out) == want["n_free"]
+    assert np.array_equal(t.block_table.cpu().numpy(), want["block_table"])
+    k, v = cache_pair(torch, st["n_blocks"], block, 1, 8, torch.bfloat16, "nhd")
+    new = torch.arange(8, device="cuda").bfloat16().view(1, 1, 8).expand(most, 1, 8)
+    ts.ts_kv_append(sampler.handle, ts.KvCache(k, v), ts.KvTokens(new, new, slots))
+    torch.cuda.synchronize()
+    assert sampler.read_status() == want["status"] == 0
+    there = np.zeros(st["n_blocks"] * block, bool)
+    there[want["slots"][:n]] = True
+    before = raw(torch, cache_pair(torch, 1, 1, 1, 8, torch.bfloat16, "nhd")[0])[0, 0, 0]
+    for x in (k, v):
+        got = raw(torch, x).reshape(-1, 8)
+        assert np.array_equal(got[there], np.broadcast_to(raw(torch, new[0, 0]), (n, 8)))
+        assert np.array_equal(got[~there], np.broadcast_to(before, (there.size - n, 8)))
+
+
 def test_tables_refusals(ts, sampler):
     import torch
     st = tables_state(np.random.default_rng(8), 6, block_size=16, len_hi=50, new_hi=1)
