@@ -17,12 +17,12 @@ static_assert(ts::kRowBadBlock == TS_ROW_BAD_BLOCK && ts::kRowNoBlocks == TS_ROW
 static_assert(ts::kTablesMaxRequests == TS_KV_MAX_REQUESTS && ts::kPagedMaxDim == TS_KV_MAX_HEAD_DIM,
               "limits");
 
-// Workspace of ts_reserve_kv: paged attention's pieces, then one length per
-// request and the free count of a table update in place.
+// Workspace of ts_reserve_kv: paged attention's pieces, then the free count of a
+// table update in place and the lengths of as many requests as any call may have.
 struct ts_kv_state {
   void *mem;
   int ctas;          // pieces for this many CTAs
-  int max_requests;
+  int max_requests;  // as reserved: tables of more are refused
   ts::PagedParts *parts;
   uint32_t *arrived;
   float *acc;
@@ -161,7 +161,10 @@ extern "C" {
 
 ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests) {
   if (!s || max_requests < 0) return TS_ERR_INVALID_ARG;
-  if (max_requests > 0 && s->kv && max_requests <= s->kv->max_requests) return TS_OK;
+  if (max_requests > 0 && s->kv) {  // the memory stays: captured graphs hold its addresses
+    s->kv->max_requests = std::max(s->kv->max_requests, max_requests);
+    return TS_OK;
+  }
   int prev = 0;
   cudaGetDevice(&prev);
   cudaError_t e = cudaSetDevice(s->device);
@@ -176,7 +179,7 @@ ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests) {
       for (const auto &width : kind)
         for (const PagedKernel &k : width) ctas = std::max(ctas, k.occupancy * s->num_sms);
     const size_t pieces = ts::paged_workspace_bytes(ctas);
-    const size_t bytes = pieces + (static_cast<size_t>(max_requests) + 1) * sizeof(int32_t);
+    const size_t bytes = pieces + (static_cast<size_t>(TS_KV_MAX_REQUESTS) + 1) * sizeof(int32_t);
     ts_kv_state *kv = new (std::nothrow) ts_kv_state;
     if (!kv) {
       rc = TS_ERR_NO_MEMORY;

@@ -403,9 +403,11 @@ ts_status ts_lm_head_sample(ts_sampler *s, const ts_lm_head *h, const ts_batch *
 
 /* Allocates the workspace of the calls below: the pieces that
  * ts_paged_attention joins (about 40 MB) and, for ts_kv_tables calls that
- * update in place, 4 bytes per request.  Call it before any stream capture and
- * not concurrently with work on the sampler; a smaller request than the
- * current size keeps it, 0 frees it.  ts_paged_attention and ts_kv_tables return
+ * update in place, 32 KB.  Call it before any stream capture and not
+ * concurrently with work on the sampler.  A further call keeps the memory, so
+ * that graphs captured with it stay valid, and raises the number of requests that
+ * ts_kv_tables takes if max_requests is larger; 0 frees it, after which such
+ * graphs must not be launched again.  ts_paged_attention and ts_kv_tables return
  * TS_ERR_INVALID_ARG without it.  Calls share it: two calls on one sampler must
  * not overlap on the GPU (order them on one stream or with events). */
 ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests);

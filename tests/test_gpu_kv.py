@@ -850,3 +850,52 @@ def test_options_and_reserve(ts):
     s.reserve_kv(100)
     s.reserve_kv(0)
     s.close()
+
+
+def test_a_larger_reserve_keeps_captured_graphs(ts):
+    """Tables updated in place by several blocks and a joined attention, captured
+    with room for four requests: the same results when they are replayed after the
+    workspace has been asked for more."""
+    import torch
+    s = ts.Sampler(0)
+    s.reserve_kv(4)
+    c = attention_case(torch, 31, [3000, 2000, 5, 900], heads=2, group=4, dim=64, block=16, layout="nhd", kind="bf16", stale=False)
+    want = want_attention(torch, c)
+    out, lse = torch.zeros_like(c["q"]), torch.zeros(c["q"].shape[:2], device="cuda")
+    cache = ts.KvCache(c["k"], c["v"])
+    query = ts.PagedQuery(c["q"], out, torch.from_numpy(c["table"]).cuda(), torch.from_numpy(c["lens"]).cuda(),
+                          scale=c["scale"], lse=lse)
+    n_new = torch.tensor([3000, 1, 0, 2500], dtype=torch.int32, device="cuda")
+    t = ts.KvTables(4, 600, 2400, 16, max_tokens=9000, n_new=n_new)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ts.ts_kv_tables(s.handle, t)
+        ts.ts_paged_attention(s.handle, cache, query)
+    s.reserve_kv(8192)
+    s.reserve_kv(3)
+    for i in range(1, 4):
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert t.lens.tolist() == [3000 * i, i, 0, 2500 * i]
+        assert int(t.n_free) == 2400 - sum(-(-x // 16) for x in t.lens.tolist())
+        assert_attention(c, want, out.float().cpu().numpy(), lse.cpu().numpy())
+    assert s.read_status() == 0
+    many = ts.KvTables(8192, 1, 8192, 16, max_tokens=8192)  # the larger number is served
+    ts.ts_kv_tables(s.handle, many)
+    torch.cuda.synchronize()
+    assert bool((many.lens == 1).all()) and sorted(many.block_table[:, 0].tolist()) == list(range(8192))
+    s.close()
+
+
+def test_reserved_requests_bound_the_tables(ts):
+    """Tables of more requests than were asked for are refused, as before."""
+    s = ts.Sampler(0)
+    s.reserve_kv(4)
+    with pytest.raises(ts.SamplerError) as e:
+        ts.ts_kv_tables(s.handle, ts.KvTables(5, 2, 10, 16, max_tokens=5))
+    assert e.value.status == ts.TS_ERR_INVALID_ARG
+    s.reserve_kv(5)
+    ts.ts_kv_tables(s.handle, ts.KvTables(5, 2, 10, 16, max_tokens=5))
+    assert s.read_status() == 0
+    s.close()
