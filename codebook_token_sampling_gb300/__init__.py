@@ -50,6 +50,7 @@ TS_OPT_WARPS_PER_ROW = 5
 TS_OPT_FAIL_LAUNCH = 6
 TS_OPT_KV_CTAS = 7
 TS_OPT_KV_JOIN = 8
+TS_OPT_KV_LOST = 9
 TS_MAX_VOCAB_BF16 = 163840
 TS_MAX_VOCAB_F32 = 81920
 TS_NOALLOC_SCRATCH_BYTES = 4194304

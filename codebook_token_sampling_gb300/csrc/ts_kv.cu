@@ -24,7 +24,7 @@ struct ts_kv_state {
   int ctas;          // pieces for this many CTAs
   int max_requests;  // as reserved: tables of more are refused
   ts::PagedParts *parts;
-  uint32_t *arrived;
+  unsigned long long *arrived, *calls;
   float *acc;
   float2 *ml;
   int32_t *lens, *n_free;
@@ -149,6 +149,21 @@ const void *append_kernel(bool wide, bool rows) {
 
 }  // namespace
 
+cudaError_t ts_host::kv_lose_parts(ts_sampler *s, int n) {
+  const ts_kv_state *kv = s->kv;
+  int prev = 0;
+  cudaGetDevice(&prev);
+  cudaError_t e = cudaSetDevice(s->device);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  unsigned long long calls = 0;  // all entries are equal
+  if (e == cudaSuccess) e = cudaMemcpy(&calls, kv->calls, sizeof calls, cudaMemcpyDeviceToHost);
+  const unsigned long long left = ((calls ? calls - 1 : 0) << ts::kCallShift) + static_cast<unsigned>(n);
+  for (int b = 0; b < kv->ctas && e == cudaSuccess; ++b)
+    e = cudaMemcpy(kv->arrived + b, &left, sizeof left, cudaMemcpyHostToDevice);
+  cudaSetDevice(prev);
+  return e;
+}
+
 cudaError_t ts_host::kv_free(ts_sampler *s) {
   if (!s->kv) return cudaSuccess;
   const cudaError_t e = cudaFree(s->kv->mem);
@@ -203,7 +218,8 @@ ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests) {
         at += 2 * static_cast<size_t>(ctas) * ts::kPagedRows * sizeof(float2);
         kv->parts = reinterpret_cast<ts::PagedParts *>(at);
         at += 2 * static_cast<size_t>(ctas) * sizeof(ts::PagedParts);
-        kv->arrived = reinterpret_cast<uint32_t *>(at);
+        kv->arrived = reinterpret_cast<unsigned long long *>(at);
+        kv->calls = kv->arrived + ctas;
         kv->n_free = reinterpret_cast<int32_t *>(static_cast<char *>(kv->mem) + pieces);
         kv->lens = kv->n_free + 1;
         s->kv = kv;
@@ -435,6 +451,7 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   p.by_block = ts::FastDiv::of(static_cast<uint32_t>(c->block_size));
   p.parts = s->kv->parts;
   p.arrived = s->kv->arrived;
+  p.all_ctas = s->kv->ctas;
   p.acc = s->kv->acc;
   p.ml = s->kv->ml;
   const int64_t items = static_cast<int64_t>(p.pieces) * p.kv_heads * q->n_requests;
@@ -448,6 +465,7 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
   // Parts of an item, about: the CTAs that share it, no more than its tiles.
   const int64_t parts = std::min<int64_t>(p.ctas / items + 2, item_tiles);
   p.join_here = s->kv_join ? s->kv_join - 1 : parts <= kJoinHere ? 1 : 0;
+  p.calls = p.join_here && item_tiles > 1 ? s->kv->calls : nullptr;  // one tile: one part
   p.out_f32 = f32 ? 1 : 0;
   p.status = s->status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -409,7 +409,9 @@ ts_status ts_lm_head_sample(ts_sampler *s, const ts_lm_head *h, const ts_batch *
  * ts_kv_tables takes if max_requests is larger; 0 frees it, after which such
  * graphs must not be launched again.  ts_paged_attention and ts_kv_tables return
  * TS_ERR_INVALID_ARG without it.  Calls share it: two calls on one sampler must
- * not overlap on the GPU (order them on one stream or with events). */
+ * not overlap on the GPU (order them on one stream or with events), and lengths
+ * must not change while a call runs.  Where they do, those calls' results are
+ * undefined, later calls' are not. */
 ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests);
 
 /* Block tables and slot maps.  The cache is n_blocks blocks of block_size
@@ -615,6 +617,10 @@ ts_status ts_read_status(ts_sampler *s, uint32_t *bits, void *stream);
 /* TS_OPT_KV_JOIN: how ts_paged_attention joins the parts of its work (0 =
  * automatic, 1 = by a launch of their own, 2 = by the last CTA to come). */
 #define TS_OPT_KV_JOIN 8
+/* TS_OPT_KV_LOST (tests only): leaves ts_paged_attention's counters in the
+ * workspace as a call would whose lengths changed while it ran, so that parts of
+ * its work were lost after `value` (0 .. 1000) of them had come.  Synchronises. */
+#define TS_OPT_KV_LOST 9
 ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value);
 
 /* Describes the kernel that ts_sample would launch for `b` (path 1 .. 4,

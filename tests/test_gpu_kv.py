@@ -899,3 +899,37 @@ def test_reserved_requests_bound_the_tables(ts):
     ts.ts_kv_tables(s.handle, ts.KvTables(5, 2, 10, 16, max_tokens=5))
     assert s.read_status() == 0
     s.close()
+
+
+@pytest.mark.parametrize("kind,group", [("bf16", 4), ("e4m3", 16), ("f32", 2)])
+def test_attention_after_a_call_that_lost_parts(ts, sampler, kind, group):
+    """Counters left behind by a call that lost parts do not reach the next ones,
+    whatever number of CTAs these and the calls between have."""
+    import torch
+    c = attention_case(torch, 41, [1000, 3, 0, 700, 64, 1, 2000], heads=2, group=group, dim=128, block=16, layout="hnd",
+                       kind=kind)
+    other = attention_case(torch, 42, [900, 350], heads=1, group=1, dim=256, block=16, layout="nhd", kind="f32")
+    want = want_attention(torch, c)
+    sampler.set_option(ts.TS_OPT_KV_JOIN, 2)
+    try:
+        for ctas in (7, 40, 3, 0, 41):
+            sampler.set_option(ts.TS_OPT_KV_CTAS, ctas)
+            first = run_attention(ts, sampler, c)
+            for lost in (1, 2, 5, 1000, 0):
+                sampler.set_option(ts.TS_OPT_KV_LOST, lost)
+                got = run_attention(ts, sampler, c)
+                assert got[2] == 0
+                assert_attention(c, want, got[0], got[1])
+                again = run_attention(ts, sampler, c)
+                for x, y, z in zip(first, got, again):
+                    assert np.array_equal(x, y) and np.array_equal(x, z)
+                check_attention(ts, sampler, other)
+    finally:
+        sampler.set_option(ts.TS_OPT_KV_JOIN, 0)
+        sampler.set_option(ts.TS_OPT_KV_CTAS, 0)
+    fresh = ts.Sampler(0)
+    with pytest.raises(ts.SamplerError):
+        fresh.set_option(ts.TS_OPT_KV_LOST, 1)  # no workspace
+    fresh.close()
+    with pytest.raises(ts.SamplerError):
+        sampler.set_option(ts.TS_OPT_KV_LOST, 1001)
