@@ -8,7 +8,8 @@ only for device memory and streams.  The functions keep the C names:
     ts_sample_steps, ts_reserve, ts_sample_noalloc, ts_advance_steps,
     ts_read_status, ts_set_option, ts_plan, ts_status_string, ts_last_error,
     ts_lm_head_logits, ts_lm_head_sample, ts_sample_host,
-    ts_reserve_kv, ts_kv_tables, ts_kv_append, ts_paged_attention
+    ts_reserve_kv, ts_kv_tables, ts_kv_append, ts_paged_attention,
+    ts_kv_debug_lose_parts
 
 ``Sampler`` wraps a handle; ``DeviceBatch`` holds one step's per-row arrays on
 the GPU with a prebuilt ``ts_batch`` so that repeated calls marshal nothing;
@@ -50,7 +51,6 @@ TS_OPT_WARPS_PER_ROW = 5
 TS_OPT_FAIL_LAUNCH = 6
 TS_OPT_KV_CTAS = 7
 TS_OPT_KV_JOIN = 8
-TS_OPT_KV_LOST = 9
 TS_MAX_VOCAB_BF16 = 163840
 TS_MAX_VOCAB_F32 = 81920
 TS_NOALLOC_SCRATCH_BYTES = 4194304
@@ -66,7 +66,8 @@ EXPORTED = ("ts_create", "ts_destroy", "ts_max_top_k", "ts_sample", "ts_sample_d
             "ts_sample_steps", "ts_reserve", "ts_sample_noalloc", "ts_advance_steps",
             "ts_read_status", "ts_set_option", "ts_plan", "ts_status_string", "ts_last_error",
             "ts_lm_head_logits", "ts_lm_head_sample", "ts_sample_host",
-            "ts_reserve_kv", "ts_kv_tables", "ts_kv_append", "ts_paged_attention")
+            "ts_reserve_kv", "ts_kv_tables", "ts_kv_append", "ts_paged_attention",
+             "ts_kv_debug_lose_parts")
 
 
 class TsBatch(ctypes.Structure):
@@ -257,6 +258,7 @@ def _load(path: str):
                          ctypes.c_int),
         "ts_paged_attention": ([vp, ctypes.POINTER(TsKvCache), ctypes.POINTER(TsPagedQuery), vp],
                                ctypes.c_int),
+        "ts_kv_debug_lose_parts": ([vp, i32], ctypes.c_int),
         "ts_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "ts_last_error": ([], ctypes.c_char_p),
     }
@@ -426,6 +428,11 @@ def ts_paged_attention(handle: int, cache: "KvCache", query: "PagedQuery", strea
             raise ValueError(f"key_mask: {query.key_mask.shape[1]} columns for tables of {tokens} tokens")
     _check(_lib.ts_paged_attention(handle, ctypes.byref(cache.c), ctypes.byref(query.c),
                                    _stream_ptr(stream)), "ts_paged_attention")
+
+
+def ts_kv_debug_lose_parts(handle: int, come: int) -> None:
+    """For tests: the workspace's counters as a call leaves them that lost parts."""
+    _check(_lib.ts_kv_debug_lose_parts(handle, come), "ts_kv_debug_lose_parts")
 
 
 def ts_status_string(status: int) -> str:

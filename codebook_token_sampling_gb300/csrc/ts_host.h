@@ -40,8 +40,4 @@ ts_status cuda_fail(cudaError_t e, const char *what);
 // Frees the paged cache's workspace (the device is current).
 cudaError_t kv_free(ts_sampler *s);
 
-// Tests: leaves the counters of arrived parts as a call would that lost parts
-// after n had come (there is a workspace).
-cudaError_t kv_lose_parts(ts_sampler *s, int n);
-
 }  // namespace ts_host

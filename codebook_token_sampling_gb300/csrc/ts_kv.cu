@@ -149,21 +149,6 @@ const void *append_kernel(bool wide, bool rows) {
 
 }  // namespace
 
-cudaError_t ts_host::kv_lose_parts(ts_sampler *s, int n) {
-  const ts_kv_state *kv = s->kv;
-  int prev = 0;
-  cudaGetDevice(&prev);
-  cudaError_t e = cudaSetDevice(s->device);
-  if (e == cudaSuccess) e = cudaDeviceSynchronize();
-  unsigned long long calls = 0;  // all entries are equal
-  if (e == cudaSuccess) e = cudaMemcpy(&calls, kv->calls, sizeof calls, cudaMemcpyDeviceToHost);
-  const unsigned long long left = ((calls ? calls - 1 : 0) << ts::kCallShift) + static_cast<unsigned>(n);
-  for (int b = 0; b < kv->ctas && e == cudaSuccess; ++b)
-    e = cudaMemcpy(kv->arrived + b, &left, sizeof left, cudaMemcpyHostToDevice);
-  cudaSetDevice(prev);
-  return e;
-}
-
 cudaError_t ts_host::kv_free(ts_sampler *s) {
   if (!s->kv) return cudaSuccess;
   const cudaError_t e = cudaFree(s->kv->mem);
@@ -228,6 +213,22 @@ ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests) {
   }
   cudaSetDevice(prev);
   return rc;
+}
+
+ts_status ts_kv_debug_lose_parts(ts_sampler *s, int32_t come) {
+  if (!s || !s->kv || come < 0 || come > 1000) return TS_ERR_INVALID_ARG;
+  const ts_kv_state *kv = s->kv;
+  int prev = 0;
+  cudaGetDevice(&prev);
+  cudaError_t e = cudaSetDevice(s->device);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  unsigned long long calls = 0;  // all entries are equal
+  if (e == cudaSuccess) e = cudaMemcpy(&calls, kv->calls, sizeof calls, cudaMemcpyDeviceToHost);
+  const unsigned long long left = ((calls ? calls - 1 : 0) << ts::kCallShift) + static_cast<unsigned>(come);
+  for (int b = 0; b < kv->ctas && e == cudaSuccess; ++b)
+    e = cudaMemcpy(kv->arrived + b, &left, sizeof left, cudaMemcpyHostToDevice);
+  cudaSetDevice(prev);
+  return e == cudaSuccess ? TS_OK : cuda_fail(e, "ts_kv_debug_lose_parts");
 }
 
 ts_status ts_kv_tables(ts_sampler *s, const ts_kv_tables_args *t, void *stream) {

@@ -961,11 +961,6 @@ ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value) {
     s->kv_join = value;
     return TS_OK;
   }
-  if (option == TS_OPT_KV_LOST) {
-    if (value < 0 || value > 1000 || !s->kv) return TS_ERR_INVALID_ARG;
-    const cudaError_t e = ts_host::kv_lose_parts(s, value);
-    return e == cudaSuccess ? TS_OK : cuda_fail(e, "TS_OPT_KV_LOST");
-  }
   if (option == TS_OPT_FAIL_LAUNCH) {
     if (value != 0 && value != 2 && value != 3) return TS_ERR_INVALID_ARG;
     s->fail_launch = value;

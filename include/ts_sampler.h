@@ -571,6 +571,12 @@ typedef struct {
 ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged_query *q,
                              void *stream);
 
+/* For tests: leaves ts_paged_attention's counters in the workspace as a call would
+ * whose lengths changed while it ran, so that parts of its work were lost after
+ * `come` (0 .. 1000) of them had come.  Synchronises.  TS_ERR_INVALID_ARG without a
+ * workspace. */
+ts_status ts_kv_debug_lose_parts(ts_sampler *s, int32_t come);
+
 /* step[i] += 1 for i < n_streams, on the device (graph-capturable).  Call it
  * after the step's ts_sample so that sibling rows of one stream share a step
  * (or set ts_batch.advance_steps, which does the same inside the call). */
@@ -617,10 +623,6 @@ ts_status ts_read_status(ts_sampler *s, uint32_t *bits, void *stream);
 /* TS_OPT_KV_JOIN: how ts_paged_attention joins the parts of its work (0 =
  * automatic, 1 = by a launch of their own, 2 = by the last CTA to come). */
 #define TS_OPT_KV_JOIN 8
-/* TS_OPT_KV_LOST (tests only): leaves ts_paged_attention's counters in the
- * workspace as a call would whose lengths changed while it ran, so that parts of
- * its work were lost after `value` (0 .. 1000) of them had come.  Synchronises. */
-#define TS_OPT_KV_LOST 9
 ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value);
 
 /* Describes the kernel that ts_sample would launch for `b` (path 1 .. 4,

@@ -916,7 +916,7 @@ def test_attention_after_a_call_that_lost_parts(ts, sampler, kind, group):
             sampler.set_option(ts.TS_OPT_KV_CTAS, ctas)
             first = run_attention(ts, sampler, c)
             for lost in (1, 2, 5, 1000, 0):
-                sampler.set_option(ts.TS_OPT_KV_LOST, lost)
+                ts.ts_kv_debug_lose_parts(sampler.handle, lost)
                 got = run_attention(ts, sampler, c)
                 assert got[2] == 0
                 assert_attention(c, want, got[0], got[1])
@@ -929,7 +929,7 @@ def test_attention_after_a_call_that_lost_parts(ts, sampler, kind, group):
         sampler.set_option(ts.TS_OPT_KV_CTAS, 0)
     fresh = ts.Sampler(0)
     with pytest.raises(ts.SamplerError):
-        fresh.set_option(ts.TS_OPT_KV_LOST, 1)  # no workspace
+        ts.ts_kv_debug_lose_parts(fresh.handle, 1)  # no workspace
     fresh.close()
     with pytest.raises(ts.SamplerError):
-        sampler.set_option(ts.TS_OPT_KV_LOST, 1001)
+        ts.ts_kv_debug_lose_parts(sampler.handle, 1001)
