@@ -68,8 +68,13 @@ PagedKernel paged_kernel_for(int kind, int width, bool page16) {
 }
 
 // Items of up to about this many parts are joined by the last CTA to come (32
-// streams of up to 1500 tokens: 25.2 us, 27.9 with the launch), those of more by
-// a launch of their own (one request of 131,071: 50 us, 70 by the last CTA).
+// streams of up to 1500 tokens: 19.6 us, 23.7 with the launch), those of more by
+// a launch of their own (one request of 131,071: 50 us, 75 by the last CTA).  The
+// host knows no lengths: it goes by what the table's width allows and by requests
+// of equal lengths.  So few requests that are much shorter than their table take
+// the launch for nothing (four of up to 40 tokens, a table of 2048: 6.4 us, 4.5
+// without it), and one long request among short ones is joined by the last CTA
+// (131,071 tokens beside 31 times 500: 75 us, 60 with the launch).
 constexpr int kJoinHere = 10;
 
 // Per device, once: the kernels' shared-memory limits and occupancies.

@@ -365,7 +365,9 @@ constexpr int kAppendThreads = 256;
 // Units per thread and round: 4 of 16 bytes, one of the 32 or 64 bytes that make
 // 16 e4m3 values (five CTAs per SM then hide what their arithmetic takes: 65 us
 // for 65,536 tokens of 8 x 128 bf16, against 80 with two units and two CTAs;
-// three CTAs for the others: 41 us for 32,768 tokens, 46 with two or five).
+// three CTAs for the others: 41 us for 32,768 tokens, 46 with two or five).  fp32
+// tokens for an e4m3 cache hold twice the words and spill about 100 bytes a thread
+// at five CTAs: 63.6 us for 32,768 tokens, 49.4 at the rate of DRAM.
 template <class Src, int VEC>
 constexpr int kAppendUnroll = sizeof(Src) * VEC == 16 ? 4 : 1;
 

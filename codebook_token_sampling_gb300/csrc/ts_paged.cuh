@@ -7,7 +7,8 @@
 // Every key and value row is read once and serves the G query heads that
 // share it: 2 G flops per element (54 TFLOP/s for G = 8 and 2 bytes at the rate
 // of DRAM), so the bound is DRAM: 128 requests of up to 8000 tokens, 8 x 4 heads
-// of 128 in bf16, 2.1 GB, take 308 us, 7.0 TB/s.
+// of 128 in bf16, 2.1 GB, take 308 us, 7.0 TB/s.  More than 16 query heads (fp32:
+// 8) read it once per 16 (8).
 //
 // Work.  An item is one (request, key head, piece of at most kRows query
 // heads); its tokens are cut into tiles of 16 to 128 (a step of every warp), and
@@ -453,7 +454,8 @@ struct MmaCore {
     // numbers, its upper half and what is left, so that less than 2^-16 of it
     // is lost and the output's own rounding stays the largest error.  The
     // second number is kept above zero (by 2^-20 of the weight): an attended
-    // infinity in V then comes out as one, not as the NaN of 0 times it.  An
+    // infinity in V then comes out as one, not as the NaN of 0 times it (where its
+    // weight is above 2^-113 of the largest; below, both can be zero).  An
     // f16 weight (e4m3 values, which have no infinities) keeps 11 bits.  f16's
     // range is short, and many small weights may make up the output beside a
     // large one whose value is zero: so the largest is 2^kLift, at the range's
@@ -736,9 +738,15 @@ struct PagedShape {
   static constexpr int kThreads = 32 * Core::kWarps;
   static constexpr int kCost = Core::kDim > 128 ? 2 : 1;  // of an item's end, in tiles
   static constexpr uint32_t kSmem = Core::kWarps * (kRing + Core::kWarpBytes) + Core::kQBytes;
-  // CTAs per SM that the registers have to allow
+  // CTAs per SM that the registers have to allow, of those that shared memory
+  // holds.  Of four warps: four for up to eight query heads (128 registers), three
+  // for rows of 96 where four spill (72.4 us and 74.9 for e4m3, 123.9 and 124.3 for
+  // bf16, 71.0 and 81.0 for eight fp32 heads), three for sixteen heads and rows of
+  // 64 (75.8 us, 83.6 with four: e4m3), two for sixteen and wider rows (three fit
+  // rows of 96 only, and serve them better: 80.2 us against 87.2 for bf16).  Rows
+  // wider than 128 have the registers that their sums need, 168 or 256.
   static constexpr int kFit = static_cast<int>(226 * 1024 / (kSmem + 2048));
-    static constexpr int kFour = Core::kDim == 96 && (!Core::kFma || Core::kRows > 4) ? 3 : 4;
+  static constexpr int kFour = Core::kDim == 96 && (!Core::kFma || Core::kRows > 4) ? 3 : 4;
   static constexpr int kMost = (Core::kFma || Core::kRows <= 8 ? kFour : Core::kDim > 64 ? 2 : 3) * 4 / Core::kWarps;
   static constexpr int kRegs = Core::kDim <= 128 ? kMost
                                : Core::kElemBytes == 1 && Core::kRows <= 8 ? 3

@@ -56,7 +56,9 @@ class DecodeLoop:
                                             "pad_id": max(vocabs)})
         self.head = ts.LmHead(head, device)
 
-        # one block table for all layers; a cache per layer
+        # one block table for all layers; a cache per layer.  There are blocks for every
+        # stream's longest run, so no stream is ever refused one (with fewer, a step
+        # would have to look at token_starts for streams that got no token)
         wide = -(-steps // block_size)
         self.n_blocks = streams * wide
         self.tables = ts.KvTables(streams, wide, self.n_blocks, block_size, max_tokens=streams,

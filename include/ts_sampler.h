@@ -429,6 +429,13 @@ ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests);
  *   - but nothing (and the status bit TS_ROW_NO_BLOCKS) where a_i > 0 and either
  *     need_i > 0 and the needs of requests 0 .. i add up to more than the stack
  *     holds, or a_0 + .. + a_i exceeds max_tokens (finished requests count 0).
+ * The sums count what was asked for, so a request that is refused leaves none of
+ * what it asked for to those behind it in the same call.  The status bit is the
+ * call's; which requests were refused shows in token_starts: request i got
+ * token_starts[i + 1] - token_starts[i] tokens, 0 instead of a_i.  Nothing else
+ * takes notice of it: attention sees such a request's earlier tokens only, and the
+ * sampler goes on, so a caller that can run out of blocks has to hold the stream
+ * back or repeat its step.
  * The new tokens are packed in request order: request i's start at
  * token_starts[i], token_starts[n_requests] is their number, and token x has
  * slots[x], positions[x] and requests[x]; entries from that number to max_tokens
