@@ -138,9 +138,29 @@ ts_status check_cache(const ts_kv_cache *c) {
   return TS_OK;
 }
 
-// Whether [a, a + n) and [b, b + n) overlap without being the same.
-bool overlap_in_part(const int32_t *a, const int32_t *b, int64_t n) {
-  return a != b && a < b + n && b < a + n;
+// Whether an array that ts_kv_tables writes shares memory with one that it reads
+// or with another that it writes.  (Lengths and the free count may be updated in
+// place; the table's rows, which may be strided, are not looked at.)
+bool tables_overlap(const ts_kv_tables_args *t) {
+  struct Range {
+    uintptr_t at;
+    size_t bytes;
+  };
+  const size_t n = static_cast<size_t>(t->n_requests), most = static_cast<size_t>(t->max_tokens);
+  const auto range = [](const void *p, size_t bytes) {
+    return Range{reinterpret_cast<uintptr_t>(p), p ? bytes : 0};
+  };
+  const bool lens_apart = t->lens_out != t->lens, free_apart = t->n_free_out != t->n_free;
+  constexpr int kWritten = 7, kAll = 11;
+  const Range r[kAll] = {
+      range(lens_apart ? t->lens_out : nullptr, 4 * n), range(free_apart ? t->n_free_out : nullptr, 4),
+      range(t->token_starts, 4 * (n + 1)), range(t->slots, 8 * most), range(t->positions, 4 * most),
+      range(t->requests, 4 * most), range(t->free_blocks, 4 * static_cast<size_t>(t->free_len)),
+      range(t->lens, 4 * n), range(t->n_new, 4 * n), range(t->finished, n), range(t->n_free, 4)};
+  for (int i = 0; i < kWritten; ++i)
+    for (int j = i + 1; j < kAll; ++j)
+      if (r[i].bytes && r[j].bytes && r[i].at < r[j].at + r[j].bytes && r[j].at < r[i].at + r[i].bytes) return true;
+  return false;
 }
 
 template <class Src, class Dst, int VEC>
@@ -248,7 +268,7 @@ ts_status ts_kv_tables(ts_sampler *s, const ts_kv_tables_args *t, void *stream) 
   if (t->n_requests > TS_KV_MAX_REQUESTS || t->block_size > 65536 ||
       static_cast<int64_t>(t->max_blocks) * t->block_size > TS_KV_MAX_LEN)
     return TS_ERR_UNSUPPORTED;
-  if (t->lens_out && overlap_in_part(t->lens, t->lens_out, t->n_requests)) return TS_ERR_INVALID_ARG;
+  if (tables_overlap(t)) return TS_ERR_INVALID_ARG;
   if (!s->kv || s->kv->max_requests < t->n_requests) return TS_ERR_INVALID_ARG;
 
   const bool lens_in_place = !t->lens_out || t->lens_out == t->lens;

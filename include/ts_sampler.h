@@ -443,8 +443,9 @@ ts_status ts_reserve_kv(ts_sampler *s, int32_t max_requests);
  *
  * Errors.  Host side: TS_ERR_INVALID_ARG for a NULL pointer (n_new, finished,
  * lens_out, n_free_out, positions and requests may be NULL), a negative size, a
- * table_stride below max_blocks, or output arrays that overlap their inputs in
- * part; TS_ERR_UNSUPPORTED for more than TS_KV_MAX_REQUESTS requests,
+ * table_stride below max_blocks, or an output array (free_blocks among them, not
+ * the table) that overlaps an input or another output, but for lens_out = lens and
+ * n_free_out = n_free; TS_ERR_UNSUPPORTED for more than TS_KV_MAX_REQUESTS requests,
  * block_size above 65536, or max_blocks * block_size above TS_KV_MAX_LEN.  Per
  * request: a negative length or a_i, or a length beyond max_blocks blocks, sets
  * TS_ROW_BAD_SHAPE and leaves the request as it is without new tokens; a table

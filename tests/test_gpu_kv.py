@@ -231,6 +231,45 @@ def test_tables_refusals(ts, sampler):
     assert sampler.read_status() == 0
 
 
+def test_tables_overlapping_arrays(ts, sampler):
+    """An output that shares memory with an input or another output is refused;
+    arrays side by side, and lengths and free count in place, are not."""
+    import torch
+    n, most = 6, 8
+
+    def make(**at):
+        t = ts.KvTables(n, 3, 18, 16, max_tokens=most, double=True, n_new=torch.ones(n, dtype=torch.int32, device="cuda"),
+                        finished=torch.zeros(n, dtype=torch.uint8, device="cuda"))
+        for name, value in at.items():
+            setattr(t.c, name, value(t))
+        return t
+    outs = {"lens_out": 4 * n, "n_free_out": 4, "token_starts": 4 * (n + 1), "slots": 8 * most, "positions": 4 * most,
+            "requests": 4 * most, "free_blocks": 4 * 18}
+    ins = {"lens": 4 * n, "n_new": 4 * n, "finished": n, "n_free": 4}
+    sampler.read_status()
+    for out in outs:
+        for other, size in {**ins, **outs}.items():
+            if other == out:
+                continue
+            inside = [0, size - 1 & ~7] if out == "slots" else [0, size - 1 & ~3]
+            for by in inside:
+                if by == 0 and (out, other) in (("lens_out", "lens"), ("n_free_out", "n_free")):
+                    continue
+                with pytest.raises(ts.SamplerError) as e:
+                    ts.ts_kv_tables(sampler.handle, make(**{out: lambda t, b=by: getattr(t.c, other) + b}))
+                assert e.value.status == ts.TS_ERR_INVALID_ARG, (out, other, by)
+    whole = torch.zeros(64, dtype=torch.int32, device="cuda")  # one array after the other
+    at = whole.data_ptr()
+    for t in (make(lens_out=lambda t: t.c.lens, n_free_out=lambda t: t.c.n_free),
+              make(lens_out=lambda t: at, token_starts=lambda t: at + 4 * n, positions=lambda t: at + 4 * (2 * n + 1),
+                   requests=lambda t: at + 4 * (2 * n + 1 + most), n_free_out=lambda t: at + 4 * (2 * n + 1 + 2 * most))):
+        ts.ts_kv_tables(sampler.handle, t)
+    torch.cuda.synchronize()
+    want = [1] * n + list(range(n + 1)) + [0] * n + [-1] * 2 + list(range(n)) + [-1] * 2 + [12]
+    assert whole.tolist()[:len(want)] == want and not whole[len(want):].any()
+    assert sampler.read_status() == 0
+
+
 # --------------------------------------------------------------------------
 # Cache writes (bits: equal)
 # --------------------------------------------------------------------------
