@@ -9,13 +9,16 @@ only for device memory and streams.  The functions keep the C names:
     ts_read_status, ts_set_option, ts_plan, ts_status_string, ts_last_error,
     ts_lm_head_logits, ts_lm_head_sample, ts_sample_host,
     ts_reserve_kv, ts_kv_tables, ts_kv_append, ts_paged_attention,
-    ts_kv_debug_lose_parts
+    ts_kv_debug_lose_parts,
+    ts_rms_norm, ts_gate, ts_linear_e4m3, ts_rotary, ts_kv_append_rotary,
+    ts_rotary_frequencies
 
 ``Sampler`` wraps a handle; ``DeviceBatch`` holds one step's per-row arrays on
 the GPU with a prebuilt ``ts_batch`` so that repeated calls marshal nothing;
 ``LmHead`` holds a frame's hidden states and output heads with a prebuilt
 ``ts_lm_head``; ``KvTables``, ``KvCache``, ``KvTokens`` and ``PagedQuery`` do the
-same for the paged key-value cache's calls.
+same for the paged key-value cache's calls, ``RmsNorm``, ``Gate``,
+``LinearE4m3`` and ``Rotary`` for the layer operators around it.
 Importing this module loads the compiled library and raises if it is missing;
 there is no fallback.
 """
@@ -43,6 +46,7 @@ TS_ROW_BAD_SLOT = 8
 TS_ROW_NOT_READY = 16
 TS_ROW_BAD_BLOCK = 32
 TS_ROW_NO_BLOCKS = 64
+TS_ROW_STALLED = 128
 TS_OPT_PATH = 1
 TS_OPT_CLUSTER = 2
 TS_OPT_PDL = 3
@@ -51,6 +55,7 @@ TS_OPT_WARPS_PER_ROW = 5
 TS_OPT_FAIL_LAUNCH = 6
 TS_OPT_KV_CTAS = 7
 TS_OPT_KV_JOIN = 8
+TS_OPT_LINEAR_SPLIT = 9
 TS_MAX_VOCAB_BF16 = 163840
 TS_MAX_VOCAB_F32 = 81920
 TS_NOALLOC_SCRATCH_BYTES = 4194304
@@ -61,13 +66,28 @@ TS_KV_MAX_REQUESTS = 8192
 TS_KV_MAX_LEN = 2147482624
 TS_KV_MAX_HEAD_DIM = 256
 TS_KV_MAX_HEADS = 65536
+TS_SCALE_BLOCK = 128
+TS_NORM_MAX_DIM = 32768
+TS_GATE_MAX_DIM = 1048576
+TS_LINEAR_MAX_DIM = 1048576
+TS_ROTARY_MAX_HEAD_DIM = 1024
+TS_ACT_NONE = 0
+TS_ACT_SILU = 1
+TS_ACT_GELU = 2
+TS_ACT_GELU_TANH = 3
+TS_ROPE_PLAIN = 0
+TS_ROPE_LINEAR = 1
+TS_ROPE_NTK = 2
+TS_ROPE_BY_PARTS = 3
 
 EXPORTED = ("ts_create", "ts_destroy", "ts_max_top_k", "ts_sample", "ts_sample_debug",
             "ts_sample_steps", "ts_reserve", "ts_sample_noalloc", "ts_advance_steps",
             "ts_read_status", "ts_set_option", "ts_plan", "ts_status_string", "ts_last_error",
             "ts_lm_head_logits", "ts_lm_head_sample", "ts_sample_host",
             "ts_reserve_kv", "ts_kv_tables", "ts_kv_append", "ts_paged_attention",
-             "ts_kv_debug_lose_parts")
+             "ts_kv_debug_lose_parts",
+            "ts_rms_norm", "ts_gate", "ts_linear_e4m3", "ts_rotary", "ts_kv_append_rotary",
+            "ts_rotary_frequencies")
 
 
 class TsBatch(ctypes.Structure):
@@ -220,6 +240,92 @@ class TsPagedQuery(ctypes.Structure):
     ]
 
 
+class TsNorm(ctypes.Structure):
+    """Mirror of ``ts_norm_args``."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("residual_out", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_scale", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("n_rows", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64),
+        ("residual_out_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("out_scale_stride", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+    ]
+
+
+class TsGate(ctypes.Structure):
+    """Mirror of ``ts_gate_args``."""
+    _fields_ = [
+        ("up", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_scale", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("n_rows", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("up_stride", ctypes.c_int64),
+        ("gate_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("out_scale_stride", ctypes.c_int64),
+    ]
+
+
+class TsLinear(ctypes.Structure):
+    """Mirror of ``ts_linear_args``."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("x_scale", ctypes.c_void_p),
+        ("w", ctypes.c_void_p),
+        ("w_scale", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_dtype", ctypes.c_int32),
+        ("n_rows", ctypes.c_int32),
+        ("in_dim", ctypes.c_int32),
+        ("out_dim", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+        ("x_scale_stride", ctypes.c_int64),
+        ("w_stride", ctypes.c_int64),
+        ("w_scale_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+    ]
+
+
+class TsRotary(ctypes.Structure):
+    """Mirror of ``ts_rotary_args``."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("x_token_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64),
+        ("out_token_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int32),
+        ("amplitude", ctypes.c_float),
+        ("freqs", ctypes.c_void_p),
+    ]
+
+
 class SamplerError(RuntimeError):
     def __init__(self, status: int, what: str):
         detail = _lib.ts_last_error().decode() if status == TS_ERR_CUDA else ""
@@ -259,6 +365,14 @@ def _load(path: str):
         "ts_paged_attention": ([vp, ctypes.POINTER(TsKvCache), ctypes.POINTER(TsPagedQuery), vp],
                                ctypes.c_int),
         "ts_kv_debug_lose_parts": ([vp, i32], ctypes.c_int),
+        "ts_rms_norm": ([vp, ctypes.POINTER(TsNorm), vp], ctypes.c_int),
+        "ts_gate": ([vp, ctypes.POINTER(TsGate), vp], ctypes.c_int),
+        "ts_linear_e4m3": ([vp, ctypes.POINTER(TsLinear), vp], ctypes.c_int),
+        "ts_rotary": ([vp, ctypes.POINTER(TsRotary), vp], ctypes.c_int),
+        "ts_kv_append_rotary": ([vp, ctypes.POINTER(TsKvCache), ctypes.POINTER(TsKvTokens),
+                                 ctypes.POINTER(TsRotary), vp], ctypes.c_int),
+        "ts_rotary_frequencies": ([vp, i32] + [ctypes.c_double, i32] + [ctypes.c_double] * 4
+                                  + [ctypes.POINTER(ctypes.c_float)], ctypes.c_int),
         "ts_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "ts_last_error": ([], ctypes.c_char_p),
     }
@@ -433,6 +547,52 @@ def ts_paged_attention(handle: int, cache: "KvCache", query: "PagedQuery", strea
 def ts_kv_debug_lose_parts(handle: int, come: int) -> None:
     """For tests: the workspace's counters as a call leaves them that lost parts."""
     _check(_lib.ts_kv_debug_lose_parts(handle, come), "ts_kv_debug_lose_parts")
+
+
+def ts_rms_norm(handle: int, norm: "RmsNorm", stream=None) -> None:
+    """The residual's sum, its root-mean-square norm and 8-bit rows of it (see the header)."""
+    _check(_lib.ts_rms_norm(handle, ctypes.byref(norm.c), _stream_ptr(stream)), "ts_rms_norm")
+
+
+def ts_gate(handle: int, gate: "Gate", stream=None) -> None:
+    """A gated activation, or only the rounding to 8-bit rows (see the header)."""
+    _check(_lib.ts_gate(handle, ctypes.byref(gate.c), _stream_ptr(stream)), "ts_gate")
+
+
+def ts_linear_e4m3(handle: int, linear: "LinearE4m3", stream=None) -> None:
+    """The product of 8-bit rows and 8-bit weights with block scales (see the header)."""
+    _check(_lib.ts_linear_e4m3(handle, ctypes.byref(linear.c), _stream_ptr(stream)), "ts_linear_e4m3")
+
+
+def ts_rotary(handle: int, rotary: "Rotary", stream=None) -> None:
+    """Rotary positions of one tensor's heads (see the header)."""
+    _check(_lib.ts_rotary(handle, ctypes.byref(rotary.c), _stream_ptr(stream)), "ts_rotary")
+
+
+def ts_kv_append_rotary(handle: int, cache: "KvCache", tokens: "KvTokens", rotary: "Rotary",
+                        stream=None) -> None:
+    """``ts_rotary`` of the queries and ``ts_kv_append`` of the same tokens, whose keys
+    are turned alike, in one launch.  Tokens have the cache's heads, row width and
+    device, queries its row width and device (ValueError)."""
+    if tokens.rows_of != cache.rows_of:
+        raise ValueError(f"tokens of {tokens.rows_of} for a cache of {cache.rows_of}")
+    if rotary.rows_of != cache.rows_of[1:]:
+        raise ValueError(f"queries of {rotary.rows_of} for a cache of {cache.rows_of[1:]}")
+    _check(_lib.ts_kv_append_rotary(handle, ctypes.byref(cache.c), ctypes.byref(tokens.c),
+                                    ctypes.byref(rotary.c), _stream_ptr(stream)), "ts_kv_append_rotary")
+
+
+def ts_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = TS_ROPE_PLAIN, *,
+                          factor: float = 1.0, original_len: float = 1.0, low: float = 1.0,
+                          high: float = 32.0):
+    """The frequencies that ``Rotary`` takes, as a float64 array on the host, and the
+    amplitude that belongs to them (see the header)."""
+    _need(0 < rotary_dim <= TS_ROTARY_MAX_HEAD_DIM, "rotary_dim: from 2 to a head's largest width")
+    freqs = np.zeros(max(1, rotary_dim // 2), np.float64)
+    amplitude = ctypes.c_float()
+    _check(_lib.ts_rotary_frequencies(freqs.ctypes.data, rotary_dim, base, scaling, factor, original_len,
+                                      low, high, ctypes.byref(amplitude)), "ts_rotary_frequencies")
+    return freqs, float(amplitude.value)
 
 
 def ts_status_string(status: int) -> str:
@@ -881,3 +1041,144 @@ class PagedQuery:
         self.lens = lens
         self.c.lens = _vector(lens, self.c.n_requests, torch.int32, self.q.device,
                               "lens: int32 [n_requests]")
+
+
+# --------------------------------------------------------------------------
+# The layer operators around it
+# --------------------------------------------------------------------------
+def _rows_of(t, shape, dtypes, device, what: str):
+    """``t``: rows of contiguous elements [n, dim] of one of ``dtypes`` on ``device``,
+    which do not overlap; its address and row stride (a single row's says nothing)."""
+    _need(t.dim() == 2 and tuple(t.shape) == tuple(shape) and t.dtype in dtypes and t.device == device, what)
+    n, dim = t.shape
+    _need((dim < 2 or t.stride(1) == 1) and (n < 2 or t.stride(0) >= dim), f"{what}: contiguous rows of their own")
+    return t.data_ptr(), t.stride(0) if n > 1 else dim
+
+
+def _scales_of(t, n: int, dim: int, out, what: str):
+    """The scales of 8-bit rows ``out`` of ``n`` x ``dim``, which other types do not have."""
+    import torch
+    _need((t is not None) == (out.dtype == torch.float8_e4m3fn), f"{what}: for 8-bit rows, and only for them")
+    blocks = -(-dim // TS_SCALE_BLOCK)
+    return (None, 0) if t is None else _rows_of(t, (n, blocks), (torch.float32,), out.device,
+                                                f"{what}: float32 [n_rows, {blocks}]")
+
+
+class RmsNorm:
+    """``out`` [n, dim] = the root-mean-square norm of ``x`` (+ ``residual``, whose sum
+    goes to ``residual_out``) times ``weight`` (+ ``weight_offset``), with a prebuilt
+    ``ts_norm_args``.  ``x`` and ``residual`` are bfloat16 or float32, ``weight`` [dim]
+    either; ``out`` is one of the two, or float8_e4m3fn with ``out_scale`` (float32
+    [n, ceil(dim / 128)]).  Rows may be strided; ``residual_out`` may be ``residual`` or
+    ``x``, ``out`` may be ``x``."""
+
+    def __init__(self, x, out, weight=None, *, residual=None, residual_out=None, out_scale=None,
+                 eps: float = 1e-6, weight_offset: float = 0.0):
+        import torch
+        real = (torch.float32, torch.bfloat16)
+        _need(x.dim() == 2, "x: [n_rows, dim]")
+        n, dim = x.shape
+        self.x, self.out, self.weight, self.out_scale = x, out, weight, out_scale
+        self.residual, self.residual_out = residual, residual_out
+        c = TsNorm()
+        c.x, c.x_stride = _rows_of(x, (n, dim), real, x.device, "x: bfloat16 or float32 [n_rows, dim]")
+        for name, t in (("residual", residual), ("residual_out", residual_out)):
+            if t is not None:
+                at, stride = _rows_of(t, (n, dim), (x.dtype,), x.device, f"{name}: as x")
+                setattr(c, name, at)
+                setattr(c, name + "_stride", stride)
+        c.out, c.out_stride = _rows_of(out, (n, dim), (*real, torch.float8_e4m3fn), x.device, "out: [n_rows, dim]")
+        c.out_scale, c.out_scale_stride = _scales_of(out_scale, n, dim, out, "out_scale")
+        if weight is not None:
+            _need(weight.dtype in real, "weight: bfloat16 or float32")
+            c.weight = _vector(weight, dim, weight.dtype, x.device, "weight: [dim]")
+            c.weight_dtype = _kv_dtype(weight)
+        c.dtype, c.out_dtype = _kv_dtype(x), _kv_dtype(out)
+        c.n_rows, c.dim = n, dim
+        c.eps, c.weight_offset = eps, weight_offset
+        self.c = c
+
+
+class Gate:
+    """``out`` [n, dim] = activation(``gate``) * ``up``, with a prebuilt ``ts_gate_args``;
+    ``activation`` is "silu", "gelu", "gelu_tanh", or "none" (``out`` = ``up``, without a
+    gate).  ``up`` and ``gate`` are bfloat16 or float32, e.g. the halves of one product's
+    rows; ``out`` is one of the two, or float8_e4m3fn with ``out_scale`` (float32
+    [n, ceil(dim / 128)])."""
+
+    ACTIVATIONS = {"none": TS_ACT_NONE, "silu": TS_ACT_SILU, "gelu": TS_ACT_GELU, "gelu_tanh": TS_ACT_GELU_TANH}
+
+    def __init__(self, up, out, gate=None, *, activation: str = "silu", out_scale=None):
+        import torch
+        real = (torch.float32, torch.bfloat16)
+        _need(activation in self.ACTIVATIONS, f"activation: one of {', '.join(self.ACTIVATIONS)}")
+        _need((gate is None) == (activation == "none"), "gate: with an activation, and only with one")
+        _need(up.dim() == 2, "up: [n_rows, dim]")
+        n, dim = up.shape
+        self.up, self.gate, self.out, self.out_scale = up, gate, out, out_scale
+        c = TsGate()
+        c.up, c.up_stride = _rows_of(up, (n, dim), real, up.device, "up: bfloat16 or float32 [n_rows, dim]")
+        if gate is not None:
+            c.gate, c.gate_stride = _rows_of(gate, (n, dim), (up.dtype,), up.device, "gate: as up")
+        c.out, c.out_stride = _rows_of(out, (n, dim), (*real, torch.float8_e4m3fn), up.device, "out: [n_rows, dim]")
+        c.out_scale, c.out_scale_stride = _scales_of(out_scale, n, dim, out, "out_scale")
+        c.dtype, c.out_dtype, c.act = _kv_dtype(up), _kv_dtype(out), self.ACTIVATIONS[activation]
+        c.n_rows, c.dim = n, dim
+        self.c = c
+
+
+class LinearE4m3:
+    """``out`` [n, out_dim] = ``x`` [n, in_dim] times ``w`` [out_dim, in_dim] transposed,
+    both float8_e4m3fn with float32 scales, ``x_scale`` for each row's 128 elements [n,
+    ceil(in_dim / 128)] and ``w_scale`` for each 128 x 128 of the weights; ``out`` is
+    bfloat16 or float32.  With a prebuilt ``ts_linear_args``."""
+
+    def __init__(self, x, x_scale, w, w_scale, out):
+        import torch
+        e4m3, f32 = (torch.float8_e4m3fn,), (torch.float32,)
+        _need(x.dim() == 2 and w.dim() == 2, "x: [n_rows, in_dim], w: [out_dim, in_dim]")
+        n, k = x.shape
+        m = w.shape[0]
+        blocks = -(-k // TS_SCALE_BLOCK)
+        self.x, self.x_scale, self.w, self.w_scale, self.out = x, x_scale, w, w_scale, out
+        c = TsLinear()
+        c.x, c.x_stride = _rows_of(x, (n, k), e4m3, x.device, "x: float8_e4m3fn [n_rows, in_dim]")
+        c.x_scale, c.x_scale_stride = _rows_of(x_scale, (n, blocks), f32, x.device, f"x_scale: float32 [n_rows, {blocks}]")
+        c.w, c.w_stride = _rows_of(w, (m, k), e4m3, x.device, "w: float8_e4m3fn [out_dim, in_dim]")
+        c.w_scale, c.w_scale_stride = _rows_of(w_scale, (-(-m // TS_SCALE_BLOCK), blocks), f32, x.device,
+                                               f"w_scale: float32 [ceil(out_dim / 128), {blocks}]")
+        c.out, c.out_stride = _rows_of(out, (n, m), (torch.bfloat16, torch.float32), x.device,
+                                       "out: bfloat16 or float32 [n_rows, out_dim]")
+        c.out_dtype, c.n_rows, c.in_dim, c.out_dim = _kv_dtype(out), n, k, m
+        self.c = c
+
+
+class Rotary:
+    """Rotary positions of the heads ``x`` [n_rows, n_heads, head_dim] (bfloat16 or float32,
+    any strides with head_dim contiguous) to ``out`` (which may be ``x``), with a prebuilt
+    ``ts_rotary_args``.  Token t is row t, or with ``rows`` (int32) row ``rows[t]``;
+    ``positions`` (int32) below 0 skip it.  ``freqs`` (float64 [rotary_dim / 2] on the
+    device, see ``ts_rotary_frequencies``) gives the width that is turned; ``interleaved``
+    pairs neighbours instead of halves."""
+
+    def __init__(self, x, out, positions, freqs, *, rows=None, interleaved: bool = False,
+                 amplitude: float = 1.0):
+        import torch
+        _need(x.dim() == 3 and x.shape == out.shape and x.dtype == out.dtype and x.device == out.device,
+              "x and out: [n_rows, n_heads, head_dim] of one type")
+        _need(x.dtype in (torch.float32, torch.bfloat16), "x and out: bfloat16 or float32")
+        _need(x.shape[2] < 2 or (x.stride(2) == 1 and out.stride(2) == 1), "x and out: head_dim is contiguous")
+        _need(freqs.dim() == 1 and 0 < 2 * freqs.numel() <= x.shape[2], "freqs: [rotary_dim / 2], at most head_dim / 2")
+        self.x, self.out, self.positions, self.freqs, self.rows = x, out, positions, freqs, rows
+        self.rows_of = (x.shape[2], x.device)
+        c = TsRotary()
+        c.x, c.out, c.dtype = x.data_ptr(), out.data_ptr(), _kv_dtype(x)
+        c.n_rows, c.n_heads, c.head_dim = x.shape
+        c.n_tokens = x.shape[0] if rows is None else rows.numel()
+        c.rotary_dim, c.interleaved, c.amplitude = 2 * freqs.numel(), int(interleaved), amplitude
+        c.x_token_stride, c.x_head_stride = _strides(x)
+        c.out_token_stride, c.out_head_stride = _strides(out)
+        c.positions = _vector(positions, c.n_tokens, torch.int32, x.device, "positions: int32 [n_tokens]")
+        c.rows = _vector(rows, c.n_tokens, torch.int32, x.device, "rows: int32 [n_tokens]")
+        c.freqs = _vector(freqs, freqs.numel(), torch.float64, x.device, "freqs: float64 [rotary_dim / 2]")
+        self.c = c

@@ -30,6 +30,7 @@ struct ts_sampler {
   struct ts_kv_state *kv;  // the paged cache's workspace (ts_reserve_kv), or null
   int kv_ctas;        // paged attention: 0 auto, else its number of CTAs (testing)
   int kv_join;        // 0 auto, 1 joins by a launch of their own, 2 by the last CTA (testing)
+  int linear_split;   // ts_linear_e4m3: 0 auto, else the CTAs that share a tile (testing)
 };
 
 namespace ts_host {
@@ -39,5 +40,38 @@ ts_status cuda_fail(cudaError_t e, const char *what);
 
 // Frees the paged cache's workspace (the device is current).
 cudaError_t kv_free(ts_sampler *s);
+
+// Once per ts_create, on the current device: what ts_linear_e4m3 needs of it.
+ts_status linear_setup();
+
+// One launch, with programmatic dependent launch if `pdl`.
+cudaError_t launch(const void *fn, dim3 grid, dim3 block, size_t smem, bool pdl, cudaStream_t st, void **args);
+
+inline int size_of(int dtype) { return dtype == TS_DTYPE_F32 ? 4 : dtype == TS_DTYPE_BF16 ? 2 : 1; }
+inline bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+// A cache write's sizes, strides and types (ts_kv_append), then its arrays.
+ts_status check_append(const ts_kv_cache *c, const ts_kv_tokens *t);
+ts_status check_append_arrays(const ts_kv_tokens *t);
+
+// The bytes of an array of rows (none for NULL).
+struct Span {
+  uintptr_t from, to;     // of the first element, behind the last
+  uintptr_t pitch, wide;  // from row to row (0: one row), and of a row
+  // Whether two arrays share bytes.  Columns of one buffer side by side do not; arrays
+  // of different pitch that lie within one another count as if they did.
+  bool meets(const Span &o) const {
+    if (from >= o.to || o.from >= to) return false;
+    if (!pitch || pitch != o.pitch) return true;
+    const uintptr_t shift = (o.from >= from ? o.from - from : pitch - (from - o.from) % pitch) % pitch;
+    return shift < wide || shift + o.wide > pitch;
+  }
+};
+inline Span rows_span(const void *p, int64_t rows, int64_t dim, int64_t stride, int64_t es) {
+  if (!p || rows < 1) return {0, 0, 0, 0};
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uintptr_t pitch = rows > 1 ? static_cast<uintptr_t>(stride * es) : 0, wide = static_cast<uintptr_t>(dim * es);
+  return {at, at + static_cast<uintptr_t>(rows - 1) * pitch + wide, pitch, wide};
+}
 
 }  // namespace ts_host

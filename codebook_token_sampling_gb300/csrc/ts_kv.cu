@@ -32,31 +32,14 @@ struct ts_kv_state {
 
 namespace {
 
+using ts_host::aligned;
 using ts_host::cuda_fail;
+using ts_host::launch;
+using ts_host::size_of;
 using ts_host::PagedKernel;
 using ts_host::paged_kernel_bf16;
 using ts_host::paged_kernel_e4m3;
 using ts_host::paged_kernel_f32;
-
-cudaError_t launch(const void *fn, dim3 grid, int threads, size_t smem, bool pdl, cudaStream_t st,
-                   void **args) {
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelExC(&cfg, fn, args);
-}
-
-int size_of(int dtype) { return dtype == TS_DTYPE_F32 ? 4 : dtype == TS_DTYPE_BF16 ? 2 : 1; }
-
-bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
 // --------------------------------------------------------------------------
 // Paged attention's kernels
@@ -173,6 +156,37 @@ const void *append_kernel(bool wide, bool rows) {
 }
 
 }  // namespace
+
+cudaError_t ts_host::launch(const void *fn, dim3 grid, dim3 block, size_t smem, bool pdl, cudaStream_t st,
+                            void **args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+ts_status ts_host::check_append(const ts_kv_cache *c, const ts_kv_tokens *t) {
+  const ts_status rc = check_cache(c);
+  if (rc != TS_OK) return rc;
+  if (t->n_tokens < 0 || (t->rows && t->n_rows < 0) || (t->dtype != TS_DTYPE_F32 && t->dtype != TS_DTYPE_BF16))
+    return TS_ERR_INVALID_ARG;
+  if (t->k_token_stride < 0 || t->k_head_stride < 0 || t->v_token_stride < 0 || t->v_head_stride < 0)
+    return TS_ERR_INVALID_ARG;
+  return c->dtype != t->dtype && c->dtype != TS_DTYPE_E4M3 ? TS_ERR_UNSUPPORTED : TS_OK;
+}
+
+ts_status ts_host::check_append_arrays(const ts_kv_tokens *t) {
+  const size_t es = static_cast<size_t>(size_of(t->dtype));
+  return !t->k || !t->v || !t->slots || !aligned(t->k, es) || !aligned(t->v, es) ? TS_ERR_INVALID_ARG : TS_OK;
+}
 
 cudaError_t ts_host::kv_free(ts_sampler *s) {
   if (!s->kv) return cudaSuccess;
@@ -331,17 +345,12 @@ ts_status ts_kv_tables(ts_sampler *s, const ts_kv_tables_args *t, void *stream) 
 
 ts_status ts_kv_append(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *t, void *stream) {
   if (!s || !t) return TS_ERR_INVALID_ARG;
-  const ts_status rc = check_cache(c);
+  ts_status rc = ts_host::check_append(c, t);
   if (rc != TS_OK) return rc;
-  if (t->n_tokens < 0 || (t->rows && t->n_rows < 0) || (t->dtype != TS_DTYPE_F32 && t->dtype != TS_DTYPE_BF16))
-    return TS_ERR_INVALID_ARG;
-  if (t->k_token_stride < 0 || t->k_head_stride < 0 || t->v_token_stride < 0 || t->v_head_stride < 0)
-    return TS_ERR_INVALID_ARG;
-  if (c->dtype != t->dtype && c->dtype != TS_DTYPE_E4M3) return TS_ERR_UNSUPPORTED;
   if (t->n_tokens == 0) return TS_OK;
+  rc = ts_host::check_append_arrays(t);
+  if (rc != TS_OK) return rc;
   const int es = size_of(t->dtype);
-  if (!t->k || !t->v || !t->slots || !aligned(t->k, es) || !aligned(t->v, es))
-    return TS_ERR_INVALID_ARG;
 
   const int vec = c->dtype == TS_DTYPE_E4M3 ? 16 : 16 / es;
   const bool wide = aligned(t->k, 16) && aligned(t->v, 16) && t->k_token_stride * es % 16 == 0 &&

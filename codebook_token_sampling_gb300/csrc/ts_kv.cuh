@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "ts_e4m3.cuh"
 #include "ts_kv_common.cuh"
 
 namespace ts {
@@ -403,23 +404,6 @@ __device__ __forceinline__ uint4 e4m3x16_of(const float (&y)[16]) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// y = x / scale correctly rounded, given inv = 1 / scale correctly rounded:
-// Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor" (1990): with q within a unit of the quotient, q + (x - q scale) inv
-// rounds to it where nothing over- or underflows.  The sign is q's, for zeros.
-// Returns whether it serves: the scales that quotient_inverse gives an inverse
-// for lie within 2^-90 .. 2^90, so x - q scale underflows only where the quotient
-// rounds to an e4m3 zero, and quotients of 2^20 and more, infinite and NaN ones
-// are left to the division.
-__device__ __forceinline__ bool quotient(float x, float scale, float inv, float &y) {
-  const float q = x * inv;
-  y = copysignf(fmaf(fmaf(-q, scale, x), inv, q), q);
-  return fabsf(q) < 0x1p20f;
-}
-__device__ __forceinline__ float quotient_inverse(float scale) {
-  const float a = fabsf(scale);
-  return a >= 0x1p-90f && a <= 0x1p90f ? __fdiv_rn(1.0f, scale) : 0.0f;
-}
 // The rare values by division (out of line: the common ones keep the
 // instruction cache).
 __device__ __noinline__ uint4 divided_e4m3x16(const float *x, float scale) {

@@ -1,0 +1,376 @@
+// ts_layer.cu -- host side of the layer operators that work row by row (ts_rms_norm,
+// ts_gate, ts_rotary, ts_kv_append_rotary): argument checks, kernel choice and
+// launches on the caller's stream; and the rotary frequencies.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "ts_gate.cuh"
+#include "ts_host.h"
+#include "ts_norm.cuh"
+#include "ts_rotary.cuh"
+
+static_assert(ts::kScaleBlock == TS_SCALE_BLOCK, "8-bit rows");
+static_assert(ts::kActNone == TS_ACT_NONE && ts::kActSilu == TS_ACT_SILU && ts::kActGelu == TS_ACT_GELU &&
+                  ts::kActGeluTanh == TS_ACT_GELU_TANH, "activations");
+
+namespace {
+
+using ts_host::aligned;
+using ts_host::cuda_fail;
+using ts_host::launch;
+using ts_host::rows_span;
+using ts_host::size_of;
+using ts_host::Span;
+
+bool real_type(int32_t dtype) { return dtype == TS_DTYPE_F32 || dtype == TS_DTYPE_BF16; }
+bool out_type(int32_t dtype) { return real_type(dtype) || dtype == TS_DTYPE_E4M3; }
+int64_t scales_of(int64_t dim) { return (dim + TS_SCALE_BLOCK - 1) / TS_SCALE_BLOCK; }
+
+// An array of rows: where it is, its stride and its elements' size.
+struct Rows {
+  const void *p;
+  int64_t stride;
+  int es;
+};
+// Whether rows of `dim` can be moved in pieces of eight elements.
+bool in_pieces(const Rows &r, int64_t n_rows) {
+  const int64_t to = r.es == 1 ? 8 : 16;
+  return aligned(r.p, static_cast<size_t>(to)) && (n_rows == 1 || r.stride * r.es % to == 0);
+}
+
+// --------------------------------------------------------------------------
+// Norm
+// --------------------------------------------------------------------------
+template <class Src, class Out>
+const void *norm_kernel(int v, bool wide) {
+  if (wide)
+    return v == 1 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 1, true>)
+         : v == 2 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 2, true>)
+                  : reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 4, true>);
+  return v == 1 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 1, false>)
+       : v == 2 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 2, false>)
+       : v == 4 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 4, false>)
+                : reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 8, false>);
+}
+template <class Src>
+const void *norm_kernel_to(int32_t out, int v, bool wide) {
+  return out == TS_DTYPE_F32 ? norm_kernel<Src, float>(v, wide)
+       : out == TS_DTYPE_BF16 ? norm_kernel<Src, uint16_t>(v, wide) : norm_kernel<Src, uint8_t>(v, wide);
+}
+
+// --------------------------------------------------------------------------
+// Gate
+// --------------------------------------------------------------------------
+template <class Src>
+const void *gate_kernel_to(int32_t out, bool wide) {
+  if (wide)
+    return out == TS_DTYPE_F32 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, float, true>)
+         : out == TS_DTYPE_BF16 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, uint16_t, true>)
+                                : reinterpret_cast<const void *>(ts::gate_kernel<Src, uint8_t, true>);
+  return out == TS_DTYPE_F32 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, float, false>)
+       : out == TS_DTYPE_BF16 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, uint16_t, false>)
+                              : reinterpret_cast<const void *>(ts::gate_kernel<Src, uint8_t, false>);
+}
+
+// --------------------------------------------------------------------------
+// Rotary positions
+// --------------------------------------------------------------------------
+template <class Src, class Dst, bool CACHE>
+const void *rotary_kernel(int piece) {
+  return piece == 8 ? reinterpret_cast<const void *>(ts::rotary_kernel<Src, Dst, 8, CACHE>)
+       : piece == 4 ? reinterpret_cast<const void *>(ts::rotary_kernel<Src, Dst, 4, CACHE>)
+                    : reinterpret_cast<const void *>(ts::rotary_kernel<Src, Dst, 1, CACHE>);
+}
+
+ts_status check_rotary(const ts_rotary_args *a) {
+  if (!a || a->n_tokens < 0 || a->head_dim < 1 || a->rotary_dim < 2 || a->rotary_dim % 2 ||
+      a->rotary_dim > a->head_dim || !real_type(a->dtype) || (a->rows && a->n_rows < 0) || !std::isfinite(a->amplitude))
+    return TS_ERR_INVALID_ARG;
+  for (int64_t x : {a->x_token_stride, a->x_head_stride, a->out_token_stride, a->out_head_stride})
+    if (x < 0) return TS_ERR_INVALID_ARG;
+  if (a->head_dim > TS_ROTARY_MAX_HEAD_DIM || a->n_heads > TS_KV_MAX_HEADS) return TS_ERR_UNSUPPORTED;
+  return TS_OK;
+}
+ts_status check_rotary_arrays(const ts_rotary_args *a, bool queries) {
+  const int es = size_of(a->dtype);
+  if (!a->positions || !a->freqs || !aligned(a->freqs, 8)) return TS_ERR_INVALID_ARG;
+  if (!queries) return TS_OK;
+  if (!a->x || !a->out || !aligned(a->x, es) || !aligned(a->out, es)) return TS_ERR_INVALID_ARG;
+  if (a->x == a->out && (a->x_token_stride != a->out_token_stride || a->x_head_stride != a->out_head_stride))
+    return TS_ERR_INVALID_ARG;
+  return TS_OK;
+}
+// The largest piece (8, 4 or 1 elements) that divides the pairs and the head and that
+// addresses and strides allow.
+int piece_of(const ts_rotary_args *a, const ts_kv_tokens *t, bool queries) {
+  const int es = size_of(a->dtype);
+  const auto fits = [&](int piece) {
+    if (a->rotary_dim / 2 % piece || a->head_dim % piece) return false;
+    const int64_t to = std::min(16, piece * es);
+    const auto ok = [&](const void *p, int64_t token, int64_t head) {
+      return aligned(p, static_cast<size_t>(to)) && token * es % to == 0 && head * es % to == 0;
+    };
+    if (queries && (!ok(a->x, a->x_token_stride, a->x_head_stride) || !ok(a->out, a->out_token_stride, a->out_head_stride)))
+      return false;
+    return !t || (ok(t->k, t->k_token_stride, t->k_head_stride) && ok(t->v, t->v_token_stride, t->v_head_stride));
+  };
+  return fits(8) ? 8 : fits(4) ? 4 : 1;
+}
+
+// The parts of the parameters that both calls share, and the launch.
+ts_status launch_rotary(const ts_sampler *s, const ts_rotary_args *a, ts::RotaryParams &p, const void *fn, int piece,
+                        void *stream) {
+  const bool queries = a->x != nullptr;
+  p.x = a->x;
+  p.out = a->out;
+  p.x_token = a->x_token_stride;
+  p.x_head = a->x_head_stride;
+  p.out_token = a->out_token_stride;
+  p.out_head = a->out_head_stride;
+  p.positions = a->positions;
+  p.rows = a->rows;
+  p.freqs = a->freqs;
+  p.amplitude = a->amplitude;
+  p.n_tokens = a->n_tokens;
+  p.n_rows = a->n_rows;
+  p.heads = queries ? a->n_heads : 0;
+  p.dim = a->head_dim;
+  p.half = a->rotary_dim / 2;
+  p.interleaved = a->interleaved != 0;
+  p.in_place = a->x == a->out;
+  p.status = s->status;
+  const int64_t per_head = (a->head_dim + 2 * piece - 1) / (2 * piece);
+  const int64_t per_token = per_head * (p.heads + 2 * static_cast<int64_t>(p.kv_heads));
+  if (per_token > (1 << 23)) return TS_ERR_UNSUPPORTED;
+  // whole tokens, about eight units per thread, fewer while SMs would idle
+  const int64_t n = a->n_tokens, fill = ts::kRotaryThreads * 8;
+  int64_t tokens = std::min<int64_t>(fill / per_token, (n + s->num_sms - 1) / s->num_sms);
+  tokens = std::min<int64_t>(tokens, std::min<int64_t>(ts::kRotaryTokens, ts::kRotaryTableFloats / a->rotary_dim));
+  p.tokens_per_cta = static_cast<int32_t>(std::max<int64_t>(1, tokens));
+  p.by_token = ts::FastDiv::of(static_cast<uint32_t>(per_token));
+  p.by_head = ts::FastDiv::of(static_cast<uint32_t>(per_head));
+  const size_t smem = static_cast<size_t>(p.tokens_per_cta) * a->rotary_dim * sizeof(float);
+  void *args[] = {&p};
+  const cudaError_t e = launch(fn, dim3(static_cast<unsigned>((n + p.tokens_per_cta - 1) / p.tokens_per_cta)),
+                               ts::kRotaryThreads, smem, s->pdl != 0, static_cast<cudaStream_t>(stream), args);
+  return e == cudaSuccess ? TS_OK : cuda_fail(e, "rotary launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream) {
+  if (!s || !a) return TS_ERR_INVALID_ARG;
+  if (a->n_rows < 0 || a->dim < 1 || !real_type(a->dtype) || !out_type(a->out_dtype) ||
+      (a->weight && !real_type(a->weight_dtype)) || !std::isfinite(a->eps) || a->eps < 0.0f ||
+      !std::isfinite(a->weight_offset))
+    return TS_ERR_INVALID_ARG;
+  const bool e4m3 = a->out_dtype == TS_DTYPE_E4M3;
+  if (a->out_scale ? !e4m3 : e4m3 && a->n_rows > 0) return TS_ERR_INVALID_ARG;
+  const int es = size_of(a->dtype), os = size_of(a->out_dtype);
+  const int64_t n = a->n_rows, dim = a->dim;
+  const Rows x = {a->x, a->x_stride, es}, res = {a->residual, a->residual_stride, es},
+             sum = {a->residual_out, a->residual_out_stride, es}, out = {a->out, a->out_stride, os};
+  for (const Rows &r : {x, res, sum, out})
+    if (r.p && (r.stride < 0 || (n > 1 && r.stride < dim) || !aligned(r.p, static_cast<size_t>(r.es))))
+      return TS_ERR_INVALID_ARG;
+  if (e4m3 && (a->out_scale_stride < 0 || (n > 1 && a->out_scale_stride < scales_of(dim)) || !aligned(a->out_scale, 4)))
+    return TS_ERR_INVALID_ARG;
+  if (a->dim > TS_NORM_MAX_DIM) return TS_ERR_UNSUPPORTED;
+  if (n == 0) return TS_OK;
+  const int ws = a->weight ? size_of(a->weight_dtype) : 0;
+  if (!a->x || !a->out || (ws && !aligned(a->weight, static_cast<size_t>(ws)))) return TS_ERR_INVALID_ARG;
+  const auto span = [&](const Rows &r) { return rows_span(r.p, n, dim, r.stride, r.es); };
+  const auto same = [](const Rows &u, const Rows &v) { return u.p == v.p && u.stride == v.stride && u.es == v.es; };
+  const Span scale = rows_span(a->out_scale, n, scales_of(dim), a->out_scale_stride, 4);
+  const Span weight = rows_span(a->weight, 1, dim, dim, ws);
+  if (span(out).meets(weight) || span(sum).meets(weight) || scale.meets(weight) || span(out).meets(span(sum)) ||
+      span(out).meets(scale) || span(sum).meets(scale) || scale.meets(span(x)) || scale.meets(span(res)))
+    return TS_ERR_INVALID_ARG;
+  if ((!same(out, x) && span(out).meets(span(x))) || (!same(out, res) && span(out).meets(span(res))) ||
+      (!same(sum, x) && span(sum).meets(span(x))) || (!same(sum, res) && span(sum).meets(span(res))))
+    return TS_ERR_INVALID_ARG;
+
+  bool wide = dim % 8 == 0 && (!ws || aligned(a->weight, 16));
+  for (const Rows &r : {x, res, sum, out}) wide = wide && (!r.p || in_pieces(r, n));
+  ts::NormParams p;
+  std::memset(&p, 0, sizeof p);
+  p.x = a->x;
+  p.residual = a->residual;
+  p.residual_out = a->residual_out;
+  p.weight = a->weight;
+  p.out = a->out;
+  p.scale = a->out_scale;
+  p.x_stride = a->x_stride;
+  p.residual_stride = a->residual_stride;
+  p.residual_out_stride = a->residual_out_stride;
+  p.out_stride = a->out_stride;
+  p.scale_stride = a->out_scale_stride;
+  p.n_rows = a->n_rows;
+  p.dim = a->dim;
+  p.weight_f32 = a->weight && a->weight_dtype == TS_DTYPE_F32 ? 1 : 0;
+  p.eps = a->eps;
+  p.weight_offset = a->weight_offset;
+
+  // threads of a row: as few units each as 512 threads allow, then up to 1024 threads
+  const int units = static_cast<int>(wide ? (dim + 7) / 8 : scales_of(dim) * 32);
+  int v = 1;
+  while (v < 2 && units > 512 * v) v *= 2;
+  while (units > 1024 * v) v *= 2;
+  const int threads = ((units + v - 1) / v + 31) / 32 * 32;
+  const int rows = threads == 32 ? 8 : 1;
+  const void *fn = a->dtype == TS_DTYPE_F32 ? norm_kernel_to<float>(a->out_dtype, v, wide)
+                                            : norm_kernel_to<uint16_t>(a->out_dtype, v, wide);
+  void *args[] = {&p};
+  const cudaError_t e =
+      launch(fn, dim3(static_cast<unsigned>((n + rows - 1) / rows)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(rows)),
+             0, s->pdl != 0, static_cast<cudaStream_t>(stream), args);
+  return e == cudaSuccess ? TS_OK : cuda_fail(e, "norm launch");
+}
+
+ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream) {
+  if (!s || !a) return TS_ERR_INVALID_ARG;
+  if (a->n_rows < 0 || a->dim < 1 || !real_type(a->dtype) || !out_type(a->out_dtype) || a->act < TS_ACT_NONE ||
+      a->act > TS_ACT_GELU_TANH)
+    return TS_ERR_INVALID_ARG;
+  const bool e4m3 = a->out_dtype == TS_DTYPE_E4M3, act = a->act != TS_ACT_NONE;
+  if (a->out_scale ? !e4m3 : e4m3 && a->n_rows > 0) return TS_ERR_INVALID_ARG;
+  const int es = size_of(a->dtype), os = size_of(a->out_dtype);
+  const int64_t n = a->n_rows, dim = a->dim;
+  const Rows up = {a->up, a->up_stride, es}, gate = {act ? a->gate : nullptr, a->gate_stride, es},
+             out = {a->out, a->out_stride, os};
+  for (const Rows &r : {up, gate, out})
+    if (r.p && (r.stride < 0 || (n > 1 && r.stride < dim) || !aligned(r.p, static_cast<size_t>(r.es))))
+      return TS_ERR_INVALID_ARG;
+  if (e4m3 && (a->out_scale_stride < 0 || (n > 1 && a->out_scale_stride < scales_of(dim)) || !aligned(a->out_scale, 4)))
+    return TS_ERR_INVALID_ARG;
+  if (a->dim > TS_GATE_MAX_DIM) return TS_ERR_UNSUPPORTED;
+  if (n == 0) return TS_OK;
+  if (!a->up || !a->out || (act && !a->gate)) return TS_ERR_INVALID_ARG;
+  const auto span = [&](const Rows &r) { return rows_span(r.p, n, dim, r.stride, r.es); };
+  const auto same = [](const Rows &u, const Rows &v) { return u.p == v.p && u.stride == v.stride && u.es == v.es; };
+  const Span scale = rows_span(a->out_scale, n, scales_of(dim), a->out_scale_stride, 4);
+  if (scale.meets(span(up)) || scale.meets(span(gate)) || scale.meets(span(out)) ||
+      (!same(out, up) && span(out).meets(span(up))) || (!same(out, gate) && span(out).meets(span(gate))))
+    return TS_ERR_INVALID_ARG;
+
+  bool wide = dim % 8 == 0;
+  for (const Rows &r : {up, gate, out}) wide = wide && (!r.p || in_pieces(r, n));
+  ts::GateParams p;
+  std::memset(&p, 0, sizeof p);
+  p.up = a->up;
+  p.gate = a->gate;
+  p.out = a->out;
+  p.scale = a->out_scale;
+  p.up_stride = a->up_stride;
+  p.gate_stride = a->gate_stride;
+  p.out_stride = a->out_stride;
+  p.scale_stride = a->out_scale_stride;
+  p.dim = a->dim;
+  p.act = a->act;
+  const int64_t per_row = scales_of(dim) * (wide ? 16 : 32);
+  p.by_row = ts::FastDiv::of(static_cast<uint32_t>(per_row));
+  p.units = n * per_row;
+  const int64_t per_cta = ts::kGateThreads * ts::kGateUnits, grid = (p.units + per_cta - 1) / per_cta;
+  if (grid > INT32_MAX) return TS_ERR_UNSUPPORTED;
+  const void *fn = a->dtype == TS_DTYPE_F32 ? gate_kernel_to<float>(a->out_dtype, wide)
+                                            : gate_kernel_to<uint16_t>(a->out_dtype, wide);
+  void *args[] = {&p};
+  const cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), ts::kGateThreads, 0, s->pdl != 0,
+                               static_cast<cudaStream_t>(stream), args);
+  return e == cudaSuccess ? TS_OK : cuda_fail(e, "gate launch");
+}
+
+ts_status ts_rotary(ts_sampler *s, const ts_rotary_args *a, void *stream) {
+  if (!s) return TS_ERR_INVALID_ARG;
+  ts_status rc = check_rotary(a);
+  if (rc != TS_OK) return rc;
+  if (a->n_heads < 1) return TS_ERR_INVALID_ARG;
+  if (a->n_tokens == 0) return TS_OK;
+  rc = check_rotary_arrays(a, true);
+  if (rc != TS_OK) return rc;
+  ts::RotaryParams p;
+  std::memset(&p, 0, sizeof p);
+  const int piece = piece_of(a, nullptr, true);
+  const void *fn = a->dtype == TS_DTYPE_F32 ? rotary_kernel<float, float, false>(piece)
+                                            : rotary_kernel<uint16_t, uint16_t, false>(piece);
+  return launch_rotary(s, a, p, fn, piece, stream);
+}
+
+ts_status ts_kv_append_rotary(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *t, const ts_rotary_args *a,
+                              void *stream) {
+  if (!s || !t) return TS_ERR_INVALID_ARG;
+  ts_status rc = ts_host::check_append(c, t);
+  if (rc != TS_OK) return rc;
+  rc = check_rotary(a);
+  if (rc != TS_OK) return rc;
+  const bool queries = a->x != nullptr;
+  if (queries ? a->n_heads < 1 : a->n_heads != 0) return TS_ERR_INVALID_ARG;
+  if (a->n_tokens != t->n_tokens || a->rows != t->rows || (a->rows && a->n_rows != t->n_rows) || a->dtype != t->dtype ||
+      a->head_dim != c->head_dim)
+    return TS_ERR_INVALID_ARG;
+  if (t->n_tokens == 0) return TS_OK;
+  rc = ts_host::check_append_arrays(t);
+  if (rc != TS_OK) return rc;
+  rc = check_rotary_arrays(a, queries);
+  if (rc != TS_OK) return rc;
+
+  ts::RotaryParams p;
+  std::memset(&p, 0, sizeof p);
+  p.src[0] = t->k;
+  p.src[1] = t->v;
+  p.src_token[0] = t->k_token_stride;
+  p.src_token[1] = t->v_token_stride;
+  p.src_head[0] = t->k_head_stride;
+  p.src_head[1] = t->v_head_stride;
+  p.dst[0] = c->k;
+  p.dst[1] = c->v;
+  p.dst_block[0] = c->k_block_stride;
+  p.dst_block[1] = c->v_block_stride;
+  p.dst_token[0] = c->k_token_stride;
+  p.dst_token[1] = c->v_token_stride;
+  p.dst_head[0] = c->k_head_stride;
+  p.dst_head[1] = c->v_head_stride;
+  p.scale[0] = c->k_scale;
+  p.scale[1] = c->v_scale;
+  p.slots = t->slots;
+  p.block_size = c->block_size;
+  p.n_slots = static_cast<int64_t>(c->n_blocks) * c->block_size;
+  p.kv_heads = c->n_kv_heads;
+  const int piece = piece_of(a, t, queries);
+  const bool f32 = a->dtype == TS_DTYPE_F32;
+  const void *fn = c->dtype == TS_DTYPE_E4M3
+                       ? (f32 ? rotary_kernel<float, uint8_t, true>(piece) : rotary_kernel<uint16_t, uint8_t, true>(piece))
+                       : (f32 ? rotary_kernel<float, float, true>(piece) : rotary_kernel<uint16_t, uint16_t, true>(piece));
+  return launch_rotary(s, a, p, fn, piece, stream);
+}
+
+ts_status ts_rotary_frequencies(double *freqs, int32_t rotary_dim, double base, int32_t scaling, double factor,
+                                double original_len, double low, double high, float *amplitude) {
+  if (!freqs || rotary_dim < 2 || rotary_dim % 2 || !std::isfinite(base) || base <= 0.0 || scaling < TS_ROPE_PLAIN ||
+      scaling > TS_ROPE_BY_PARTS)
+    return TS_ERR_INVALID_ARG;
+  if (scaling != TS_ROPE_PLAIN && (!std::isfinite(factor) || factor < 1.0)) return TS_ERR_INVALID_ARG;
+  if (scaling == TS_ROPE_NTK && rotary_dim < 4) return TS_ERR_INVALID_ARG;
+  if (scaling == TS_ROPE_BY_PARTS &&
+      (!std::isfinite(original_len) || original_len < 1.0 || !std::isfinite(low) || !std::isfinite(high) || low >= high))
+    return TS_ERR_INVALID_ARG;
+  const double d = rotary_dim;
+  if (scaling == TS_ROPE_NTK) base *= std::pow(factor, d / (d - 2.0));
+  const double two_pi = 6.283185307179586;
+  for (int32_t i = 0; i < rotary_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / d);
+    freqs[i] = f;
+    if (scaling == TS_ROPE_LINEAR) freqs[i] = f / factor;
+    if (scaling == TS_ROPE_BY_PARTS) {
+      const double r = std::min(1.0, std::max(0.0, (original_len * f / two_pi - low) / (high - low)));
+      freqs[i] = f * ((1.0 - r) / factor + r);
+    }
+  }
+  if (amplitude) *amplitude = scaling == TS_ROPE_BY_PARTS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return TS_OK;
+}
+
+}  // extern "C"

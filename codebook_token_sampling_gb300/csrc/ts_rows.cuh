@@ -1,0 +1,117 @@
+// ts_rows.cuh -- rows of a decode layer as the layer operators read and write them:
+// a thread's piece of a row in fp32, and 8-bit rows with a scale for each 128
+// elements.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "ts_e4m3.cuh"
+
+namespace ts {
+
+constexpr int kScaleBlock = 128;
+
+// A block of 128 elements is shared by 16 lanes of 8 neighbours each (WIDE: moved
+// in 16-byte pieces), or by a warp whose lane l has elements l, l + 32, l + 64 and
+// l + 96 (any alignment and width, still one row segment per load).
+template <bool WIDE>
+struct RowUnit {
+  static constexpr int kElems = WIDE ? 8 : 4;
+  static constexpr int kLanes = kScaleBlock / kElems;  // that share a block
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  uint32_t w;
+  memcpy(&w, &v, 4);
+  return w;
+}
+__device__ __forceinline__ uint16_t bf16_of(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ float value_of(float x) { return x; }
+__device__ __forceinline__ float value_of(uint16_t bits) { return __uint_as_float(static_cast<uint32_t>(bits) << 16); }
+
+// Eight neighbours from a 16-byte aligned address.
+__device__ __forceinline__ void load8(const uint16_t *p, float (&v)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(u[i]);
+    v[2 * i + 1] = bf16_hi(u[i]);
+  }
+}
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8]) {
+  *reinterpret_cast<uint4 *>(p) =
+      make_uint4(bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]), bf16x2_of(v[4], v[5]), bf16x2_of(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(uint8_t *p, const float (&v)[8]) {
+  *reinterpret_cast<uint2 *>(p) =
+      make_uint2(e4m3x4_of(v[0], v[1], v[2], v[3]), e4m3x4_of(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = bf16_of(v); }
+__device__ __forceinline__ void store1(uint8_t *p, float v) { *p = e4m3_of(v); }
+
+// A unit at element `at` of a row (WIDE: its first of eight neighbours; else its
+// lane's first of four, 32 apart); elements from `dim` on are 0 and not read.
+template <bool WIDE, class T>
+__device__ __forceinline__ void load_unit(const T *row, int64_t at, int64_t dim, float (&v)[RowUnit<WIDE>::kElems]) {
+  if constexpr (WIDE) {
+    if (at < dim) {
+      load8(row + at, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = at + 32 * e < dim ? value_of(row[at + 32 * e]) : 0.0f;
+  }
+}
+template <bool WIDE, class T>
+__device__ __forceinline__ void store_unit(T *row, int64_t at, int64_t dim, const float (&v)[RowUnit<WIDE>::kElems]) {
+  if constexpr (WIDE) {
+    if (at < dim) store8(row + at, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (at + 32 * e < dim) store1(row + at + 32 * e, v[e]);
+  }
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The scale of the block that a unit belongs to (the lanes that share it take
+// part), and the unit's elements over it.
+template <bool WIDE>
+__device__ __forceinline__ float scaled_block(float (&v)[RowUnit<WIDE>::kElems]) {
+  float a = fabsf(v[0]);
+#pragma unroll
+  for (int e = 1; e < RowUnit<WIDE>::kElems; ++e) a = max_nan(a, fabsf(v[e]));
+#pragma unroll
+  for (int o = RowUnit<WIDE>::kLanes / 2; o; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+  float scale = __fdiv_rn(fmaxf(a, 0x1p-64f), 448.0f);
+  if (!(a < INFINITY)) scale = __int_as_float(0x7FC00000);  // a NaN or an infinity in the block
+  const float inv = __fdiv_rn(1.0f, scale);
+#pragma unroll
+  for (int e = 0; e < RowUnit<WIDE>::kElems; ++e) v[e] *= inv;
+  return scale;
+}
+
+}  // namespace ts

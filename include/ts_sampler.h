@@ -42,8 +42,9 @@
  * stay valid until the work queued on `stream` has run.  The library never
  * allocates, frees or synchronises inside ts_sample / ts_sample_debug /
  * ts_sample_steps / ts_advance_steps / ts_lm_head_* / ts_kv_tables /
- * ts_kv_append / ts_paged_attention, so those calls may be captured into a
- * CUDA graph.  They
+ * ts_kv_append / ts_paged_attention / ts_rms_norm / ts_gate /
+ * ts_linear_e4m3 / ts_rotary / ts_kv_append_rotary, so those calls may be
+ * captured into a CUDA graph.  They
  * run on the device that is current when they are called, which must be the
  * device the sampler was created on.
  */
@@ -64,7 +65,8 @@ typedef enum {
   TS_ERR_NO_MEMORY = 4     /* host or device allocation failed in ts_create */
 } ts_status;
 
-/* TS_DTYPE_E4M3 (8 bits, no infinities, at most 448): key-value caches only. */
+/* TS_DTYPE_E4M3 (8 bits, no infinities, at most 448): key-value caches, and the
+ * 8-bit rows of the layer operators (ts_rms_norm and those after it) only. */
 typedef enum { TS_DTYPE_F32 = 0, TS_DTYPE_BF16 = 1, TS_DTYPE_E4M3 = 2 } ts_dtype;
 
 /* Per-row error bits.  A row with an error gets out_ids = -1, out_eos = 0
@@ -585,6 +587,200 @@ ts_status ts_paged_attention(ts_sampler *s, const ts_kv_cache *c, const ts_paged
  * workspace. */
 ts_status ts_kv_debug_lose_parts(ts_sampler *s, int32_t come);
 
+/* --------------------------------------------------------------------------
+ * The operators around the paged cache in a decode layer.
+ *
+ * The Drama 3 article's backbone keeps its weights in block-scaled 8-bit
+ * floating point ("Drama 3 本体"); the calls below are a layer around that cache:
+ *   ts_rms_norm          the residual's sum, its norm, and 8-bit rows of it,
+ *   ts_linear_e4m3       the product of 8-bit rows and 8-bit weights,
+ *   ts_rotary            rotary positions of queries and keys,
+ *   ts_kv_append_rotary  the same on the way into the cache,
+ *   ts_gate              a gated activation, or only the rounding to 8-bit rows.
+ * One layer of a decode step is ts_rms_norm, ts_linear_e4m3 (queries, keys,
+ * values), ts_kv_append_rotary, ts_paged_attention, ts_gate (no gate: 8-bit rows
+ * of its output), ts_linear_e4m3, ts_rms_norm, ts_linear_e4m3 (gate and up),
+ * ts_gate, ts_linear_e4m3.  They use no workspace: calls on several streams of
+ * one sampler may overlap.  Like the calls above they are asynchronous, read no
+ * device memory on the host, never allocate and may be captured.
+ *
+ * 8-bit rows.  A row of `dim` elements has one fp32 scale for each block of
+ * TS_SCALE_BLOCK elements (the last block may be shorter) and holds code j of
+ * block b for the value code * scale[b].  What the calls below write is
+ *   scale[b] = max(a, 2^-64) / 448, a = the block's largest size,
+ *   code     = the nearest e4m3 value (ties to even, at most 448) of y * (1 / scale[b]),
+ * every quotient and product rounded to fp32.  A block with a NaN or an infinity gets a NaN scale and NaN codes.
+ *
+ * Strides are in elements.  Outputs may not overlap inputs except where a call
+ * says so. */
+#define TS_SCALE_BLOCK 128
+
+/* Root-mean-square norm of the residual's sum.  For each row, in fp32:
+ *   h = x + residual                     (x where residual is NULL),
+ *   residual_out = h                     (rounded to dtype; NULL: not written),
+ *   y = h / sqrt(mean(h h) + eps) * (weight + weight_offset)   (NULL weight: 1),
+ *   out = y                              (rounded to out_dtype once).
+ * The norm is that of h before its rounding to dtype.  A row whose squares leave
+ * fp32's range is summed again with its elements scaled by a power of two, so any
+ * finite h has its norm.  residual_out may be x or residual themselves (the same
+ * address and stride), out may be x itself where the types are the same.
+ *
+ * Types: x, residual and residual_out F32 or BF16; out F32, BF16 or E4M3; weight
+ * F32 or BF16.  Any alignment to the types' own sizes; rows whose addresses and
+ * strides in bytes are multiples of 16, and dim one of 8, are moved in 16-byte
+ * pieces (an E4M3 out: 8).  TS_ERR_INVALID_ARG for a NULL pointer that is needed,
+ * a negative size or stride, dim < 1, eps negative or not finite, weight_offset
+ * not finite, a stride below dim (for more than one row), out_scale missing for
+ * E4M3 or given for another type, or an overlap of an output that the host can
+ * see; TS_ERR_UNSUPPORTED for dim above TS_NORM_MAX_DIM. */
+#define TS_NORM_MAX_DIM 32768
+typedef struct {
+  const void *x;             /* [n_rows][dim] */
+  const void *residual;      /* the same, or NULL */
+  void *residual_out;        /* the same, or NULL */
+  const void *weight;        /* [dim], or NULL */
+  void *out;                 /* [n_rows][dim] */
+  float *out_scale;          /* [n_rows][ceil(dim / 128)], E4M3 only */
+  int32_t dtype;
+  int32_t weight_dtype;      /* looked at with weight only */
+  int32_t out_dtype;
+  int32_t n_rows;            /* 0 is allowed: nothing runs */
+  int32_t dim;
+  int64_t x_stride, residual_stride, residual_out_stride, out_stride, out_scale_stride;
+  float eps;
+  float weight_offset;
+} ts_norm_args;
+ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream);
+
+/* out = act(gate) * up, in fp32, rounded to out_dtype once; TS_ACT_NONE: out = up
+ * (gate is not looked at), which makes 8-bit rows of anything.  TS_ACT_SILU:
+ * g / (1 + exp(-g)); TS_ACT_GELU: g (1 + erf(g / sqrt 2)) / 2; TS_ACT_GELU_TANH:
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.  gate and up may be the halves
+ * of one product's rows (strides); out may be up or gate themselves where the types
+ * are the same.  Types, alignment and refusals as for ts_rms_norm; dim up to
+ * TS_GATE_MAX_DIM. */
+#define TS_GATE_MAX_DIM 1048576
+typedef enum { TS_ACT_NONE = 0, TS_ACT_SILU = 1, TS_ACT_GELU = 2, TS_ACT_GELU_TANH = 3 } ts_act;
+typedef struct {
+  const void *up;            /* [n_rows][dim] */
+  const void *gate;          /* the same; NULL with TS_ACT_NONE only */
+  void *out;                 /* [n_rows][dim] */
+  float *out_scale;          /* [n_rows][ceil(dim / 128)], E4M3 only */
+  int32_t dtype;             /* of up and gate: F32 or BF16 */
+  int32_t out_dtype;         /* F32, BF16 or E4M3 */
+  int32_t act;
+  int32_t n_rows;            /* 0 is allowed: nothing runs */
+  int32_t dim;
+  int64_t up_stride, gate_stride, out_stride, out_scale_stride;
+} ts_gate_args;
+ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream);
+
+/* The product of 8-bit rows x [n_rows][in_dim] and 8-bit weights w [out_dim]
+ * [in_dim], both E4M3: with b counting blocks of 128 along in_dim,
+ *   out[m][n] = sum_b x_scale[m][b] w_scale[n / 128][b] sum_{k in b} x[m][k] w[n][k].
+ * A block's products are summed by the tensor cores in fp32, the blocks' sums are
+ * scaled and added in fp32, and the result is rounded to out_dtype once.  The order
+ * of the blocks' additions depends on the sizes, and is the same in every run.
+ *
+ * x and w are 16-byte aligned and their strides multiples of 16; in_dim may be any
+ * size (what follows it in a row is not used).  out_dtype: F32 or BF16, any stride.
+ * Rows and columns that x and w do not have are not written.  TS_ERR_INVALID_ARG for
+ * a NULL pointer, a misaligned one, a negative n_rows, in_dim or out_dim < 1, a
+ * stride below its row (x, out and x_scale of one row: any), or an out that overlaps
+ * an input; TS_ERR_UNSUPPORTED for an in_dim above TS_LINEAR_MAX_DIM, a stride of
+ * 2^40 or more, or where the driver offers no tensor maps.  A copy that does not come
+ * within a kernel's waiting limit (which nothing that the call allows brings about)
+ * sets TS_ROW_STALLED and leaves a part of out unwritten. */
+#define TS_LINEAR_MAX_DIM 1048576
+#define TS_ROW_STALLED 128u
+typedef struct {
+  const void *x;             /* [n_rows][in_dim] */
+  const float *x_scale;      /* [n_rows][ceil(in_dim / 128)] */
+  const void *w;             /* [out_dim][in_dim] */
+  const float *w_scale;      /* [ceil(out_dim / 128)][ceil(in_dim / 128)] */
+  void *out;                 /* [n_rows][out_dim] */
+  int32_t out_dtype;
+  int32_t n_rows;            /* 0 is allowed: nothing runs */
+  int32_t in_dim;
+  int32_t out_dim;
+  int64_t x_stride, x_scale_stride, w_stride, w_scale_stride, out_stride;
+} ts_linear_args;
+ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void *stream);
+
+/* Rotary positions.  Token t's heads x[r][h] (r = rows[t], or t where rows is NULL;
+ * strides) have their first rotary_dim elements turned in rotary_dim / 2 pairs: pair
+ * i is elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where interleaved is set,
+ * and with c, s = amplitude * (cos, sin)(positions[t] * freqs[i])
+ *   (a, b) -> (a c - b s, b c + a s)
+ * in fp32, rounded to dtype once.  The head's other elements are copied.  The angle
+ * is the exact product of the position and the frequency (radians per position, 64
+ * bits) up to 2^-33 turns for positions below 2^20, and 2^-22 for any; cosine and
+ * sine are within 2^-22.  A negative position skips the token: its rows are neither
+ * read nor written.  out may be x itself (the same address and strides).  Tokens of
+ * one call have rows of their own.  A row outside [0, n_rows) sets TS_ROW_BAD_SLOT
+ * and skips the token.
+ *
+ * Types: F32 or BF16.  TS_ERR_INVALID_ARG for a NULL pointer, a negative size or
+ * stride, n_heads or head_dim < 1, an odd rotary_dim or one outside [2, head_dim],
+ * an amplitude that is not finite, or an out that is x with other strides.
+ * TS_ERR_UNSUPPORTED for head_dim above TS_ROTARY_MAX_HEAD_DIM, n_heads above
+ * TS_KV_MAX_HEADS or more than 2^24 elements per token. */
+#define TS_ROTARY_MAX_HEAD_DIM 1024
+typedef struct {
+  const void *x;             /* [rows][n_heads][head_dim] by strides */
+  void *out;                 /* the same */
+  int32_t dtype;
+  int32_t n_tokens;          /* 0 is allowed: nothing runs */
+  int32_t n_heads;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int64_t x_token_stride, x_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  const int32_t *positions;  /* [n_tokens] */
+  const int32_t *rows;       /* [n_tokens] or NULL */
+  int32_t n_rows;            /* rows of x and out; looked at with rows only */
+  float amplitude;
+  const double *freqs;       /* [rotary_dim / 2] */
+} ts_rotary_args;
+ts_status ts_rotary(ts_sampler *s, const ts_rotary_args *a, void *stream);
+
+/* ts_rotary of the queries and ts_kv_append of the same tokens' keys and values in
+ * one launch, the keys turned like the queries before they are rounded, once, to
+ * the cache's type (for an e4m3 cache: turned in fp32, divided by the scale,
+ * rounded).  The ts_kv_tables maps serve as they are: slots, positions and requests
+ * (the rows).  A token with a negative slot or position is skipped, queries and all.
+ * a->x may be NULL (with n_heads 0): keys and values only.
+ * Checks are those of the two calls; besides, TS_ERR_INVALID_ARG where n_tokens,
+ * rows, n_rows (with rows), dtype or head_dim differ between tokens, queries and
+ * cache. */
+ts_status ts_kv_append_rotary(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *t,
+                              const ts_rotary_args *a, void *stream);
+
+/* The frequencies that ts_rotary takes, on the host (no CUDA call): freqs[i] for
+ * i < rotary_dim / 2 from f_i = base^(-2 i / rotary_dim), scaled for contexts that
+ * are `factor` times as long as the training's `original_len`:
+ *   TS_ROPE_PLAIN    f_i,
+ *   TS_ROPE_LINEAR   f_i / factor (Chen et al., "Extending context window of large
+ *                    language models via positional interpolation", 2023),
+ *   TS_ROPE_NTK      f_i with base * factor^(rotary_dim / (rotary_dim - 2)): the
+ *                    lowest frequency is divided by factor, the highest kept,
+ *   TS_ROPE_BY_PARTS f_i ((1 - r_i) / factor + r_i), r_i rising linearly from 0 to 1
+ *                    as the turns over original_len, original_len f_i / (2 pi), go
+ *                    from `low` to `high` (Peng et al., "YaRN: efficient context
+ *                    window extension of large language models", 2023).
+ * *amplitude (may be NULL) gets 1, for TS_ROPE_BY_PARTS that paper's 0.1 ln(factor)
+ * + 1.  TS_ERR_INVALID_ARG for a NULL freqs, a rotary_dim that is odd or < 2 (NTK: < 4),
+ * a base that is not finite or <= 0, a factor that is not finite or < 1, and by parts for an
+ * original_len < 1 or low, high not finite with low < high. */
+#define TS_ROPE_PLAIN 0
+#define TS_ROPE_LINEAR 1
+#define TS_ROPE_NTK 2
+#define TS_ROPE_BY_PARTS 3
+ts_status ts_rotary_frequencies(double *freqs, int32_t rotary_dim, double base, int32_t scaling,
+                                double factor, double original_len, double low, double high,
+                                float *amplitude);
+
 /* step[i] += 1 for i < n_streams, on the device (graph-capturable).  Call it
  * after the step's ts_sample so that sibling rows of one stream share a step
  * (or set ts_batch.advance_steps, which does the same inside the call). */
@@ -631,6 +827,9 @@ ts_status ts_read_status(ts_sampler *s, uint32_t *bits, void *stream);
 /* TS_OPT_KV_JOIN: how ts_paged_attention joins the parts of its work (0 =
  * automatic, 1 = by a launch of their own, 2 = by the last CTA to come). */
 #define TS_OPT_KV_JOIN 8
+/* TS_OPT_LINEAR_SPLIT: the CTAs (a cluster) that share a tile of ts_linear_e4m3
+ * along in_dim: 0 = automatic, or 1, 2, 4 or 8. */
+#define TS_OPT_LINEAR_SPLIT 9
 ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value);
 
 /* Describes the kernel that ts_sample would launch for `b` (path 1 .. 4,
