@@ -56,6 +56,7 @@ TS_OPT_FAIL_LAUNCH = 6
 TS_OPT_KV_CTAS = 7
 TS_OPT_KV_JOIN = 8
 TS_OPT_LINEAR_SPLIT = 9
+TS_OPT_LINEAR_PATH = 10
 TS_MAX_VOCAB_BF16 = 163840
 TS_MAX_VOCAB_F32 = 81920
 TS_NOALLOC_SCRATCH_BYTES = 4194304
@@ -70,6 +71,7 @@ TS_SCALE_BLOCK = 128
 TS_NORM_MAX_DIM = 32768
 TS_GATE_MAX_DIM = 1048576
 TS_LINEAR_MAX_DIM = 1048576
+TS_LINEAR_MAX_ROWS = 2147482624
 TS_ROTARY_MAX_HEAD_DIM = 1024
 TS_ACT_NONE = 0
 TS_ACT_SILU = 1

@@ -30,6 +30,8 @@ struct ts_sampler {
   struct ts_kv_state *kv;  // the paged cache's workspace (ts_reserve_kv), or null
   int kv_ctas;        // paged attention: 0 auto, else its number of CTAs (testing)
   int kv_join;        // 0 auto, 1 joins by a launch of their own, 2 by the last CTA (testing)
+  int linear_pairs;   // ts_linear_e4m3: pairs of CTAs that the GPU holds at once
+  int linear_path;    // ts_linear_e4m3: 0 auto, else its kernel (testing)
   int linear_split;   // ts_linear_e4m3: 0 auto, else the CTAs that share a tile (testing)
 };
 
@@ -42,7 +44,7 @@ ts_status cuda_fail(cudaError_t e, const char *what);
 cudaError_t kv_free(ts_sampler *s);
 
 // Once per ts_create, on the current device: what ts_linear_e4m3 needs of it.
-ts_status linear_setup();
+ts_status linear_setup(ts_sampler *s);
 
 // One launch, with programmatic dependent launch if `pdl`.
 cudaError_t launch(const void *fn, dim3 grid, dim3 block, size_t smem, bool pdl, cudaStream_t st, void **args);

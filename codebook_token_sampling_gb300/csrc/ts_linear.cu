@@ -28,31 +28,104 @@ bool tensor_map(CUtensorMap *m, const void *p, int64_t columns, int64_t rows, in
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct FewKernel {
+// The kernels: tokens as the products' columns (16, 32 or 64), as their rows, and the
+// latter by pairs of CTAs.
+struct LinearKernel {
   const void *fn;
   uint32_t smem;
-  int columns;
+  int threads;
 };
 template <int TN>
-FewKernel few_kernel() {
-  return {reinterpret_cast<const void *>(ts::linear_few_kernel<TN>), ts::FewTile<TN>::kSmemBytes, TN};
+LinearKernel few_kernel() {
+  return {reinterpret_cast<const void *>(ts::linear_few_kernel<TN>), ts::FewTile<TN>::kSmemBytes, ts::kFewThreads};
 }
-FewKernel few_kernel_for(int i) {
-  return i == 0 ? few_kernel<16>() : i == 1 ? few_kernel<32>() : i == 2 ? few_kernel<64>() : few_kernel<128>();
+template <int CH, bool PAIR>
+LinearKernel rows_kernel() {
+  return {reinterpret_cast<const void *>(ts::linear_rows_kernel<CH, PAIR>), ts::RowsTile<CH, PAIR>::kSmemBytes,
+          ts::kRowsThreads};
+}
+constexpr int kKernels = 5;
+LinearKernel kernel_for(int i) {
+  return i == 0 ? few_kernel<16>() : i == 1 ? few_kernel<32>() : i == 2 ? few_kernel<64>()
+       : i == 3 ? rows_kernel<2, false>() : rows_kernel<4, true>();
 }
 
-int64_t blocks_of(int64_t dim) { return (dim + TS_SCALE_BLOCK - 1) / TS_SCALE_BLOCK; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t blocks_of(int64_t dim) { return ceil_div(dim, TS_SCALE_BLOCK); }
+
+// What a call launches: the kernel, its tile (rows of x by weight rows) and the CTAs
+// that share one along in_dim.
+struct LinearPlan {
+  int kernel, rows, columns, split;
+};
+
+// CTAs of a cluster for `tiles` tiles: as many as leave none waiting for an SM.
+int split_for(int64_t tiles, int64_t blocks, int num_sms) {
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= num_sms && split * 2 <= blocks) split *= 2;
+  return split;
+}
+
+LinearPlan plan_few(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
+  LinearPlan plan = {m <= 16 ? 0 : m <= 32 ? 1 : 2, m <= 16 ? 16 : m <= 32 ? 32 : 64, 128, 1};
+  plan.split = split_for(ceil_div(n, 128) * ceil_div(m, plan.rows), blocks, s->num_sms);
+  return plan;
+}
+LinearPlan plan_rows(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
+  // the least time by a count of what a CTA takes in (48 bytes per cycle) and of the
+  // cycles around it
+  LinearPlan best = {3, 128, 128, 1};
+  double least = 1e30;
+  for (int columns = 32; columns <= 128; columns += 32) {
+    const int64_t tiles = ceil_div(m, 128) * ceil_div(n, columns);
+    const int split = split_for(tiles, blocks, s->num_sms);
+    const double waves = static_cast<double>(ceil_div(tiles * split, s->num_sms));
+    const double cycles = waves * (ceil_div(blocks, split) * (128 + columns) * 128 / 48.0 + 3000.0);
+    if (cycles <= least) {
+      least = cycles;
+      best.columns = columns;
+      best.split = split;
+    }
+  }
+  return best;
+}
+LinearPlan plan_for(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
+  const int64_t pairs = ceil_div(m, 256) * ceil_div(n, 256);
+  const int path = s->linear_path ? s->linear_path : m <= 64 ? 1 : pairs >= s->num_sms / 2 ? 3 : 2;
+  LinearPlan plan = path == 1 ? plan_few(s, m, n, blocks)
+                  : path == 2 ? plan_rows(s, m, n, blocks) : LinearPlan{4, 256, 256, 1};
+  if (s->linear_split && path != 3) {
+    plan.split = s->linear_split;
+    while (plan.split > blocks) plan.split /= 2;
+  }
+  return plan;
+}
 
 }  // namespace
 
 // Shared-memory limits of the kernels, and the driver's encoder of tensor maps.
-ts_status ts_host::linear_setup() {
-  for (int i = 0; i < 4; ++i) {
-    const FewKernel k = few_kernel_for(i);
+ts_status ts_host::linear_setup(ts_sampler *s) {
+  for (int i = 0; i < kKernels; ++i) {
+    const LinearKernel k = kernel_for(i);
     const cudaError_t e =
         cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   }
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  const LinearKernel k = kernel_for(kKernels - 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(s->num_sms / 2 * 2));
+  cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
+  cfg.dynamicSmemBytes = k.smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(&s->linear_pairs, k.fn, &cfg);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+  if (s->linear_pairs < 1) s->linear_pairs = 1;
   void *fn = nullptr;
   cudaDriverEntryPointQueryResult found;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) == cudaSuccess &&
@@ -75,7 +148,8 @@ extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void
   if ((a->out_dim > 1 && a->w_stride < a->in_dim) || (a->out_dim > TS_SCALE_BLOCK && a->w_scale_stride < blocks))
     return TS_ERR_INVALID_ARG;
   if ((a->n_rows > 1 && a->x_stride % 16) || (a->out_dim > 1 && a->w_stride % 16)) return TS_ERR_INVALID_ARG;
-  if (a->in_dim > TS_LINEAR_MAX_DIM) return TS_ERR_UNSUPPORTED;
+  if (a->in_dim > TS_LINEAR_MAX_DIM || a->n_rows > TS_LINEAR_MAX_ROWS || a->out_dim > TS_LINEAR_MAX_ROWS)
+    return TS_ERR_UNSUPPORTED;
   for (int64_t x : {a->x_stride, a->x_scale_stride, a->w_stride, a->w_scale_stride, a->out_stride})
     if (x >= (1ll << 40)) return TS_ERR_UNSUPPORTED;
   if (a->n_rows == 0) return TS_OK;
@@ -103,43 +177,48 @@ extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void
   p.n_rows = a->n_rows;
   p.out_dim = a->out_dim;
   p.blocks = static_cast<int32_t>(blocks);
-  p.tiles_n = static_cast<int32_t>(blocks_of(a->out_dim));
   p.status = s->status;
+  p.wide_out = aligned(a->out, 16) && (a->n_rows == 1 || a->out_stride * es % 16 == 0);
 
   const int32_t m = a->n_rows;
-  const FewKernel k = few_kernel_for(m <= 16 ? 0 : m <= 32 ? 1 : m <= 64 ? 2 : 3);
-  const int64_t tiles = p.tiles_n * ((static_cast<int64_t>(m) + k.columns - 1) / k.columns);
-  if (tiles > INT32_MAX) return TS_ERR_UNSUPPORTED;
-  int split = s->linear_split;
-  if (!split)
-    for (split = 1; split < 8 && tiles * split * 2 <= s->num_sms;) split *= 2;
-  while (split > blocks) split /= 2;
-  p.split = split;
+  const LinearPlan plan = plan_for(s, m, a->out_dim, blocks);
+  const LinearKernel k = kernel_for(plan.kernel);
+  const bool few = plan.kernel < 3, pair = plan.kernel == 4;
+  const int64_t tiles_n = ceil_div(a->out_dim, plan.columns), tiles_m = ceil_div(m, plan.rows), tiles = tiles_n * tiles_m;
+  if (tiles * plan.split > INT32_MAX / 2) return TS_ERR_UNSUPPORTED;
+  p.tiles_n = static_cast<int32_t>(tiles_n);
+  p.tiles_m = static_cast<int32_t>(tiles_m);
+  p.tiles = static_cast<int32_t>(tiles);
+  p.columns = plan.columns;
+  p.split = plan.split;
 
   // one row's stride says nothing
   const auto pitch = [&](int64_t rows, int64_t stride) {
     return rows > 1 ? stride : (static_cast<int64_t>(a->in_dim) + 15) / 16 * 16;
   };
+  const int boxes_x = few ? plan.rows : 128, boxes_w = pair ? plan.columns / 2 : plan.columns;
   CUtensorMap map_w, map_x;
-  if (!tensor_map(&map_w, a->w, a->in_dim, a->out_dim, pitch(a->out_dim, a->w_stride), 128) ||
-      !tensor_map(&map_x, a->x, a->in_dim, m, pitch(m, a->x_stride), k.columns))
+  if (!tensor_map(&map_w, a->w, a->in_dim, a->out_dim, pitch(a->out_dim, a->w_stride), boxes_w) ||
+      !tensor_map(&map_x, a->x, a->in_dim, m, pitch(m, a->x_stride), boxes_x))
     return TS_ERR_UNSUPPORTED;
 
+  const int cluster = pair ? 2 : plan.split;
+  const int64_t grid = pair ? 2 * std::min<int64_t>(tiles, s->linear_pairs) : tiles * plan.split;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(split));
-  cfg.blockDim = dim3(ts::kFewThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
   cfg.dynamicSmemBytes = k.smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = s->pdl ? 1 : 0;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = static_cast<unsigned>(split);
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  void *args[] = {&map_w, &map_x, &p};
-  const cudaError_t e = cudaLaunchKernelExC(&cfg, k.fn, args);
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  void *few_args[] = {&map_w, &map_x, &p}, *rows_args[] = {&map_x, &map_w, &p};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, k.fn, few ? few_args : rows_args);
   return e == cudaSuccess ? TS_OK : cuda_fail(e, "linear launch");
 }

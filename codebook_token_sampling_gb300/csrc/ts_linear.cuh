@@ -16,8 +16,11 @@ struct LinearParams {
   void *out;
   int32_t out_f32, n_rows, out_dim;
   int32_t blocks;     // of 128 along in_dim
-  int32_t tiles_n;    // of 128 weight rows
+  int32_t tiles_n;    // tiles along the weight rows
   int32_t split;      // CTAs of a cluster that share a tile along in_dim
+  int32_t tiles_m, tiles;  // tiles along the rows, and all (linear_rows_kernel, as the next)
+  int32_t columns;    // weight rows of a tile
+  int32_t wide_out;   // out's rows can be stored in pieces of 16 bytes
   uint32_t *status;
 };
 
@@ -31,7 +34,7 @@ struct LinearParams {
 template <int TN>
 struct FewTile {
   static constexpr int kStageA = 128 * 128, kStageB = TN * 128;
-  static constexpr int kStages = TN == 16 ? 11 : TN == 32 ? 10 : TN == 64 ? 8 : 6;
+  static constexpr int kStages = TN == 16 ? 11 : TN == 32 ? 10 : 8;
   static constexpr int kBuffers = 4;
   static constexpr uint32_t kColumns = kBuffers * TN;  // of TMEM: a power of two, 32 at least
   static constexpr uint32_t kSmemBytes = kStages * (kStageA + kStageB) + 1024;
@@ -50,7 +53,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __shared__ __align__(16) float scales[4][2][TN];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
-  const int t = static_cast<int>(threadIdx.x), lane = t & 31, warp = t >> 5;
+  const int t = static_cast<int>(threadIdx.x), lane = t & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, t >> 5, 0);  // known to be the same in all lanes
   unsigned char *ring =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(linear_smem) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t full = smem_addr(bars), empty = full + 8 * NS, summed = empty + 8 * NS, taken = summed + 8 * NB;
@@ -58,7 +62,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const auto stalled = [&]() { return *static_cast<volatile int *>(&gave_up) != 0; };
 
   const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int tile = static_cast<int>(blockIdx.x);
+  const int tile = static_cast<int>(blockIdx.x) / p.split;
   const int tile_m = tile / p.tiles_n, tile_n = tile - tile_m * p.tiles_n;
   const int32_t n0 = tile_n * 128, m0 = tile_m * TN;
   const int b0 = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / p.split);
@@ -113,24 +117,28 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int j = max(0, i - NS); j < i; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
     }
   } else if (warp == 5) {
-    if (lane == 0) {
-      constexpr uint32_t kind = e4m3_product(TN);
-      for (int i = 0; i < nb; ++i) {
-        const int s = i % NS, b = i % NB;
-        if (!mbar_wait(taken + 8 * b, ((i / NB) & 1) ^ 1, &gave_up)) break;
-        if (!mbar_wait(full + 8 * s, (i / NS) & 1, &gave_up)) break;
-        tc_fence_after();
-        const uint32_t a = smem_addr(ring) + s * (Tile::kStageA + Tile::kStageB);
+    constexpr uint32_t kind = e4m3_product(128, TN);
+    const uint64_t ring_a = operand_of(smem_addr(ring)), ring_b = operand_of(smem_addr(ring) + Tile::kStageA);
+    int s = 0, b = 0;
+    uint32_t s_phase = 0, b_phase = 1;
+    for (int i = 0; i < nb; ++i) {
+      if (!mbar_wait(taken + 8 * b, b_phase, &gave_up) || !mbar_wait(full + 8 * s, s_phase, &gave_up)) break;
+      tc_fence_after();
+      if (elected()) {
+        const uint64_t a = ring_a + s * ((Tile::kStageA + Tile::kStageB) >> 4);
+        const uint64_t x = ring_b + s * ((Tile::kStageA + Tile::kStageB) >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_e4m3(tmem + b * TN, operand_of(a + 32 * k), operand_of(a + Tile::kStageA + 32 * k), kind, k > 0);
+        for (int k = 0; k < 4; ++k) mma_e4m3(tmem + b * TN, a + 2 * k, x + 2 * k, kind, k > 0);
         mma_commit(empty + 8 * s);
         mma_commit(summed + 8 * b);
       }
-      if (stalled()) {
-        mma_commit(done);
-        mbar_drain(done, 0);
-      }
+      __syncwarp();
+      if (++s == NS) s = 0, s_phase ^= 1;
+      if (++b == NB) b = 0, b_phase ^= 1;
+    }
+    if (stalled() && elected()) {
+      mma_commit(done);
+      mbar_drain(done, 0);
     }
   } else {
     // four blocks' scales are fetched while the four before them are used
@@ -233,6 +241,379 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 5) tmem_free(tmem, Tile::kColumns);
+  if (t == 0 && stalled()) atomicOr(p.status, kRowStalled);
+}
+
+// Two fp32 products and sums at once.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void parts_of(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// More rows: 128 tokens are the product's rows and `columns` weight rows (a multiple of
+// 32) its columns, so a thread's sums belong to one token and a block's scales are one
+// number for 32 of them.  Eight warps add the blocks' sums (a warp: 32 tokens, half of
+// the columns), one streams, one issues the products.
+// PAIR: two CTAs share a tile of 256 tokens by `columns`: each brings its tokens and
+// half of the weights, the first one's thread issues the products of both, and the CTAs
+// walk over the tiles; otherwise a CTA (or a cluster along in_dim) has one tile.
+template <int CH, bool PAIR>
+struct RowsTile {
+  static constexpr int kMaxColumns = 64 * CH;
+  static constexpr int kStageA = 128 * 128, kStageB = (PAIR ? kMaxColumns / 2 : kMaxColumns) * 128;
+  static constexpr int kStages = 196608 / (kStageA + kStageB);
+  static constexpr int kBuffers = 512 / kMaxColumns;
+  static constexpr int kStaging = PAIR ? 8 * 32 * 32 * 4 : 0;  // a warp's 32 x 32 outputs
+  static constexpr int kPitch = kMaxColumns + 4;               // floats from a tile's row to the next
+  static constexpr uint32_t kSmemBytes = kStages * (kStageA + kStageB) + kStaging + 1024;
+  static_assert(PAIR || 128 * kPitch * 4 <= kStages * (kStageA + kStageB), "a tile's sums fit the ring");
+};
+// Three warpgroups: two that add, one of which a warp streams and one issues products.
+// Pairs: 384 x 168 registers at launch, 256 x 232 + 128 x 40 from then on.
+constexpr int kRowsThreads = 384;
+
+template <int CH, bool PAIR>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    linear_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                       const LinearParams p) {
+  using Tile = RowsTile<CH, PAIR>;
+  constexpr int NS = Tile::kStages, NB = Tile::kBuffers, kStage = Tile::kStageA + Tile::kStageB;
+  extern __shared__ unsigned char linear_smem[];
+  __shared__ __align__(8) uint64_t bars[2 * NS + 2 * NB + 1];
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+  const int t = static_cast<int>(threadIdx.x), lane = t & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, t >> 5, 0);  // known to be the same in all lanes
+  unsigned char *ring =
+      reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(linear_smem) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t full = smem_addr(bars), empty = full + 8 * NS, summed = empty + 8 * NS, taken = summed + 8 * NB;
+  const uint32_t done = taken + 8 * NB;
+  const auto stalled = [&]() { return *static_cast<volatile int *>(&gave_up) != 0; };
+
+  const int shared_by = PAIR ? 2 : p.split;  // CTAs of the cluster
+  const int rank = shared_by > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / shared_by, step = static_cast<int>(gridDim.x) / shared_by;
+  const int split = PAIR ? 1 : p.split;
+  const int b0 = PAIR ? 0 : static_cast<int>(static_cast<int64_t>(p.blocks) * rank / split);
+  const int nb = PAIR ? p.blocks : static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / split) - b0;
+  // neighbouring tiles share their weights: sixteen tiles of tokens before the next columns
+  const auto place = [&](int tile, int32_t &m0, int32_t &n0) {
+    const int per = p.tiles_n * 16, group = tile / per, in = tile - group * per;
+    const int high = min(16, p.tiles_m - group * 16);
+    n0 = in / high * p.columns;
+    m0 = (group * 16 + in % high) * (PAIR ? 256 : 128) + (PAIR ? rank * 128 : 0);
+  };
+
+  if (warp == 9) {
+    if (lane == 0) {
+      for (int i = 0; i < NS; ++i) {
+        mbar_init(full + 8 * i, 1);
+        mbar_init(empty + 8 * i, 1);
+      }
+      for (int i = 0; i < NB; ++i) {
+        mbar_init(summed + 8 * i, 1);
+        mbar_init(taken + 8 * i, PAIR ? 16 : 8);
+      }
+      mbar_init(done, 1);
+      gave_up = 0;
+      mbar_init_fence();
+    }
+    __syncwarp();
+    tmem_alloc<PAIR>(smem_addr(&tmem_base), 512);
+    tc_fence_before();
+  }
+  if (warp == 8 && lane == 0) {
+    tensor_map_prefetch(&map_x);
+    tensor_map_prefetch(&map_w);
+  }
+  if constexpr (PAIR) cluster_sync_all();
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait_and_release();
+
+  if (warp >= 8) {
+    if constexpr (PAIR) registers_less<40>();
+    if (warp == 8 && lane == 0) {
+      const uint64_t policy = l2_evict_normal();
+      const uint32_t bytes = (PAIR ? 2 * Tile::kStageA : Tile::kStageA) + static_cast<uint32_t>(p.columns) * 128;
+      const uint32_t counted = PAIR ? cluster_addr(full, 0) : full;  // the first CTA counts both CTAs' copies
+      int i = 0;  // stages so far
+      bool fine = true;
+      for (int tile = first; tile < p.tiles && fine; tile += step) {
+        int32_t m0, n0;
+        place(tile, m0, n0);
+        const int32_t w0 = n0 + (PAIR ? rank * (p.columns / 2) : 0);
+        for (int b = 0; b < nb; ++b, ++i) {
+          const int s = i % NS;
+          fine = mbar_wait(empty + 8 * s, ((i / NS) & 1) ^ 1, &gave_up);
+          if (!fine) break;
+          const uint32_t a = smem_addr(ring) + s * kStage;
+          if (rank == 0 || !PAIR) mbar_expect(full + 8 * s, bytes);
+          if constexpr (PAIR) {
+            tensor_load_2d_pair(a, &map_x, (b0 + b) * 128, m0, counted + 8 * s, policy);
+            tensor_load_2d_pair(a + Tile::kStageA, &map_w, (b0 + b) * 128, w0, counted + 8 * s, policy);
+          } else {
+            tensor_load_2d(a, &map_x, (b0 + b) * 128, m0, counted + 8 * s, policy);
+            tensor_load_2d(a + Tile::kStageA, &map_w, (b0 + b) * 128, w0, counted + 8 * s, policy);
+          }
+        }
+      }
+      if (stalled() && (rank == 0 || !PAIR))
+        for (int j = max(0, i - NS); j < i; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
+    }
+    if (warp == 9 && (rank == 0 || !PAIR)) {
+      const uint32_t kind = e4m3_product(PAIR ? 256 : 128, p.columns);
+      const uint64_t ring_a = operand_of(smem_addr(ring)), ring_b = operand_of(smem_addr(ring) + Tile::kStageA);
+      int s = 0, buf = 0;
+      uint32_t s_phase = 0, buf_phase = 1;
+      bool fine = true;
+      for (int tile = first; tile < p.tiles && fine; tile += step) {
+        for (int b = 0; b < nb; ++b) {
+          fine = mbar_wait(taken + 8 * buf, buf_phase, &gave_up) && mbar_wait(full + 8 * s, s_phase, &gave_up);
+          if (!fine) break;
+          tc_fence_after();
+          if (elected()) {
+            const uint32_t d = tmem + buf * Tile::kMaxColumns;
+            const uint64_t a = ring_a + s * (kStage >> 4), w = ring_b + s * (kStage >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_e4m3<PAIR>(d, a + 2 * k, w + 2 * k, kind, k > 0);
+            mma_commit<PAIR>(empty + 8 * s);
+            mma_commit<PAIR>(summed + 8 * buf);
+          }
+          __syncwarp();
+          if (++s == NS) s = 0, s_phase ^= 1;
+          if (++buf == NB) buf = 0, buf_phase ^= 1;
+        }
+      }
+      if (stalled() && elected()) {
+        mma_commit<PAIR>(done);
+        mbar_drain(done, 0);
+      }
+    }
+  } else {
+    if constexpr (PAIR) registers_more<232>();
+    const int quarter = warp & 3, half = warp >> 2;
+    const int all = p.columns / 32, c0 = half ? (all + 1) / 2 : 0, chunks = half ? all / 2 : (all + 1) / 2;
+    const uint32_t counted = PAIR ? cluster_addr(taken, 0) : taken;
+    const int row = quarter * 32 + lane;
+    // four blocks' scales are fetched while the four before them are used (registers that
+    // moved on with every block would wait for the newest): the row's, and in lane 8 u + j
+    // that of the warp's chunk j of the columns in block u
+    float xs[4], ws;
+    const float *x_from = p.x_scale, *w_from = p.w_scale;
+    bool x_there = false, w_there = false;
+    const auto fetch = [&](int i0) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) xs[u] = x_there && i0 + u < nb ? x_from[i0 + u] : 0.0f;
+      ws = w_there && i0 + (lane >> 3) < nb ? w_from[i0 + (lane >> 3)] : 0.0f;
+    };
+    const auto release = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_remote(counted + 8 * buf);
+        else mbar_arrive(counted + 8 * buf);
+      }
+    };
+    const auto scales_at = [&](int32_t m0, int32_t n0) {
+      const int n = n0 + 32 * (c0 + (lane & 7));
+      x_there = m0 + row < p.n_rows;
+      w_there = (lane & 7) < chunks && n < p.out_dim;
+      x_from = p.x_scale + (m0 + row) * p.x_scale_stride + b0;
+      w_from = p.w_scale + (n >> 7) * p.w_scale_stride + b0;
+      fetch(0);
+    };
+    int i = 0;
+    bool fine = true;
+    int32_t m0 = 0, n0 = 0;
+    if (first < p.tiles) {
+      place(first, m0, n0);
+      scales_at(m0, n0);
+    }
+    for (int tile = first; tile < p.tiles && fine; tile += step) {
+      uint64_t acc[CH][16];
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int c = 0; c < 16; ++c) acc[j][c] = 0;
+      for (int g = 0; g < nb && fine; g += 4) {
+        float x_now[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x_now[u] = xs[u];
+        const float w_now = ws;
+        fetch(g + 4);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (g + u >= nb || !fine) continue;
+          const int buf = i % NB;
+          uint64_t scale[CH];
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            const float f = x_now[u] * __shfl_sync(0xFFFFFFFFu, w_now, 8 * u + j);
+            scale[j] = pair_of(f, f);
+          }
+          fine = __all_sync(0xFFFFFFFFu, mbar_wait(summed + 8 * buf, (i / NB) & 1, &gave_up));
+          ++i;
+          if (!fine) continue;
+          tc_fence_after();
+          const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * Tile::kMaxColumns + 32 * c0;
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            if (j >= chunks) continue;
+            float v[32];
+            tmem_load(from + 32 * j, v);
+            tmem_load_wait(v);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) acc[j][c] = fma2(pair_of(v[2 * c], v[2 * c + 1]), scale[j], acc[j][c]);
+          }
+          release(buf);
+        }
+      }
+      if (!fine) break;
+      if constexpr (PAIR) {
+        const int32_t m_now = m0, n_now = n0;
+        if (tile + step < p.tiles) {
+          place(tile + step, m0, n0);
+          scales_at(m0, n0);
+        }
+        // a chunk's 32 x 32 outputs through the warp's own 4 KB, so that rows are stored in
+        // segments of 64 or 128 bytes (16-byte columns are swapped by row: no bank twice)
+        float *staging = reinterpret_cast<float *>(ring + NS * kStage) + warp * 1024;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          if (j >= chunks) continue;
+          const int32_t n = n_now + 32 * (c0 + j);
+          const int32_t m = m_now + quarter * 32;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float4 f;
+            parts_of(acc[j][2 * c], f.x, f.y);
+            parts_of(acc[j][2 * c + 1], f.z, f.w);
+            reinterpret_cast<float4 *>(staging)[lane * 8 + (c ^ (lane & 7))] = f;
+          }
+          __syncwarp();
+          const int rows = min(32, p.n_rows - m);
+          if (p.wide_out && n + 32 <= p.out_dim) {
+            if (p.out_f32) {
+#pragma unroll 1
+              for (int r0 = 0; r0 < 32; r0 += 4) {
+                const int r = r0 + (lane >> 3), c = lane & 7;
+                if (r < rows)
+                  *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + (m + r) * p.out_stride + n + 4 * c) =
+                      reinterpret_cast<const float4 *>(staging)[r * 8 + (c ^ (r & 7))];
+              }
+            } else {
+#pragma unroll 1
+              for (int r0 = 0; r0 < 32; r0 += 8) {
+                const int r = r0 + (lane >> 2), c = 2 * (lane & 3);
+                if (r < rows) {
+                  const float4 f = reinterpret_cast<const float4 *>(staging)[r * 8 + (c ^ (r & 7))];
+                  const float4 g = reinterpret_cast<const float4 *>(staging)[r * 8 + ((c + 1) ^ (r & 7))];
+                  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (m + r) * p.out_stride + n + 4 * c) =
+                      make_uint4(bf16x2_of(f.x, f.y), bf16x2_of(f.z, f.w), bf16x2_of(g.x, g.y), bf16x2_of(g.z, g.w));
+                }
+              }
+            }
+          } else {
+            for (int r = 0; r < rows; ++r) {
+              const float f = staging[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)];
+              if (n + lane < p.out_dim) {
+                if (p.out_f32) static_cast<float *>(p.out)[(m + r) * p.out_stride + n + lane] = f;
+                else static_cast<uint16_t *>(p.out)[(m + r) * p.out_stride + n + lane] = bf16_of(f);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+        // the tile's products have read the ring: it holds the sums now, row by row
+        float *sums = reinterpret_cast<float *>(ring) + row * Tile::kPitch;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          if (j >= chunks) continue;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float4 f;
+            parts_of(acc[j][2 * c], f.x, f.y);
+            parts_of(acc[j][2 * c + 1], f.z, f.w);
+            reinterpret_cast<float4 *>(sums + 32 * (c0 + j))[c] = f;
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if constexpr (!PAIR) {
+    if (split > 1) cluster_sync_all();
+    else __syncthreads();
+    int lost = stalled();
+    for (int q = 0; split > 1 && q < split; ++q) lost |= static_cast<int>(dsmem_ld_u32(dsmem_addr(&gave_up, q)));
+    if (warp < 8 && first < p.tiles && !lost) {
+      int32_t m0, n0;
+      place(first, m0, n0);
+      const float *sums = reinterpret_cast<const float *>(ring);
+      // rows in turn over the cluster's CTAs and their warps, four columns per lane; the
+      // CTAs' sums are added in rank order
+      const int c = 4 * lane;
+      for (int r = rank * 8 + warp; r < 128 && m0 + r < p.n_rows; r += 8 * split) {
+        if (c >= p.columns) continue;
+        float f[4];
+        if (split == 1) {
+          const float4 v = *reinterpret_cast<const float4 *>(sums + r * Tile::kPitch + c);
+          f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+        } else {
+          uint4 v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (q < split) v[q] = dsmem_ld_v4(dsmem_addr(sums + r * Tile::kPitch + c, q));
+          f[0] = f[1] = f[2] = f[3] = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (q < split) {
+              f[0] += __uint_as_float(v[q].x);
+              f[1] += __uint_as_float(v[q].y);
+              f[2] += __uint_as_float(v[q].z);
+              f[3] += __uint_as_float(v[q].w);
+            }
+        }
+        const int32_t n = n0 + c;
+        if (p.out_f32) {
+          float *to = static_cast<float *>(p.out) + (m0 + r) * p.out_stride + n;
+          if (p.wide_out && n + 4 <= p.out_dim) {
+            *reinterpret_cast<float4 *>(to) = make_float4(f[0], f[1], f[2], f[3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < p.out_dim) to[e] = f[e];
+          }
+        } else {
+          uint16_t *to = static_cast<uint16_t *>(p.out) + (m0 + r) * p.out_stride + n;
+          if (p.wide_out && n + 4 <= p.out_dim) {
+            *reinterpret_cast<uint2 *>(to) = make_uint2(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < p.out_dim) to[e] = bf16_of(f[e]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  if (shared_by > 1) cluster_sync_all();  // no CTA leaves while another needs its memory
+  else __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_free<PAIR>(tmem, 512);
   if (t == 0 && stalled()) atomicOr(p.status, kRowStalled);
 }
 

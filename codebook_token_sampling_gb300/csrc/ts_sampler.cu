@@ -672,6 +672,8 @@ ts_status ts_create(int device, int max_top_k, ts_sampler **out) {
   s->kv_ctas = 0;
   s->kv_join = 0;
   s->linear_split = 0;
+  s->linear_path = 0;
+  s->linear_pairs = 0;
   ts_status rc = TS_OK;
   e = cudaDeviceGetAttribute(&s->num_sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) rc = cuda_fail(e, "cudaDeviceGetAttribute");
@@ -687,7 +689,7 @@ ts_status ts_create(int device, int max_top_k, ts_sampler **out) {
   }
   if (rc == TS_OK) rc = set_attributes(device);
   if (rc == TS_OK) rc = warp_occupancy(s);
-  if (rc == TS_OK) rc = ts_host::linear_setup();
+  if (rc == TS_OK) rc = ts_host::linear_setup(s);
   cudaSetDevice(prev);
   if (rc != TS_OK) {
     if (s->status) cudaFree(s->status);
@@ -966,6 +968,11 @@ ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value) {
   if (option == TS_OPT_LINEAR_SPLIT) {
     if (value != 0 && value != 1 && value != 2 && value != 4 && value != 8) return TS_ERR_INVALID_ARG;
     s->linear_split = value;
+    return TS_OK;
+  }
+  if (option == TS_OPT_LINEAR_PATH) {
+    if (value < 0 || value > 3) return TS_ERR_INVALID_ARG;
+    s->linear_path = value;
     return TS_OK;
   }
   if (option == TS_OPT_FAIL_LAUNCH) {

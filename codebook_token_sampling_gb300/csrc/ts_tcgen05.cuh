@@ -36,37 +36,41 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase of the given parity to end, kWaitNs at most; false where it did
-// not, or where another wait of the CTA gave up.
-constexpr uint64_t kWaitNs = 2000000000ull;
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t ns;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(ns));
-  return ns;
-}
-__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *gave_up) {
-  const uint64_t start = global_ns();
-  do {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try(bar, parity)) return true;
-    if (*gave_up) return false;
-  } while (global_ns() - start < kWaitNs);
-  *gave_up = 1;
-  return false;
-}
+// Waits for the phase of the given parity to end, kWaitCycles (about two seconds) at
+// most; false where it did not, or where another wait of the CTA gave up.  (No calls: a
+// call would spill what the caller holds in registers.  And no %globaltimer, whose
+// reading takes about 2000 cycles.)
+constexpr long long kWaitCycles = 4000000000ll;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+  if (mbar_try(bar, parity)) return true;
+  const long long start = clock64();
 #pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try(bar, parity)) return true;
-  return mbar_wait_long(bar, parity, gave_up);
+  for (int i = 1; !mbar_try(bar, parity); ++i) {
+    if ((i & 63) == 0 && (*gave_up || clock64() - start > kWaitCycles)) {
+      *gave_up = 1;
+      return false;
+    }
+  }
+  return true;
 }
 // The same for copies or products that a CTA waits for after it gave up: they come to
-// their end before it leaves, within kWaitNs.
-__device__ __noinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-  const uint64_t start = global_ns();
-  while (!mbar_try(bar, parity) && global_ns() - start < kWaitNs) {
+// their end before it leaves, within kWaitCycles.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const long long start = clock64();
+  while (!mbar_try(bar, parity) && clock64() - start < kWaitCycles) {
   }
+}
+
+// An arrival at a barrier of another CTA of the cluster (its address from cluster_addr).
+// It orders nothing in memory for that CTA: what it says is that TMEM has been read
+// (released at the cluster's scope it takes about 2000 cycles).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+  return r;
 }
 
 // ---- tensor copies ----
@@ -83,20 +87,50 @@ __device__ __forceinline__ void tensor_load_2d(uint32_t dst, const CUtensorMap *
       "l"(m), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
+// The same from one CTA of a pair, counted by a barrier of either.
+__device__ __forceinline__ void tensor_load_2d_pair(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y,
+                                                    uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ uint64_t l2_evict_normal() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
   return pol;
 }
 
-// ---- tensor memory ----
-__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(columns)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+// Registers of a thread from here on, for whole warpgroups (of the launch's own: the
+// warpgroups' shares add up to threads x registers at launch).
+template <int N>
+__device__ __forceinline__ void registers_less() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+template <int N>
+__device__ __forceinline__ void registers_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---- tensor memory ----
+// (PAIR: by a warp of each CTA of the pair, in both)
+template <bool PAIR = false>
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t columns) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+}
+template <bool PAIR = false>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+  if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+  else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -147,28 +181,55 @@ __device__ __forceinline__ void tmem_load_wait(float (&v)[32]) {
 }
 
 // ---- products ----
+// One lane of a whole warp, known as such to the compiler where it is asked for right
+// at the branch: a block's products and commits issued under a test of the lane's number
+// take 420 cycles instead of 130.
+__device__ __forceinline__ bool elected() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
 // An operand tile in shared memory whose rows are 128 bytes along k, in the 128-byte
 // swizzle that a tensor copy leaves: eight rows are 1024 bytes.  `addr` is 1024-byte
-// aligned, plus 32 bytes for each step of 32 elements along k.
+// aligned; a step of 32 elements along k adds 32 bytes, 2 to the operand.
 __device__ __forceinline__ uint64_t operand_of(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
-// fp32 sums of e4m3 products, both operands with k as the fastest dimension, 128 rows
-// and `columns` columns.
-__host__ __device__ constexpr uint32_t e4m3_product(int columns) {
-  return (1u << 4) | (static_cast<uint32_t>(columns / 8) << 17) | (static_cast<uint32_t>(128 / 16) << 24);
+// fp32 sums of e4m3 products, both operands with k as the fastest dimension, `rows` (128,
+// for a pair of CTAs 256) by `columns`.
+__host__ __device__ constexpr uint32_t e4m3_product(int rows, int columns) {
+  return (1u << 4) | (static_cast<uint32_t>(columns / 8) << 17) | (static_cast<uint32_t>(rows / 16) << 24);
 }
+// PAIR: the rows of both CTAs, each with its half of the columns' operand, into both TMEMs.
+template <bool PAIR = false>
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
+        : "memory");
 }
-// `bar` gets an arrival once the products that this thread has issued are done.
+// `bar` (PAIR: that of each CTA of the pair) gets an arrival once the products that this
+// thread has issued are done.
+template <bool PAIR = false>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 }  // namespace ts

@@ -687,11 +687,13 @@ ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream);
  * Rows and columns that x and w do not have are not written.  TS_ERR_INVALID_ARG for
  * a NULL pointer, a misaligned one, a negative n_rows, in_dim or out_dim < 1, a
  * stride below its row (x, out and x_scale of one row: any), or an out that overlaps
- * an input; TS_ERR_UNSUPPORTED for an in_dim above TS_LINEAR_MAX_DIM, a stride of
- * 2^40 or more, or where the driver offers no tensor maps.  A copy that does not come
+ * an input; TS_ERR_UNSUPPORTED for an in_dim above TS_LINEAR_MAX_DIM, n_rows or
+ * out_dim above TS_LINEAR_MAX_ROWS, a stride of 2^40 or more, or where the driver
+ * offers no tensor maps.  A copy that does not come
  * within a kernel's waiting limit (which nothing that the call allows brings about)
  * sets TS_ROW_STALLED and leaves a part of out unwritten. */
 #define TS_LINEAR_MAX_DIM 1048576
+#define TS_LINEAR_MAX_ROWS 2147482624
 #define TS_ROW_STALLED 128u
 typedef struct {
   const void *x;             /* [n_rows][in_dim] */
@@ -830,6 +832,9 @@ ts_status ts_read_status(ts_sampler *s, uint32_t *bits, void *stream);
 /* TS_OPT_LINEAR_SPLIT: the CTAs (a cluster) that share a tile of ts_linear_e4m3
  * along in_dim: 0 = automatic, or 1, 2, 4 or 8. */
 #define TS_OPT_LINEAR_SPLIT 9
+/* TS_OPT_LINEAR_PATH: the kernel of ts_linear_e4m3: 0 = automatic, 1 = tokens as the
+ * products' columns, 2 = tokens as their rows, 3 = the same by pairs of CTAs. */
+#define TS_OPT_LINEAR_PATH 10
 ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value);
 
 /* Describes the kernel that ts_sample would launch for `b` (path 1 .. 4,

@@ -299,11 +299,17 @@ SIZES = [(1, 1, 1), (1, 128, 128), (1, 4096, 1024), (2, 129, 130), (7, 100, 16),
 @pytest.mark.parametrize("out_kind", ["bf16", "f32"])
 @pytest.mark.parametrize("m,n,k", SIZES)
 def test_linear(ts, sampler, m, n, k, out_kind):
+    """Every size by the kernel that it gets, and by each of the others."""
     rng = np.random.default_rng([m, n, k])
     x, xs, w, ws = linear_case(rng, m, n, k)
-    got = run_linear(ts, sampler, x, xs, w, ws, out_kind, pad=(m + n) % 3)
     want, size = olayer.linear(x, xs, w, ws)
-    close(got, want, linear_bound(size, k, out_kind, want))
+    try:
+        for path in range(4):
+            sampler.set_option(ts.TS_OPT_LINEAR_PATH, path)
+            got = run_linear(ts, sampler, x, xs, w, ws, out_kind, pad=(m + n) % 3)
+            close(got, want, linear_bound(size, k, out_kind, want), path)
+    finally:
+        sampler.set_option(ts.TS_OPT_LINEAR_PATH, 0)
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 300, 1100), (30, 260, 4096), (61, 129, 900), (130, 700, 2048), (700, 650, 1500), (1500, 1100, 640)])
@@ -317,10 +323,13 @@ def test_linear_of_whole_numbers(ts, sampler, m, n, k):
     want, size = olayer.linear(cx, xs, cw, ws)
     assert size.max() < 2 ** 24
     try:
-        for split in (0, 1, 2, 4, 8):
-            sampler.set_option(ts.TS_OPT_LINEAR_SPLIT, split)
-            assert np.array_equal(run_linear(ts, sampler, cx, xs, cw, ws, "f32"), want), split
+        for path in range(4):
+            sampler.set_option(ts.TS_OPT_LINEAR_PATH, path)
+            for split in (0, 1, 2, 4, 8):
+                sampler.set_option(ts.TS_OPT_LINEAR_SPLIT, split)
+                assert np.array_equal(run_linear(ts, sampler, cx, xs, cw, ws, "f32"), want), (path, split)
     finally:
+        sampler.set_option(ts.TS_OPT_LINEAR_PATH, 0)
         sampler.set_option(ts.TS_OPT_LINEAR_SPLIT, 0)
 
 
