@@ -140,20 +140,38 @@ ts_status launch_rotary(const ts_sampler *s, const ts_rotary_args *a, ts::Rotary
   p.interleaved = a->interleaved != 0;
   p.in_place = a->x == a->out;
   p.status = s->status;
-  const int64_t per_head = (a->head_dim + 2 * piece - 1) / (2 * piece);
+  const int64_t per_head = (a->head_dim + 2 * piece - 1) / (2 * piece), turned = p.half / piece;
   const int64_t per_token = per_head * (p.heads + 2 * static_cast<int64_t>(p.kv_heads));
   if (per_token > (1 << 23)) return TS_ERR_UNSUPPORTED;
   // whole tokens, about eight units per thread, fewer while SMs would idle
   const int64_t n = a->n_tokens, fill = ts::kRotaryThreads * 8;
   int64_t tokens = std::min<int64_t>(fill / per_token, (n + s->num_sms - 1) / s->num_sms);
   tokens = std::min<int64_t>(tokens, std::min<int64_t>(ts::kRotaryTokens, ts::kRotaryTableFloats / a->rotary_dim));
-  p.tokens_per_cta = static_cast<int32_t>(std::max<int64_t>(1, tokens));
-  p.by_token = ts::FastDiv::of(static_cast<uint32_t>(per_token));
-  p.by_head = ts::FastDiv::of(static_cast<uint32_t>(per_head));
-  const size_t smem = static_cast<size_t>(p.tokens_per_cta) * a->rotary_dim * sizeof(float);
+  tokens = std::max<int64_t>(1, tokens);
+  p.tokens_per_cta = static_cast<int32_t>(tokens);
+  // runs of units: pairs of queries and keys, their other elements, values
+  uint32_t end = 0;
+  const auto add = [&](int k, int which, bool rotates, int64_t heads, int64_t units) {
+    ts::RotaryRun &r = p.run[k];
+    const int64_t all = heads * units;
+    r.first = end;
+    r.which = which;
+    r.rotates = rotates;
+    r.from = which == 2 || rotates ? 0 : a->rotary_dim;
+    r.by_head = ts::FastDiv::of(static_cast<uint32_t>(std::max<int64_t>(1, units)));
+    r.by_token = ts::FastDiv::of(static_cast<uint32_t>(std::max<int64_t>(1, all)));
+    end += static_cast<uint32_t>((tokens * all + 31) / 32 * 32);
+  };
+  add(0, 0, true, p.heads, turned);
+  add(1, 1, true, p.kv_heads, turned);
+  add(2, 0, false, p.in_place ? 0 : p.heads, per_head - turned);
+  add(3, 1, false, p.kv_heads, per_head - turned);
+  add(4, 2, false, p.kv_heads, per_head);
+  p.units = end;
+  const size_t smem = static_cast<size_t>(tokens) * a->rotary_dim * sizeof(float);
   void *args[] = {&p};
-  const cudaError_t e = launch(fn, dim3(static_cast<unsigned>((n + p.tokens_per_cta - 1) / p.tokens_per_cta)),
-                               ts::kRotaryThreads, smem, s->pdl != 0, static_cast<cudaStream_t>(stream), args);
+  const cudaError_t e = launch(fn, dim3(static_cast<unsigned>((n + tokens - 1) / tokens)), ts::kRotaryThreads, smem,
+                               s->pdl != 0, static_cast<cudaStream_t>(stream), args);
   return e == cudaSuccess ? TS_OK : cuda_fail(e, "rotary launch");
 }
 
@@ -214,18 +232,22 @@ ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream) {
   p.eps = a->eps;
   p.weight_offset = a->weight_offset;
 
-  // threads of a row: as few units each as 512 threads allow, then up to 1024 threads
+  // Threads of a row: one unit each up to 512 of them where rows are few, two from 256 units
+  // on where they are many (more loads on their way), more for the widest.
   const int units = static_cast<int>(wide ? (dim + 7) / 8 : scales_of(dim) * 32);
-  int v = 1;
-  while (v < 2 && units > 512 * v) v *= 2;
-  while (units > 1024 * v) v *= 2;
+  const bool many = n > 4 * s->num_sms;
+  int v = units > 512 || (many && units > 128) ? 2 : 1;
+  if (units > 1024) v = units > 4096 ? 8 : 4;
   const int threads = ((units + v - 1) / v + 31) / 32 * 32;
   const int rows = threads == 32 ? 8 : 1;
+  // as many CTAs as the GPU holds (64 registers a thread)
+  const int64_t ctas = std::min<int64_t>((n + rows - 1) / rows,
+                                         static_cast<int64_t>(s->num_sms) * std::max(1, 1024 / (threads * rows)));
   const void *fn = a->dtype == TS_DTYPE_F32 ? norm_kernel_to<float>(a->out_dtype, v, wide)
                                             : norm_kernel_to<uint16_t>(a->out_dtype, v, wide);
   void *args[] = {&p};
   const cudaError_t e =
-      launch(fn, dim3(static_cast<unsigned>((n + rows - 1) / rows)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(rows)),
+      launch(fn, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(rows)),
              0, s->pdl != 0, static_cast<cudaStream_t>(stream), args);
   return e == cudaSuccess ? TS_OK : cuda_fail(e, "norm launch");
 }
@@ -336,7 +358,7 @@ ts_status ts_kv_append_rotary(ts_sampler *s, const ts_kv_cache *c, const ts_kv_t
   p.scale[0] = c->k_scale;
   p.scale[1] = c->v_scale;
   p.slots = t->slots;
-  p.block_size = c->block_size;
+  p.by_block = ts::FastDiv::of(static_cast<uint32_t>(c->block_size));
   p.n_slots = static_cast<int64_t>(c->n_blocks) * c->block_size;
   p.kv_heads = c->n_kv_heads;
   const int piece = piece_of(a, t, queries);

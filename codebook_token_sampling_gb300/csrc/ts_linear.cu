@@ -53,7 +53,7 @@ LinearKernel kernel_for(int i) {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t blocks_of(int64_t dim) { return ceil_div(dim, TS_SCALE_BLOCK); }
 
-// What a call launches: the kernel, its tile (rows of x by weight rows) and the CTAs
+// What a call launches: the kernel, its tile (rows of x by weight rows), and the CTAs
 // that share one along in_dim.
 struct LinearPlan {
   int kernel, rows, columns, split;
@@ -71,30 +71,34 @@ LinearPlan plan_few(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
   plan.split = split_for(ceil_div(n, 128) * ceil_div(m, plan.rows), blocks, s->num_sms);
   return plan;
 }
-LinearPlan plan_rows(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
-  // the least time by a count of what a CTA takes in (48 bytes per cycle) and of the
-  // cycles around it
-  LinearPlan best = {3, 128, 128, 1};
-  double least = 1e30;
+// The least cycles by what a tile takes: for each block the chain from its copy to its
+// sums (590 for 128 tokens by 96, 1080 for a pair's 256 by 256), or what all CTAs take in
+// through L2 together (about 5000 bytes a cycle); and about 9000 around them.  4096 x 4096
+// weights: 512 rows 16 us (pairs 19), 1024 rows 20 by pairs (33); 2048 x 2048 and 2048
+// rows 12 by pairs (21).
+LinearPlan plan_rows(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks, bool pairs) {
+  const double pair_waves = static_cast<double>(ceil_div(ceil_div(m, 256) * ceil_div(n, 256), s->linear_pairs));
+  LinearPlan best = {4, 256, 256, 1};
+  double least = pairs ? pair_waves * blocks * 1080.0 + 8000.0 : 1e30;
   for (int columns = 32; columns <= 128; columns += 32) {
     const int64_t tiles = ceil_div(m, 128) * ceil_div(n, columns);
     const int split = split_for(tiles, blocks, s->num_sms);
     const double waves = static_cast<double>(ceil_div(tiles * split, s->num_sms));
-    const double cycles = waves * (ceil_div(blocks, split) * (128 + columns) * 128 / 48.0 + 3000.0);
-    if (cycles <= least) {
+    const double at_once = static_cast<double>(std::min<int64_t>(tiles * split, s->num_sms));
+    const double block = std::max(350.0 + 2.5 * columns, (128.0 + columns) * 128.0 * at_once / 5000.0);
+    const double cycles = waves * (ceil_div(blocks, split) * block + 5000.0 + 40.0 * columns);
+    if (cycles < least) {
       least = cycles;
-      best.columns = columns;
-      best.split = split;
+      best = {3, 128, columns, split};
     }
   }
   return best;
 }
 LinearPlan plan_for(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
-  const int64_t pairs = ceil_div(m, 256) * ceil_div(n, 256);
-  const int path = s->linear_path ? s->linear_path : m <= 64 ? 1 : pairs >= s->num_sms / 2 ? 3 : 2;
-  LinearPlan plan = path == 1 ? plan_few(s, m, n, blocks)
-                  : path == 2 ? plan_rows(s, m, n, blocks) : LinearPlan{4, 256, 256, 1};
-  if (s->linear_split && path != 3) {
+  const int path = s->linear_path;
+  LinearPlan plan = path == 1 || (path == 0 && m <= 64) ? plan_few(s, m, n, blocks)
+                  : path == 3 ? LinearPlan{4, 256, 256, 1} : plan_rows(s, m, n, blocks, path == 0);
+  if (s->linear_split && plan.kernel != 4) {
     plan.split = s->linear_split;
     while (plan.split > blocks) plan.split /= 2;
   }
@@ -203,7 +207,7 @@ extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void
     return TS_ERR_UNSUPPORTED;
 
   const int cluster = pair ? 2 : plan.split;
-  const int64_t grid = pair ? 2 * std::min<int64_t>(tiles, s->linear_pairs) : tiles * plan.split;
+  const int64_t grid = pair ? 2 * std::min<int64_t>(tiles, s->linear_pairs) : tiles * cluster;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(static_cast<unsigned>(grid));

@@ -28,15 +28,16 @@ struct LinearParams {
 // tile costs no more columns than there are tokens (sixteen at least).  A tensor-copy
 // warp streams stages of one block of 128 along in_dim (weights and tokens, 128 bytes
 // a row, swizzled) through a ring; one thread of another warp issues a stage's four
-// products into one of four accumulators in TMEM; four warps add each block's sums,
-// times its scales, to fp32 sums in registers (row = lane).  CTAs of a cluster may
+// products into one of eight accumulators in TMEM; four warps add four blocks' sums at a
+// time, times their scales, to fp32 sums in registers (row = lane).  CTAs of a cluster may
 // share a tile along in_dim; their sums are added in rank order through shared memory.
 template <int TN>
 struct FewTile {
   static constexpr int kStageA = 128 * 128, kStageB = TN * 128;
   static constexpr int kStages = TN == 16 ? 11 : TN == 32 ? 10 : 8;
-  static constexpr int kBuffers = 4;
-  static constexpr uint32_t kColumns = kBuffers * TN;  // of TMEM: a power of two, 32 at least
+  static constexpr int kGroup = 4;  // blocks that the warps are told of at once (see below)
+  static constexpr int kBuffers = 2;  // of a group's accumulators
+  static constexpr uint32_t kColumns = kBuffers * kGroup * TN;  // of TMEM: a power of two, 32 at least
   static constexpr uint32_t kSmemBytes = kStages * (kStageA + kStageB) + 1024;
 };
 constexpr int kFewThreads = 192;
@@ -46,11 +47,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                       const LinearParams p) {
   using Tile = FewTile<TN>;
-  constexpr int NS = Tile::kStages, NB = Tile::kBuffers;
+  constexpr int NS = Tile::kStages, NB = Tile::kBuffers, G = Tile::kGroup;
   constexpr int kPer = (TN + 31) / 32;  // tokens whose scales a lane fetches
   extern __shared__ unsigned char linear_smem[];
   __shared__ __align__(8) uint64_t bars[2 * NS + 2 * NB + 1];
-  __shared__ __align__(16) float scales[4][2][TN];
+  __shared__ __align__(16) float scales[4][4][TN];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
   const int t = static_cast<int>(threadIdx.x), lane = t & 31;
@@ -100,40 +101,48 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   for (int c = 0; c < TN; ++c) acc[c] = 0.0f;
 
   if (warp == 4) {
-    if (lane == 0) {
-      const uint64_t again = l2_evict_normal();
-      // weights that no other tile reads leave L2 to the rest
-      const uint64_t w_policy = p.n_rows <= TN ? l2_evict_first() : again;
-      int i = 0;
-      for (; i < nb; ++i) {
-        const int s = i % NS;
-        if (!mbar_wait(empty + 8 * s, ((i / NS) & 1) ^ 1, &gave_up)) break;
-        const uint32_t a = smem_addr(ring) + s * (Tile::kStageA + Tile::kStageB);
-        mbar_expect(full + 8 * s, Tile::kStageA + Tile::kStageB);
-        tensor_load_2d(a, &map_w, (b0 + i) * 128, n0, full + 8 * s, w_policy);
-        tensor_load_2d(a + Tile::kStageA, &map_x, (b0 + i) * 128, m0, full + 8 * s, again);
+    const uint64_t again = l2_evict_normal();
+    // weights that no other tile reads leave L2 to the rest
+    const uint64_t w_policy = p.n_rows <= TN ? l2_evict_first() : again;
+    int s = 0, issued = 0;
+    uint32_t phase = 1;
+    for (int i = 0; i < nb; ++i) {
+      mbar_wait(empty + 8 * s, phase, &gave_up);
+      const bool go = !stalled();
+      issued += go;
+      if (elected() && go) {
+        const uint32_t a = smem_addr(ring) + s * (Tile::kStageA + Tile::kStageB), bar = full + 8 * s;
+        mbar_expect(bar, Tile::kStageA + Tile::kStageB);
+        tensor_load_2d(a, &map_w, (b0 + i) * 128, n0, bar, w_policy);
+        tensor_load_2d(a + Tile::kStageA, &map_x, (b0 + i) * 128, m0, bar, again);
       }
-      if (stalled())
-        for (int j = max(0, i - NS); j < i; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
+      __syncwarp();
+      if (++s == NS) s = 0, phase ^= 1;
     }
+    if (stalled() && elected())
+      for (int j = max(0, issued - NS); j < issued; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
   } else if (warp == 5) {
     constexpr uint32_t kind = e4m3_product(128, TN);
     const uint64_t ring_a = operand_of(smem_addr(ring)), ring_b = operand_of(smem_addr(ring) + Tile::kStageA);
     int s = 0, b = 0;
     uint32_t s_phase = 0, b_phase = 1;
-    for (int i = 0; i < nb; ++i) {
-      if (!mbar_wait(taken + 8 * b, b_phase, &gave_up) || !mbar_wait(full + 8 * s, s_phase, &gave_up)) break;
-      tc_fence_after();
-      if (elected()) {
-        const uint64_t a = ring_a + s * ((Tile::kStageA + Tile::kStageB) >> 4);
-        const uint64_t x = ring_b + s * ((Tile::kStageA + Tile::kStageB) >> 4);
+    for (int g = 0; g < nb; g += G) {
+      mbar_wait(taken + 8 * b, b_phase, &gave_up);
+      const int count = min(G, nb - g);
+      for (int u = 0; u < count; ++u) {
+        mbar_wait(full + 8 * s, s_phase, &gave_up);
+        tc_fence_after();
+        if (elected()) {
+          const uint64_t a = ring_a + s * ((Tile::kStageA + Tile::kStageB) >> 4);
+          const uint64_t x = ring_b + s * ((Tile::kStageA + Tile::kStageB) >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_e4m3(tmem + b * TN, a + 2 * k, x + 2 * k, kind, k > 0);
-        mma_commit(empty + 8 * s);
-        mma_commit(summed + 8 * b);
+          for (int k = 0; k < 4; ++k) mma_e4m3(tmem + (b * G + u) * TN, a + 2 * k, x + 2 * k, kind, k > 0);
+          mma_commit(empty + 8 * s);
+          if (u == count - 1) mma_commit(summed + 8 * b);
+        }
+        __syncwarp();
+        if (++s == NS) s = 0, s_phase ^= 1;
       }
-      __syncwarp();
-      if (++s == NS) s = 0, s_phase ^= 1;
       if (++b == NB) b = 0, b_phase ^= 1;
     }
     if (stalled() && elected()) {
@@ -156,32 +165,32 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
     };
     fetch(0);
-    bool fine = true;
-    for (int i0 = 0; i0 < nb && fine; i0 += 4) {
+    for (int i0 = 0; i0 < nb; i0 += 4) {
       float now[4][kPer];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int q = 0; q < kPer; ++q) now[u][q] = xs[u][q] * ws[u];
       fetch(i0 + 4);
-#pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u, b = i % NB;
-        if (i >= nb || !fine) continue;
-        float *sc = scales[warp][i & 1];
+        float *sc = scales[warp][u];
 #pragma unroll
         for (int q = 0; q < kPer; ++q)
           if (lane + 32 * q < TN) sc[lane + 32 * q] = now[u][q];
-        __syncwarp();
-        fine = mbar_wait(summed + 8 * b, (i / NB) & 1, &gave_up);
-        fine = __all_sync(0xFFFFFFFFu, fine);
-        if (!fine) continue;
-        tc_fence_after();
+      }
+      __syncwarp();
+      const int b = (i0 / G) % NB;
+      mbar_wait(summed + 8 * b, (i0 / G / NB) & 1, &gave_up);
+      tc_fence_after();
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        if (i0 + u >= nb) continue;
+        const float *sc = scales[warp][u];
         constexpr int C = TN < 32 ? 16 : 32;
 #pragma unroll
         for (int c0 = 0; c0 < TN; c0 += C) {
           float v[C];
-          tmem_load(tmem + (static_cast<uint32_t>(warp * 32) << 16) + b * TN + c0, v);
+          tmem_load(tmem + (static_cast<uint32_t>(warp * 32) << 16) + (b * G + u) * TN + c0, v);
           tmem_load_wait(v);
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
@@ -192,10 +201,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             acc[c0 + c + 3] = fmaf(v[c + 3], f.w, acc[c0 + c + 3]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(taken + 8 * b);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(taken + 8 * b);
     }
   }
   __syncwarp();
@@ -271,7 +280,11 @@ struct RowsTile {
   static constexpr int kMaxColumns = 64 * CH;
   static constexpr int kStageA = 128 * 128, kStageB = (PAIR ? kMaxColumns / 2 : kMaxColumns) * 128;
   static constexpr int kStages = 196608 / (kStageA + kStageB);
-  static constexpr int kBuffers = 512 / kMaxColumns;
+  // Blocks that the adding warps are told of at once.  Waits, commits and arrivals cost a
+  // block about 500 cycles, as much as its products: a tile of 256 columns has no room for
+  // more than two blocks' sums, narrower ones have.
+  static constexpr int kGroup = PAIR ? 1 : 2;
+  static constexpr int kBuffers = 512 / kMaxColumns / kGroup;
   static constexpr int kStaging = PAIR ? 8 * 32 * 32 * 4 : 0;  // a warp's 32 x 32 outputs
   static constexpr int kPitch = kMaxColumns + 4;               // floats from a tile's row to the next
   static constexpr uint32_t kSmemBytes = kStages * (kStageA + kStageB) + kStaging + 1024;
@@ -286,7 +299,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     linear_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const LinearParams p) {
   using Tile = RowsTile<CH, PAIR>;
-  constexpr int NS = Tile::kStages, NB = Tile::kBuffers, kStage = Tile::kStageA + Tile::kStageB;
+  constexpr int NS = Tile::kStages, NB = Tile::kBuffers, G = Tile::kGroup, kStage = Tile::kStageA + Tile::kStageB;
   extern __shared__ unsigned char linear_smem[];
   __shared__ __align__(8) uint64_t bars[2 * NS + 2 * NB + 1];
   __shared__ uint32_t tmem_base;
@@ -303,8 +316,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const int rank = shared_by > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int first = static_cast<int>(blockIdx.x) / shared_by, step = static_cast<int>(gridDim.x) / shared_by;
   const int split = PAIR ? 1 : p.split;
-  const int b0 = PAIR ? 0 : static_cast<int>(static_cast<int64_t>(p.blocks) * rank / split);
-  const int nb = PAIR ? p.blocks : static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / split) - b0;
+  const int b0 = split == 1 ? 0 : static_cast<int>(static_cast<int64_t>(p.blocks) * rank / split);
+  const int nb = split == 1 ? p.blocks : static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / split) - b0;
   // neighbouring tiles share their weights: sixteen tiles of tokens before the next columns
   const auto place = [&](int tile, int32_t &m0, int32_t &n0) {
     const int per = p.tiles_n * 16, group = tile / per, in = tile - group * per;
@@ -335,7 +348,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     tensor_map_prefetch(&map_x);
     tensor_map_prefetch(&map_w);
   }
-  if constexpr (PAIR) cluster_sync_all();
+  if constexpr (PAIR) cluster_sync_all();  // the other's barriers are there
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
@@ -343,55 +356,61 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 
   if (warp >= 8) {
     if constexpr (PAIR) registers_less<40>();
-    if (warp == 8 && lane == 0) {
+    if (warp == 8) {
       const uint64_t policy = l2_evict_normal();
       const uint32_t bytes = (PAIR ? 2 * Tile::kStageA : Tile::kStageA) + static_cast<uint32_t>(p.columns) * 128;
       const uint32_t counted = PAIR ? cluster_addr(full, 0) : full;  // the first CTA counts both CTAs' copies
-      int i = 0;  // stages so far
-      bool fine = true;
-      for (int tile = first; tile < p.tiles && fine; tile += step) {
+      int s = 0, issued = 0;
+      uint32_t phase = 1;
+      for (int tile = first; tile < p.tiles; tile += step) {
         int32_t m0, n0;
         place(tile, m0, n0);
         const int32_t w0 = n0 + (PAIR ? rank * (p.columns / 2) : 0);
-        for (int b = 0; b < nb; ++b, ++i) {
-          const int s = i % NS;
-          fine = mbar_wait(empty + 8 * s, ((i / NS) & 1) ^ 1, &gave_up);
-          if (!fine) break;
-          const uint32_t a = smem_addr(ring) + s * kStage;
-          if (rank == 0 || !PAIR) mbar_expect(full + 8 * s, bytes);
-          if constexpr (PAIR) {
-            tensor_load_2d_pair(a, &map_x, (b0 + b) * 128, m0, counted + 8 * s, policy);
-            tensor_load_2d_pair(a + Tile::kStageA, &map_w, (b0 + b) * 128, w0, counted + 8 * s, policy);
-          } else {
-            tensor_load_2d(a, &map_x, (b0 + b) * 128, m0, counted + 8 * s, policy);
-            tensor_load_2d(a + Tile::kStageA, &map_w, (b0 + b) * 128, w0, counted + 8 * s, policy);
+        for (int b = b0; b < b0 + nb; ++b) {
+          mbar_wait(empty + 8 * s, phase, &gave_up);
+          const bool go = !stalled();
+          issued += go;
+          if (elected() && go) {
+            const uint32_t a = smem_addr(ring) + s * kStage;
+            if (rank == 0 || !PAIR) mbar_expect(full + 8 * s, bytes);
+            if constexpr (PAIR) {
+              tensor_load_2d_pair(a, &map_x, b * 128, m0, counted + 8 * s, policy);
+              tensor_load_2d_pair(a + Tile::kStageA, &map_w, b * 128, w0, counted + 8 * s, policy);
+            } else {
+              tensor_load_2d(a, &map_x, b * 128, m0, counted + 8 * s, policy);
+              tensor_load_2d(a + Tile::kStageA, &map_w, b * 128, w0, counted + 8 * s, policy);
+            }
           }
+          __syncwarp();
+          if (++s == NS) s = 0, phase ^= 1;
         }
       }
-      if (stalled() && (rank == 0 || !PAIR))
-        for (int j = max(0, i - NS); j < i; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
+      if (stalled() && (rank == 0 || !PAIR) && elected())
+        for (int j = max(0, issued - NS); j < issued; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
     }
     if (warp == 9 && (rank == 0 || !PAIR)) {
       const uint32_t kind = e4m3_product(PAIR ? 256 : 128, p.columns);
       const uint64_t ring_a = operand_of(smem_addr(ring)), ring_b = operand_of(smem_addr(ring) + Tile::kStageA);
       int s = 0, buf = 0;
       uint32_t s_phase = 0, buf_phase = 1;
-      bool fine = true;
-      for (int tile = first; tile < p.tiles && fine; tile += step) {
-        for (int b = 0; b < nb; ++b) {
-          fine = mbar_wait(taken + 8 * buf, buf_phase, &gave_up) && mbar_wait(full + 8 * s, s_phase, &gave_up);
-          if (!fine) break;
-          tc_fence_after();
-          if (elected()) {
-            const uint32_t d = tmem + buf * Tile::kMaxColumns;
-            const uint64_t a = ring_a + s * (kStage >> 4), w = ring_b + s * (kStage >> 4);
+      for (int tile = first; tile < p.tiles; tile += step) {
+        for (int g = 0; g < nb; g += G) {
+          mbar_wait(taken + 8 * buf, buf_phase, &gave_up);
+          const int count = G == 1 ? 1 : min(G, nb - g);
+          for (int u = 0; u < count; ++u) {
+            mbar_wait(full + 8 * s, s_phase, &gave_up);
+            tc_fence_after();
+            if (elected()) {
+              const uint32_t d = tmem + (buf * G + u) * Tile::kMaxColumns;
+              const uint64_t a = ring_a + s * (kStage >> 4), w = ring_b + s * (kStage >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_e4m3<PAIR>(d, a + 2 * k, w + 2 * k, kind, k > 0);
-            mma_commit<PAIR>(empty + 8 * s);
-            mma_commit<PAIR>(summed + 8 * buf);
+              for (int k = 0; k < 4; ++k) mma_e4m3<PAIR>(d, a + 2 * k, w + 2 * k, kind, k > 0);
+              mma_commit<PAIR>(empty + 8 * s);
+              if (u == count - 1) mma_commit<PAIR>(summed + 8 * buf);
+            }
+            __syncwarp();
+            if (++s == NS) s = 0, s_phase ^= 1;
           }
-          __syncwarp();
-          if (++s == NS) s = 0, s_phase ^= 1;
           if (++buf == NB) buf = 0, buf_phase ^= 1;
         }
       }
@@ -434,52 +453,57 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       fetch(0);
     };
     int i = 0;
-    bool fine = true;
     int32_t m0 = 0, n0 = 0;
     if (first < p.tiles) {
       place(first, m0, n0);
       scales_at(m0, n0);
     }
-    for (int tile = first; tile < p.tiles && fine; tile += step) {
+    for (int tile = first; tile < p.tiles; tile += step) {
       uint64_t acc[CH][16];
 #pragma unroll
       for (int j = 0; j < CH; ++j)
 #pragma unroll
         for (int c = 0; c < 16; ++c) acc[j][c] = 0;
-      for (int g = 0; g < nb && fine; g += 4) {
+      for (int g = 0; g < nb; g += 4) {
         float x_now[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) x_now[u] = xs[u];
         const float w_now = ws;
         fetch(g + 4);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (g + u >= nb || !fine) continue;
+        for (int u0 = 0; u0 < 4; u0 += G) {
+          if (g + u0 >= nb) continue;
           const int buf = i % NB;
-          uint64_t scale[CH];
+          uint64_t scale[G][CH];
 #pragma unroll
-          for (int j = 0; j < CH; ++j) {
-            const float f = x_now[u] * __shfl_sync(0xFFFFFFFFu, w_now, 8 * u + j);
-            scale[j] = pair_of(f, f);
-          }
-          fine = __all_sync(0xFFFFFFFFu, mbar_wait(summed + 8 * buf, (i / NB) & 1, &gave_up));
+          for (int u = 0; u < G; ++u)
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+              const float f = x_now[u0 + u] * __shfl_sync(0xFFFFFFFFu, w_now, 8 * (u0 + u) + j);
+              scale[u][j] = pair_of(f, f);
+            }
+          mbar_wait(summed + 8 * buf, (i / NB) & 1, &gave_up);
           ++i;
-          if (!fine) continue;
           tc_fence_after();
-          const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * Tile::kMaxColumns + 32 * c0;
+          const uint32_t from =
+              tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * G * Tile::kMaxColumns + 32 * c0;
 #pragma unroll
-          for (int j = 0; j < CH; ++j) {
-            if (j >= chunks) continue;
-            float v[32];
-            tmem_load(from + 32 * j, v);
-            tmem_load_wait(v);
+          for (int u = 0; u < G; ++u) {
+            if (u > 0 && g + u0 + u >= nb) continue;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) acc[j][c] = fma2(pair_of(v[2 * c], v[2 * c + 1]), scale[j], acc[j][c]);
+            for (int j = 0; j < CH; ++j) {
+              if (j >= chunks) continue;
+              float v[32];
+              tmem_load(from + u * Tile::kMaxColumns + 32 * j, v);
+              tmem_load_wait(v);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) acc[j][c] = fma2(pair_of(v[2 * c], v[2 * c + 1]), scale[u][j], acc[j][c]);
+            }
           }
           release(buf);
         }
       }
-      if (!fine) break;
+      if (stalled()) break;
       if constexpr (PAIR) {
         const int32_t m_now = m0, n_now = n0;
         if (tile + step < p.tiles) {
@@ -558,15 +582,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     else __syncthreads();
     int lost = stalled();
     for (int q = 0; split > 1 && q < split; ++q) lost |= static_cast<int>(dsmem_ld_u32(dsmem_addr(&gave_up, q)));
-    if (warp < 8 && first < p.tiles && !lost) {
+    if (first < p.tiles && !lost) {
       int32_t m0, n0;
       place(first, m0, n0);
       const float *sums = reinterpret_cast<const float *>(ring);
-      // rows in turn over the cluster's CTAs and their warps, four columns per lane; the
-      // CTAs' sums are added in rank order
-      const int c = 4 * lane;
-      for (int r = rank * 8 + warp; r < 128 && m0 + r < p.n_rows; r += 8 * split) {
-        if (c >= p.columns) continue;
+      // groups of four neighbouring sums in turn over the threads (of the cluster's CTAs along
+      // in_dim, whose sums are added in rank order)
+      const int per_row = p.columns / 4, threads = kRowsThreads * split;
+      const int groups = min(128, p.n_rows - m0) * per_row;
+#pragma unroll 4
+      for (int g = (split > 1 ? rank : 0) * kRowsThreads + t; g < groups; g += threads) {
+        const int r = g / per_row, c = (g - r * per_row) * 4;
         float f[4];
         if (split == 1) {
           const float4 v = *reinterpret_cast<const float4 *>(sums + r * Tile::kPitch + c);
@@ -587,24 +613,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             }
         }
         const int32_t n = n0 + c;
-        if (p.out_f32) {
-          float *to = static_cast<float *>(p.out) + (m0 + r) * p.out_stride + n;
-          if (p.wide_out && n + 4 <= p.out_dim) {
-            *reinterpret_cast<float4 *>(to) = make_float4(f[0], f[1], f[2], f[3]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (n + e < p.out_dim) to[e] = f[e];
-          }
+        const int64_t at = (m0 + r) * p.out_stride + n;
+        if (p.wide_out && n + 4 <= p.out_dim) {
+          if (p.out_f32) *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(f[0], f[1], f[2], f[3]);
+          else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = make_uint2(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]));
         } else {
-          uint16_t *to = static_cast<uint16_t *>(p.out) + (m0 + r) * p.out_stride + n;
-          if (p.wide_out && n + 4 <= p.out_dim) {
-            *reinterpret_cast<uint2 *>(to) = make_uint2(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]));
-          } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (n + e < p.out_dim) to[e] = bf16_of(f[e]);
-          }
+          for (int e = 0; e < 4; ++e)
+            if (n + e < p.out_dim) {
+              if (p.out_f32) static_cast<float *>(p.out)[at + e] = f[e];
+              else static_cast<uint16_t *>(p.out)[at + e] = bf16_of(f[e]);
+            }
         }
       }
     }

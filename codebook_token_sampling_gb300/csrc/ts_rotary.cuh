@@ -8,8 +8,17 @@
 namespace ts {
 
 constexpr int kRotaryThreads = 256;
-constexpr int kRotaryTokens = 64;       // of a CTA at most
+constexpr int kRotaryTokens = 64;         // of a CTA at most
 constexpr int kRotaryTableFloats = 8192;  // cosines and sines of a CTA's tokens, at most
+constexpr int kRotaryRuns = 5;
+
+// Units of one kind of a CTA's tokens: of the queries (which 0), keys (1) or values (2).
+struct RotaryRun {
+  uint32_t first;            // a multiple of 32
+  FastDiv by_token, by_head;  // units per token and per head
+  int32_t which, rotates;
+  int32_t from;              // first element that is copied
+};
 
 struct RotaryParams {
   const void *x;                   // queries
@@ -22,7 +31,8 @@ struct RotaryParams {
   int32_t n_tokens, n_rows, heads, dim, half;  // half: pairs of a head
   int32_t interleaved, in_place;
   int32_t tokens_per_cta;
-  FastDiv by_token, by_head;       // units of 2 P elements per token and per head
+  uint32_t units;                  // of a CTA: the end of the last run
+  RotaryRun run[kRotaryRuns];
   uint32_t *status;
   // the cache's part
   const void *src[2];              // keys and values of the new tokens
@@ -31,7 +41,8 @@ struct RotaryParams {
   int64_t dst_block[2], dst_token[2], dst_head[2];
   const float *scale[2];           // or null
   const int64_t *slots;
-  int64_t n_slots, block_size;
+  int64_t n_slots;
+  FastDiv by_block;
   int32_t kv_heads;
 };
 
@@ -110,21 +121,48 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[P], floa
 
 // A frequency (radians per position) as turns in units of 2^-64, modulo a turn: the
 // product with a position, modulo 2^64, is then the angle's exact fraction of a turn.
+// By whole numbers (64-bit floating point arithmetic would take longer than the rest of a
+// frame): freq = m 2^e, and 2^66 / (2 pi) to 64 bits.
 __device__ __forceinline__ uint64_t turns_of(double freq) {
-  const double t = freq * 0.15915494309189535;  // 1 / (2 pi)
-  return static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(freq));
+  const int exponent = static_cast<int>((bits >> 52) & 0x7FF);
+  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (exponent ? 1ull << 52 : 0);
+  const uint64_t per_radian = 0xA2F9836E4E441529ull;
+  const uint64_t high = __umul64hi(m, per_radian), low = m * per_radian;
+  const int right = 1075 + 2 - max(exponent, 1);  // (high, low) 2^-right
+  uint64_t turns;
+  if (right >= 128) turns = 0;
+  else if (right > 64) turns = high >> (right - 64);
+  else if (right == 64) turns = high;
+  else if (right > 0) turns = (low >> right) | (high << (64 - right));
+  else turns = right > -64 ? low << -right : 0;
+  return bits >> 63 ? 0 - turns : turns;
 }
 
-// A CTA takes whole tokens.  Each angle's cosine and sine are computed once for all
-// of a token's heads and go through shared memory; a unit is P elements and the P
-// that they are paired with (or 2 P that are only copied).  Bound by DRAM for
-// prompts, by latency for a frame.  CACHE: Dst is the cache's type.
+// The cosine and sine of a position's angle, times the amplitude.
+__device__ __forceinline__ void angle_of(uint64_t freq, int32_t pos, float amplitude, float &cosine, float &sine) {
+  const uint64_t turn = freq * static_cast<uint64_t>(static_cast<int64_t>(pos));
+  // the nearest 2^-32 of a turn, as half turns from -1 to 1
+  const int32_t top = static_cast<int32_t>((turn + 0x80000000ull) >> 32);
+  float s, c;
+  sincospif(static_cast<float>(top) * 0x1p-31f, &s, &c);
+  cosine = amplitude * c;
+  sine = amplitude * s;
+}
+
+// A CTA takes whole tokens.  Each angle's cosine and sine are computed once for all of a
+// token's heads and go through shared memory; a unit is P elements and the P that they
+// are paired with, or 2 P that are only copied.  The CTA's units lie in runs of one kind
+// (queries' and keys' pairs, their copied elements, values), each from a multiple of 32
+// on, so that a warp's 32 units go the same way (dealt as they lie in a token, half of
+// the lanes waited for the others: 370 instructions a unit, 252 us for 32,768 tokens).
+// Bound by DRAM for prompts, by latency for a frame.  CACHE: Dst is the cache's type.
 template <class Src, class Dst, int P, bool CACHE>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryParams p) {
-  constexpr int kUnroll = P == 8 && sizeof(Src) == 4 ? 2 : 4;
+__global__ void __launch_bounds__(kRotaryThreads, P == 8 ? 3 : 4) rotary_kernel(const RotaryParams p) {
+  constexpr int kUnroll = 2;
   extern __shared__ __align__(16) float rotary_smem[];
   __shared__ int64_t row_of[kRotaryTokens];
-  __shared__ int32_t block_of[kRotaryTokens], off_of[kRotaryTokens];
+  __shared__ int64_t slot_of[CACHE ? 2 : 1][kRotaryTokens];  // where keys and values go
   const int t = static_cast<int>(threadIdx.x);
   const int32_t t0 = static_cast<int32_t>(blockIdx.x) * p.tokens_per_cta;
   const int nt = min(p.tokens_per_cta, p.n_tokens - t0);
@@ -139,109 +177,110 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryPara
     bool skip = pos < 0 || slot < 0;
     if (!skip && p.rows) {
       row = p.rows[t0 + t];
-      if (row < 0 || row >= p.n_rows) {
-        skip = true;
-        bits |= kRowBadSlot;
-      }
+      skip = row < 0 || row >= p.n_rows;
+      if (skip) bits |= kRowBadSlot;
     }
     if constexpr (CACHE) {
       if (!skip && slot >= p.n_slots) {
         skip = true;
         bits |= kRowBadSlot;
       }
+      // a cache of 2^31 slots and more takes the 64-bit division
+      const int64_t blk = skip ? 0 : p.n_slots <= 0x7FFFFFFF ? static_cast<int64_t>(p.by_block.div(static_cast<uint32_t>(slot)))
+                                                             : slot / p.by_block.d;
+      const int64_t off = skip ? 0 : slot - blk * p.by_block.d;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) slot_of[kv][t] = blk * p.dst_block[kv] + off * p.dst_token[kv];
     }
     row_of[t] = skip ? -1 : row;
-    if constexpr (CACHE) {
-      const int64_t blk = skip ? 0 : slot / p.block_size;
-      block_of[t] = static_cast<int32_t>(blk);
-      off_of[t] = static_cast<int32_t>(skip ? 0 : slot - blk * p.block_size);
-    }
   }
   for (int i0 = 0; i0 < p.half; i0 += kRotaryThreads) {
     const int width = min(kRotaryThreads, p.half - i0), groups = kRotaryThreads / width;
     const int g = t / width, i = i0 + t - g * width;
     if (g < groups) {
       const uint64_t f = turns_of(p.freqs[i]);
-      for (int k = g; k < nt; k += groups) {
-        const uint64_t turn = f * static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + k]));
-        // the nearest 2^-32 of a turn, as half turns from -1 to 1
-        const int32_t top = static_cast<int32_t>((turn + 0x80000000ull) >> 32);
-        float s, c;
-        sincospif(static_cast<float>(top) * 0x1p-31f, &s, &c);
-        cosines[k * p.half + i] = p.amplitude * c;
-        sines[k * p.half + i] = p.amplitude * s;
-      }
+      for (int k = g; k < nt; k += groups)
+        angle_of(f, p.positions[t0 + k], p.amplitude, cosines[k * p.half + i], sines[k * p.half + i]);
     }
   }
   __syncthreads();
 
-  const uint32_t units = static_cast<uint32_t>(nt) * p.by_token.d;
-  const int rot_units = p.half / P;
   struct Unit {
-    int token, head, u, which, a, b;  // which: 0 queries, 1 keys, 2 values
-    bool rotates;
+    int64_t to;                // element of the output or the cache
+    int token, head, u, a, b;  // token < 0: nothing to do
   };
-  const auto unit_of = [&](uint32_t x) {
+  const auto run_of = [&](uint32_t x) {  // the same for a warp
+    int r = 0;
+#pragma unroll
+    for (int k = 1; k < kRotaryRuns; ++k) r += x >= p.run[k].first;
+    return r;
+  };
+  const auto unit_of = [&](uint32_t x, const RotaryRun &run, const void *&from) {
     Unit n;
-    n.token = static_cast<int>(p.by_token.div(x));
-    const uint32_t in = x - static_cast<uint32_t>(n.token) * p.by_token.d;
-    n.head = static_cast<int>(p.by_head.div(in));
-    n.u = static_cast<int>(in) - n.head * static_cast<int>(p.by_head.d);
-    n.which = 0;
-    if constexpr (CACHE) {
-      if (n.head >= p.heads) {
-        n.head -= p.heads;
-        n.which = 1;
-        if (n.head >= p.kv_heads) {
-          n.head -= p.kv_heads;
-          n.which = 2;
-        }
-      }
+    x -= run.first;
+    n.token = static_cast<int>(run.by_token.div(x));
+    if (n.token >= nt) {
+      n.token = -1;
+      return n;
     }
-    n.rotates = n.which != 2 && n.u < rot_units;
-    if (n.rotates && !p.interleaved) {
+    const uint32_t in = x - static_cast<uint32_t>(n.token) * run.by_token.d;
+    n.head = static_cast<int>(run.by_head.div(in));
+    n.u = static_cast<int>(in - static_cast<uint32_t>(n.head) * run.by_head.d);
+    if (run.rotates && !p.interleaved) {
       n.a = n.u * P;
       n.b = p.half + n.a;
     } else {  // neighbours, rotated or copied
-      n.a = n.u * 2 * P;
+      n.a = run.from + n.u * 2 * P;
       n.b = n.a + P;
+    }
+    const int64_t row = row_of[n.token];
+    if (row < 0) {
+      n.token = -1;
+      return n;
+    }
+    if (!CACHE || run.which == 0) {
+      from = static_cast<const Src *>(p.x) + row * p.x_token + n.head * p.x_head;
+      n.to = row * p.out_token + n.head * p.out_head;
+    } else {
+      const int kv = run.which - 1;
+      from = static_cast<const Src *>(p.src[kv]) + row * p.src_token[kv] + n.head * p.src_head[kv];
+      n.to = slot_of[CACHE ? kv : 0][n.token] + n.head * p.dst_head[kv];
     }
     return n;
   };
 
+  const uint32_t units = p.units;
   for (uint32_t x0 = t; x0 < units; x0 += kRotaryThreads * kUnroll) {
     Piece<Src, P> va[kUnroll], vb[kUnroll];
-    bool there[kUnroll];
+    Unit n[kUnroll];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       const uint32_t x = x0 + j * kRotaryThreads;
-      there[j] = x < units;
-      if (!there[j]) continue;
-      const Unit n = unit_of(x);
-      const int64_t row = row_of[n.token];
-      there[j] = row >= 0 && !(n.which == 0 && p.in_place && !n.rotates);
-      if (!there[j]) continue;
-      const Src *from;
-      if (!CACHE || n.which == 0) from = static_cast<const Src *>(p.x) + row * p.x_token + n.head * p.x_head;
-      else from = static_cast<const Src *>(p.src[n.which - 1]) + row * p.src_token[n.which - 1] + n.head * p.src_head[n.which - 1];
-      va[j].load(from + n.a);
-      if (n.b < p.dim) vb[j].load(from + n.b);
+      n[j].token = -1;
+      if (x >= units) continue;
+      const void *from = nullptr;
+      n[j] = unit_of(x, p.run[run_of(x & ~31u)], from);
+      if (n[j].token < 0) continue;
+      va[j].load(static_cast<const Src *>(from) + n[j].a);
+      if (n[j].b < p.dim) vb[j].load(static_cast<const Src *>(from) + n[j].b);
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      if (!there[j]) continue;
-      const Unit n = unit_of(x0 + j * kRotaryThreads);
-      const bool both = n.b < p.dim;
+      const uint32_t x = x0 + j * kRotaryThreads;
+      if (x >= units) continue;
+      const RotaryRun &run = p.run[run_of(x & ~31u)];
+      if (n[j].token < 0) continue;
+      const bool both = n[j].b < p.dim;
       float a[P], b[P];
-      if (n.rotates || (CACHE && n.which != 0 && sizeof(Dst) == 1)) {
+      if (run.rotates || (CACHE && run.which != 0 && sizeof(Dst) == 1)) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           a[i] = va[j].at(i);
           b[i] = both ? vb[j].at(i) : 0.0f;
         }
       }
-      if (n.rotates) {
-        const float *c = cosines + n.token * p.half + n.u * P, *s = sines + n.token * p.half + n.u * P;
+      if (run.rotates) {
+        const float *c = cosines + n[j].token * p.half + n[j].u * P, *s = sines + n[j].token * p.half + n[j].u * P;
         if (P == 1 || !p.interleaved) {
 #pragma unroll
           for (int i = 0; i < P; ++i) {
@@ -261,34 +300,33 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryPara
           }
         }
       }
-      if (CACHE && n.which != 0) {
-        const int kv = n.which - 1;
-        Dst *to = static_cast<Dst *>(p.dst[kv]) + block_of[n.token] * p.dst_block[kv] + off_of[n.token] * p.dst_token[kv] +
-                  n.head * p.dst_head[kv];
+      if (CACHE && run.which != 0) {
+        const int kv = run.which - 1;
+        Dst *to = static_cast<Dst *>(p.dst[kv]) + n[j].to;
         if constexpr (sizeof(Dst) == 1) {
           float scale = 1.0f, inv = 1.0f;
           if (p.scale[kv]) {
-            scale = p.scale[kv][n.head];
+            scale = p.scale[kv][n[j].head];
             inv = quotient_inverse(scale);
           }
-          store_e4m3<P>(reinterpret_cast<uint8_t *>(to) + n.a, a, scale, inv);
-          if (both) store_e4m3<P>(reinterpret_cast<uint8_t *>(to) + n.b, b, scale, inv);
+          store_e4m3<P>(reinterpret_cast<uint8_t *>(to) + n[j].a, a, scale, inv);
+          if (both) store_e4m3<P>(reinterpret_cast<uint8_t *>(to) + n[j].b, b, scale, inv);
         } else {
-          if (n.rotates) {
+          if (run.rotates) {
             va[j].set(a);
             vb[j].set(b);
           }
-          va[j].store(reinterpret_cast<Src *>(to) + n.a);
-          if (both) vb[j].store(reinterpret_cast<Src *>(to) + n.b);
+          va[j].store(reinterpret_cast<Src *>(to) + n[j].a);
+          if (both) vb[j].store(reinterpret_cast<Src *>(to) + n[j].b);
         }
       } else {
-        Src *to = static_cast<Src *>(p.out) + row_of[n.token] * p.out_token + n.head * p.out_head;
-        if (n.rotates) {
+        Src *to = static_cast<Src *>(p.out) + n[j].to;
+        if (run.rotates) {
           va[j].set(a);
           vb[j].set(b);
         }
-        va[j].store(to + n.a);
-        if (both) vb[j].store(to + n.b);
+        va[j].store(to + n[j].a);
+        if (both) vb[j].store(to + n[j].b);
       }
     }
   }

@@ -106,9 +106,11 @@ __device__ __forceinline__ float scaled_block(float (&v)[RowUnit<WIDE>::kElems])
   for (int e = 1; e < RowUnit<WIDE>::kElems; ++e) a = max_nan(a, fabsf(v[e]));
 #pragma unroll
   for (int o = RowUnit<WIDE>::kLanes / 2; o; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-  float scale = __fdiv_rn(fmaxf(a, 0x1p-64f), 448.0f);
+  // a / 448 correctly rounded (the quotient and one correction by its remainder, as above)
+  const float top = fmaxf(a, 0x1p-64f), q = top * (1.0f / 448.0f);
+  float scale = fmaf(fmaf(-q, 448.0f, top), 1.0f / 448.0f, q);
   if (!(a < INFINITY)) scale = __int_as_float(0x7FC00000);  // a NaN or an infinity in the block
-  const float inv = __fdiv_rn(1.0f, scale);
+  const float inv = __frcp_rn(scale);
 #pragma unroll
   for (int e = 0; e < RowUnit<WIDE>::kElems; ++e) v[e] *= inv;
   return scale;

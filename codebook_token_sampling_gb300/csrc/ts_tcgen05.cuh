@@ -37,21 +37,22 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Waits for the phase of the given parity to end, kWaitCycles (about two seconds) at
-// most; false where it did not, or where another wait of the CTA gave up.  (No calls: a
-// call would spill what the caller holds in registers.  And no %globaltimer, whose
-// reading takes about 2000 cycles.)
+// most: then, or where another wait of the CTA gave up, *gave_up is set, what comes after
+// works on what there is, and nothing of it is stored.  (No answer: loops whose end
+// depended on one would not count as the same in all lanes, and their products' operands
+// would be moved one by one, 400 cycles a block instead of 100.  No calls: a call would
+// spill what the caller holds in registers.  No %globaltimer, whose reading is slow.)
 constexpr long long kWaitCycles = 4000000000ll;
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
-  if (mbar_try(bar, parity)) return true;
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+  if (mbar_try(bar, parity)) return;
   const long long start = clock64();
 #pragma unroll 1
   for (int i = 1; !mbar_try(bar, parity); ++i) {
     if ((i & 63) == 0 && (*gave_up || clock64() - start > kWaitCycles)) {
       *gave_up = 1;
-      return false;
+      break;
     }
   }
-  return true;
 }
 // The same for copies or products that a CTA waits for after it gave up: they come to
 // their end before it leaves, within kWaitCycles.
