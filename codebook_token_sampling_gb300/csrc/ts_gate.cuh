@@ -8,7 +8,8 @@
 namespace ts {
 
 constexpr int kGateThreads = 256;
-constexpr int kGateUnits = 2;  // per thread
+constexpr int kGateUnits = 1;  // per thread at once
+constexpr int kGateCtas = 5;   // per SM
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3;
 
 struct GateParams {
@@ -16,9 +17,10 @@ struct GateParams {
   void *out;
   float *scale;
   int64_t up_stride, gate_stride, out_stride, scale_stride;
-  int64_t units;   // of all rows: whole blocks of 128 elements each
-  int32_t dim, act;
-  FastDiv by_row;  // units per row
+  int64_t step_rows;   // from a CTA's units to its next ones: rows, and units of a row
+  uint32_t step_units;
+  int32_t n_rows, dim, act;
+  FastDiv by_row;  // units per row: whole blocks of 128 elements
 };
 
 // 1 / x and 2^x within two units in the last place, subnormal results as zeros
@@ -37,19 +39,25 @@ constexpr float kLog2E = 1.44269504f;
 // g / (1 + exp(-z))
 __device__ __forceinline__ float logistic(float g, float z) { return g * reciprocal(1.0f + power_of_2(-kLog2E * z)); }
 
-// g (1 + erf(g / sqrt 2)) / 2 = max(g, 0) - |g| erfc(|g| / sqrt 2) / 2, with Hastings's
-// erfc(x) = t (a1 + t (a2 + .. t a5)) exp(-x x), t = 1 / (1 + p x), to 1.5e-7 ("Approximations
-// for digital computers", 1955; 7.1.26 in Abramowitz and Stegun).  A third of the
-// instructions of erff, which took longer than the loads (273 us for 16,384 x 11,008).
-__device__ __forceinline__ float gelu(float g) {
-  const float a = fabsf(g);
-  const float t = reciprocal(fmaf(0.3275911f * 0.70710678f, a, 1.0f));
-  float w = fmaf(t, 0.5f * 1.061405429f, -0.5f * 1.453152027f);
-  w = fmaf(t, w, 0.5f * 1.421413741f);
-  w = fmaf(t, w, -0.5f * 0.284496736f);
-  w = fmaf(t, w, 0.5f * 0.254829592f);
-  w = w * t * power_of_2(-0.5f * kLog2E * a * a);
-  return fmaf(-fminf(a, 3e38f), w, fmaxf(g, 0.0f));
+// y g (1 + erf(g / sqrt 2)) / 2 of two elements: g (1 + erf) / 2 = max(g, 0) - |g| erfc(|g| /
+// sqrt 2) / 2, with Hastings's erfc(x) = t (a1 + t (a2 + .. t a5)) exp(-x x), t = 1 / (1 + p x),
+// to 1.5e-7 ("Approximations for digital computers", 1955; 7.1.26 in Abramowitz and
+// Stegun).  erff took longer than the loads (16,384 x 11,008: 273 us; this one element by
+// element 193).
+__device__ __forceinline__ uint64_t gelu2(uint64_t y, float g0, float g1) {
+  const float a0 = fminf(fabsf(g0), 3e38f), a1 = fminf(fabsf(g1), 3e38f);
+  const uint64_t a = pair_of(a0, a1);
+  float u0, u1, e0, e1;
+  parts_of(fma2(a, both_of(0.3275911f * 0.70710678f), both_of(1.0f)), u0, u1);
+  parts_of(mul2(mul2(a, a), both_of(-0.5f * kLog2E)), e0, e1);
+  const uint64_t t = pair_of(reciprocal(u0), reciprocal(u1)), e = pair_of(power_of_2(e0), power_of_2(e1));
+  uint64_t w = fma2(t, both_of(-0.5f * 1.061405429f), both_of(0.5f * 1.453152027f));
+  w = fma2(t, w, both_of(-0.5f * 1.421413741f));
+  w = fma2(t, w, both_of(0.5f * 0.284496736f));
+  w = fma2(t, w, both_of(-0.5f * 0.254829592f));  // minus the half of it
+  w = mul2(mul2(w, t), e);
+  // a NaN is in w, whatever the others take it for
+  return mul2(y, fma2(a, w, pair_of(fmaxf(g0, 0.0f), fmaxf(g1, 0.0f))));
 }
 
 template <int E>
@@ -59,7 +67,7 @@ __device__ __forceinline__ void gated(float (&y)[E], const float (&g)[E], int ac
     for (int e = 0; e < E; ++e) y[e] *= logistic(g[e], g[e]);
   } else if (act == kActGelu) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] *= gelu(g[e]);
+    for (int e = 0; e < E; e += 2) parts_of(gelu2(pair_of(y[e], y[e + 1]), g[e], g[e + 1]), y[e], y[e + 1]);
   } else {  // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -67,42 +75,73 @@ __device__ __forceinline__ void gated(float (&y)[E], const float (&g)[E], int ac
   }
 }
 
-// The rows' units end to end, kGateUnits per thread, a CTA's next to one another:
-// bound by DRAM.
+// The rows' units end to end, kGateUnits of a thread at once, its next ones' loads on
+// their way while it works on these: bound by DRAM, for gelu nearly by its arithmetic.
 template <class Src, class Out, bool WIDE>
-__global__ void __launch_bounds__(kGateThreads) gate_kernel(const GateParams p) {
+__global__ void __launch_bounds__(kGateThreads, kGateCtas) gate_kernel(const GateParams p) {
   using U = RowUnit<WIDE>;
   constexpr int E = U::kElems;
-  constexpr int kUnits = kGateUnits;
+  constexpr int N = kGateUnits;
   pdl_wait_and_release();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * (kGateThreads * kUnits);
-  const int64_t r0 = base / p.by_row.d;
-  const uint32_t off0 = static_cast<uint32_t>(base - r0 * p.by_row.d) + threadIdx.x;
   const bool act = p.act != kActNone;
-  float y[kUnits][E], g[kUnits][E];
-  int64_t row[kUnits];
-  int32_t at[kUnits];
+  const uint32_t per_row = p.by_row.d;
+  int64_t row[N];
+  uint32_t in[N];  // unit of the row
+  {
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * (kGateThreads * N);
+    const int64_t r0 = base / per_row;
+    const uint32_t off0 = static_cast<uint32_t>(base - r0 * per_row) + threadIdx.x;
 #pragma unroll
-  for (int j = 0; j < kUnits; ++j) {
-    const uint32_t u = off0 + j * kGateThreads;
-    const uint32_t r = p.by_row.div(u), c = u - r * p.by_row.d;
-    row[j] = r0 + r;
-    at[j] = WIDE ? static_cast<int32_t>(c * 8) : static_cast<int32_t>((c >> 5) * kScaleBlock + (c & 31));
-    const bool there = base + threadIdx.x + j * kGateThreads < p.units;
-    const int32_t dim = there ? p.dim : 0;  // no elements
-    load_unit<WIDE>(static_cast<const Src *>(p.up) + row[j] * p.up_stride, at[j], dim, y[j]);
-    if (act) load_unit<WIDE>(static_cast<const Src *>(p.gate) + row[j] * p.gate_stride, at[j], dim, g[j]);
-    if (!there) at[j] = p.dim + kScaleBlock;
-  }
-#pragma unroll
-  for (int j = 0; j < kUnits; ++j) {
-    if (act) gated<E>(y[j], g[j], p.act);
-    if constexpr (sizeof(Out) == 1) {
-      const float scale = scaled_block<WIDE>(y[j]);
-      const int first = static_cast<int>(lane_id()) & (U::kLanes - 1);
-      if (first == 0 && at[j] < p.dim) p.scale[row[j] * p.scale_stride + at[j] / kScaleBlock] = scale;
+    for (int j = 0; j < N; ++j) {
+      const uint32_t u = off0 + j * kGateThreads, r = p.by_row.div(u);
+      row[j] = r0 + r;
+      in[j] = u - r * per_row;
     }
-    store_unit<WIDE>(static_cast<Out *>(p.out) + row[j] * p.out_stride, at[j], p.dim, y[j]);
+  }
+  RawUnit<Src, WIDE> up[N], gate[N];
+  const auto at = [&](uint32_t c) {
+    return WIDE ? static_cast<int32_t>(c * 8) : static_cast<int32_t>((c >> 5) * kScaleBlock + (c & 31));
+  };
+  const auto fetch = [&]() {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int32_t dim = row[j] < p.n_rows ? p.dim : 0;  // behind the last row: no elements
+      up[j].load(static_cast<const Src *>(p.up) + row[j] * p.up_stride, at(in[j]), dim);
+      if (act) gate[j].load(static_cast<const Src *>(p.gate) + row[j] * p.gate_stride, at(in[j]), dim);
+    }
+  };
+  fetch();
+  while (__any_sync(0xFFFFFFFFu, row[0] < p.n_rows)) {
+    float y[N][E], g[N][E];
+    int64_t now[N];
+    int32_t here[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        y[j][e] = up[j].at(e);
+        g[j][e] = gate[j].at(e);
+      }
+      now[j] = row[j];
+      here[j] = row[j] < p.n_rows ? at(in[j]) : p.dim + kScaleBlock;
+      row[j] += p.step_rows;
+      in[j] += p.step_units;
+      if (in[j] >= per_row) {
+        in[j] -= per_row;
+        ++row[j];
+      }
+    }
+    fetch();
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (act) gated<E>(y[j], g[j], p.act);
+      if constexpr (sizeof(Out) == 1) {
+        const float scale = scaled_block<WIDE>(y[j]);
+        const int first = static_cast<int>(lane_id()) & (U::kLanes - 1);
+        if (first == 0 && here[j] < p.dim) p.scale[now[j] * p.scale_stride + here[j] / kScaleBlock] = scale;
+      }
+      store_unit<WIDE>(static_cast<Out *>(p.out) + now[j] * p.out_stride, here[j], p.dim, y[j]);
+    }
   }
 }
 

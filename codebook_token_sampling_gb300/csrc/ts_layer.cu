@@ -143,31 +143,30 @@ ts_status launch_rotary(const ts_sampler *s, const ts_rotary_args *a, ts::Rotary
   const int64_t per_head = (a->head_dim + 2 * piece - 1) / (2 * piece), turned = p.half / piece;
   const int64_t per_token = per_head * (p.heads + 2 * static_cast<int64_t>(p.kv_heads));
   if (per_token > (1 << 23)) return TS_ERR_UNSUPPORTED;
-  // whole tokens, about eight units per thread, fewer while SMs would idle
-  const int64_t n = a->n_tokens, fill = ts::kRotaryThreads * 8;
-  int64_t tokens = std::min<int64_t>(fill / per_token, (n + s->num_sms - 1) / s->num_sms);
+  // whole tokens, eight of a thread's units (or one of each of a wide token's) where SMs are
+  // busy all the same
+  const int64_t n = a->n_tokens;
+  int64_t tokens = std::min<int64_t>(std::max<int64_t>(ts::kRotaryThreads * 8 / per_token, 8), (n + 4 * s->num_sms - 1) / (4 * s->num_sms));
   tokens = std::min<int64_t>(tokens, std::min<int64_t>(ts::kRotaryTokens, ts::kRotaryTableFloats / a->rotary_dim));
   tokens = std::max<int64_t>(1, tokens);
   p.tokens_per_cta = static_cast<int32_t>(tokens);
   // runs of units: pairs of queries and keys, their other elements, values
-  uint32_t end = 0;
   const auto add = [&](int k, int which, bool rotates, int64_t heads, int64_t units) {
     ts::RotaryRun &r = p.run[k];
-    const int64_t all = heads * units;
-    r.first = end;
+    r.first = p.units;
+    r.units = static_cast<int32_t>(heads * units);
     r.which = which;
     r.rotates = rotates;
     r.from = which == 2 || rotates ? 0 : a->rotary_dim;
     r.by_head = ts::FastDiv::of(static_cast<uint32_t>(std::max<int64_t>(1, units)));
-    r.by_token = ts::FastDiv::of(static_cast<uint32_t>(std::max<int64_t>(1, all)));
-    end += static_cast<uint32_t>((tokens * all + 31) / 32 * 32);
+    p.units += (r.units + 31) / 32 * 32;
   };
   add(0, 0, true, p.heads, turned);
   add(1, 1, true, p.kv_heads, turned);
   add(2, 0, false, p.in_place ? 0 : p.heads, per_head - turned);
   add(3, 1, false, p.kv_heads, per_head - turned);
   add(4, 2, false, p.kv_heads, per_head);
-  p.units = end;
+  p.group = std::min(p.units, ts::kRotaryThreads);
   const size_t smem = static_cast<size_t>(tokens) * a->rotary_dim * sizeof(float);
   void *args[] = {&p};
   const cudaError_t e = launch(fn, dim3(static_cast<unsigned>((n + tokens - 1) / tokens)), ts::kRotaryThreads, smem,
@@ -294,9 +293,11 @@ ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream) {
   p.act = a->act;
   const int64_t per_row = scales_of(dim) * (wide ? 16 : 32);
   p.by_row = ts::FastDiv::of(static_cast<uint32_t>(per_row));
-  p.units = n * per_row;
-  const int64_t per_cta = ts::kGateThreads * ts::kGateUnits, grid = (p.units + per_cta - 1) / per_cta;
-  if (grid > INT32_MAX) return TS_ERR_UNSUPPORTED;
+  const int64_t per_cta = ts::kGateThreads * ts::kGateUnits, all = (n * per_row + per_cta - 1) / per_cta;
+  const int64_t grid = std::min<int64_t>(all, ts::kGateCtas * s->num_sms);
+  p.n_rows = a->n_rows;
+  p.step_rows = grid * per_cta / per_row;
+  p.step_units = static_cast<uint32_t>(grid * per_cta % per_row);
   const void *fn = a->dtype == TS_DTYPE_F32 ? gate_kernel_to<float>(a->out_dtype, wide)
                                             : gate_kernel_to<uint16_t>(a->out_dtype, wide);
   void *args[] = {&p};

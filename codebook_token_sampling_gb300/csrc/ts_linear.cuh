@@ -253,21 +253,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (t == 0 && stalled()) atomicOr(p.status, kRowStalled);
 }
 
-// Two fp32 products and sums at once.
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void parts_of(uint64_t v, float &a, float &b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // More rows: 128 tokens are the product's rows and `columns` weight rows (a multiple of
 // 32) its columns, so a thread's sums belong to one token and a block's scales are one
 // number for 32 of them.  Eight warps add the blocks' sums (a warp: 32 tokens, half of

@@ -15,31 +15,6 @@ struct NormParams {
   float eps, weight_offset;
 };
 
-// A unit as it is stored, on its way while the row before it is worked on.
-template <class T, bool WIDE>
-struct RawUnit {
-  static constexpr int E = RowUnit<WIDE>::kElems;
-  uint32_t w[E * sizeof(T) / 4];
-  __device__ __forceinline__ void load(const T *row, int at, int dim) {
-    if constexpr (WIDE) {
-#pragma unroll
-      for (int i = 0; i < E * static_cast<int>(sizeof(T)) / 16; ++i) {
-        const uint4 v = at < dim ? reinterpret_cast<const uint4 *>(row + at)[i] : make_uint4(0, 0, 0, 0);
-        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-      }
-    } else {
-      T e[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) e[i] = at + 32 * i < dim ? row[at + 32 * i] : T(0);
-      memcpy(w, e, sizeof w);
-    }
-  }
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-    else return (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
-  }
-};
-
 // A CTA walks over rows (or, of one-warp rows, each of its blockDim.y warps does), its V
 // units per thread held in registers between the sum of squares and the output, so every
 // element is read once and written once.  With one or two units a thread has the next

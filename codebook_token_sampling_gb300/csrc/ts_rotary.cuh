@@ -12,10 +12,11 @@ constexpr int kRotaryTokens = 64;         // of a CTA at most
 constexpr int kRotaryTableFloats = 8192;  // cosines and sines of a CTA's tokens, at most
 constexpr int kRotaryRuns = 5;
 
-// Units of one kind of a CTA's tokens: of the queries (which 0), keys (1) or values (2).
+// A token's units of one kind: of the queries (which 0), keys (1) or values (2).
 struct RotaryRun {
-  uint32_t first;            // a multiple of 32
-  FastDiv by_token, by_head;  // units per token and per head
+  int32_t first;             // a multiple of 32
+  int32_t units;
+  FastDiv by_head;           // units per head
   int32_t which, rotates;
   int32_t from;              // first element that is copied
 };
@@ -31,7 +32,8 @@ struct RotaryParams {
   int32_t n_tokens, n_rows, heads, dim, half;  // half: pairs of a head
   int32_t interleaved, in_place;
   int32_t tokens_per_cta;
-  uint32_t units;                  // of a CTA: the end of the last run
+  int32_t units;                   // of a token: the end of the last run
+  int32_t group;                   // threads that share a token: a multiple of 32
   RotaryRun run[kRotaryRuns];
   uint32_t *status;
   // the cache's part
@@ -103,8 +105,20 @@ template <int P>
 __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[P], float scale, float inv) {
   float y[P];
   bool fine = inv != 0.0f;
+  if constexpr (P == 1) {
+    fine &= quotient(v[0], scale, inv, y[0]);
+  } else {  // the same, two at once
 #pragma unroll
-  for (int i = 0; i < P; ++i) fine &= quotient(v[i], scale, inv, y[i]);
+    for (int i = 0; i < P; i += 2) {
+      const uint64_t x = pair_of(v[i], v[i + 1]), r = both_of(inv), q = mul2(x, r);
+      float q0, q1;
+      parts_of(q, q0, q1);
+      parts_of(fma2(fma2(q, both_of(-scale), x), r, q), y[i], y[i + 1]);
+      y[i] = copysignf(y[i], q0);
+      y[i + 1] = copysignf(y[i + 1], q1);
+      fine &= fabsf(q0) < 0x1p20f && fabsf(q1) < 0x1p20f;
+    }
+  }
   if (!fine) {
 #pragma unroll 1
     for (int i = 0; i < P; ++i) p[i] = e4m3_of(__fdiv_rn(v[i], scale));
@@ -150,12 +164,24 @@ __device__ __forceinline__ void angle_of(uint64_t freq, int32_t pos, float ampli
   sine = amplitude * s;
 }
 
+// One, two or four values side by side.
+__device__ __forceinline__ void read_side(const float *p, float (&v)[1]) { v[0] = p[0]; }
+__device__ __forceinline__ void read_side(const float *p, float (&v)[2]) {
+  const float2 f = *reinterpret_cast<const float2 *>(p);
+  v[0] = f.x, v[1] = f.y;
+}
+__device__ __forceinline__ void read_side(const float *p, float (&v)[4]) {
+  const float4 f = *reinterpret_cast<const float4 *>(p);
+  v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+}
+
 // A CTA takes whole tokens.  Each angle's cosine and sine are computed once for all of a
 // token's heads and go through shared memory; a unit is P elements and the P that they
-// are paired with, or 2 P that are only copied.  The CTA's units lie in runs of one kind
+// are paired with, or 2 P that are only copied.  A token's units lie in runs of one kind
 // (queries' and keys' pairs, their copied elements, values), each from a multiple of 32
-// on, so that a warp's 32 units go the same way (dealt as they lie in a token, half of
-// the lanes waited for the others: 370 instructions a unit, 252 us for 32,768 tokens).
+// on, so that a warp's 32 units go the same way, and a thread keeps its unit from token to
+// token, so that it is found once (found for every token it took 294 instructions a unit,
+// 192 us for 32,768 tokens; with lanes of several kinds 370 and 252).
 // Bound by DRAM for prompts, by latency for a frame.  CACHE: Dst is the cache's type.
 template <class Src, class Dst, int P, bool CACHE>
 __global__ void __launch_bounds__(kRotaryThreads, P == 8 ? 3 : 4) rotary_kernel(const RotaryParams p) {
@@ -199,134 +225,115 @@ __global__ void __launch_bounds__(kRotaryThreads, P == 8 ? 3 : 4) rotary_kernel(
     const int g = t / width, i = i0 + t - g * width;
     if (g < groups) {
       const uint64_t f = turns_of(p.freqs[i]);
+      // a unit's eight pairs in two places, so that lanes read 16 bytes side by side
+      const int place = P == 8 && !p.interleaved ? ((i >> 2) & 1) * (p.half / 2) + (i >> 3) * 4 + (i & 3) : i;
       for (int k = g; k < nt; k += groups)
-        angle_of(f, p.positions[t0 + k], p.amplitude, cosines[k * p.half + i], sines[k * p.half + i]);
+        angle_of(f, p.positions[t0 + k], p.amplitude, cosines[k * p.half + place], sines[k * p.half + place]);
     }
   }
   __syncthreads();
 
-  struct Unit {
-    int64_t to;                // element of the output or the cache
-    int token, head, u, a, b;  // token < 0: nothing to do
-  };
-  const auto run_of = [&](uint32_t x) {  // the same for a warp
-    int r = 0;
+  // groups of threads take tokens in turn where a token's units are few
+  const int width = p.group, group = t / width, groups = kRotaryThreads / width;
+  if (group < groups) {
+    for (int x = t - group * width; x < p.units; x += width) {
+      int r = 0;
 #pragma unroll
-    for (int k = 1; k < kRotaryRuns; ++k) r += x >= p.run[k].first;
-    return r;
-  };
-  const auto unit_of = [&](uint32_t x, const RotaryRun &run, const void *&from) {
-    Unit n;
-    x -= run.first;
-    n.token = static_cast<int>(run.by_token.div(x));
-    if (n.token >= nt) {
-      n.token = -1;
-      return n;
-    }
-    const uint32_t in = x - static_cast<uint32_t>(n.token) * run.by_token.d;
-    n.head = static_cast<int>(run.by_head.div(in));
-    n.u = static_cast<int>(in - static_cast<uint32_t>(n.head) * run.by_head.d);
-    if (run.rotates && !p.interleaved) {
-      n.a = n.u * P;
-      n.b = p.half + n.a;
-    } else {  // neighbours, rotated or copied
-      n.a = run.from + n.u * 2 * P;
-      n.b = n.a + P;
-    }
-    const int64_t row = row_of[n.token];
-    if (row < 0) {
-      n.token = -1;
-      return n;
-    }
-    if (!CACHE || run.which == 0) {
-      from = static_cast<const Src *>(p.x) + row * p.x_token + n.head * p.x_head;
-      n.to = row * p.out_token + n.head * p.out_head;
-    } else {
-      const int kv = run.which - 1;
-      from = static_cast<const Src *>(p.src[kv]) + row * p.src_token[kv] + n.head * p.src_head[kv];
-      n.to = slot_of[CACHE ? kv : 0][n.token] + n.head * p.dst_head[kv];
-    }
-    return n;
-  };
-
-  const uint32_t units = p.units;
-  for (uint32_t x0 = t; x0 < units; x0 += kRotaryThreads * kUnroll) {
-    Piece<Src, P> va[kUnroll], vb[kUnroll];
-    Unit n[kUnroll];
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const uint32_t x = x0 + j * kRotaryThreads;
-      n[j].token = -1;
-      if (x >= units) continue;
-      const void *from = nullptr;
-      n[j] = unit_of(x, p.run[run_of(x & ~31u)], from);
-      if (n[j].token < 0) continue;
-      va[j].load(static_cast<const Src *>(from) + n[j].a);
-      if (n[j].b < p.dim) vb[j].load(static_cast<const Src *>(from) + n[j].b);
-    }
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const uint32_t x = x0 + j * kRotaryThreads;
-      if (x >= units) continue;
-      const RotaryRun &run = p.run[run_of(x & ~31u)];
-      if (n[j].token < 0) continue;
-      const bool both = n[j].b < p.dim;
-      float a[P], b[P];
-      if (run.rotates || (CACHE && run.which != 0 && sizeof(Dst) == 1)) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          a[i] = va[j].at(i);
-          b[i] = both ? vb[j].at(i) : 0.0f;
-        }
+      for (int k = 1; k < kRotaryRuns; ++k) r += (x & ~31) >= p.run[k].first;  // the same for a warp
+      const int rotates = p.run[r].rotates, which = p.run[r].which;
+      const uint32_t in = static_cast<uint32_t>(x - p.run[r].first);
+      const int head = static_cast<int>(p.run[r].by_head.div(in));
+      const int u = static_cast<int>(in) - head * static_cast<int>(p.run[r].by_head.d);
+      if (static_cast<int>(in) >= p.run[r].units) continue;
+      // a piece and the one half of the run's width behind it: the halves' pairs; neighbours'
+      // pairs and copied elements lie in a piece of their own, and lanes side by side
+      const bool single = P == 1 && rotates && p.interleaved;  // but for single elements
+      const int apart = single ? 1 : static_cast<int>(p.run[r].by_head.d) * P;
+      const int a_at = p.run[r].from + (single ? 2 : P) * u, b_at = a_at + apart;
+      const bool both = b_at < p.dim;
+      const bool queries = !CACHE || which == 0;
+      const int kv = queries ? 0 : which - 1;
+      const Src *src = queries ? static_cast<const Src *>(p.x) + head * p.x_head
+                               : static_cast<const Src *>(p.src[kv]) + head * p.src_head[kv];
+      const int64_t src_token = queries ? p.x_token : p.src_token[kv];
+      Src *out = static_cast<Src *>(p.out) + head * p.out_head;
+      Dst *cache = queries ? nullptr : static_cast<Dst *>(p.dst[kv]) + head * p.dst_head[kv];
+      float scale = 1.0f, inv = 1.0f;
+      if (CACHE && sizeof(Dst) == 1 && !queries && p.scale[kv]) {
+        scale = p.scale[kv][head];
+        inv = quotient_inverse(scale);
       }
-      if (run.rotates) {
-        const float *c = cosines + n[j].token * p.half + n[j].u * P, *s = sines + n[j].token * p.half + n[j].u * P;
-        if (P == 1 || !p.interleaved) {
+      for (int k0 = group; k0 < nt; k0 += groups * kUnroll) {
+        Piece<Src, P> va[kUnroll], vb[kUnroll];
+        int64_t row[kUnroll];
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const float u = a[i], v = b[i];
-            a[i] = fmaf(u, c[i], -v * s[i]);
-            b[i] = fmaf(v, c[i], u * s[i]);
-          }
-        } else if constexpr (P > 1) {
+        for (int j = 0; j < kUnroll; ++j) {
+          const int k = k0 + j * groups;
+          row[j] = k < nt ? row_of[k] : -1;
+          if (row[j] < 0) continue;
+          const Src *from = src + row[j] * src_token;
+          va[j].load(from + a_at);
+          if (both) vb[j].load(from + b_at);
+        }
 #pragma unroll
-          for (int i = 0; i < P; i += 2) {
-            const float u = a[i], v = a[i + 1], y = b[i], z = b[i + 1];
-            const float ca = c[i / 2], sa = s[i / 2], cb = c[P / 2 + i / 2], sb = s[P / 2 + i / 2];
-            a[i] = fmaf(u, ca, -v * sa);
-            a[i + 1] = fmaf(v, ca, u * sa);
-            b[i] = fmaf(y, cb, -z * sb);
-            b[i + 1] = fmaf(z, cb, y * sb);
+        for (int j = 0; j < kUnroll; ++j) {
+          if (row[j] < 0) continue;
+          const int k = k0 + j * groups;
+          float a[P], b[P];
+          if (rotates || (CACHE && !queries && sizeof(Dst) == 1)) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+              a[i] = va[j].at(i);
+              b[i] = both ? vb[j].at(i) : 0.0f;
+            }
+          }
+          if (rotates) {
+            const float *c = cosines + k * p.half, *s = sines + k * p.half;
+            if (P == 1 || !p.interleaved) {
+              constexpr int kSide = P == 1 ? 1 : 4;  // read at once
+#pragma unroll
+              for (int h = 0; h < P / kSide; ++h) {
+                float cs[kSide], sn[kSide];
+                read_side(c + h * (p.half / 2) + u * kSide, cs);
+                read_side(s + h * (p.half / 2) + u * kSide, sn);
+#pragma unroll
+                for (int i = 0; i < kSide; ++i) {
+                  const float v = a[kSide * h + i], w = b[kSide * h + i];
+                  a[kSide * h + i] = fmaf(v, cs[i], -w * sn[i]);
+                  b[kSide * h + i] = fmaf(w, cs[i], v * sn[i]);
+                }
+              }
+            } else if constexpr (P > 1) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float cs[P / 2], sn[P / 2];
+                read_side(c + h * (p.half / 2) + u * (P / 2), cs);
+                read_side(s + h * (p.half / 2) + u * (P / 2), sn);
+#pragma unroll
+                for (int i = 0; i < P / 2; ++i) {
+                  float &v = h ? b[2 * i] : a[2 * i], &w = h ? b[2 * i + 1] : a[2 * i + 1];
+                  const float v0 = v;
+                  v = fmaf(v0, cs[i], -w * sn[i]);
+                  w = fmaf(w, cs[i], v0 * sn[i]);
+                }
+              }
+            }
+          }
+          if (CACHE && sizeof(Dst) == 1 && !queries) {
+            uint8_t *to = reinterpret_cast<uint8_t *>(cache + slot_of[CACHE ? kv : 0][k]);
+            store_e4m3<P>(to + a_at, a, scale, inv);
+            if (both) store_e4m3<P>(to + b_at, b, scale, inv);
+          } else {
+            if (rotates) {
+              va[j].set(a);
+              vb[j].set(b);
+            }
+            Src *to = out + row[j] * p.out_token;
+            if (!queries) to = reinterpret_cast<Src *>(cache + slot_of[CACHE ? kv : 0][k]);
+            va[j].store(to + a_at);
+            if (both) vb[j].store(to + b_at);
           }
         }
-      }
-      if (CACHE && run.which != 0) {
-        const int kv = run.which - 1;
-        Dst *to = static_cast<Dst *>(p.dst[kv]) + n[j].to;
-        if constexpr (sizeof(Dst) == 1) {
-          float scale = 1.0f, inv = 1.0f;
-          if (p.scale[kv]) {
-            scale = p.scale[kv][n[j].head];
-            inv = quotient_inverse(scale);
-          }
-          store_e4m3<P>(reinterpret_cast<uint8_t *>(to) + n[j].a, a, scale, inv);
-          if (both) store_e4m3<P>(reinterpret_cast<uint8_t *>(to) + n[j].b, b, scale, inv);
-        } else {
-          if (run.rotates) {
-            va[j].set(a);
-            vb[j].set(b);
-          }
-          va[j].store(reinterpret_cast<Src *>(to) + n[j].a);
-          if (both) vb[j].store(reinterpret_cast<Src *>(to) + n[j].b);
-        }
-      } else {
-        Src *to = static_cast<Src *>(p.out) + n[j].to;
-        if (run.rotates) {
-          va[j].set(a);
-          vb[j].set(b);
-        }
-        va[j].store(to + n[j].a);
-        if (both) vb[j].store(to + n[j].b);
       }
     }
   }

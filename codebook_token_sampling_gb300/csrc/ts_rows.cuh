@@ -63,6 +63,27 @@ __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = bf16_of(v); }
 __device__ __forceinline__ void store1(uint8_t *p, float v) { *p = e4m3_of(v); }
 
+// Two fp32 products and sums at once.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void parts_of(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t both_of(float a) { return pair_of(a, a); }
+
 // A unit at element `at` of a row (WIDE: its first of eight neighbours; else its
 // lane's first of four, 32 apart); elements from `dim` on are 0 and not read.
 template <bool WIDE, class T>
@@ -90,10 +111,40 @@ __device__ __forceinline__ void store_unit(T *row, int64_t at, int64_t dim, cons
   }
 }
 
-// max that keeps a NaN
+// A unit as it is stored, on its way while the one before it is worked on.
+template <class T, bool WIDE>
+struct RawUnit {
+  static constexpr int E = RowUnit<WIDE>::kElems;
+  uint32_t w[E * sizeof(T) / 4];
+  __device__ __forceinline__ void load(const T *row, int at, int dim) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < E * static_cast<int>(sizeof(T)) / 16; ++i) {
+        const uint4 v = at < dim ? reinterpret_cast<const uint4 *>(row + at)[i] : make_uint4(0, 0, 0, 0);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else {
+      T e[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = at + 32 * i < dim ? row[at + 32 * i] : T(0);
+      memcpy(w, e, sizeof w);
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+  }
+};
+
+// max that keeps a NaN, of two and of three sizes
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_size(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -101,9 +152,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // part), and the unit's elements over it.
 template <bool WIDE>
 __device__ __forceinline__ float scaled_block(float (&v)[RowUnit<WIDE>::kElems]) {
-  float a = fabsf(v[0]);
+  float a = max_size(v[0], v[1], v[2]);
 #pragma unroll
-  for (int e = 1; e < RowUnit<WIDE>::kElems; ++e) a = max_nan(a, fabsf(v[e]));
+  for (int e = 3; e + 1 < RowUnit<WIDE>::kElems; e += 2) a = max_size(a, v[e], v[e + 1]);
+  a = max_size(a, v[RowUnit<WIDE>::kElems - 1], 0.0f);
 #pragma unroll
   for (int o = RowUnit<WIDE>::kLanes / 2; o; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
   // a / 448 correctly rounded (the quotient and one correction by its remainder, as above)
