@@ -17,13 +17,12 @@ struct NormParams {
 
 // A CTA walks over rows (or, of one-warp rows, each of its blockDim.y warps does), its V
 // units per thread held in registers between the sum of squares and the output, so every
-// element is read once and written once.  With one or two units a thread has the next
-// row's on their way meanwhile: bound by DRAM.
-template <class Src, class Out, int V, bool WIDE>
-__global__ void __launch_bounds__(V <= 2 ? 512 : 1024, V <= 2 ? 2 : 1) rms_norm_kernel(const NormParams p) {
+// element is read once and written once.  AHEAD: a thread has the next row's on their way
+// meanwhile (one or two units, up to 512 threads): bound by DRAM.
+template <class Src, class Out, int V, bool WIDE, bool AHEAD>
+__global__ void __launch_bounds__(AHEAD ? 512 : 1024, AHEAD ? 2 : 1) rms_norm_kernel(const NormParams p) {
   using U = RowUnit<WIDE>;
   constexpr int E = U::kElems;
-  constexpr bool kAhead = V <= 2;
   __shared__ float part[2][32];
   const int t = static_cast<int>(threadIdx.x), lane = t & 31, warp = t >> 5, nt = static_cast<int>(blockDim.x);
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
@@ -72,7 +71,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024, V <= 2 ? 2 : 1) rms_norm_
 #pragma unroll
         for (int e = 0; e < E; ++e) h[j][e] += res[j].at(e);
     }
-    if (kAhead && r + step < p.n_rows) fetch(r + step);
+    if (AHEAD && r + step < p.n_rows) fetch(r + step);
     if (p.residual_out) {
       Src *ro = static_cast<Src *>(p.residual_out) + r * p.residual_out_stride;
 #pragma unroll
@@ -144,7 +143,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024, V <= 2 ? 2 : 1) rms_norm_
       }
       store_unit<WIDE>(out, at(j), p.dim, y);
     }
-    if (!kAhead && r + step < p.n_rows) fetch(r + step);
+    if (!AHEAD && r + step < p.n_rows) fetch(r + step);
   }
 }
 

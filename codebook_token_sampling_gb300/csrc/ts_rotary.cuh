@@ -100,29 +100,27 @@ struct Piece {
   }
 };
 
-// P quotients by a scale, rounded to e4m3 (as ts_kv_append rounds them).
+// P quotients by a scale, rounded to e4m3 as ts_kv_append rounds them: a quotient of 2^20
+// and more (or infinite, or NaN) is 448 (or NaN) without its correction too; a scale
+// that has no inverse here takes divisions.
 template <int P>
 __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[P], float scale, float inv) {
   float y[P];
-  bool fine = inv != 0.0f;
-  if constexpr (P == 1) {
-    fine &= quotient(v[0], scale, inv, y[0]);
-  } else {  // the same, two at once
+  if (inv == 0.0f) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) y[i] = __fdiv_rn(v[i], scale);
+  } else if constexpr (P == 1) {
+    if (!quotient(v[0], scale, inv, y[0])) y[0] = v[0] * inv;
+  } else {  // two at once
 #pragma unroll
     for (int i = 0; i < P; i += 2) {
       const uint64_t x = pair_of(v[i], v[i + 1]), r = both_of(inv), q = mul2(x, r);
-      float q0, q1;
+      float q0, q1, y0, y1;
       parts_of(q, q0, q1);
-      parts_of(fma2(fma2(q, both_of(-scale), x), r, q), y[i], y[i + 1]);
-      y[i] = copysignf(y[i], q0);
-      y[i + 1] = copysignf(y[i + 1], q1);
-      fine &= fabsf(q0) < 0x1p20f && fabsf(q1) < 0x1p20f;
+      parts_of(fma2(fma2(q, both_of(-scale), x), r, q), y0, y1);
+      y[i] = fabsf(q0) < 0x1p20f ? copysignf(y0, q0) : q0;
+      y[i + 1] = fabsf(q1) < 0x1p20f ? copysignf(y1, q1) : q1;
     }
-  }
-  if (!fine) {
-#pragma unroll 1
-    for (int i = 0; i < P; ++i) p[i] = e4m3_of(__fdiv_rn(v[i], scale));
-    return;
   }
   if constexpr (P == 8) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(e4m3x4_of(y[0], y[1], y[2], y[3]), e4m3x4_of(y[4], y[5], y[6], y[7]));
@@ -184,8 +182,8 @@ __device__ __forceinline__ void read_side(const float *p, float (&v)[4]) {
 // 192 us for 32,768 tokens; with lanes of several kinds 370 and 252).
 // Bound by DRAM for prompts, by latency for a frame.  CACHE: Dst is the cache's type.
 template <class Src, class Dst, int P, bool CACHE>
-__global__ void __launch_bounds__(kRotaryThreads, P == 8 ? 3 : 4) rotary_kernel(const RotaryParams p) {
-  constexpr int kUnroll = 2;
+__global__ void __launch_bounds__(kRotaryThreads, P == 1 ? 4 : 3) rotary_kernel(const RotaryParams p) {
+  constexpr int kAhead = 2;
   extern __shared__ __align__(16) float rotary_smem[];
   __shared__ int64_t row_of[kRotaryTokens];
   __shared__ int64_t slot_of[CACHE ? 2 : 1][kRotaryTokens];  // where keys and values go
@@ -263,28 +261,32 @@ __global__ void __launch_bounds__(kRotaryThreads, P == 8 ? 3 : 4) rotary_kernel(
         scale = p.scale[kv][head];
         inv = quotient_inverse(scale);
       }
-      for (int k0 = group; k0 < nt; k0 += groups * kUnroll) {
-        Piece<Src, P> va[kUnroll], vb[kUnroll];
-        int64_t row[kUnroll];
+      // the next kAhead tokens' pieces are on their way
+      Piece<Src, P> va[kAhead], vb[kAhead];
+      int64_t row[kAhead];
+      const auto fetch = [&](int j, int k) {
+        row[j] = k < nt ? row_of[k] : -1;
+        if (row[j] < 0) return;
+        const Src *from = src + row[j] * src_token;
+        va[j].load(from + a_at);
+        if (both) vb[j].load(from + b_at);
+      };
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          const int k = k0 + j * groups;
-          row[j] = k < nt ? row_of[k] : -1;
-          if (row[j] < 0) continue;
-          const Src *from = src + row[j] * src_token;
-          va[j].load(from + a_at);
-          if (both) vb[j].load(from + b_at);
-        }
+      for (int j = 0; j < kAhead; ++j) fetch(j, group + j * groups);
+      for (int k0 = group; k0 < nt; k0 += groups * kAhead) {
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          if (row[j] < 0) continue;
+        for (int j = 0; j < kAhead; ++j) {
           const int k = k0 + j * groups;
+          const int64_t here = row[j];
+          Piece<Src, P> pa = va[j], pb = vb[j];
+          fetch(j, k + kAhead * groups);
+          if (here < 0) continue;
           float a[P], b[P];
           if (rotates || (CACHE && !queries && sizeof(Dst) == 1)) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-              a[i] = va[j].at(i);
-              b[i] = both ? vb[j].at(i) : 0.0f;
+              a[i] = pa.at(i);
+              b[i] = both ? pb.at(i) : 0.0f;
             }
           }
           if (rotates) {
@@ -325,13 +327,13 @@ __global__ void __launch_bounds__(kRotaryThreads, P == 8 ? 3 : 4) rotary_kernel(
             if (both) store_e4m3<P>(to + b_at, b, scale, inv);
           } else {
             if (rotates) {
-              va[j].set(a);
-              vb[j].set(b);
+              pa.set(a);
+              pb.set(b);
             }
-            Src *to = out + row[j] * p.out_token;
+            Src *to = out + here * p.out_token;
             if (!queries) to = reinterpret_cast<Src *>(cache + slot_of[CACHE ? kv : 0][k]);
-            va[j].store(to + a_at);
-            if (both) vb[j].store(to + b_at);
+            pa.store(to + a_at);
+            if (both) pb.store(to + b_at);
           }
         }
       }

@@ -116,7 +116,7 @@ def norm_error(dim):
                                                   ("f32", "bf16", "bf16"), ("f32", "e4m3", "f32")])
 @pytest.mark.parametrize("rows,dim,pad", [(1, 1, 0), (3, 7, 0), (1, 128, 0), (5, 127, 3), (9, 129, 0), (33, 256, 8), (17, 1000, 16), (2, 1024, 0),
                                           (7, 2049, 1), (4, 4096, 0), (3, 5000, 8), (2, 8200, 0), (2, 11111, 5), (1, 32768, 0), (2, 32767, 0),
-                                          (2, 16384, 4)])
+                                          (2, 16384, 4), (700, 200, 0), (700, 1025, 0), (650, 1032, 3), (620, 2500, 8), (611, 4100, 1)])
 def test_norm(ts, sampler, rows, dim, pad, kind, out_kind, w_kind):
     rng = np.random.default_rng([rows, dim])
     x, w = rng.normal(0, 3, (rows, dim)), rng.normal(1, 0.3, dim)
@@ -528,6 +528,40 @@ def test_append_rotary(ts, sampler, tokens, heads, kv, dim, rot, block, hnd, kin
         close(kk[slots[used]], want, copied)
     rest = np.setdiff1d(np.arange(n_blocks * block), slots[used])
     assert np.all(kk[rest] == 0.5)
+
+
+@pytest.mark.parametrize("dim", [18, 64, 72])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_append_rotary_rounds_as_append(ts, sampler, kind, dim):
+    """Values of every size, infinities and NaN among them, and scales that are zero, tiny,
+    huge, infinite or NaN: the bytes that ts_kv_append writes.  Keys at position 0 (an
+    angle of zero) too, but for their zeros' signs and infinities (inf - 0 inf)."""
+    import torch
+    rng = np.random.default_rng(dim)
+    tokens, kv = 40, 8
+    x = (rng.normal(0, 1, (tokens, 2 * kv, dim)) * 10.0 ** rng.integers(-40, 38, (tokens, 2 * kv, 1))).astype(np.float32)
+    x[3, :, 0], x[4, kv:, 1], x[5, kv:, 2], x[6, kv:] = 0.0, np.inf, np.nan, -np.inf
+    pad = -dim % 16  # the cache's rows are whole pieces of 16 bytes
+    rows = put(np.pad(x, ((0, 0), (0, 0), (0, pad))), kind)
+    wide = dim + pad
+    scale = put(np.array([0.02, 0.0, 1e-38, 1e38, np.inf, np.nan, 1e-45, 3e-28]))
+    pos = torch.zeros(tokens, dtype=torch.int32, device="cuda")
+    slots = torch.arange(tokens, device="cuda")
+    f = torch.ones(dim // 2, dtype=torch.float64, device="cuda")
+    caches = []
+    for fused in (True, False):
+        k, v = (torch.zeros((3, 16, kv, wide), dtype=torch.uint8, device="cuda").view(kind_of("e4m3")) for _ in range(2))
+        cache, t = ts.KvCache(k, v, scale, scale), ts.KvTokens(rows[:, :kv], rows[:, kv:], slots)
+        if fused:
+            call = ts.Rotary(rows[:, :kv], torch.empty_like(rows[:, :kv]), pos, f)
+            ts.ts_kv_append_rotary(sampler.handle, cache, t, call)
+        else:
+            ts.ts_kv_append(sampler.handle, cache, t)
+        caches.append((codes(k), codes(v)))
+    assert np.array_equal(caches[0][1], caches[1][1])
+    same = caches[0][0] == caches[1][0]
+    zeros = ((caches[0][0] | caches[1][0]) & 0x7F) == 0
+    assert np.all(same | zeros) and sampler.read_status() == 0
 
 
 def test_append_rotary_bad_maps(ts, sampler):
