@@ -182,6 +182,7 @@ extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void
   p.out_dim = a->out_dim;
   p.blocks = static_cast<int32_t>(blocks);
   p.status = s->status;
+  p.wide_scales = aligned(a->x_scale, 16) && (a->n_rows == 1 || a->x_scale_stride % 4 == 0);
   p.wide_out = aligned(a->out, 16) && (a->n_rows == 1 || a->out_stride * es % 16 == 0);
 
   const int32_t m = a->n_rows;
