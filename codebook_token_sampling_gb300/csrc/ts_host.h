@@ -30,7 +30,8 @@ struct ts_sampler {
   struct ts_kv_state *kv;  // the paged cache's workspace (ts_reserve_kv), or null
   int kv_ctas;        // paged attention: 0 auto, else its number of CTAs (testing)
   int kv_join;        // 0 auto, 1 joins by a launch of their own, 2 by the last CTA (testing)
-  int linear_pairs;   // ts_linear_e4m3: pairs of CTAs that the GPU holds at once
+  int linear_clusters[5][4];  // ts_linear_e4m3: clusters of 1, 2, 4 and 8 CTAs of each kernel
+                              // that the GPU holds at once
   int linear_path;    // ts_linear_e4m3: 0 auto, else its kernel (testing)
   int linear_split;   // ts_linear_e4m3: 0 auto, else the CTAs that share a tile (testing)
 };

@@ -59,16 +59,19 @@ struct LinearPlan {
   int kernel, rows, columns, split;
 };
 
-// CTAs of a cluster for `tiles` tiles: as many as leave none waiting for an SM.
-int split_for(int64_t tiles, int64_t blocks, int num_sms) {
+// CTAs of a cluster for `tiles` tiles: as many as leave none waiting for an SM (1 x 4096 x
+// 4096: 5.3 us by clusters of four, 6.2 by eight to two CTAs an SM) or for room in a GPC
+// (128 x 1024 x 4096: 7.2 us by eleven clusters of eight, 11.8 by sixteen).
+int split_for(const ts_sampler *s, int kernel, int64_t tiles, int64_t blocks) {
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= num_sms && split * 2 <= blocks) split *= 2;
+  for (int i = 1; i < 4 && tiles << i <= s->num_sms && tiles <= s->linear_clusters[kernel][i] && (1 << i) <= blocks; ++i)
+    split = 1 << i;
   return split;
 }
 
 LinearPlan plan_few(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
   LinearPlan plan = {m <= 16 ? 0 : m <= 32 ? 1 : 2, m <= 16 ? 16 : m <= 32 ? 32 : 64, 128, 1};
-  plan.split = split_for(ceil_div(n, 128) * ceil_div(m, plan.rows), blocks, s->num_sms);
+  plan.split = split_for(s, plan.kernel, ceil_div(n, 128) * ceil_div(m, plan.rows), blocks);
   return plan;
 }
 // The least cycles by what a tile takes: for each block the chain from its copy to its
@@ -77,12 +80,12 @@ LinearPlan plan_few(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
 // weights: 512 rows 16 us (pairs 19), 1024 rows 20 by pairs (33); 2048 x 2048 and 2048
 // rows 12 by pairs (21).
 LinearPlan plan_rows(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks, bool pairs) {
-  const double pair_waves = static_cast<double>(ceil_div(ceil_div(m, 256) * ceil_div(n, 256), s->linear_pairs));
+  const double pair_waves = static_cast<double>(ceil_div(ceil_div(m, 256) * ceil_div(n, 256), s->linear_clusters[4][1]));
   LinearPlan best = {4, 256, 256, 1};
   double least = pairs ? pair_waves * blocks * 1080.0 + 8000.0 : 1e30;
   for (int columns = 32; columns <= 128; columns += 32) {
     const int64_t tiles = ceil_div(m, 128) * ceil_div(n, columns);
-    const int split = split_for(tiles, blocks, s->num_sms);
+    const int split = split_for(s, 3, tiles, blocks);
     const double waves = static_cast<double>(ceil_div(tiles * split, s->num_sms));
     const double at_once = static_cast<double>(std::min<int64_t>(tiles * split, s->num_sms));
     const double block = std::max(350.0 + 2.5 * columns, (128.0 + columns) * 128.0 * at_once / 5000.0);
@@ -115,21 +118,25 @@ ts_status ts_host::linear_setup(ts_sampler *s) {
         cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   }
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof cfg);
-  const LinearKernel k = kernel_for(kKernels - 1);
-  cfg.gridDim = dim3(static_cast<unsigned>(s->num_sms / 2 * 2));
-  cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
-  cfg.dynamicSmemBytes = k.smem;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaOccupancyMaxActiveClusters(&s->linear_pairs, k.fn, &cfg);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
-  if (s->linear_pairs < 1) s->linear_pairs = 1;
+  for (int i = 0; i < kKernels; ++i)
+    for (int j = 0; j < 4; ++j) {
+      const LinearKernel k = kernel_for(i);
+      cudaLaunchConfig_t cfg;
+      std::memset(&cfg, 0, sizeof cfg);
+      cfg.gridDim = dim3(static_cast<unsigned>(s->num_sms >> j << j));
+      cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
+      cfg.dynamicSmemBytes = k.smem;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 1u << j;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int held = 0;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&held, k.fn, &cfg);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+      s->linear_clusters[i][j] = std::max(held, 1);
+    }
   void *fn = nullptr;
   cudaDriverEntryPointQueryResult found;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) == cudaSuccess &&
@@ -208,7 +215,7 @@ extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void
     return TS_ERR_UNSUPPORTED;
 
   const int cluster = pair ? 2 : plan.split;
-  const int64_t grid = pair ? 2 * std::min<int64_t>(tiles, s->linear_pairs) : tiles * cluster;
+  const int64_t grid = pair ? 2 * std::min<int64_t>(tiles, s->linear_clusters[4][1]) : tiles * cluster;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(static_cast<unsigned>(grid));

@@ -28,23 +28,27 @@ struct LinearParams {
 // Few rows: 128 weight rows are the product's rows and TN tokens its columns, so a
 // tile costs no more columns than there are tokens (sixteen at least).  A tensor-copy
 // warp streams stages of one block of 128 along in_dim (weights and tokens, 128 bytes
-// a row, swizzled) through a ring; one thread of another warp issues a stage's four
-// products into one of eight accumulators in TMEM; four warps add four blocks' sums at a
-// time, times their scales, to fp32 sums in registers (row = lane).  CTAs of a cluster may
-// share a tile along in_dim; their sums are added in rank order through shared memory.
+// a row, swizzled) through a ring; a warp issues a stage's four products into an
+// accumulator in TMEM; four warps add a group of blocks' sums at a time, times their
+// scales, to fp32 sums in registers (row = lane).  CTAs of a cluster may share a tile
+// along in_dim; their sums are added in rank order through shared memory.
+// Two CTAs to an SM: half of its TMEM each, so that both always get theirs, and a ring
+// of which two fit and three do not.
 template <int TN>
 struct FewTile {
   static constexpr int kStageA = 128 * 128, kStageB = TN * 128;
-  static constexpr int kStages = TN == 16 ? 11 : TN == 32 ? 10 : 8;
-  static constexpr int kGroup = 4;  // blocks that the warps are told of at once (see below)
+  static constexpr int kStages = TN == 64 ? 4 : 5;
+  static constexpr int kGroup = TN == 64 ? 2 : 4;  // blocks that the warps are told of at once
   static constexpr int kBuffers = 2;  // of a group's accumulators
-  static constexpr uint32_t kColumns = kBuffers * kGroup * TN;  // of TMEM: a power of two, 32 at least
+  static constexpr uint32_t kColumns = kBuffers * kGroup * TN;  // of TMEM: a power of two
   static constexpr uint32_t kSmemBytes = kStages * (kStageA + kStageB) + 1024;
+  static_assert(kColumns >= 32 && kColumns <= 256, "half of TMEM at most");
+  static_assert(kSmemBytes > 76 * 1024 && kSmemBytes < 110 * 1024, "two CTAs to an SM");
 };
 constexpr int kFewThreads = 192;
 
 template <int TN>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(kFewThreads, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                       const LinearParams p) {
   using Tile = FewTile<TN>;
@@ -71,26 +75,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int nb = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / p.split) - b0;
 
   if (warp == 5) {
-    if (lane == 0) {
-      for (int i = 0; i < NS; ++i) {
-        mbar_init(full + 8 * i, 1);
-        mbar_init(empty + 8 * i, 1);
-      }
-      for (int i = 0; i < NB; ++i) {
-        mbar_init(summed + 8 * i, 1);
-        mbar_init(taken + 8 * i, 4);
-      }
-      mbar_init(done, 1);
-      gave_up = 0;
-      mbar_init_fence();
-    }
-    __syncwarp();
     tmem_alloc(smem_addr(&tmem_base), Tile::kColumns);
     tc_fence_before();
-  }
-  if (warp == 4 && lane == 0) {
-    tensor_map_prefetch(&map_w);
-    tensor_map_prefetch(&map_x);
+  } else if (warp == 4) {
+    if (lane == 0) {
+      tensor_map_prefetch(&map_w);
+      tensor_map_prefetch(&map_x);
+    }
+  } else if (warp == 0) {  // a lane a barrier
+    if (lane < 2 * (NS + NB) + 1) mbar_init(full + 8 * lane, lane >= 2 * NS + NB && lane < 2 * (NS + NB) ? 4 : 1);
+    if (lane == 0) gave_up = 0;
+    mbar_init_fence();
   }
   __syncthreads();
   tc_fence_after();
@@ -180,32 +175,36 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           if (lane + 32 * q < TN) sc[lane + 32 * q] = now[u][q];
       }
       __syncwarp();
-      const int b = (i0 / G) % NB;
-      mbar_wait(summed + 8 * b, (i0 / G / NB) & 1, &gave_up);
-      tc_fence_after();
 #pragma unroll
-      for (int u = 0; u < G; ++u) {
-        if (i0 + u >= nb) continue;
-        const float *sc = scales[warp][u];
-        constexpr int C = TN < 32 ? 16 : 32;
+      for (int g = 0; g < 4; g += G) {
+        if (i0 + g >= nb) continue;
+        const int group = (i0 + g) / G, b = group % NB;
+        mbar_wait(summed + 8 * b, (group / NB) & 1, &gave_up);
+        tc_fence_after();
 #pragma unroll
-        for (int c0 = 0; c0 < TN; c0 += C) {
-          float v[C];
-          tmem_load(tmem + (static_cast<uint32_t>(warp * 32) << 16) + (b * G + u) * TN + c0, v);
-          tmem_load_wait(v);
+        for (int u = 0; u < G; ++u) {
+          if (i0 + g + u >= nb) continue;
+          const float *sc = scales[warp][g + u];
+          constexpr int C = TN < 32 ? 16 : 32;
 #pragma unroll
-          for (int c = 0; c < C; c += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(sc + c0 + c);
-            acc[c0 + c] = fmaf(v[c], f.x, acc[c0 + c]);
-            acc[c0 + c + 1] = fmaf(v[c + 1], f.y, acc[c0 + c + 1]);
-            acc[c0 + c + 2] = fmaf(v[c + 2], f.z, acc[c0 + c + 2]);
-            acc[c0 + c + 3] = fmaf(v[c + 3], f.w, acc[c0 + c + 3]);
+          for (int c0 = 0; c0 < TN; c0 += C) {
+            float v[C];
+            tmem_load(tmem + (static_cast<uint32_t>(warp * 32) << 16) + (b * G + u) * TN + c0, v);
+            tmem_load_wait(v);
+#pragma unroll
+            for (int c = 0; c < C; c += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(sc + c0 + c);
+              acc[c0 + c] = fmaf(v[c], f.x, acc[c0 + c]);
+              acc[c0 + c + 1] = fmaf(v[c + 1], f.y, acc[c0 + c + 1]);
+              acc[c0 + c + 2] = fmaf(v[c + 2], f.z, acc[c0 + c + 2]);
+              acc[c0 + c + 3] = fmaf(v[c + 3], f.w, acc[c0 + c + 3]);
+            }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(taken + 8 * b);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(taken + 8 * b);
     }
   }
   __syncwarp();
@@ -315,26 +314,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   };
 
   if (warp == 9) {
-    if (lane == 0) {
-      for (int i = 0; i < NS; ++i) {
-        mbar_init(full + 8 * i, 1);
-        mbar_init(empty + 8 * i, 1);
-      }
-      for (int i = 0; i < NB; ++i) {
-        mbar_init(summed + 8 * i, 1);
-        mbar_init(taken + 8 * i, PAIR ? 16 : 8);
-      }
-      mbar_init(done, 1);
-      gave_up = 0;
-      mbar_init_fence();
-    }
-    __syncwarp();
     tmem_alloc<PAIR>(smem_addr(&tmem_base), 512);
     tc_fence_before();
-  }
-  if (warp == 8 && lane == 0) {
-    tensor_map_prefetch(&map_x);
-    tensor_map_prefetch(&map_w);
+  } else if (warp == 8) {
+    if (lane == 0) {
+      tensor_map_prefetch(&map_x);
+      tensor_map_prefetch(&map_w);
+    }
+  } else if (warp == 0) {  // a lane a barrier
+    static_assert(2 * (NS + NB) + 1 <= 32, "barriers");
+    if (lane < 2 * (NS + NB) + 1)
+      mbar_init(full + 8 * lane, lane >= 2 * NS + NB && lane < 2 * (NS + NB) ? (PAIR ? 16 : 8) : 1);
+    if (lane == 0) gave_up = 0;
+    mbar_init_fence();
   }
   if constexpr (PAIR) cluster_sync_all();  // the other's barriers are there
   else __syncthreads();

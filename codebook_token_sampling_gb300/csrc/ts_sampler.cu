@@ -673,7 +673,7 @@ ts_status ts_create(int device, int max_top_k, ts_sampler **out) {
   s->kv_join = 0;
   s->linear_split = 0;
   s->linear_path = 0;
-  s->linear_pairs = 0;
+  std::memset(s->linear_clusters, 0, sizeof s->linear_clusters);
   ts_status rc = TS_OK;
   e = cudaDeviceGetAttribute(&s->num_sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) rc = cuda_fail(e, "cudaDeviceGetAttribute");
