@@ -572,44 +572,78 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       int32_t m0, n0;
       place(first, m0, n0);
       const float *sums = reinterpret_cast<const float *>(ring);
-      // groups of four neighbouring sums in turn over the threads (of the cluster's CTAs along
-      // in_dim, whose sums are added in rank order)
-      const int per_row = p.columns / 4, threads = kRowsThreads * split;
-      const int groups = min(128, p.n_rows - m0) * per_row;
+      // Rows in turn over the warps (of the cluster's CTAs along in_dim, whose sums are
+      // added in rank order), lanes along them: four neighbouring sums of a lane where rows
+      // lie on 16 bytes, one where they do not, so that stores lie side by side either way.
+      constexpr int kWarps = kRowsThreads / 32;
+      const int rows = min(128, p.n_rows - m0), w0 = (split > 1 ? rank : 0) * kWarps + warp, warps = kWarps * split;
+      if (p.wide_out) {
+        const int per_row = p.columns / 4, at_once = 32 / per_row, sub = lane / per_row, c = (lane - sub * per_row) * 4;
 #pragma unroll 4
-      for (int g = (split > 1 ? rank : 0) * kRowsThreads + t; g < groups; g += threads) {
-        const int r = g / per_row, c = (g - r * per_row) * 4;
-        float f[4];
-        if (split == 1) {
-          const float4 v = *reinterpret_cast<const float4 *>(sums + r * Tile::kPitch + c);
-          f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-        } else {
-          uint4 v[8];
+        for (int r0 = w0 * at_once; r0 < rows; r0 += warps * at_once) {
+          const int r = r0 + sub;
+          if (sub >= at_once || r >= rows) continue;
+          float f[4];
+          if (split == 1) {
+            const float4 v = *reinterpret_cast<const float4 *>(sums + r * Tile::kPitch + c);
+            f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+          } else {
+            f[0] = f[1] = f[2] = f[3] = 0.0f;
+            uint4 v[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (q < split) v[q] = dsmem_ld_v4(dsmem_addr(sums + r * Tile::kPitch + c, q));
-          f[0] = f[1] = f[2] = f[3] = 0.0f;
+            for (int q = 0; q < 8; ++q)
+              if (q < split) v[q] = dsmem_ld_v4(dsmem_addr(sums + r * Tile::kPitch + c, q));
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (q < split) {
-              f[0] += __uint_as_float(v[q].x);
-              f[1] += __uint_as_float(v[q].y);
-              f[2] += __uint_as_float(v[q].z);
-              f[3] += __uint_as_float(v[q].w);
-            }
+            for (int q = 0; q < 8; ++q)
+              if (q < split) {
+                f[0] += __uint_as_float(v[q].x);
+                f[1] += __uint_as_float(v[q].y);
+                f[2] += __uint_as_float(v[q].z);
+                f[3] += __uint_as_float(v[q].w);
+              }
+          }
+          const int32_t n = n0 + c;
+          const int64_t at = (m0 + r) * p.out_stride + n;
+          if (n + 4 <= p.out_dim) {
+            if (p.out_f32) *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(f[0], f[1], f[2], f[3]);
+            else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = make_uint2(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < p.out_dim) {
+                if (p.out_f32) static_cast<float *>(p.out)[at + e] = f[e];
+                else static_cast<uint16_t *>(p.out)[at + e] = bf16_of(f[e]);
+              }
+          }
         }
-        const int32_t n = n0 + c;
-        const int64_t at = (m0 + r) * p.out_stride + n;
-        if (p.wide_out && n + 4 <= p.out_dim) {
-          if (p.out_f32) *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(f[0], f[1], f[2], f[3]);
-          else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = make_uint2(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]));
-        } else {
+      } else {
+#pragma unroll 2
+        for (int r = w0; r < rows; r += warps) {
+          const float *at = sums + r * Tile::kPitch + lane;
+          float f[2 * CH];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < p.out_dim) {
-              if (p.out_f32) static_cast<float *>(p.out)[at + e] = f[e];
-              else static_cast<uint16_t *>(p.out)[at + e] = bf16_of(f[e]);
+          for (int k = 0; k < 2 * CH; ++k) {
+            f[k] = 0.0f;
+            if (32 * k >= p.columns) continue;
+            if (split == 1) {
+              f[k] = at[32 * k];
+            } else {
+              uint32_t v[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                if (q < split) v[q] = dsmem_ld_u32(dsmem_addr(at + 32 * k, q));
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                if (q < split) f[k] += __uint_as_float(v[q]);
             }
+          }
+          const int64_t to = (m0 + r) * p.out_stride + n0 + lane;
+#pragma unroll
+          for (int k = 0; k < 2 * CH; ++k) {
+            if (32 * k >= p.columns || n0 + lane + 32 * k >= p.out_dim) continue;
+            if (p.out_f32) static_cast<float *>(p.out)[to + 32 * k] = f[k];
+            else static_cast<uint16_t *>(p.out)[to + 32 * k] = bf16_of(f[k]);
+          }
         }
       }
     }
