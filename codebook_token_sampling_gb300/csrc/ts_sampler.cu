@@ -672,6 +672,7 @@ ts_status ts_create(int device, int max_top_k, ts_sampler **out) {
   s->kv_ctas = 0;
   s->kv_join = 0;
   s->linear_split = 0;
+  s->linear_share = 0;
   s->linear_path = 0;
   std::memset(s->linear_clusters, 0, sizeof s->linear_clusters);
   ts_status rc = TS_OK;
@@ -968,6 +969,11 @@ ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value) {
   if (option == TS_OPT_LINEAR_SPLIT) {
     if (value != 0 && value != 1 && value != 2 && value != 4 && value != 8) return TS_ERR_INVALID_ARG;
     s->linear_split = value;
+    return TS_OK;
+  }
+  if (option == TS_OPT_LINEAR_SHARE) {
+    if (value != 0 && value != 1 && value != 2 && value != 4) return TS_ERR_INVALID_ARG;
+    s->linear_share = value;
     return TS_OK;
   }
   if (option == TS_OPT_LINEAR_PATH) {

@@ -328,7 +328,13 @@ def test_linear_of_whole_numbers(ts, sampler, m, n, k):
             for split in (0, 1, 2, 4, 8):
                 sampler.set_option(ts.TS_OPT_LINEAR_SPLIT, split)
                 assert np.array_equal(run_linear(ts, sampler, cx, xs, cw, ws, "f32"), want), (path, split)
+        sampler.set_option(ts.TS_OPT_LINEAR_SPLIT, 1)
+        sampler.set_option(ts.TS_OPT_LINEAR_PATH, 2)
+        for share in (1, 2, 4):
+            sampler.set_option(ts.TS_OPT_LINEAR_SHARE, share)
+            assert np.array_equal(run_linear(ts, sampler, cx, xs, cw, ws, "f32"), want), share
     finally:
+        sampler.set_option(ts.TS_OPT_LINEAR_SHARE, 0)
         sampler.set_option(ts.TS_OPT_LINEAR_PATH, 0)
         sampler.set_option(ts.TS_OPT_LINEAR_SPLIT, 0)
 
