@@ -10,11 +10,14 @@ Per step, for every stream:
                         ts_paged_attention over the cached tokens; x += out W'
     ts_lm_head_sample   the frame's logits and tokens, EOS and length stops
 
+With --weights e4m3 a layer is the library's from end to end (Layer8 below): norms,
+8-bit products, rotary positions on the way into the cache, a gated feed-forward block.
+
 The block table, lengths and slot maps are shared by all layers, the stops that
 the sampler finds in one step are what the tables release in the next, and
 nothing goes through the host.
 
-    python examples/decode_loop.py [--streams 8] [--steps 40] [--cache bf16|e4m3]
+    python examples/decode_loop.py [--streams 8] [--steps 40] [--cache bf16|e4m3] [--weights bf16|e4m3]
 """
 import argparse
 import os
@@ -29,9 +32,58 @@ import codebook_token_sampling_gb300 as ts  # noqa: E402
 import workloads  # noqa: E402
 
 
+def e4m3_weight(w):
+    """Weights [out, in] as 8-bit codes and a scale for each 128 x 128 of them."""
+    n, k = w.shape
+    pad = torch.nn.functional.pad(w.float(), (0, -k % 128, 0, -n % 128))
+    tiles = pad.view(pad.shape[0] // 128, 128, pad.shape[1] // 128, 128)
+    scale = tiles.abs().amax((1, 3)).clamp(min=2.0 ** -64) / 448
+    codes = (tiles / scale[:, None, :, None]).to(torch.float8_e4m3fn).view(pad.shape)
+    return codes[:n, :k].contiguous(), scale
+
+
+class Layer8:
+    """One layer on 8-bit weights: the calls of a step, with their buffers.  ``x`` is what
+    the layer before left to be added to the hidden state ``h``, and what this one leaves."""
+
+    def __init__(self, x, h, weights, cache, tables, freqs, heads, kv_heads, head_dim, ffn):
+        streams, dim = x.shape
+        e4m3, bf16 = torch.float8_e4m3fn, torch.bfloat16
+
+        def rows(wide, kind=bf16):
+            return torch.zeros((streams, wide), device=x.device, dtype=kind)
+
+        def rows8(wide):  # 8-bit rows and their scales
+            return rows(wide, e4m3), rows(-(-wide // 128), torch.float32)
+
+        def norm(out8):
+            return ts.RmsNorm(x, out8[0], torch.ones(dim, device=x.device), residual=h, residual_out=h, out_scale=out8[1])
+        qkv = rows((heads + 2 * kv_heads) * head_dim).view(streams, -1, head_dim)
+        q, attended = (rows(heads * head_dim).view(streams, heads, head_dim) for _ in range(2))
+        a8, o8, b8, f8, up = rows8(dim), rows8(heads * head_dim), rows8(dim), rows8(ffn), rows(2 * ffn)
+        w_qkv, w_out, w_up, w_down = (e4m3_weight(w) for w in weights)
+        self.calls = [
+            (ts.ts_rms_norm, norm(a8)),
+            (ts.ts_linear_e4m3, ts.LinearE4m3(*a8, *w_qkv, qkv.view(streams, -1))),
+            (ts.ts_kv_append_rotary, cache,
+             ts.KvTokens(qkv[:, heads:heads + kv_heads], qkv[:, heads + kv_heads:], tables.slots, tables.requests),
+             ts.Rotary(qkv[:, :heads], q, tables.positions, freqs, rows=tables.requests)),
+            (ts.ts_paged_attention, cache, ts.PagedQuery(q, attended, tables.block_table, tables.lens)),
+            (ts.ts_gate, ts.Gate(attended.view(streams, -1), o8[0], activation="none", out_scale=o8[1])),
+            (ts.ts_linear_e4m3, ts.LinearE4m3(*o8, *w_out, x)),
+            (ts.ts_rms_norm, norm(b8)),
+            (ts.ts_linear_e4m3, ts.LinearE4m3(*b8, *w_up, up)),
+            (ts.ts_gate, ts.Gate(up[:, ffn:], f8[0], up[:, :ffn], out_scale=f8[1])),
+            (ts.ts_linear_e4m3, ts.LinearE4m3(*f8, *w_down, x))]
+
+    def step(self, handle):
+        for call, *args in self.calls:
+            call(handle, *args)
+
+
 class DecodeLoop:
     def __init__(self, streams=8, steps=40, layers=2, heads=8, kv_heads=4, head_dim=64, block_size=16,
-                 vocabs=(256, 128, 128), cache="bf16", seed=0, device="cuda"):
+                 vocabs=(256, 128, 128), cache="bf16", weights="bf16", seed=0, device="cuda"):
         gen = torch.Generator(device=device).manual_seed(seed)
         dim = heads * head_dim
         q = len(vocabs)
@@ -77,6 +129,30 @@ class DecodeLoop:
             scales = [torch.full((kv_heads,), 0.02, device=device) for _ in range(2)] if cache == "e4m3" else (None, None)
             self.caches.append(ts.KvCache(k, v, *scales))
         self.batch.feedback.fill_(0)
+        self.layers8 = None
+        if weights == "e4m3":
+            ffn, wide = 2 * dim, heads * head_dim
+            freqs = torch.from_numpy(ts.ts_rotary_frequencies(head_dim)[0]).to(device)
+            self.h = torch.zeros_like(self.x)
+            self.layers8 = [Layer8(self.x, self.h, (a.t(), b.t(), weight(2 * ffn, dim), weight(dim, ffn)), c, self.tables, freqs,
+                                   heads, kv_heads, head_dim, ffn)
+                            for a, b, c in zip(self.w_qkv, self.w_out, self.caches)]
+            # the last norm, and the hidden states of all codebooks
+            last8 = (torch.zeros((streams, dim), device=device, dtype=torch.float8_e4m3fn),
+                     torch.zeros((streams, -(-dim // 128)), device=device))
+            hidden = self.head.hidden.view(torch.bfloat16).view(streams, q * wide)
+            self.last = [(ts.ts_rms_norm, ts.RmsNorm(self.x, last8[0], residual=self.h, out_scale=last8[1])),
+                         (ts.ts_linear_e4m3, ts.LinearE4m3(*last8, *e4m3_weight(self.w_codebook.t()), hidden))]
+
+    def step8(self, x):
+        """The layers on 8-bit weights, from the frame's embedding to the heads' hidden states."""
+        handle = self.sampler.handle
+        self.x.copy_(x)
+        self.h.zero_()
+        for layer in self.layers8:
+            layer.step(handle)
+        for call, *args in self.last:
+            call(handle, *args)
 
     def step(self):
         """One frame of every stream, queued on the current stream."""
@@ -84,6 +160,10 @@ class DecodeLoop:
         ts.ts_kv_tables(handle, self.tables)
         frame = self.batch.feedback.view(streams, -1).long()
         x = self.embed[frame].float().mean(1).bfloat16()
+        if self.layers8 is not None:
+            self.step8(x)
+            ts.ts_lm_head_sample(handle, self.head, self.batch)
+            return
         for cache, w_qkv, w_out in zip(self.caches, self.w_qkv, self.w_out):
             self.qkv.view(streams, -1).copy_(x @ w_qkv)
             ts.ts_kv_append(handle, cache, self.tokens)
@@ -117,8 +197,9 @@ def main():
     ap.add_argument("--streams", type=int, default=8)
     ap.add_argument("--steps", type=int, default=40)
     ap.add_argument("--cache", choices=("bf16", "e4m3"), default="bf16")
+    ap.add_argument("--weights", choices=("bf16", "e4m3"), default="bf16")
     a = ap.parse_args()
-    loop = DecodeLoop(streams=a.streams, steps=a.steps, cache=a.cache)
+    loop = DecodeLoop(streams=a.streams, steps=a.steps, cache=a.cache, weights=a.weights)
     graph = loop.capture()
     for i in range(a.steps + 1):  # the last call releases what stopped at the cap
         graph.replay()

@@ -762,3 +762,36 @@ def test_plain_launches(ts):
         got.append(out.view(torch.int16))
         s.close()
     assert torch.equal(*got)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_decode_loop_on_8_bit_weights(cache):
+    """The example's steps on 8-bit weights: graph replays against plain calls, every
+    stream's length follows its steps until it ends, all blocks come back."""
+    import os
+    import sys
+    import torch
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    try:
+        import decode_loop
+    finally:
+        sys.path.pop(0)
+    runs = []
+    for replay in (False, True):
+        loop = decode_loop.DecodeLoop(streams=6, steps=29, cache=cache, weights="e4m3", seed=3)
+        step = loop.capture().replay if replay else loop.step
+        seen = []
+        for _ in range(31):
+            step()
+            seen.append([t.clone() for t in (loop.batch.out_ids, loop.batch.finish_reason, loop.tables.lens, loop.h)])
+        torch.cuda.synchronize()
+        assert loop.sampler.read_status() == 0 and loop.tables.n_free.item() == loop.n_blocks
+        runs.append(seen)
+    for a, b in zip(*runs):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    done = torch.zeros(6, dtype=torch.bool, device="cuda")
+    for i, (_, finish, lens, h) in enumerate(runs[0]):
+        assert torch.equal(lens, torch.where(done, 0, i + 1).int()) and bool(torch.isfinite(h[~done]).all())
+        done = finish > 0
+    assert bool(done.all())
