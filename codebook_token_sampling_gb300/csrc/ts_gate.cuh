@@ -9,7 +9,7 @@ namespace ts {
 
 constexpr int kGateThreads = 256;
 constexpr int kGateUnits = 1;  // per thread at once
-constexpr int kGateCtas = 5;   // per SM
+constexpr int kGateCtas = 6;   // per SM
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3;
 
 struct GateParams {

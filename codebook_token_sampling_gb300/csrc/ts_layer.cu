@@ -143,10 +143,10 @@ ts_status launch_rotary(const ts_sampler *s, const ts_rotary_args *a, ts::Rotary
   const int64_t per_head = (a->head_dim + 2 * piece - 1) / (2 * piece), turned = p.half / piece;
   const int64_t per_token = per_head * (p.heads + 2 * static_cast<int64_t>(p.kv_heads));
   if (per_token > (1 << 23)) return TS_ERR_UNSUPPORTED;
-  // whole tokens, eight of a thread's units (or one of each of a wide token's) where SMs are
-  // busy all the same
+  // whole tokens: eight of a thread's units, twelve tokens at least (138 us with eight, 136),
+  // fewer while SMs would idle
   const int64_t n = a->n_tokens;
-  int64_t tokens = std::min<int64_t>(std::max<int64_t>(ts::kRotaryThreads * 8 / per_token, 8), (n + 4 * s->num_sms - 1) / (4 * s->num_sms));
+  int64_t tokens = std::min<int64_t>(std::max<int64_t>(ts::kRotaryThreads * 8 / per_token, 12), (n + 4 * s->num_sms - 1) / (4 * s->num_sms));
   tokens = std::min<int64_t>(tokens, std::min<int64_t>(ts::kRotaryTokens, ts::kRotaryTableFloats / a->rotary_dim));
   tokens = std::max<int64_t>(1, tokens);
   p.tokens_per_cta = static_cast<int32_t>(tokens);

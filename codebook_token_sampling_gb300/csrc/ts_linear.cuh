@@ -496,11 +496,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               float v[32];
               tmem_load(from + u * Tile::kMaxColumns + 32 * j, v);
               tmem_load_wait(v);
+              if (PAIR && j == CH - 1) release(buf);  // the last ones have come
 #pragma unroll
               for (int c = 0; c < 16; ++c) acc[j][c] = fma2(pair_of(v[2 * c], v[2 * c + 1]), scale[u][j], acc[j][c]);
             }
           }
-          release(buf);
+          if constexpr (!PAIR) release(buf);
         }
       }
       if (stalled()) break;
@@ -512,48 +513,60 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
         // a chunk's 32 x 32 outputs through the warp's own 4 KB, so that rows are stored in
         // segments of 64 or 128 bytes (16-byte columns are swapped by row: no bank twice)
-        float *staging = reinterpret_cast<float *>(ring + NS * kStage) + warp * 1024;
+        float4 *staging = reinterpret_cast<float4 *>(ring + NS * kStage) + warp * 256;
+        const int32_t m = m_now + quarter * 32;
+        const int rows = min(32, p.n_rows - m);
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
           if (j >= chunks) continue;
           const int32_t n = n_now + 32 * (c0 + j);
-          const int32_t m = m_now + quarter * 32;
+          const bool wide = p.wide_out && n + 32 <= p.out_dim;
+          if (wide && !p.out_f32) {
+            uint4 *packed = reinterpret_cast<uint4 *>(staging);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float4 f;
-            parts_of(acc[j][2 * c], f.x, f.y);
-            parts_of(acc[j][2 * c + 1], f.z, f.w);
-            reinterpret_cast<float4 *>(staging)[lane * 8 + (c ^ (lane & 7))] = f;
-          }
-          __syncwarp();
-          const int rows = min(32, p.n_rows - m);
-          if (p.wide_out && n + 32 <= p.out_dim) {
-            if (p.out_f32) {
-#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float lo, hi;
+                parts_of(acc[j][4 * c + e], lo, hi);
+                w[e] = bf16x2_of(lo, hi);
+              }
+              packed[lane * 4 + (c ^ ((lane >> 1) & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+              const int r = r0 + (lane >> 2), c = lane & 3;
+              if (r < rows)
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (m + r) * p.out_stride + n + 8 * c) =
+                    packed[r * 4 + (c ^ ((r >> 1) & 3))];
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              float4 f;
+              parts_of(acc[j][2 * c], f.x, f.y);
+              parts_of(acc[j][2 * c + 1], f.z, f.w);
+              staging[lane * 8 + (c ^ (lane & 7))] = f;
+            }
+            __syncwarp();
+            if (wide) {
+#pragma unroll 2
               for (int r0 = 0; r0 < 32; r0 += 4) {
                 const int r = r0 + (lane >> 3), c = lane & 7;
                 if (r < rows)
                   *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + (m + r) * p.out_stride + n + 4 * c) =
-                      reinterpret_cast<const float4 *>(staging)[r * 8 + (c ^ (r & 7))];
+                      staging[r * 8 + (c ^ (r & 7))];
               }
             } else {
-#pragma unroll 1
-              for (int r0 = 0; r0 < 32; r0 += 8) {
-                const int r = r0 + (lane >> 2), c = 2 * (lane & 3);
-                if (r < rows) {
-                  const float4 f = reinterpret_cast<const float4 *>(staging)[r * 8 + (c ^ (r & 7))];
-                  const float4 g = reinterpret_cast<const float4 *>(staging)[r * 8 + ((c + 1) ^ (r & 7))];
-                  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (m + r) * p.out_stride + n + 4 * c) =
-                      make_uint4(bf16x2_of(f.x, f.y), bf16x2_of(f.z, f.w), bf16x2_of(g.x, g.y), bf16x2_of(g.z, g.w));
+#pragma unroll 2
+              for (int r = 0; r < rows; ++r) {
+                const float f = reinterpret_cast<const float *>(staging)[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)];
+                if (n + lane < p.out_dim) {
+                  if (p.out_f32) static_cast<float *>(p.out)[(m + r) * p.out_stride + n + lane] = f;
+                  else static_cast<uint16_t *>(p.out)[(m + r) * p.out_stride + n + lane] = bf16_of(f);
                 }
-              }
-            }
-          } else {
-            for (int r = 0; r < rows; ++r) {
-              const float f = staging[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)];
-              if (n + lane < p.out_dim) {
-                if (p.out_f32) static_cast<float *>(p.out)[(m + r) * p.out_stride + n + lane] = f;
-                else static_cast<uint16_t *>(p.out)[(m + r) * p.out_stride + n + lane] = bf16_of(f);
               }
             }
           }
