@@ -76,7 +76,10 @@ __device__ __forceinline__ void gated(float (&y)[E], const float (&g)[E], int ac
 }
 
 // The rows' units end to end, kGateUnits of a thread at once, its next ones' loads on
-// their way while it works on these: bound by DRAM, for gelu nearly by its arithmetic.
+// their way while it works on these (six CTAs to an SM: 175 us for gelu on 16,384 x 11,008
+// to 8 bits, 5.2 TB/s; 178 with five, 209 with eight, 193 with a CTA for each two units).
+// Bound by instructions there (eight elements take 226, 73% of the issue slots, and
+// 16 of the special functions), with silu and without a gate by DRAM.
 template <class Src, class Out, bool WIDE>
 __global__ void __launch_bounds__(kGateThreads, kGateCtas) gate_kernel(const GateParams p) {
   using U = RowUnit<WIDE>;
