@@ -45,7 +45,8 @@ __device__ __forceinline__ float logistic(float g, float z) { return g * recipro
 // Stegun).  erff took longer than the loads (16,384 x 11,008: 273 us; this one element by
 // element 193).
 __device__ __forceinline__ uint64_t gelu2(uint64_t y, float g0, float g1) {
-  const float a0 = fminf(fabsf(g0), 3e38f), a1 = fminf(fabsf(g1), 3e38f);
+  // |g|, but for +inf, whose product with erfc's zero is no part of the result; a NaN stays
+  const float a0 = max_nan(-g0, min_nan(g0, 3e38f)), a1 = max_nan(-g1, min_nan(g1, 3e38f));
   const uint64_t a = pair_of(a0, a1);
   float u0, u1, e0, e1;
   parts_of(fma2(a, both_of(0.3275911f * 0.70710678f), both_of(1.0f)), u0, u1);
@@ -56,7 +57,6 @@ __device__ __forceinline__ uint64_t gelu2(uint64_t y, float g0, float g1) {
   w = fma2(t, w, both_of(0.5f * 0.284496736f));
   w = fma2(t, w, both_of(-0.5f * 0.254829592f));  // minus the half of it
   w = mul2(mul2(w, t), e);
-  // a NaN is in w, whatever the others take it for
   return mul2(y, fma2(a, w, pair_of(fmaxf(g0, 0.0f), fmaxf(g1, 0.0f))));
 }
 

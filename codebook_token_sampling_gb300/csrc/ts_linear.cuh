@@ -386,6 +386,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           if (++s == NS) s = 0, phase ^= 1;
         }
       }
+      // the last arrivals from the cluster's other CTAs come before this one leaves
+      if (PAIR || share > 1)
+        for (int j = 0; j < NS; ++j) {
+          mbar_wait(empty + 8 * s, phase, &gave_up);
+          if (++s == NS) s = 0, phase ^= 1;
+        }
       if (stalled() && (rank == 0 || !PAIR) && elected())
         for (int j = max(0, issued - NS); j < issued; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
     }

@@ -136,7 +136,12 @@ struct RawUnit {
   }
 };
 
-// max that keeps a NaN, of two and of three sizes
+// min and max that keep a NaN, the latter also of three sizes
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));

@@ -743,7 +743,7 @@ typedef struct {
   const int32_t *rows;       /* [n_tokens] or NULL */
   int32_t n_rows;            /* rows of x and out; looked at with rows only */
   float amplitude;
-  const double *freqs;       /* [rotary_dim / 2] */
+  const double *freqs;       /* [rotary_dim / 2], finite */
 } ts_rotary_args;
 ts_status ts_rotary(ts_sampler *s, const ts_rotary_args *a, void *stream);
 

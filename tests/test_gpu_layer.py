@@ -251,6 +251,30 @@ def test_gate_extremes(ts, sampler):
         close(get(out), want, rel * np.abs(want) + absolute + TINY["f32"], act)
 
 
+@pytest.mark.parametrize("dim", [16, 21])
+@pytest.mark.parametrize("kind,out_kind", [("bf16", "bf16"), ("f32", "f32"), ("f32", "e4m3")])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_gate_values_that_are_not_finite(ts, sampler, act, kind, out_kind, dim):
+    """NaN and infinite gates and factors come out as the definition has them: NaN where it
+    is inf times zero, the infinity where it is the gate itself."""
+    inf, nan = np.inf, np.nan
+    g = np.array([nan, inf, -inf, 2, 0, 3, -nan, 1] + [0.5] * (dim - 8), np.float32)
+    up = np.array([2, 3, 4, nan, inf, -inf, 0, 1] + [-2.0] * (dim - 8), np.float32)
+    rows = np.stack([np.roll(np.arange(dim), r) for r in range(dim)])
+    gate, factor = put(g[rows], kind), put(up[rows], kind)
+    with np.errstate(all="ignore"):
+        want = olayer.activation(get(gate), act) * get(factor)
+    out = put(np.zeros((dim, dim)), out_kind)
+    scale = put(np.zeros((dim, 1))) if out_kind == "e4m3" else None
+    ts.ts_gate(sampler.handle, ts.Gate(factor, out, gate, activation=act, out_scale=scale))
+    if out_kind == "e4m3":  # one block a row
+        assert bool(scale.isnan().all()) and np.all(codes(out) & 0x7F == 0x7F)
+        return
+    got, there = get(out), np.isfinite(want)
+    assert np.array_equal(np.where(there, 0, got), np.where(there, 0, want), equal_nan=True)
+    assert np.all(np.abs(got[there] - want[there]) <= 2.0 ** -6 * np.abs(want[there]))
+
+
 # --------------------------------------------------------------------------
 # The 8-bit product
 # --------------------------------------------------------------------------
