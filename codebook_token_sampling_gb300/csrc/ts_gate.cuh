@@ -8,8 +8,10 @@
 namespace ts {
 
 constexpr int kGateThreads = 256;
-constexpr int kGateUnits = 1;  // per thread at once
-constexpr int kGateCtas = 6;   // per SM
+// CTAs per SM: four where elements of 32 bits are on their way (fp32 to 8 bits, gelu on 16,384 x
+// 11,008: 242 us, 383 with five and spills; bf16 to fp32 213, 251), else five (bf16 to 8
+// bits, silu: 140 us, 147 with four; no gate 98, 107; gelu 174, 169; bf16 to bf16 159, 167).
+constexpr int gate_ctas(int in_bytes, int out_bytes) { return in_bytes == 4 || out_bytes == 4 ? 4 : 5; }
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3;
 
 struct GateParams {
@@ -17,8 +19,13 @@ struct GateParams {
   void *out;
   float *scale;
   int64_t up_stride, gate_stride, out_stride, scale_stride;
-  int64_t step_rows;   // from a CTA's units to its next ones: rows, and units of a row
-  uint32_t step_units;
+  // from a thread's unit to its next one: rows, elements along a row, and what the
+  // addresses move by, with what that is off by where the row's end is passed
+  struct Move {
+    int64_t up, gate, out, scale;
+  } step, wrap;
+  uint32_t step_rows;
+  int32_t step_elems, row_elems;  // row_elems: a row's, up to whole blocks
   int32_t n_rows, dim, act;
   FastDiv by_row;  // units per row: whole blocks of 128 elements
 };
@@ -75,76 +82,72 @@ __device__ __forceinline__ void gated(float (&y)[E], const float (&g)[E], int ac
   }
 }
 
-// The rows' units end to end, kGateUnits of a thread at once, its next ones' loads on
-// their way while it works on these (six CTAs to an SM: 175 us for gelu on 16,384 x 11,008
-// to 8 bits, 5.2 TB/s; 178 with five, 209 with eight, 193 with a CTA for each two units).
-// Bound by instructions there (eight elements take 226, 73% of the issue slots, and
-// 16 of the special functions), with silu and without a gate by DRAM.
+// The rows' units end to end, a thread's next one's loads on their way while it works on
+// this one; addresses move along by additions (16,384 x 11,008 bf16 to 8 bits, gelu: 174 us,
+// 5.2 TB/s; 193 with a CTA for each two units).  Bound by instructions there (about 210 for
+// eight elements, 16 of them special functions), with silu (140 us, 6.5 TB/s) and without a
+// gate by DRAM.
 template <class Src, class Out, bool WIDE>
-__global__ void __launch_bounds__(kGateThreads, kGateCtas) gate_kernel(const GateParams p) {
+__global__ void __launch_bounds__(kGateThreads, gate_ctas(sizeof(Src), sizeof(Out))) gate_kernel(const GateParams p) {
   using U = RowUnit<WIDE>;
   constexpr int E = U::kElems;
-  constexpr int N = kGateUnits;
   pdl_wait_and_release();
   const bool act = p.act != kActNone;
   const uint32_t per_row = p.by_row.d;
-  int64_t row[N];
-  uint32_t in[N];  // unit of the row
+  uint32_t row;    // of the unit that is fetched next
+  int32_t at;      // its (lane's) first element
+  const Src *up_at, *gate_at;
+  Out *out_next;
+  float *scale_next;
   {
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * (kGateThreads * N);
-    const int64_t r0 = base / per_row;
-    const uint32_t off0 = static_cast<uint32_t>(base - r0 * per_row) + threadIdx.x;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const uint32_t u = off0 + j * kGateThreads, r = p.by_row.div(u);
-      row[j] = r0 + r;
-      in[j] = u - r * per_row;
-    }
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * kGateThreads, r0 = base / per_row;
+    const uint32_t u = static_cast<uint32_t>(base - r0 * per_row) + threadIdx.x, r = p.by_row.div(u), c = u - r * per_row;
+    row = static_cast<uint32_t>(r0) + r;
+    at = WIDE ? static_cast<int32_t>(c * 8) : static_cast<int32_t>((c >> 5) * kScaleBlock + (c & 31));
+    up_at = static_cast<const Src *>(p.up) + row * p.up_stride + at;
+    gate_at = static_cast<const Src *>(p.gate) + row * p.gate_stride + at;
+    out_next = static_cast<Out *>(p.out) + row * p.out_stride + at;
+    scale_next = p.scale + row * p.scale_stride + at / kScaleBlock;
   }
-  RawUnit<Src, WIDE> up[N], gate[N];
-  const auto at = [&](uint32_t c) {
-    return WIDE ? static_cast<int32_t>(c * 8) : static_cast<int32_t>((c >> 5) * kScaleBlock + (c & 31));
-  };
+  const uint32_t n_rows = static_cast<uint32_t>(p.n_rows);
+  RawUnit<Src, WIDE> up, gate;
   const auto fetch = [&]() {
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int32_t dim = row[j] < p.n_rows ? p.dim : 0;  // behind the last row: no elements
-      up[j].load(static_cast<const Src *>(p.up) + row[j] * p.up_stride, at(in[j]), dim);
-      if (act) gate[j].load(static_cast<const Src *>(p.gate) + row[j] * p.gate_stride, at(in[j]), dim);
-    }
+    const int32_t left = row < n_rows ? p.dim - at : 0;  // behind the last row: no elements
+    up.load(up_at, 0, left);
+    if (act) gate.load(gate_at, 0, left);
   };
   fetch();
-  while (__any_sync(0xFFFFFFFFu, row[0] < p.n_rows)) {
-    float y[N][E], g[N][E];
-    int64_t now[N];
-    int32_t here[N];
+  while (__any_sync(0xFFFFFFFFu, row < n_rows)) {
+    float y[E], g[E];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        y[j][e] = up[j].at(e);
-        g[j][e] = gate[j].at(e);
-      }
-      now[j] = row[j];
-      here[j] = row[j] < p.n_rows ? at(in[j]) : p.dim + kScaleBlock;
-      row[j] += p.step_rows;
-      in[j] += p.step_units;
-      if (in[j] >= per_row) {
-        in[j] -= per_row;
-        ++row[j];
-      }
+    for (int e = 0; e < E; ++e) {
+      y[e] = up.at(e);
+      g[e] = gate.at(e);
+    }
+    const int32_t left = row < n_rows ? p.dim - at : 0;
+    Out *out = out_next;
+    float *scale_at = scale_next;
+    row += p.step_rows;
+    at += p.step_elems;
+    up_at += p.step.up;
+    gate_at += p.step.gate;
+    out_next += p.step.out;
+    scale_next += p.step.scale;
+    if (at >= p.row_elems) {
+      ++row;
+      at -= p.row_elems;
+      up_at += p.wrap.up;
+      gate_at += p.wrap.gate;
+      out_next += p.wrap.out;
+      scale_next += p.wrap.scale;
     }
     fetch();
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if (act) gated<E>(y[j], g[j], p.act);
-      if constexpr (sizeof(Out) == 1) {
-        const float scale = scaled_block<WIDE>(y[j]);
-        const int first = static_cast<int>(lane_id()) & (U::kLanes - 1);
-        if (first == 0 && here[j] < p.dim) p.scale[now[j] * p.scale_stride + here[j] / kScaleBlock] = scale;
-      }
-      store_unit<WIDE>(static_cast<Out *>(p.out) + now[j] * p.out_stride, here[j], p.dim, y[j]);
+    if (act) gated<E>(y, g, p.act);
+    if constexpr (sizeof(Out) == 1) {
+      const float scale = scaled_block<WIDE>(y);
+      if ((lane_id() & (U::kLanes - 1)) == 0 && left > 0) *scale_at = scale;
     }
+    store_unit<WIDE>(out, 0, left, y);
   }
 }
 

@@ -293,11 +293,23 @@ ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream) {
   p.act = a->act;
   const int64_t per_row = scales_of(dim) * (wide ? 16 : 32);
   p.by_row = ts::FastDiv::of(static_cast<uint32_t>(per_row));
-  const int64_t per_cta = ts::kGateThreads * ts::kGateUnits, all = (n * per_row + per_cta - 1) / per_cta;
-  const int64_t grid = std::min<int64_t>(all, ts::kGateCtas * s->num_sms);
+  const int64_t all = (n * per_row + ts::kGateThreads - 1) / ts::kGateThreads;
+  const int64_t grid = std::min<int64_t>(all, static_cast<int64_t>(ts::gate_ctas(es, os)) * s->num_sms), step = grid * ts::kGateThreads;
+  // whole blocks: the threads and a row's units are multiples of a block's
+  const int64_t step_rows = step / per_row, step_elems = step % per_row * (wide ? 8 : 4);
   p.n_rows = a->n_rows;
-  p.step_rows = grid * per_cta / per_row;
-  p.step_units = static_cast<uint32_t>(grid * per_cta % per_row);
+  p.step_rows = static_cast<uint32_t>(step_rows);
+  p.step_elems = static_cast<int32_t>(step_elems);
+  p.row_elems = static_cast<int32_t>(scales_of(dim) * TS_SCALE_BLOCK);
+  const auto move = [&](int64_t stride, int64_t in_row, int64_t row, int64_t *step_by, int64_t *wrap_by) {
+    if (n == 1) stride = 0;  // says nothing
+    *step_by = step_rows * stride + in_row;
+    *wrap_by = stride - row;
+  };
+  move(a->up_stride, step_elems, p.row_elems, &p.step.up, &p.wrap.up);
+  move(a->gate_stride, step_elems, p.row_elems, &p.step.gate, &p.wrap.gate);
+  move(a->out_stride, step_elems, p.row_elems, &p.step.out, &p.wrap.out);
+  move(a->out_scale_stride, step_elems / TS_SCALE_BLOCK, scales_of(dim), &p.step.scale, &p.wrap.scale);
   const void *fn = a->dtype == TS_DTYPE_F32 ? gate_kernel_to<float>(a->out_dtype, wide)
                                             : gate_kernel_to<uint16_t>(a->out_dtype, wide);
   void *args[] = {&p};
