@@ -8,10 +8,13 @@
 namespace ts {
 
 constexpr int kGateThreads = 256;
-// CTAs per SM: four where elements of 32 bits are on their way (fp32 to 8 bits, gelu on 16,384 x
-// 11,008: 242 us, 383 with five and spills; bf16 to fp32 213, 251), else five (bf16 to 8
-// bits, silu: 140 us, 147 with four; no gate 98, 107; gelu 174, 169; bf16 to bf16 159, 167).
-constexpr int gate_ctas(int in_bytes, int out_bytes) { return in_bytes == 4 || out_bytes == 4 ? 4 : 5; }
+// CTAs per SM: three of sixteen elements a lane (bf16 to 8 bits, gelu on 16,384 x 11,008: 140
+// us, 225 with four and spills), four where elements of 32 bits are on their way (fp32 to 8
+// bits 242 us, 383 with five and spills; bf16 to fp32 213, 251), else five (bf16 to bf16 159,
+// 167 with four).
+constexpr int gate_ctas(int in_bytes, int out_bytes, int width) {
+  return width == 16 ? 3 : in_bytes == 4 || out_bytes == 4 ? 4 : 5;
+}
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3;
 
 struct GateParams {
@@ -83,14 +86,13 @@ __device__ __forceinline__ void gated(float (&y)[E], const float (&g)[E], int ac
 }
 
 // The rows' units end to end, a thread's next one's loads on their way while it works on
-// this one; addresses move along by additions (16,384 x 11,008 bf16 to 8 bits, gelu: 174 us,
-// 5.2 TB/s; 193 with a CTA for each two units).  Bound by instructions there (about 210 for
-// eight elements, 16 of them special functions), with silu (140 us, 6.5 TB/s) and without a
-// gate by DRAM.
-template <class Src, class Out, bool WIDE>
-__global__ void __launch_bounds__(kGateThreads, gate_ctas(sizeof(Src), sizeof(Out))) gate_kernel(const GateParams p) {
-  using U = RowUnit<WIDE>;
-  constexpr int E = U::kElems;
+// this one; addresses move along by additions.  16,384 x 11,008 bf16 to 8 bits, sixteen
+// elements a lane: gelu 140 us, 6.5 TB/s, bound by DRAM like silu (134 us) and no gate (94).
+// With eight elements a lane 174 us, bound by instructions (about 210 for eight, half of them
+// for the block's scale, addresses and the loop); a CTA for each two units 193.
+template <class Src, class Out, int W>
+__global__ void __launch_bounds__(kGateThreads, gate_ctas(sizeof(Src), sizeof(Out), W)) gate_kernel(const GateParams p) {
+  using U = RowUnit<W>;
   pdl_wait_and_release();
   const bool act = p.act != kActNone;
   const uint32_t per_row = p.by_row.d;
@@ -103,14 +105,14 @@ __global__ void __launch_bounds__(kGateThreads, gate_ctas(sizeof(Src), sizeof(Ou
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kGateThreads, r0 = base / per_row;
     const uint32_t u = static_cast<uint32_t>(base - r0 * per_row) + threadIdx.x, r = p.by_row.div(u), c = u - r * per_row;
     row = static_cast<uint32_t>(r0) + r;
-    at = WIDE ? static_cast<int32_t>(c * 8) : static_cast<int32_t>((c >> 5) * kScaleBlock + (c & 31));
+    at = U::kWide ? static_cast<int32_t>(c * W) : static_cast<int32_t>((c >> 5) * kScaleBlock + (c & 31));
     up_at = static_cast<const Src *>(p.up) + row * p.up_stride + at;
     gate_at = static_cast<const Src *>(p.gate) + row * p.gate_stride + at;
     out_next = static_cast<Out *>(p.out) + row * p.out_stride + at;
     scale_next = p.scale + row * p.scale_stride + at / kScaleBlock;
   }
   const uint32_t n_rows = static_cast<uint32_t>(p.n_rows);
-  RawUnit<Src, WIDE> up, gate;
+  RawUnit<Src, W> up, gate;
   const auto fetch = [&]() {
     const int32_t left = row < n_rows ? p.dim - at : 0;  // behind the last row: no elements
     up.load(up_at, 0, left);
@@ -118,9 +120,9 @@ __global__ void __launch_bounds__(kGateThreads, gate_ctas(sizeof(Src), sizeof(Ou
   };
   fetch();
   while (__any_sync(0xFFFFFFFFu, row < n_rows)) {
-    float y[E], g[E];
+    float y[W], g[W];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
+    for (int e = 0; e < W; ++e) {
       y[e] = up.at(e);
       g[e] = gate.at(e);
     }
@@ -142,12 +144,12 @@ __global__ void __launch_bounds__(kGateThreads, gate_ctas(sizeof(Src), sizeof(Ou
       scale_next += p.wrap.scale;
     }
     fetch();
-    if (act) gated<E>(y, g, p.act);
+    if (act) gated<W>(y, g, p.act);
     if constexpr (sizeof(Out) == 1) {
-      const float scale = scaled_block<WIDE>(y);
+      const float scale = scaled_block<W>(y);
       if ((lane_id() & (U::kLanes - 1)) == 0 && left > 0) *scale_at = scale;
     }
-    store_unit<WIDE>(out, 0, left, y);
+    store_unit<W>(out, 0, left, y);
   }
 }
 

@@ -33,9 +33,9 @@ struct Rows {
   int64_t stride;
   int es;
 };
-// Whether rows of `dim` can be moved in pieces of eight elements.
-bool in_pieces(const Rows &r, int64_t n_rows) {
-  const int64_t to = r.es == 1 ? 8 : 16;
+// Whether rows can be moved in pieces of `width` elements (8 or 16).
+bool in_pieces(const Rows &r, int64_t n_rows, int width) {
+  const int64_t to = width == 8 ? std::min(16, 8 * r.es) : 16 * r.es;
   return aligned(r.p, static_cast<size_t>(to)) && (n_rows == 1 || r.stride * r.es % to == 0);
 }
 
@@ -43,34 +43,38 @@ bool in_pieces(const Rows &r, int64_t n_rows) {
 // Norm
 // --------------------------------------------------------------------------
 template <class Src, class Out>
-const void *norm_kernel(int v, bool wide) {
-  if (wide)
-    return v == 1 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 1, true, true>)
-         : v == 2 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 2, true, true>)
-                  : reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 4, true, false>);
-  return v == 1 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 1, false, true>)
-       : v == 2 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 2, false, true>)
-       : v == 4 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 4, false, false>)
-                : reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 8, false, false>);
+const void *norm_kernel(int v, int width) {
+  if constexpr (sizeof(Src) == 2 && sizeof(Out) == 1)
+    if (width == 16) return reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 1, 16, true>);
+  if (width == 8)
+    return v == 1 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 1, 8, true>)
+         : v == 2 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 2, 8, true>)
+                  : reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 4, 8, false>);
+  return v == 1 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 1, 4, true>)
+       : v == 2 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 2, 4, true>)
+       : v == 4 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 4, 4, false>)
+                : reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 8, 4, false>);
 }
 template <class Src>
-const void *norm_kernel_to(int32_t out, int v, bool wide) {
-  return out == TS_DTYPE_F32 ? norm_kernel<Src, float>(v, wide)
-       : out == TS_DTYPE_BF16 ? norm_kernel<Src, uint16_t>(v, wide) : norm_kernel<Src, uint8_t>(v, wide);
+const void *norm_kernel_to(int32_t out, int v, int width) {
+  return out == TS_DTYPE_F32 ? norm_kernel<Src, float>(v, width)
+       : out == TS_DTYPE_BF16 ? norm_kernel<Src, uint16_t>(v, width) : norm_kernel<Src, uint8_t>(v, width);
 }
 
 // --------------------------------------------------------------------------
 // Gate
 // --------------------------------------------------------------------------
 template <class Src>
-const void *gate_kernel_to(int32_t out, bool wide) {
-  if (wide)
-    return out == TS_DTYPE_F32 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, float, true>)
-         : out == TS_DTYPE_BF16 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, uint16_t, true>)
-                                : reinterpret_cast<const void *>(ts::gate_kernel<Src, uint8_t, true>);
-  return out == TS_DTYPE_F32 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, float, false>)
-       : out == TS_DTYPE_BF16 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, uint16_t, false>)
-                              : reinterpret_cast<const void *>(ts::gate_kernel<Src, uint8_t, false>);
+const void *gate_kernel_to(int32_t out, int width) {
+  if constexpr (sizeof(Src) == 2)
+    if (width == 16) return reinterpret_cast<const void *>(ts::gate_kernel<Src, uint8_t, 16>);
+  if (width == 8)
+    return out == TS_DTYPE_F32 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, float, 8>)
+         : out == TS_DTYPE_BF16 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, uint16_t, 8>)
+                                : reinterpret_cast<const void *>(ts::gate_kernel<Src, uint8_t, 8>);
+  return out == TS_DTYPE_F32 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, float, 4>)
+       : out == TS_DTYPE_BF16 ? reinterpret_cast<const void *>(ts::gate_kernel<Src, uint16_t, 4>)
+                              : reinterpret_cast<const void *>(ts::gate_kernel<Src, uint8_t, 4>);
 }
 
 // --------------------------------------------------------------------------
@@ -210,8 +214,17 @@ ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream) {
       (!same(sum, x) && span(sum).meets(span(x))) || (!same(sum, res) && span(sum).meets(span(res))))
     return TS_ERR_INVALID_ARG;
 
-  bool wide = dim % 8 == 0 && (!ws || aligned(a->weight, 16));
-  for (const Rows &r : {x, res, sum, out}) wide = wide && (!r.p || in_pieces(r, n));
+  // Sixteen elements a lane to 8-bit rows where rows are many: a block's scale by fewer lanes
+  // (32,768 x 4096 without a residual 83 us, 125 with eight; x 1024 with one 37, 43), but for
+  // wide rows with a residual, which DRAM bounds either way (x 4096 149 us, 146 with eight).
+  const bool half = a->dtype == TS_DTYPE_BF16 && e4m3 && dim >= 512 && dim <= (a->residual ? 2048 : 4096) &&
+                    n > 4 * s->num_sms;
+  const auto fits = [&](int width) {
+    bool ok = dim % width == 0 && (!ws || aligned(a->weight, 16));
+    for (const Rows &r : {x, res, sum, out}) ok = ok && (!r.p || in_pieces(r, n, width));
+    return ok;
+  };
+  const int width = half && fits(16) ? 16 : fits(8) ? 8 : 4;
   ts::NormParams p;
   std::memset(&p, 0, sizeof p);
   p.x = a->x;
@@ -232,22 +245,22 @@ ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream) {
   p.weight_offset = a->weight_offset;
 
   // Threads of a row, 512 at most and the next row's loads on their way: one unit each, two
-  // of 16 bytes where rows are many (32,768 x 4096: 146 us, 151 with one).  The widest rows
-  // take up to 1024 threads and more units.
-  const int units = static_cast<int>(wide ? (dim + 7) / 8 : scales_of(dim) * 32);
-  const bool many = n > 4 * s->num_sms && wide && units > 128;
+  // of eight elements where rows are many (32,768 x 4096: 146 us, 151 with one).  The widest
+  // rows take up to 1024 threads and more units.
+  const int units = static_cast<int>(width > 4 ? (dim + width - 1) / width : scales_of(dim) * 32);
+  const bool many = n > 4 * s->num_sms && width == 8 && units > 128;
   const int v = units <= 512 && !many ? 1 : units <= 1024 ? 2 : units <= 4096 ? 4 : 8;
   const int threads = ((units + v - 1) / v + 31) / 32 * 32;
   const int rows = threads == 32 ? 8 : 1;
-  // as many CTAs as the GPU holds (64 registers a thread)
+  // as many CTAs as the GPU holds (64 registers a thread, 85 for sixteen elements)
   const int64_t ctas = std::min<int64_t>((n + rows - 1) / rows,
-                                         static_cast<int64_t>(s->num_sms) * std::max(1, 1024 / (threads * rows)));
-  const void *fn = a->dtype == TS_DTYPE_F32 ? norm_kernel_to<float>(a->out_dtype, v, wide)
-                                            : norm_kernel_to<uint16_t>(a->out_dtype, v, wide);
+                                         static_cast<int64_t>(s->num_sms) * std::max(1, (width == 16 ? 768 : 1024) / (threads * rows)));
+  const void *fn = a->dtype == TS_DTYPE_F32 ? norm_kernel_to<float>(a->out_dtype, v, width)
+                                            : norm_kernel_to<uint16_t>(a->out_dtype, v, width);
   void *args[] = {&p};
   const cudaError_t e =
       launch(fn, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(rows)),
-             0, s->pdl != 0, static_cast<cudaStream_t>(stream), args);
+             width == 16 && a->weight ? static_cast<size_t>(threads * rows) * 64 : 0, s->pdl != 0, static_cast<cudaStream_t>(stream), args);
   return e == cudaSuccess ? TS_OK : cuda_fail(e, "norm launch");
 }
 
@@ -277,8 +290,15 @@ ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream) {
       (!same(out, up) && span(out).meets(span(up))) || (!same(out, gate) && span(out).meets(span(gate))))
     return TS_ERR_INVALID_ARG;
 
-  bool wide = dim % 8 == 0;
-  for (const Rows &r : {up, gate, out}) wide = wide && (!r.p || in_pieces(r, n));
+  const auto fits = [&](int width) {
+    bool ok = dim % width == 0;
+    for (const Rows &r : {up, gate, out}) ok = ok && (!r.p || in_pieces(r, n, width));
+    return ok;
+  };
+  // sixteen elements a lane to 8-bit rows where every thread of the GPU has some (gelu on
+  // 16,384 x 11,008 140 us, 174 with eight)
+  const bool half = a->dtype == TS_DTYPE_BF16 && e4m3 && n * scales_of(dim) * 8 >= 4ll * s->num_sms * ts::kGateThreads;
+  const int width = half && fits(16) ? 16 : fits(8) ? 8 : 4;
   ts::GateParams p;
   std::memset(&p, 0, sizeof p);
   p.up = a->up;
@@ -291,12 +311,12 @@ ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream) {
   p.scale_stride = a->out_scale_stride;
   p.dim = a->dim;
   p.act = a->act;
-  const int64_t per_row = scales_of(dim) * (wide ? 16 : 32);
+  const int64_t per_row = scales_of(dim) * (TS_SCALE_BLOCK / width);
   p.by_row = ts::FastDiv::of(static_cast<uint32_t>(per_row));
   const int64_t all = (n * per_row + ts::kGateThreads - 1) / ts::kGateThreads;
-  const int64_t grid = std::min<int64_t>(all, static_cast<int64_t>(ts::gate_ctas(es, os)) * s->num_sms), step = grid * ts::kGateThreads;
+  const int64_t grid = std::min<int64_t>(all, static_cast<int64_t>(ts::gate_ctas(es, os, width)) * s->num_sms), step = grid * ts::kGateThreads;
   // whole blocks: the threads and a row's units are multiples of a block's
-  const int64_t step_rows = step / per_row, step_elems = step % per_row * (wide ? 8 : 4);
+  const int64_t step_rows = step / per_row, step_elems = step % per_row * width;
   p.n_rows = a->n_rows;
   p.step_rows = static_cast<uint32_t>(step_rows);
   p.step_elems = static_cast<int32_t>(step_elems);
@@ -310,8 +330,8 @@ ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream) {
   move(a->gate_stride, step_elems, p.row_elems, &p.step.gate, &p.wrap.gate);
   move(a->out_stride, step_elems, p.row_elems, &p.step.out, &p.wrap.out);
   move(a->out_scale_stride, step_elems / TS_SCALE_BLOCK, scales_of(dim), &p.step.scale, &p.wrap.scale);
-  const void *fn = a->dtype == TS_DTYPE_F32 ? gate_kernel_to<float>(a->out_dtype, wide)
-                                            : gate_kernel_to<uint16_t>(a->out_dtype, wide);
+  const void *fn = a->dtype == TS_DTYPE_F32 ? gate_kernel_to<float>(a->out_dtype, width)
+                                            : gate_kernel_to<uint16_t>(a->out_dtype, width);
   void *args[] = {&p};
   const cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), ts::kGateThreads, 0, s->pdl != 0,
                                static_cast<cudaStream_t>(stream), args);

@@ -19,14 +19,19 @@ struct NormParams {
 // units per thread held in registers between the sum of squares and the output, so every
 // element is read once and written once.  AHEAD: a thread has the next row's on their way
 // meanwhile (one or two units, up to 512 threads).  Bound by DRAM: 32,768 rows of 4096 with
-// residual and 8-bit outputs take 146 us, 6.5 TB/s (186 us with a CTA for each row); a
-// frame of 32 x 1024 by launch and two trips to memory, 1.9 us; rows of odd width by their
-// single elements' loads and stores (5000 x 1001 fp32 9.0 us, floor 4.4).
-template <class Src, class Out, int V, bool WIDE, bool AHEAD>
-__global__ void __launch_bounds__(AHEAD ? 512 : 1024, AHEAD ? 2 : 1) rms_norm_kernel(const NormParams p) {
-  using U = RowUnit<WIDE>;
-  constexpr int E = U::kElems;
+// residual and 8-bit outputs take 146 us, 6.5 TB/s (186 us with a CTA for each row); without a
+// residual by instructions too (83 us, floor 60; 125 with eight elements a lane).  A frame
+// of 32 x 1024 takes a launch and two trips to memory, 1.9 us; rows of odd width their
+// single elements' loads and stores (5000 x 1001 fp32 9.0 us, floor 4.4).  Rows above 8192
+// are not AHEAD (8192 x 16,384 fp32 to 8 bits 316 us; with the next row's loads held beside
+// this one's sums and spills 458).
+template <class Src, class Out, int V, int W, bool AHEAD>
+__global__ void __launch_bounds__(W == 16 ? 256 : AHEAD ? 512 : 1024, W == 16 ? 3 : AHEAD ? 2 : 1) rms_norm_kernel(const NormParams p) {
+  using U = RowUnit<W>;
   __shared__ float part[2][32];
+  // a thread's weights with their offset, where it keeps its elements over many rows: four
+  // pieces [4][threads]
+  extern __shared__ float4 norm_factors[];
   const int t = static_cast<int>(threadIdx.x), lane = t & 31, warp = t >> 5, nt = static_cast<int>(blockDim.x);
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
   int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -34,17 +39,22 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024, AHEAD ? 2 : 1) rms_norm_ke
   if (r >= p.n_rows) return;  // whole warps, of CTAs whose rows are warps
 
   const auto at = [&](int j) {
-    return WIDE ? (t + j * nt) * 8 : (warp + j * (nt >> 5)) * kScaleBlock + lane;
+    return U::kWide ? (t + j * nt) * W : (warp + j * (nt >> 5)) * kScaleBlock + lane;
   };
-  RawUnit<Src, WIDE> x[V], res[V];
+  // (rows that are not AHEAD: a unit's sum at once, so that no more is held than their sums)
+  RawUnit<Src, W> x[AHEAD ? V : 1], res[AHEAD ? V : 1];
   const auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) x[j].load(static_cast<const Src *>(p.x) + row * p.x_stride, at(j), p.dim);
+    for (int j = 0; j < (AHEAD ? V : 0); ++j) x[j].load(static_cast<const Src *>(p.x) + row * p.x_stride, at(j), p.dim);
     if (p.residual) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
+      for (int j = 0; j < (AHEAD ? V : 0); ++j)
         res[j].load(static_cast<const Src *>(p.residual) + row * p.residual_stride, at(j), p.dim);
     }
+  };
+  const auto weights = [&](int j, float (&w)[W]) {
+    if (p.weight_f32) load_unit<W>(static_cast<const float *>(p.weight), at(j), p.dim, w);
+    else load_unit<W>(static_cast<const uint16_t *>(p.weight), at(j), p.dim, w);
   };
   int flip = 0;
   // f's sum or largest value over the row's threads, in a fixed order
@@ -61,33 +71,71 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024, AHEAD ? 2 : 1) rms_norm_ke
     return v;
   };
 
-  fetch(r);
+  if constexpr (AHEAD) fetch(r);
+  float4 *own = norm_factors + threadIdx.y * nt + t;
+  const int apart = nt * static_cast<int>(blockDim.y);
+  if constexpr (W == 16) {
+    if (p.weight) {
+      float w[W];
+      weights(0, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        own[i * apart] = make_float4(w[4 * i] + p.weight_offset, w[4 * i + 1] + p.weight_offset,
+                                      w[4 * i + 2] + p.weight_offset, w[4 * i + 3] + p.weight_offset);
+    }
+  }
   for (; r < p.n_rows; r += step) {
-    float h[V][E];
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-      for (int e = 0; e < E; ++e) h[j][e] = x[j].at(e);
-    if (p.residual) {
+    float h[V][W];
+    if constexpr (AHEAD) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[j][e] += res[j].at(e);
+        for (int e = 0; e < W; ++e) h[j][e] = x[j].at(e);
+      if (p.residual) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+          for (int e = 0; e < W; ++e) h[j][e] += res[j].at(e);
+      }
+    } else {
+      const Src *from = static_cast<const Src *>(p.x) + r * p.x_stride;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        x[0].load(from, at(j), p.dim);
+#pragma unroll
+        for (int e = 0; e < W; ++e) h[j][e] = x[0].at(e);
+      }
+      if (p.residual) {
+        from = static_cast<const Src *>(p.residual) + r * p.residual_stride;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          res[0].load(from, at(j), p.dim);
+#pragma unroll
+          for (int e = 0; e < W; ++e) h[j][e] += res[0].at(e);
+        }
+      }
     }
-    if (AHEAD && r + step < p.n_rows) fetch(r + step);
+    if constexpr (AHEAD) {
+      if (r + step < p.n_rows) fetch(r + step);
+    }
     if (p.residual_out) {
       Src *ro = static_cast<Src *>(p.residual_out) + r * p.residual_out_stride;
 #pragma unroll
-      for (int j = 0; j < V; ++j) store_unit<WIDE>(ro, at(j), p.dim, h[j]);
+      for (int j = 0; j < V; ++j) store_unit<W>(ro, at(j), p.dim, h[j]);
     }
 
     const auto squares = [&]() {
-      float ss = 0.0f;
+      uint64_t two = 0;
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(h[j][e], h[j][e], ss);
-      return over_row(ss, [](float u, float v) { return u + v; });
+        for (int e = 0; e < W; e += 2) {
+          const uint64_t v = pair_of(h[j][e], h[j][e + 1]);
+          two = fma2(v, v, two);
+        }
+      float even, odd;
+      parts_of(two, even, odd);
+      return over_row(even + odd, [](float u, float v) { return u + v; });
     };
     float ss = squares();
     float rstd;
@@ -100,7 +148,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024, AHEAD ? 2 : 1) rms_norm_ke
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) a = max_nan(a, fabsf(h[j][e]));
+        for (int e = 0; e < W; ++e) a = max_nan(a, fabsf(h[j][e]));
       a = over_row(a, [](float u, float v) { return max_nan(u, v); });
       float down = 1.0f;
       if (a > 0.0f && a < INFINITY) {
@@ -110,7 +158,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024, AHEAD ? 2 : 1) rms_norm_ke
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-          for (int e = 0; e < E; ++e) h[j][e] *= down;
+          for (int e = 0; e < W; ++e) h[j][e] *= down;
       }
       ss = squares();
       const float scaled_eps = p.eps * down * down;
@@ -121,32 +169,44 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024, AHEAD ? 2 : 1) rms_norm_ke
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-          for (int e = 0; e < E; ++e) h[j][e] = __fdiv_rn(h[j][e], down);
+          for (int e = 0; e < W; ++e) h[j][e] = __fdiv_rn(h[j][e], down);
       }
     }
 
     Out *out = static_cast<Out *>(p.out) + r * p.out_stride;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float y[E];
+      float y[W];
       if (p.weight) {
-        float w[E];
-        if (p.weight_f32) load_unit<WIDE>(static_cast<const float *>(p.weight), at(j), p.dim, w);
-        else load_unit<WIDE>(static_cast<const uint16_t *>(p.weight), at(j), p.dim, w);
+        uint64_t f[W / 2];
+        if constexpr (W == 16) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = h[j][e] * rstd * (w[e] + p.weight_offset);
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = own[i * apart];
+            f[2 * i] = pair_of(v.x, v.y);
+            f[2 * i + 1] = pair_of(v.z, v.w);
+          }
+        } else {
+          float w[W];
+          weights(j, w);
+#pragma unroll
+          for (int e = 0; e < W; e += 2)
+            f[e / 2] = fma2(pair_of(w[e], w[e + 1]), both_of(1.0f), both_of(p.weight_offset));
+        }
+#pragma unroll
+        for (int e = 0; e < W; e += 2)
+          parts_of(mul2(mul2(pair_of(h[j][e], h[j][e + 1]), both_of(rstd)), f[e / 2]), y[e], y[e + 1]);
       } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = h[j][e] * rstd;
+        for (int e = 0; e < W; ++e) y[e] = h[j][e] * rstd;
       }
       if constexpr (sizeof(Out) == 1) {
-        const float scale = scaled_block<WIDE>(y);
+        const float scale = scaled_block<W>(y);
         if ((lane & (U::kLanes - 1)) == 0 && at(j) < p.dim)
           p.scale[r * p.scale_stride + at(j) / kScaleBlock] = scale;
       }
-      store_unit<WIDE>(out, at(j), p.dim, y);
+      store_unit<W>(out, at(j), p.dim, y);
     }
-    if (!AHEAD && r + step < p.n_rows) fetch(r + step);
   }
 }
 
