@@ -216,7 +216,7 @@ ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream) {
 
   // Sixteen elements a lane to 8-bit rows where rows are many: a block's scale by fewer lanes
   // (32,768 x 4096 without a residual 83 us, 125 with eight; x 1024 with one 37, 43), but for
-  // wide rows with a residual, which DRAM bounds either way (x 4096 149 us, 146 with eight).
+  // wide rows with a residual, which DRAM bounds either way (x 4096 149 us, 144 with eight).
   const bool half = a->dtype == TS_DTYPE_BF16 && e4m3 && dim >= 512 && dim <= (a->residual ? 2048 : 4096) &&
                     n > 4 * s->num_sms;
   const auto fits = [&](int width) {
@@ -245,7 +245,7 @@ ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream) {
   p.weight_offset = a->weight_offset;
 
   // Threads of a row, 512 at most and the next row's loads on their way: one unit each, two
-  // of eight elements where rows are many (32,768 x 4096: 146 us, 151 with one).  The widest
+  // of eight elements where rows are many (32,768 x 4096: 144 us, 151 with one).  The widest
   // rows take up to 1024 threads and more units.
   const int units = static_cast<int>(width > 4 ? (dim + width - 1) / width : scales_of(dim) * 32);
   const bool many = n > 4 * s->num_sms && width == 8 && units > 128;

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   if (t == 0 && stalled()) atomicOr(p.status, kRowStalled);
 }
 
-// More rows.  8192 x 8192 x 4096: 209 us, 2.6 PFLOP/s by pairs (732 us with tokens as the
+// More rows.  8192 x 8192 x 4096: 211 us, 2.6 PFLOP/s by pairs (732 us with tokens as the
 // products' columns, 422 us by single CTAs of 128 columns); bound by the chain from a
 // block's products to the answer that its accumulator is free, of which a tile of 256
 // columns has two.  128 x 11,008 x 4096: 15 us by 115 CTAs, bound by that chain (250 ns a
@@ -388,10 +388,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
       // the last arrivals from the cluster's other CTAs come before this one leaves
       if (PAIR || share > 1)
-        for (int j = 0; j < NS; ++j) {
-          mbar_wait(empty + 8 * s, phase, &gave_up);
-          if (++s == NS) s = 0, phase ^= 1;
-        }
+        for (int j = max(0, issued - NS); j < issued; ++j) mbar_wait(empty + 8 * (j % NS), (j / NS) & 1, &gave_up);
       if (stalled() && (rank == 0 || !PAIR) && elected())
         for (int j = max(0, issued - NS); j < issued; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
     }

@@ -19,7 +19,7 @@ struct NormParams {
 // units per thread held in registers between the sum of squares and the output, so every
 // element is read once and written once.  AHEAD: a thread has the next row's on their way
 // meanwhile (one or two units, up to 512 threads).  Bound by DRAM: 32,768 rows of 4096 with
-// residual and 8-bit outputs take 146 us, 6.5 TB/s (186 us with a CTA for each row); without a
+// residual and 8-bit outputs take 144 us, 6.6 TB/s (186 us with a CTA for each row); without a
 // residual by instructions too (83 us, floor 60; 125 with eight elements a lane).  A frame
 // of 32 x 1024 takes a launch and two trips to memory, 1.9 us; rows of odd width their
 // single elements' loads and stores (5000 x 1001 fp32 9.0 us, floor 4.4).  Rows above 8192
