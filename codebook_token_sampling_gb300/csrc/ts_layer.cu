@@ -101,6 +101,9 @@ ts_status check_rotary_arrays(const ts_rotary_args *a, bool queries) {
   if (!a->positions || !a->freqs || !aligned(a->freqs, 8)) return TS_ERR_INVALID_ARG;
   if (!queries) return TS_OK;
   if (!a->x || !a->out || !aligned(a->x, es) || !aligned(a->out, es)) return TS_ERR_INVALID_ARG;
+  const int32_t n = a->rows ? a->n_rows : a->n_tokens;
+  if ((a->n_heads > 1 && a->out_head_stride < a->head_dim) || (n > 1 && a->out_token_stride < a->head_dim))
+    return TS_ERR_INVALID_ARG;  // its rows would overlap
   if (a->x == a->out && (a->x_token_stride != a->out_token_stride || a->x_head_stride != a->out_head_stride))
     return TS_ERR_INVALID_ARG;
   return TS_OK;

@@ -724,7 +724,8 @@ ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void *stream);
  *
  * Types: F32 or BF16.  TS_ERR_INVALID_ARG for a NULL pointer, a negative size or
  * stride, n_heads or head_dim < 1, an odd rotary_dim or one outside [2, head_dim],
- * an amplitude that is not finite, or an out that is x with other strides.
+ * an amplitude that is not finite, an out that is x with other strides, or one whose
+ * heads or rows overlap (a stride below head_dim).
  * TS_ERR_UNSUPPORTED for head_dim above TS_ROTARY_MAX_HEAD_DIM, n_heads above
  * TS_KV_MAX_HEADS or more than 2^24 elements per token. */
 #define TS_ROTARY_MAX_HEAD_DIM 1024

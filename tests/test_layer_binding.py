@@ -276,6 +276,22 @@ def test_rotary_refusals(ts, blank):
             ts.Rotary(*args)
 
 
+def test_rotary_outputs_that_overlap(ts, blank):
+    """Heads or rows of out on one another; one head's and one row's strides say nothing."""
+    bad = ts.TS_ERR_INVALID_ARG
+    for field, value in (("out_head_stride", 0), ("out_head_stride", 63), ("out_token_stride", 0), ("out_token_stride", 63)):
+        call = rotary(ts)
+        setattr(call.c, field, value)
+        assert refused(ts, ts.ts_rotary, blank, call) == bad, (field, value)
+    call = rotary(ts, rows=torch.zeros(4, dtype=torch.int32))
+    call.c.out_token_stride = 0
+    assert refused(ts, ts.ts_rotary, blank, call) == bad
+    x = torch.zeros((4, 3, 64), dtype=torch.bfloat16)
+    pos, f = torch.zeros(4, dtype=torch.int32), torch.ones(32, dtype=torch.float64)
+    call = ts.Rotary(x, x[:1].expand(4, 3, 64), pos, f)
+    assert refused(ts, ts.ts_rotary, blank, call) == bad
+
+
 def test_append_rotary_refusals(ts, blank):
     bad = ts.TS_ERR_INVALID_ARG
 
