@@ -35,7 +35,7 @@ struct Rows {
 };
 // Whether rows can be moved in pieces of `width` elements (8 or 16).
 bool in_pieces(const Rows &r, int64_t n_rows, int width) {
-  const int64_t to = width == 8 ? std::min(16, 8 * r.es) : 16 * r.es;
+  const int64_t to = std::min(2 * width, width * r.es);
   return aligned(r.p, static_cast<size_t>(to)) && (n_rows == 1 || r.stride * r.es % to == 0);
 }
 
@@ -44,7 +44,7 @@ bool in_pieces(const Rows &r, int64_t n_rows, int width) {
 // --------------------------------------------------------------------------
 template <class Src, class Out>
 const void *norm_kernel(int v, int width) {
-  if constexpr (sizeof(Src) == 2 && sizeof(Out) == 1)
+  if constexpr (sizeof(Out) == 1)
     if (width == 16) return reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 1, 16, true>);
   if (width == 8)
     return v == 1 ? reinterpret_cast<const void *>(ts::rms_norm_kernel<Src, Out, 1, 8, true>)
@@ -218,10 +218,11 @@ ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream) {
     return TS_ERR_INVALID_ARG;
 
   // Sixteen elements a lane to 8-bit rows where rows are many: a block's scale by fewer lanes
-  // (32,768 x 4096 without a residual 83 us, 125 with eight; x 1024 with one 37, 43), but for
-  // wide rows with a residual, which DRAM bounds either way (x 4096 149 us, 144 with eight).
-  const bool half = a->dtype == TS_DTYPE_BF16 && e4m3 && dim >= 512 && dim <= (a->residual ? 2048 : 4096) &&
-                    n > 4 * s->num_sms;
+  // (32,768 x 4096 without a residual bf16 84 us, 125 with eight, fp32 106, 155; bf16 x 1024
+  // with one 37, 43), but not with a residual where DRAM bounds either way (bf16 x 4096 149 us,
+  // 144 with eight; fp32 x 2048 153, 146).
+  const int widest = !a->residual ? 4096 : a->dtype == TS_DTYPE_BF16 ? 2048 : 0;
+  const bool half = e4m3 && dim >= 512 && dim <= widest && n > 4 * s->num_sms;
   const auto fits = [&](int width) {
     bool ok = dim % width == 0 && (!ws || aligned(a->weight, 16));
     for (const Rows &r : {x, res, sum, out}) ok = ok && (!r.p || in_pieces(r, n, width));

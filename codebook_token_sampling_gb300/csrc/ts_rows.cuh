@@ -12,7 +12,7 @@ namespace ts {
 constexpr int kScaleBlock = 128;
 
 // A lane's W elements of a block of 128: 8 or 16 neighbours (moved in pieces of 16 bytes,
-// sixteen of 16 bits in 32), or with W 4 elements l, l + 32, l + 64 and l + 96 of lane l (any
+// sixteen in pieces of 32), or with W 4 elements l, l + 32, l + 64 and l + 96 of lane l (any
 // alignment and width, still one row segment per load).
 template <int W>
 struct RowUnit {
@@ -68,6 +68,12 @@ __device__ __forceinline__ void store16(uint16_t *p, const float *v) {
   ulonglong4_32a q;
   memcpy(&q, w, 32);
   *reinterpret_cast<ulonglong4_32a *>(p) = q;
+}
+__device__ __forceinline__ void store16(float *p, const float *v) {
+  ulonglong4_32a q[2];
+  memcpy(q, v, 64);
+  reinterpret_cast<ulonglong4_32a *>(p)[0] = q[0];
+  reinterpret_cast<ulonglong4_32a *>(p)[1] = q[1];
 }
 __device__ __forceinline__ void store16(uint8_t *p, const float *v) {
   *reinterpret_cast<uint4 *>(p) =
@@ -135,10 +141,12 @@ struct RawUnit {
   uint32_t w[W * sizeof(T) / 4];
   __device__ __forceinline__ void load(const T *row, int at, int dim) {
     if constexpr (W == 16) {
-      static_assert(sizeof(T) == 2, "32 bytes");
-      ulonglong4_32a v = {0, 0, 0, 0};
-      if (at < dim) v = *reinterpret_cast<const ulonglong4_32a *>(row + at);
-      memcpy(w, &v, 32);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+        ulonglong4_32a v = {0, 0, 0, 0};
+        if (at < dim) v = reinterpret_cast<const ulonglong4_32a *>(row + at)[i];
+        memcpy(w + 8 * i, &v, 32);
+      }
     } else if constexpr (W == 8) {
 #pragma unroll
       for (int i = 0; i < W * static_cast<int>(sizeof(T)) / 16; ++i) {
