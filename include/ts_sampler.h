@@ -628,7 +628,8 @@ ts_status ts_kv_debug_lose_parts(ts_sampler *s, int32_t come);
  * Types: x, residual and residual_out F32 or BF16; out F32, BF16 or E4M3; weight
  * F32 or BF16.  Any alignment to the types' own sizes; rows whose addresses and
  * strides in bytes are multiples of 16, and dim one of 8, are moved in 16-byte
- * pieces (an E4M3 out: 8).  TS_ERR_INVALID_ARG for a NULL pointer that is needed,
+ * pieces (an E4M3 out: 8); many rows to E4M3 go fastest with multiples of 32 (out: 16)
+ * and a dim that is one of 16.  TS_ERR_INVALID_ARG for a NULL pointer that is needed,
  * a negative size or stride, dim < 1, eps negative or not finite, weight_offset
  * not finite, a stride below dim (for more than one row), out_scale missing for
  * E4M3 or given for another type, or an overlap of an output that the host can
