@@ -8,7 +8,7 @@
 namespace ts {
 
 constexpr int kGateThreads = 256;
-// CTAs per SM: three of sixteen elements a lane (bf16 to 8 bits, gelu on 16,384 x 11,008: 140
+// CTAs per SM: three of sixteen elements a lane (bf16 to 8 bits, gelu on 16,384 x 11,008: 142
 // us, 225 with four and spills), four where elements of 32 bits are on their way (fp32 to 8
 // bits 242 us, 383 with five and spills; bf16 to fp32 213, 251), else five (bf16 to bf16 159,
 // 167 with four).
@@ -44,51 +44,84 @@ __device__ __forceinline__ float power_of_2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-constexpr float kLog2E = 1.44269504f;
+constexpr float kLog2E = 1.44269504f, kLn2 = 0.693147181f;
 
-// g / (1 + exp(-z))
-__device__ __forceinline__ float logistic(float g, float z) { return g * reciprocal(1.0f + power_of_2(-kLog2E * z)); }
-
-// y g (1 + erf(g / sqrt 2)) / 2 of two elements: g (1 + erf) / 2 = max(g, 0) - |g| erfc(|g| /
-// sqrt 2) / 2, with Hastings's erfc(x) = t (a1 + t (a2 + .. t a5)) exp(-x x), t = 1 / (1 + p x),
-// to 1.5e-7 ("Approximations for digital computers", 1955; 7.1.26 in Abramowitz and
-// Stegun).  erff took longer than the loads (16,384 x 11,008: 273 us; this one element by
-// element 193).
-__device__ __forceinline__ uint64_t gelu2(uint64_t y, float g0, float g1) {
-  // |g|, but for +inf, whose product with erfc's zero is no part of the result; a NaN stays
-  const float a0 = max_nan(-g0, min_nan(g0, 3e38f)), a1 = max_nan(-g1, min_nan(g1, 3e38f));
-  const uint64_t a = pair_of(a0, a1);
-  float u0, u1, e0, e1;
-  parts_of(fma2(a, both_of(0.3275911f * 0.70710678f), both_of(1.0f)), u0, u1);
-  parts_of(mul2(mul2(a, a), both_of(-0.5f * kLog2E)), e0, e1);
-  const uint64_t t = pair_of(reciprocal(u0), reciprocal(u1)), e = pair_of(power_of_2(e0), power_of_2(e1));
-  uint64_t w = fma2(t, both_of(-0.5f * 1.061405429f), both_of(0.5f * 1.453152027f));
-  w = fma2(t, w, both_of(-0.5f * 1.421413741f));
-  w = fma2(t, w, both_of(0.5f * 0.284496736f));
-  w = fma2(t, w, both_of(-0.5f * 0.254829592f));  // minus the half of it
-  w = mul2(mul2(w, t), e);
-  return mul2(y, fma2(a, w, pair_of(fmaxf(g0, 0.0f), fmaxf(g1, 0.0f))));
+// Two elements at once: g / (1 + exp(-z)).  exp(-z) = 2^t exp(d) with t = -z log2 e rounded
+// and d = -z - t ln 2 what that rounding left, so the exponential is right to its size at
+// any z; the quotient is within 2^-20 of it (13 roundings at most; the exponential of the
+// rounded exponent alone: 2^-23 |z| more).  Beyond 88 the quotient is g, below -88 it is
+// less than 2^-119 and counts as 0.
+__device__ __forceinline__ uint64_t logistic2(float g0, float g1, float z0, float z1) {
+  const uint64_t n = pair_of(fmaxf(fminf(-z0, 88.0f), -88.0f), fmaxf(fminf(-z1, 88.0f), -88.0f));
+  const uint64_t t = mul2(n, both_of(kLog2E)), d = fma2(t, both_of(-kLn2), n);
+  float t0, t1, u0, u1;
+  parts_of(t, t0, t1);
+  const uint64_t e = pair_of(power_of_2(t0), power_of_2(t1));
+  parts_of(add2(fma2(e, d, e), both_of(1.0f)), u0, u1);
+  return mul2(pair_of(g0, g1), pair_of(reciprocal(u0), reciprocal(u1)));
 }
 
-template <int E>
+// g (1 + erf(g / sqrt 2)) / 2 of two elements: max(g, 0) - a Q(a) with a = |g| and Q(a) =
+// erfc(a / sqrt 2) / 2 = exp(-a a / 2) R(a).  R falls from 1/2 to 1 / (a sqrt(2 pi)) and is
+// taken as a quotient of two polynomials of positive terms in the manner of Cody, "Rational
+// Chebyshev approximations for the error function" (1969), with coefficients of our own
+// (least largest relative error over 0 .. 13.3: 3.8e-7).  So the result is right relative to
+// its size wherever that is not below 2^-126: FULL within 2^-19, with the exponential's
+// argument kept as above (and SQUARES: what the square's rounding left); else 1.1 g g 2^-24
+// more, far below the rounding to 16 or 8 bits (kept for those too and with a term more in the
+// numerator, gelu on 16,384 x 11,008 bf16 to 8 bits took 161 us instead of 142).  For gates of normal distribution the error's
+// norm is 3.2e-8, 3.5e-8 by fp32's erf; a polynomial that is right to 1.5e-7 of one would be
+// off by 1% at -8, and erff took longer than the loads (273 us).
+template <bool FULL, bool SQUARES>
+__device__ __forceinline__ uint64_t gelu2(float g0, float g1) {
+  // nothing is left of Q at 16; zeros, NaN and -inf times zero come from the first term
+  const uint64_t a = pair_of(fminf(fabsf(g0), 16.0f), fminf(fabsf(g1), 16.0f));
+  const uint64_t first = mul2(pair_of(g0, g1), pair_of(g0 > 0.0f ? 1.0f : 0.0f, g1 > 0.0f ? 1.0f : 0.0f));
+  const uint64_t half = mul2(a, both_of(-0.5f)), n = mul2(half, a);
+  const uint64_t t = FULL ? mul2(n, both_of(kLog2E)) : mul2(mul2(a, a), both_of(-0.5f * kLog2E));
+  float t0, t1, u0, u1;
+  parts_of(t, t0, t1);
+  uint64_t e = pair_of(power_of_2(t0), power_of_2(t1));
+  if constexpr (FULL) {
+    uint64_t d = fma2(t, both_of(-kLn2), n);
+    if constexpr (SQUARES) d = add2(d, fma2(half, a, mul2(n, both_of(-1.0f))));
+    e = fma2(e, d, e);
+  }
+  uint64_t q = fma2(a, both_of(0.0422765017f), both_of(0.297457546f));
+  q = fma2(a, q, both_of(0.949712813f));
+  q = fma2(a, q, both_of(1.51909733f));
+  parts_of(fma2(a, q, both_of(1.0f)), u0, u1);
+  uint64_t p = fma2(a, both_of(-0.016863713f), both_of(-0.118754119f));  // minus the numerator
+  p = fma2(a, p, both_of(-0.360615194f));
+  p = fma2(a, p, both_of(-0.499999821f));
+  return fma2(a, mul2(mul2(p, pair_of(reciprocal(u0), reciprocal(u1))), e), first);
+}
+
+template <int E, bool FULL, bool SQUARES>
 __device__ __forceinline__ void gated(float (&y)[E], const float (&g)[E], int act) {
   if (act == kActSilu) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] *= logistic(g[e], g[e]);
+    for (int e = 0; e < E; e += 2)
+      parts_of(mul2(pair_of(y[e], y[e + 1]), logistic2(g[e], g[e + 1], g[e], g[e + 1])), y[e], y[e + 1]);
   } else if (act == kActGelu) {
 #pragma unroll
-    for (int e = 0; e < E; e += 2) parts_of(gelu2(pair_of(y[e], y[e + 1]), g[e], g[e + 1]), y[e], y[e + 1]);
-  } else {  // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
+    for (int e = 0; e < E; e += 2)
+      parts_of(mul2(pair_of(y[e], y[e + 1]), gelu2<FULL, SQUARES>(g[e], g[e + 1])), y[e], y[e + 1]);
+  } else {  // (1 + tanh(z / 2)) / 2 = 1 / (1 + exp(-z))
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      y[e] *= logistic(g[e], 1.5957691f * fmaf(0.044715f * g[e] * g[e], g[e], g[e]));
+    for (int e = 0; e < E; e += 2) {
+      const uint64_t v = pair_of(g[e], g[e + 1]);
+      float z0, z1;
+      parts_of(mul2(v, fma2(mul2(v, v), both_of(1.5957691216f * 0.044715f), both_of(1.5957691216f))), z0, z1);
+      parts_of(mul2(pair_of(y[e], y[e + 1]), logistic2(g[e], g[e + 1], z0, z1)), y[e], y[e + 1]);
+    }
   }
 }
 
 // The rows' units end to end, a thread's next one's loads on their way while it works on
 // this one; addresses move along by additions.  16,384 x 11,008 bf16 to 8 bits, sixteen
-// elements a lane: gelu 140 us, 6.5 TB/s, bound by DRAM like silu (134 us) and no gate (94).
-// With eight elements a lane 174 us, bound by instructions (about 210 for eight, half of them
+// elements a lane: gelu 142 us, 6.4 TB/s, bound by DRAM like silu (134 us) and no gate (94).
+// With eight elements a lane 181 us, bound by instructions (about 210 for eight, half of them
 // for the block's scale, addresses and the loop); a CTA for each two units 193.
 template <class Src, class Out, int W>
 __global__ void __launch_bounds__(kGateThreads, gate_ctas(sizeof(Src), sizeof(Out), W)) gate_kernel(const GateParams p) {
@@ -144,7 +177,7 @@ __global__ void __launch_bounds__(kGateThreads, gate_ctas(sizeof(Src), sizeof(Ou
       scale_next += p.wrap.scale;
     }
     fetch();
-    if (act) gated<W>(y, g, p.act);
+    if (act) gated<W, sizeof(Out) == 4, sizeof(Src) == 4>(y, g, p.act);
     if constexpr (sizeof(Out) == 1) {
       const float scale = scaled_block<W>(y);
       if ((lane_id() & (U::kLanes - 1)) == 0 && left > 0) *scale_at = scale;

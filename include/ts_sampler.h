@@ -656,7 +656,10 @@ ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream);
 /* out = act(gate) * up, in fp32, rounded to out_dtype once; TS_ACT_NONE: out = up
  * (gate is not looked at), which makes 8-bit rows of anything.  TS_ACT_SILU:
  * g / (1 + exp(-g)); TS_ACT_GELU: g (1 + erf(g / sqrt 2)) / 2; TS_ACT_GELU_TANH:
- * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.  gate and up may be the halves
+ * g (1 + tanh(z)) / 2, z = sqrt(2 / pi) (g + 0.044715 g^3).  The activation is right
+ * relative to its size, before it is multiplied and rounded: silu within 2^-20, gelu
+ * within 2^-19 (rounded to BF16 or E4M3: g g 2^-23 more), gelu_tanh within 2^-20 +
+ * 2^-20 |z|; sizes below 2^-119 may count as 0.  gate and up may be the halves
  * of one product's rows (strides); out may be up or gate themselves where the types
  * are the same.  Types, alignment and refusals as for ts_rms_norm; dim up to
  * TS_GATE_MAX_DIM. */
