@@ -33,7 +33,6 @@ struct ts_sampler {
   int linear_clusters[5][4];  // ts_linear_e4m3: clusters of 1, 2, 4 and 8 CTAs of each kernel
                               // that the GPU holds at once
   int linear_path;    // ts_linear_e4m3: 0 auto, else its kernel (testing)
-  int linear_share;   // ts_linear_e4m3: 0 auto, else the CTAs that share a tile's rows of x (testing)
   int linear_split;   // ts_linear_e4m3: 0 auto, else the CTAs that share a tile (testing)
 };
 

@@ -53,10 +53,14 @@ LinearKernel kernel_for(int i) {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t blocks_of(int64_t dim) { return ceil_div(dim, TS_SCALE_BLOCK); }
 
-// What a call launches: the kernel, its tile (rows of x by weight rows), the CTAs that
-// share one along in_dim, and those that share their rows of x.
+// What a call launches: the kernel, its tile (rows of x by weight rows), and the CTAs that
+// share one along in_dim.
 struct LinearPlan {
-  int kernel, rows, columns, split, share;
+  int kernel, rows, columns, split;
+};
+// How its arrays lie: rows of x and w on whole lines of 128 bytes, rows of out on pieces of 16.
+struct Layout {
+  bool whole_lines, wide_out;
 };
 
 // CTAs of a cluster for `tiles` tiles: as many as leave none waiting for an SM (1 x 4096 x
@@ -70,47 +74,46 @@ int split_for(const ts_sampler *s, int kernel, int64_t tiles, int64_t blocks) {
 }
 
 LinearPlan plan_few(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
-  LinearPlan plan = {m <= 16 ? 0 : m <= 32 ? 1 : 2, m <= 16 ? 16 : m <= 32 ? 32 : 64, 128, 1, 1};
+  LinearPlan plan = {m <= 16 ? 0 : m <= 32 ? 1 : 2, m <= 16 ? 16 : m <= 32 ? 32 : 64, 128, 1};
   plan.split = split_for(s, plan.kernel, ceil_div(n, 128) * ceil_div(m, plan.rows), blocks);
   return plan;
 }
 // The least cycles by what a tile takes: for each block the chain from its copy to its
 // sums (590 for 128 tokens by 96, 1080 for a pair's 256 by 256), or what all CTAs take in
-// through L2 together (5000 bytes a cycle, 4000 over a short in_dim, which is all ramp);
-// and about 9000 around them.  4096 x 4096 weights: 512 rows 14 us (pairs 18), 1024 rows 19
-// by pairs (27); 2048 x 2048 and 2048 rows 12 by pairs (18).  Shared rows of x pay over a
-// short in_dim (777 x 2001 x 1040: 8.5 us by fours, 9.7 without), over a long one they
-// hold CTAs to one another's pace (512 x 4096 x 4096: 15.0 us, 13.5 without).
-LinearPlan plan_rows(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks, bool pairs) {
+// through L2 together (5000 bytes a cycle; 4000 where rows do not lie on whole lines of 128
+// bytes, so that a row's piece is in two of them: 512 x 4096 x 4112 by 128 columns 22 us, by
+// pairs 18, x 4096 13.6 and 17); and about 9000 around them, for pairs 7000 more a tile whose
+// outputs cannot be stored in pieces of 16 bytes (777 x 2001 x 512 fp32 10.2 us, 5.9 by 96
+// columns; x 2048 x 512 6.9 by pairs).  70 sizes of 100 to 3000 rows, 2001 to 11,008 weight
+// rows and 512 to 4112 along in_dim: within 6% of the best of 32, 64, 96, 128 columns and
+// pairs but for seven, whose best is up to 20% faster.  512 x 4096 x 4096 13.5 us (pairs 17),
+// 1024 x 4096 x 4096 17.9 by pairs (26), 777 x 2001 x 1040 fp32 9.6.
+LinearPlan plan_rows(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks, const Layout &at, bool pairs) {
   const double pair_waves = static_cast<double>(ceil_div(ceil_div(m, 256) * ceil_div(n, 256), s->linear_clusters[4][1]));
-  LinearPlan best = {4, 256, 256, 1, 1};
-  double least = pairs ? pair_waves * blocks * 1080.0 + 8000.0 : 1e30;
-  for (int columns = 32; columns <= 128; columns += 32)
-    for (int i = 2; i >= 0; --i) {
-      const int share = s->linear_share ? s->linear_share : blocks <= 16 ? 1 << i : 1;
-      const int64_t tiles = ceil_div(m, 128) * (ceil_div(ceil_div(n, columns), share) * share);
-      const int split = share == 1 ? split_for(s, 3, tiles, blocks) : 1;
-      const int64_t held = s->linear_clusters[3][share == 4 ? 2 : share - 1] * share;
-      const double waves = static_cast<double>(ceil_div(tiles * split, held));
-      const double at_once = static_cast<double>(std::min<int64_t>(tiles * split, held));
-      const double block =
-          std::max(350.0 + 2.5 * columns, (16384.0 / share + columns * 128.0) * at_once / (blocks <= 16 ? 4000.0 : 5000.0));
-      const double cycles = waves * (ceil_div(blocks, split) * block + 5000.0 + 40.0 * columns + (share > 1 ? 500.0 : 0.0));
-      if (cycles < least) {
-        least = cycles;
-        best = {3, 128, columns, split, share};
-      }
+  LinearPlan best = {4, 256, 256, 1};
+  double least = pairs ? pair_waves * (blocks * 1080.0 + (at.wide_out ? 0.0 : 7000.0)) + 8000.0 : 1e30;
+  for (int columns = 32; columns <= 128; columns += 32) {
+    const int64_t tiles = ceil_div(m, 128) * ceil_div(n, columns), held = s->linear_clusters[3][0];
+    const int split = split_for(s, 3, tiles, blocks);
+    const double waves = static_cast<double>(ceil_div(tiles * split, held));
+    const double at_once = static_cast<double>(std::min<int64_t>(tiles * split, held));
+    const double block =
+        std::max(350.0 + 2.5 * columns, (16384.0 + columns * 128.0) * at_once / (at.whole_lines ? 5000.0 : 4000.0));
+    const double cycles = waves * (ceil_div(blocks, split) * block + 5000.0 + 40.0 * columns);
+    if (cycles < least) {
+      least = cycles;
+      best = {3, 128, columns, split};
     }
+  }
   return best;
 }
-LinearPlan plan_for(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks) {
+LinearPlan plan_for(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks, const Layout &at) {
   const int path = s->linear_path;
   LinearPlan plan = path == 1 || (path == 0 && m <= 64) ? plan_few(s, m, n, blocks)
-                  : path == 3 ? LinearPlan{4, 256, 256, 1, 1} : plan_rows(s, m, n, blocks, path == 0);
+                  : path == 3 ? LinearPlan{4, 256, 256, 1} : plan_rows(s, m, n, blocks, at, path == 0);
   if (s->linear_split && plan.kernel != 4) {
     plan.split = s->linear_split;
     while (plan.split > blocks) plan.split /= 2;
-    if (plan.split > 1) plan.share = 1;
   }
   return plan;
 }
@@ -200,29 +203,31 @@ extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void
   p.wide_out = aligned(a->out, 16) && (a->n_rows == 1 || a->out_stride * es % 16 == 0);
 
   const int32_t m = a->n_rows;
-  const LinearPlan plan = plan_for(s, m, a->out_dim, blocks);
+  const auto whole_lines = [](const void *rows, int64_t n, int64_t stride) {
+    return aligned(rows, 128) && (n == 1 || stride % 128 == 0);
+  };
+  const LinearPlan plan = plan_for(s, m, a->out_dim, blocks, {whole_lines(a->x, m, a->x_stride) && whole_lines(a->w, a->out_dim, a->w_stride), p.wide_out != 0});
   const LinearKernel k = kernel_for(plan.kernel);
   const bool few = plan.kernel < 3, pair = plan.kernel == 4;
-  const int64_t tiles_n = ceil_div(a->out_dim, plan.columns * plan.share), tiles_m = ceil_div(m, plan.rows), tiles = tiles_n * tiles_m;
-  if (tiles * plan.split * plan.share > INT32_MAX / 2) return TS_ERR_UNSUPPORTED;
+  const int64_t tiles_n = ceil_div(a->out_dim, plan.columns), tiles_m = ceil_div(m, plan.rows), tiles = tiles_n * tiles_m;
+  if (tiles * plan.split > INT32_MAX / 2) return TS_ERR_UNSUPPORTED;
   p.tiles_n = static_cast<int32_t>(tiles_n);
   p.tiles_m = static_cast<int32_t>(tiles_m);
   p.tiles = static_cast<int32_t>(tiles);
   p.columns = plan.columns;
   p.split = plan.split;
-  p.share = plan.share;
 
   // one row's stride says nothing
   const auto pitch = [&](int64_t rows, int64_t stride) {
     return rows > 1 ? stride : (static_cast<int64_t>(a->in_dim) + 15) / 16 * 16;
   };
-  const int boxes_x = few ? plan.rows : 128 / plan.share, boxes_w = pair ? plan.columns / 2 : plan.columns;
+  const int boxes_x = few ? plan.rows : 128, boxes_w = pair ? plan.columns / 2 : plan.columns;
   CUtensorMap map_w, map_x;
   if (!tensor_map(&map_w, a->w, a->in_dim, a->out_dim, pitch(a->out_dim, a->w_stride), boxes_w) ||
       !tensor_map(&map_x, a->x, a->in_dim, m, pitch(m, a->x_stride), boxes_x))
     return TS_ERR_UNSUPPORTED;
 
-  const int cluster = pair ? 2 : plan.split * plan.share;
+  const int cluster = pair ? 2 : plan.split;
   const int64_t grid = pair ? 2 * std::min<int64_t>(tiles, s->linear_clusters[4][1]) : tiles * cluster;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);

@@ -20,7 +20,6 @@ struct LinearParams {
   int32_t split;      // CTAs of a cluster that share a tile along in_dim
   int32_t tiles_m, tiles;  // tiles along the rows, and all (linear_rows_kernel, as the next)
   int32_t columns;    // weight rows of a tile
-  int32_t share;      // CTAs of a cluster that share a tile's rows of x (with split 1)
   int32_t wide_out;   // out's rows can be stored in pieces of 16 bytes
   int32_t wide_scales;  // x_scale's rows can be read in such pieces
   uint32_t *status;
@@ -269,9 +268,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 // the columns), one streams, one issues the products.
 // PAIR: two CTAs share a tile of 256 tokens by `columns`: each brings its tokens and
 // half of the weights, the first one's thread issues the products of both, and the CTAs
-// walk over the tiles; otherwise a CTA (or a cluster along in_dim) has one tile, and
-// clusters of neighbouring tiles may share their tokens, each CTA bringing its part of
-// them into the shared memory of all: L2 gives about 10 TB/s to all SMs together, which
+// walk over the tiles; otherwise a CTA (or a cluster along in_dim) has one tile, whose
+// tokens and weights it brings by itself: L2 gives about 10 TB/s to all SMs together, which
 // bounds a call of 128 tokens before DRAM does.  (The
 // pair's block as two products of 128 columns with accumulators and a warpgroup each, to
 // add one while the other is multiplied: 328 us instead of 243 for 8192 x 8192 x 4096.)
@@ -312,17 +310,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const uint32_t done = taken + 8 * NB;
   const auto stalled = [&]() { return *static_cast<volatile int *>(&gave_up) != 0; };
 
-  const int shared_by = PAIR ? 2 : p.split * p.share;  // CTAs of the cluster (one of the two is 1)
+  const int shared_by = PAIR ? 2 : p.split;  // CTAs of the cluster
   const int rank = shared_by > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int first = static_cast<int>(blockIdx.x) / shared_by, step = static_cast<int>(gridDim.x) / shared_by;
-  const int split = PAIR ? 1 : p.split, share = PAIR ? 1 : p.share;
+  const int split = PAIR ? 1 : p.split;
   const int b0 = split == 1 ? 0 : static_cast<int>(static_cast<int64_t>(p.blocks) * rank / split);
   const int nb = split == 1 ? p.blocks : static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / split) - b0;
   // neighbouring tiles share their weights: sixteen tiles of tokens before the next columns
   const auto place = [&](int tile, int32_t &m0, int32_t &n0) {
     const int per = p.tiles_n * 16, group = tile / per, in = tile - group * per;
     const int high = min(16, p.tiles_m - group * 16);
-    n0 = (in / high * share + (share > 1 ? rank : 0)) * p.columns;
+    n0 = in / high * p.columns;
     m0 = (group * 16 + in % high) * (PAIR ? 256 : 128) + (PAIR ? rank * 128 : 0);
   };
 
@@ -337,13 +335,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   } else if (warp == 0) {  // a lane a barrier
     static_assert(2 * (NS + NB) + 1 <= 32, "barriers");
     if (lane < 2 * (NS + NB) + 1) {
-      const bool is_taken = lane >= 2 * NS + NB && lane < 2 * (NS + NB), is_empty = lane >= NS && lane < 2 * NS;
-      mbar_init(full + 8 * lane, is_taken ? (PAIR ? 16 : 8) : is_empty ? static_cast<uint32_t>(share) : 1);
+      const bool is_taken = lane >= 2 * NS + NB && lane < 2 * (NS + NB);
+      mbar_init(full + 8 * lane, is_taken ? (PAIR ? 16 : 8) : 1);
     }
     if (lane == 0) gave_up = 0;
     mbar_init_fence();
   }
-  if (PAIR || share > 1) cluster_sync_all();  // the others' barriers are there
+  if constexpr (PAIR) cluster_sync_all();  // the other's barriers are there
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
@@ -372,13 +370,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               tensor_load_2d_pair(a, &map_x, b * 128, m0, counted + 8 * s, policy);
               tensor_load_2d_pair(a + Tile::kStageA, &map_w, b * 128, w0, counted + 8 * s, policy);
             } else {
-              if (share > 1) {
-                const int rows = 128 / share;
-                tensor_load_2d_shared(a + rank * rows * 128, &map_x, b * 128, m0 + rank * rows, counted + 8 * s,
-                                      static_cast<uint16_t>((1 << share) - 1), policy);
-              } else {
-                tensor_load_2d(a, &map_x, b * 128, m0, counted + 8 * s, policy);
-              }
+              tensor_load_2d(a, &map_x, b * 128, m0, counted + 8 * s, policy);
               tensor_load_2d(a + Tile::kStageA, &map_w, b * 128, w0, counted + 8 * s, policy);
             }
           }
@@ -386,8 +378,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           if (++s == NS) s = 0, phase ^= 1;
         }
       }
-      // the last arrivals from the cluster's other CTAs come before this one leaves
-      if (PAIR || share > 1)
+      // the last arrivals from the pair's other CTA come before this one leaves
+      if constexpr (PAIR)
         for (int j = max(0, issued - NS); j < issued; ++j) mbar_wait(empty + 8 * (j % NS), (j / NS) & 1, &gave_up);
       if (stalled() && (rank == 0 || !PAIR) && elected())
         for (int j = max(0, issued - NS); j < issued; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
@@ -409,9 +401,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               const uint64_t a = ring_a + s * (kStage >> 4), w = ring_b + s * (kStage >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k) mma_e4m3<PAIR>(d, a + 2 * k, w + 2 * k, kind, k > 0);
-              // a stage is empty once all that share it have used it
-              if (share > 1) mma_commit_shared(empty + 8 * s, static_cast<uint16_t>((1 << share) - 1));
-              else mma_commit<PAIR>(empty + 8 * s);
+              mma_commit<PAIR>(empty + 8 * s);
               if (u == count - 1) mma_commit<PAIR>(summed + 8 * buf);
             }
             __syncwarp();

@@ -97,16 +97,6 @@ __device__ __forceinline__ void tensor_load_2d_pair(uint32_t dst, const CUtensor
       "l"(m), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
-// The same into every CTA of the cluster in `mask`, at the same place of each and counted
-// by the same barrier of each.
-__device__ __forceinline__ void tensor_load_2d_shared(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y,
-                                                      uint32_t bar, uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint "
-      "[%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(dst),
-      "l"(m), "r"(x), "r"(y), "r"(bar), "h"(mask), "l"(policy)
-      : "memory");
-}
 __device__ __forceinline__ uint64_t l2_evict_normal() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
@@ -241,14 +231,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// The same at that barrier of every CTA of the cluster in `mask`.
-__device__ __forceinline__ void mma_commit_shared(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(mask)
-      : "memory");
 }
 
 }  // namespace ts

@@ -840,8 +840,8 @@ ts_status ts_read_status(ts_sampler *s, uint32_t *bits, void *stream);
 /* TS_OPT_LINEAR_PATH: the kernel of ts_linear_e4m3: 0 = automatic, 1 = tokens as the
  * products' columns, 2 = tokens as their rows, 3 = the same by pairs of CTAs. */
 #define TS_OPT_LINEAR_PATH 10
-/* TS_OPT_LINEAR_SHARE: the neighbouring tiles (a cluster's) whose CTAs fetch their rows
- * of x together, on path 2 without a split: 0 = automatic, or 1, 2 or 4. */
+/* TS_OPT_LINEAR_SHARE: 0, 1, 2 or 4, without effect: it was the number of CTAs that
+ * fetched their rows of x together (by multicast loads), and each fetches its own now. */
 #define TS_OPT_LINEAR_SHARE 11
 ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value);
 
