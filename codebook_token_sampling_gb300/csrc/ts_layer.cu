@@ -366,7 +366,8 @@ ts_status ts_kv_append_rotary(ts_sampler *s, const ts_kv_cache *c, const ts_kv_t
   rc = check_rotary(a);
   if (rc != TS_OK) return rc;
   const bool queries = a->x != nullptr;
-  if (queries ? a->n_heads < 1 : a->n_heads != 0) return TS_ERR_INVALID_ARG;
+  // (an empty batch has heads and no address)
+  if (queries ? a->n_heads < 1 : a->n_heads < 0 || (a->n_heads > 0 && a->n_tokens > 0)) return TS_ERR_INVALID_ARG;
   if (a->n_tokens != t->n_tokens || a->rows != t->rows || (a->rows && a->n_rows != t->n_rows) || a->dtype != t->dtype ||
       a->head_dim != c->head_dim)
     return TS_ERR_INVALID_ARG;

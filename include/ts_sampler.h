@@ -757,7 +757,7 @@ ts_status ts_rotary(ts_sampler *s, const ts_rotary_args *a, void *stream);
  * the cache's type (for an e4m3 cache: turned in fp32, divided by the scale,
  * rounded).  The ts_kv_tables maps serve as they are: slots, positions and requests
  * (the rows).  A token with a negative slot or position is skipped, queries and all.
- * a->x may be NULL (with n_heads 0): keys and values only.
+ * a->x may be NULL (with n_heads 0, or any number where n_tokens is 0): keys and values only.
  * Checks are those of the two calls; besides, TS_ERR_INVALID_ARG where n_tokens,
  * rows, n_rows (with rows), dtype or head_dim differ between tokens, queries and
  * cache. */
