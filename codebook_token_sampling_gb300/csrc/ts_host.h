@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/ts_sampler.h"
+#include "ts_overlap.h"
 
 struct ts_sampler {
   int device;
@@ -56,25 +57,5 @@ inline bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_
 // A cache write's sizes, strides and types (ts_kv_append), then its arrays.
 ts_status check_append(const ts_kv_cache *c, const ts_kv_tokens *t);
 ts_status check_append_arrays(const ts_kv_tokens *t);
-
-// The bytes of an array of rows (none for NULL).
-struct Span {
-  uintptr_t from, to;     // of the first element, behind the last
-  uintptr_t pitch, wide;  // from row to row (0: one row), and of a row
-  // Whether two arrays share bytes.  Columns of one buffer side by side do not; arrays
-  // of different pitch that lie within one another count as if they did.
-  bool meets(const Span &o) const {
-    if (from >= o.to || o.from >= to) return false;
-    if (!pitch || pitch != o.pitch) return true;
-    const uintptr_t shift = (o.from >= from ? o.from - from : pitch - (from - o.from) % pitch) % pitch;
-    return shift < wide || shift + o.wide > pitch;
-  }
-};
-inline Span rows_span(const void *p, int64_t rows, int64_t dim, int64_t stride, int64_t es) {
-  if (!p || rows < 1) return {0, 0, 0, 0};
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  const uintptr_t pitch = rows > 1 ? static_cast<uintptr_t>(stride * es) : 0, wide = static_cast<uintptr_t>(dim * es);
-  return {at, at + static_cast<uintptr_t>(rows - 1) * pitch + wide, pitch, wide};
-}
 
 }  // namespace ts_host

@@ -18,6 +18,7 @@ namespace {
 
 using ts_host::aligned;
 using ts_host::cuda_fail;
+using ts_host::Heads;
 using ts_host::launch;
 using ts_host::rows_span;
 using ts_host::size_of;
@@ -96,17 +97,38 @@ ts_status check_rotary(const ts_rotary_args *a) {
   if (a->head_dim > TS_ROTARY_MAX_HEAD_DIM || a->n_heads > TS_KV_MAX_HEADS) return TS_ERR_UNSUPPORTED;
   return TS_OK;
 }
+Heads out_heads(const ts_rotary_args *a) {
+  return Heads::of(a->out, a->rows ? a->n_rows : a->n_tokens, a->n_heads, a->out_token_stride, a->out_head_stride, a->head_dim,
+                   size_of(a->dtype));
+}
 ts_status check_rotary_arrays(const ts_rotary_args *a, bool queries) {
   const int es = size_of(a->dtype);
   if (!a->positions || !a->freqs || !aligned(a->freqs, 8)) return TS_ERR_INVALID_ARG;
   if (!queries) return TS_OK;
   if (!a->x || !a->out || !aligned(a->x, es) || !aligned(a->out, es)) return TS_ERR_INVALID_ARG;
-  const int32_t n = a->rows ? a->n_rows : a->n_tokens;
-  if ((a->n_heads > 1 && a->out_head_stride < a->head_dim) || (n > 1 && a->out_token_stride < a->head_dim))
-    return TS_ERR_INVALID_ARG;  // its rows would overlap
-  if (a->x == a->out && (a->x_token_stride != a->out_token_stride || a->x_head_stride != a->out_head_stride))
-    return TS_ERR_INVALID_ARG;
-  return TS_OK;
+  const Heads out = out_heads(a);
+  if (out.meets_itself()) return TS_ERR_INVALID_ARG;
+  if (a->x == a->out)
+    return a->x_token_stride != a->out_token_stride || a->x_head_stride != a->out_head_stride ? TS_ERR_INVALID_ARG : TS_OK;
+  return out.meets(Heads::of(a->x, out.rows, a->n_heads, a->x_token_stride, a->x_head_stride, a->head_dim, es)) ? TS_ERR_INVALID_ARG
+                                                                                                                : TS_OK;
+}
+// Queries' outputs on the new keys or values, or within the cache.
+bool out_meets_cache(const ts_rotary_args *a, const ts_kv_cache *c, const ts_kv_tokens *t) {
+  const Heads out = out_heads(a);
+  const int es = size_of(t->dtype);
+  if (out.meets(Heads::of(t->k, out.rows, c->n_kv_heads, t->k_token_stride, t->k_head_stride, c->head_dim, es)) ||
+      out.meets(Heads::of(t->v, out.rows, c->n_kv_heads, t->v_token_stride, t->v_head_stride, c->head_dim, es)))
+    return true;
+  const auto within = [&](const void *pool, int64_t block, int64_t token, int64_t head) {
+    if (out.none() || c->n_blocks < 1) return false;
+    const __int128 from = reinterpret_cast<uintptr_t>(pool);
+    const __int128 last = static_cast<__int128>(c->n_blocks - 1) * block + static_cast<__int128>(c->block_size - 1) * token +
+                          static_cast<__int128>(c->n_kv_heads - 1) * head;
+    return out.end() > from && from + (last + c->head_dim) * size_of(c->dtype) > out.from;
+  };
+  return within(c->k, c->k_block_stride, c->k_token_stride, c->k_head_stride) ||
+         within(c->v, c->v_block_stride, c->v_token_stride, c->v_head_stride);
 }
 // The largest piece (8, 4 or 1 elements) that divides the pairs and the head and that
 // addresses and strides allow.
@@ -376,6 +398,7 @@ ts_status ts_kv_append_rotary(ts_sampler *s, const ts_kv_cache *c, const ts_kv_t
   if (rc != TS_OK) return rc;
   rc = check_rotary_arrays(a, queries);
   if (rc != TS_OK) return rc;
+  if (queries && out_meets_cache(a, c, t)) return TS_ERR_INVALID_ARG;
 
   ts::RotaryParams p;
   std::memset(&p, 0, sizeof p);

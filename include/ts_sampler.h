@@ -728,8 +728,9 @@ ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void *stream);
  *
  * Types: F32 or BF16.  TS_ERR_INVALID_ARG for a NULL pointer, a negative size or
  * stride, n_heads or head_dim < 1, an odd rotary_dim or one outside [2, head_dim],
- * an amplitude that is not finite, an out that is x with other strides, or one whose
- * heads or rows overlap (a stride below head_dim).
+ * an amplitude that is not finite, an out whose heads or rows overlap (the larger of its
+ * strides has to hold all that lies along the smaller one, that a head), or one that
+ * overlaps x and is not x itself, as far as addresses and strides say.
  * TS_ERR_UNSUPPORTED for head_dim above TS_ROTARY_MAX_HEAD_DIM, n_heads above
  * TS_KV_MAX_HEADS or more than 2^24 elements per token. */
 #define TS_ROTARY_MAX_HEAD_DIM 1024
@@ -760,6 +761,7 @@ ts_status ts_rotary(ts_sampler *s, const ts_rotary_args *a, void *stream);
  * a->x may be NULL (with n_heads 0, or any number where n_tokens is 0): keys and values only.
  * Checks are those of the two calls; besides, TS_ERR_INVALID_ARG where n_tokens,
  * rows, n_rows (with rows), dtype or head_dim differ between tokens, queries and
+ * cache, or where the queries' out overlaps the new keys or values or lies within the
  * cache. */
 ts_status ts_kv_append_rotary(ts_sampler *s, const ts_kv_cache *c, const ts_kv_tokens *t,
                               const ts_rotary_args *a, void *stream);

@@ -1,0 +1,74 @@
+"""Calls of the layer operators that the header allows: where outputs may lie, and calls at
+once."""
+import numpy as np
+import pytest
+
+from test_gpu_layer import get, kind_of, put, sampler, ts  # noqa: F401  (fixtures among them)
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------
+# Rotary outputs beside what they come from
+# --------------------------------------------------------------------------
+def rotary_inputs(seed, tokens, heads, dim):
+    import torch
+    rng = np.random.default_rng(seed)
+    return (put(rng.normal(0, 3, (tokens, heads, dim)), "bf16"), torch.from_numpy(rng.integers(0, 5000, tokens).astype(np.int32)).cuda(),
+            torch.from_numpy(10000.0 ** (-np.arange(0, dim, 2) / dim)).cuda())
+
+
+@pytest.mark.parametrize("layout", ["columns of a product", "every other head", "heads before rows", "heads before rows, in place", "one row of any stride",
+                                    "one head of any stride"])
+def test_rotary_outputs_beside_their_inputs(ts, sampler, layout):
+    """Outputs in the inputs' buffer that share nothing with them: the bits of a call with
+    buffers of its own, and what is around them stays."""
+    import torch
+    tokens, heads = (1 if layout.startswith("one row") else 37), (1 if layout.startswith("one head") else 6)
+    x, pos, f = rotary_inputs(1, tokens, heads, 64)
+    want = torch.empty_like(x)
+    ts.ts_rotary(sampler.handle, ts.Rotary(x, want, pos, f))
+    if layout == "columns of a product":
+        buf = torch.full((tokens, 3 * heads + 1, 64), 7.0, device="cuda").bfloat16()
+        a, b = buf[:, :heads], buf[:, heads + 1:2 * heads + 1]
+    elif layout == "every other head":
+        buf = torch.full((tokens, 2 * heads, 64), 7.0, device="cuda").bfloat16()
+        a, b = buf[:, ::2], buf[:, 1::2]
+    elif layout.startswith("heads before rows"):
+        buf = torch.full((2 * heads, tokens, 64), 7.0, device="cuda").bfloat16()
+        a, b = buf[:heads].transpose(0, 1), buf[heads:].transpose(0, 1)
+        b = a if layout.endswith("in place") else b
+    else:
+        strides = ((16, 64, 1), (0, 64, 1)) if tokens == 1 else ((64, 16, 1), (64, 0, 1))
+        buf = torch.full((2 * x.numel() + 64,), 7.0, device="cuda").bfloat16()
+        a, b = (torch.as_strided(buf, x.shape, s, at) for s, at in zip(strides, (0, x.numel())))
+    a.copy_(x)
+    ts.ts_rotary(sampler.handle, ts.Rotary(a, b, pos, f))
+    assert torch.equal(b, want)
+    if b is not a:
+        assert torch.equal(a, x) and int((buf == 7).sum()) >= buf.numel() - 2 * x.numel()
+
+
+@pytest.mark.parametrize("layout", ["queries, keys, values", "a head's query, key and value", "outputs over queries"])
+def test_append_rotary_within_one_product(ts, sampler, layout):
+    """Queries, keys and values side by side in one product's rows, turned where they stand."""
+    import torch
+    tokens, heads, dim = 37, 4, 64
+    rows, pos, f = rotary_inputs(2, tokens, 3 * heads, dim)
+    if layout == "a head's query, key and value":
+        parts = [rows.view(tokens, heads, 3, dim)[:, :, i] for i in range(3)]
+    else:
+        parts = [rows[:, i * heads:(i + 1) * heads] for i in range(3)]
+    slots = torch.arange(tokens, device="cuda")
+    kept = rows.clone()
+    results = []
+    for own in (True, False):
+        k, v = (torch.zeros((3, 16, heads, dim), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        q, k_new, v_new = [p.contiguous() if own else p for p in parts]
+        out = torch.empty_like(q) if own else q
+        ts.ts_kv_append_rotary(sampler.handle, ts.KvCache(k, v), ts.KvTokens(k_new, v_new, slots), ts.Rotary(q, out, pos, f))
+        results.append((out.clone(), k, v))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    parts[0].copy_(kept.view(tokens, heads, 3, dim)[:, :, 0] if layout.startswith("a head's") else kept[:, :heads])
+    assert torch.equal(rows, kept)
