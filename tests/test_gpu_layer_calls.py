@@ -72,3 +72,41 @@ def test_append_rotary_within_one_product(ts, sampler, layout):
         assert torch.equal(a, b)
     parts[0].copy_(kept.view(tokens, heads, 3, dim)[:, :, 0] if layout.startswith("a head's") else kept[:, :heads])
     assert torch.equal(rows, kept)
+
+
+# --------------------------------------------------------------------------
+# Calls at once
+# --------------------------------------------------------------------------
+def test_two_graphs_of_finite_products(ts, sampler):
+    """Two captured norms and products of one sampler, replayed on two streams, with weights
+    that are all numbers: the bits of plain calls."""
+    import torch
+    rng = np.random.default_rng(6)
+    runs = []
+    for i in range(2):
+        x = put(rng.normal(0, 1, (64 + 100 * i, 1024)), "bf16")
+        e, s = put(np.zeros(x.shape), "e4m3"), put(np.zeros((x.shape[0], 8)))
+        w, ws = put(np.clip(rng.normal(0, 100, (640, 1024)), -448, 448), "e4m3"), put(rng.uniform(0.5, 1, (5, 8)))
+        out = put(np.zeros((x.shape[0], 640)))
+        calls = [(ts.ts_rms_norm, ts.RmsNorm(x, e, out_scale=s)), (ts.ts_linear_e4m3, ts.LinearE4m3(e, s, w, ws, out))]
+        for fn, c in calls:
+            fn(sampler.handle, c)
+        torch.cuda.synchronize()
+        want = out.clone()
+        assert bool(torch.isfinite(want).all()) and bool((want != 0).any())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for fn, c in calls:
+                fn(sampler.handle, c)
+        runs.append((graph, out, want, calls))
+    for _, out, _, _ in runs:
+        out.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for (graph, *_), st in zip(runs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _ in runs:
+        assert torch.equal(out, want)
