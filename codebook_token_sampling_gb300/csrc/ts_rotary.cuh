@@ -134,20 +134,23 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[P], floa
 // A frequency (radians per position) as turns in units of 2^-64, modulo a turn: the
 // product with a position, modulo 2^64, is then the angle's exact fraction of a turn.
 // By whole numbers (64-bit floating point arithmetic would take longer than the rest of a
-// frame): freq = m 2^e, and 2^66 / (2 pi) to 64 bits.
+// frame): freq = m 2^e, and 2 / pi to 128 bits, so that below 2^64 radians what is cut off
+// is no more than 1.4 units.
 __device__ __forceinline__ uint64_t turns_of(double freq) {
   const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(freq));
   const int exponent = static_cast<int>((bits >> 52) & 0x7FF);
   const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (exponent ? 1ull << 52 : 0);
-  const uint64_t per_radian = 0xA2F9836E4E441529ull;
-  const uint64_t high = __umul64hi(m, per_radian), low = m * per_radian;
-  const int right = 1075 + 2 - max(exponent, 1);  // (high, low) 2^-right
+  const uint64_t first = 0xA2F9836E4E441529ull, next = 0xFC2757D1F534DDC0ull;
+  // the product's 64-bit words, the lowest first
+  const uint64_t w0 = m * next, low = m * first, w1 = low + __umul64hi(m, next);
+  const uint64_t w2 = __umul64hi(m, first) + (w1 < low);
+  const int right = 1075 + 66 - max(exponent, 1);  // the product 2^-right
+  const uint64_t at = right < 64 ? w0 : right < 128 ? w1 : w2, above = right < 64 ? w1 : right < 128 ? w2 : 0;
+  const int by = right & 63;
   uint64_t turns;
-  if (right >= 128) turns = 0;
-  else if (right > 64) turns = high >> (right - 64);
-  else if (right == 64) turns = high;
-  else if (right > 0) turns = (low >> right) | (high << (64 - right));
-  else turns = right > -64 ? low << -right : 0;
+  if (right >= 192) turns = 0;
+  else if (right >= 0) turns = (at >> by) | (by ? above << (64 - by) : 0);
+  else turns = right > -64 ? w0 << -right : 0;
   return bits >> 63 ? 0 - turns : turns;
 }
 

@@ -1,5 +1,7 @@
 """The layer operators against the bounds that the header states: activations over every
-size of gate."""
+size of gate, rotary angles of every frequency and position."""
+import fractions
+
 import numpy as np
 import pytest
 
@@ -74,3 +76,38 @@ def test_activations_of_small_results_in_16_bits(ts, sampler, act):
     rel, absolute = activation_bound(g, act, "bf16")
     off = rel * np.abs(want) + absolute * get(up)
     close(get(out), want, off + 2.0 ** -9 * (np.abs(want) + off) * 2, act)
+
+
+# --------------------------------------------------------------------------
+# Rotary angles
+# --------------------------------------------------------------------------
+TWO_PI = fractions.Fraction("6.2831853071795864769252867665590057683943387987502116419498891846156328125724179972560696506842341359")
+
+
+def cosines_and_sines(ts, sampler, positions, freqs):
+    """cos and sin of every position and frequency as ts_rotary turns (1, 0) by them, and in
+    64 bits by exact products and their rests modulo a turn."""
+    import torch
+    n = len(freqs)
+    x = put(np.tile(np.r_[np.ones(n), np.zeros(n)], (len(positions), 1, 1)))
+    ts.ts_rotary(sampler.handle, ts.Rotary(x, x, torch.tensor(positions, dtype=torch.int32, device="cuda"),
+                                           torch.tensor(freqs, dtype=torch.float64, device="cuda")))
+    want = np.zeros((len(positions), 2 * n))
+    for t, p in enumerate(positions):
+        for i, f in enumerate(freqs):
+            turn = fractions.Fraction(float(f)) * int(p) / TWO_PI
+            angle = float((turn - round(turn)) * TWO_PI)
+            want[t, i], want[t, n + i] = np.cos(angle), np.sin(angle)
+    return get(x)[:, 0], want
+
+
+FAR = [0, 1, 2, 2 ** 20 - 1, 2 ** 24 + 1, 2 ** 30 + 12345, 2 ** 31 - 1]
+
+
+def test_rotary_angles_of_any_frequency(ts, sampler):
+    """The angle within 2^-31 turns below 2^64 radians per position, cosine and sine within
+    2^-22."""
+    rng = np.random.default_rng(5)
+    freqs = [1.0, -0.3, 0.0, 1e-9, 5e-324, 100.0, -12345.678, 1e6, 2.0 ** 40 + 0.3, 2.0 ** 63, -1.8e19, *(2.0 ** rng.uniform(-40, 64, 85))]
+    got, want = cosines_and_sines(ts, sampler, FAR, freqs)
+    close(got, want, 2 * np.pi * 2.0 ** -31 + 2.0 ** -22)
