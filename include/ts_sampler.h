@@ -721,7 +721,7 @@ ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void *stream);
  * in fp32, rounded to dtype once.  The head's other elements are copied.  The angle
  * is the exact product of the position and the frequency (radians per position, 64
  * bits) up to 2^-31 turns, for frequencies below 2^64 in size; cosine and sine are
- * within 2^-22.  A negative position skips the token: its rows are neither
+ * within 2^-23, before their product with the amplitude is rounded.  A negative position skips the token: its rows are neither
  * read nor written.  out may be x itself (the same address and strides).  Tokens of
  * one call have rows of their own.  A row outside [0, n_rows) sets TS_ROW_BAD_SLOT
  * and skips the token.

@@ -111,3 +111,13 @@ def test_rotary_angles_of_any_frequency(ts, sampler):
     freqs = [1.0, -0.3, 0.0, 1e-9, 5e-324, 100.0, -12345.678, 1e6, 2.0 ** 40 + 0.3, 2.0 ** 63, -1.8e19, *(2.0 ** rng.uniform(-40, 64, 85))]
     got, want = cosines_and_sines(ts, sampler, FAR, freqs)
     close(got, want, 2 * np.pi * 2.0 ** -31 + 2.0 ** -22)
+
+
+def test_rotary_angles_in_all_quarters(ts, sampler):
+    """Angles all around the circle and right beside its eighths: what is left beside whole
+    quarters rounded to 24 bits (an eighth of a turn: pi / 4 2^-25), one step of the functions
+    below 1, and the angle's 2^-31 turns; 2^-23 in all."""
+    turns = np.r_[np.linspace(-1, 1, 4001), (np.arange(-8, 9) / 8)[:, None].repeat(9, 1).ravel() + np.tile(np.arange(-4, 5), 17) * 2.0 ** -33]
+    for first in range(0, len(turns), 512):  # a head holds 512
+        got, want = cosines_and_sines(ts, sampler, [1], list(2 * np.pi * turns[first:first + 512]))
+        close(got, want, 2 * np.pi * 2.0 ** -31 + np.pi / 4 * 2.0 ** -25 + 2.0 ** -24, first)
