@@ -58,6 +58,7 @@ TS_OPT_KV_JOIN = 8
 TS_OPT_LINEAR_SPLIT = 9
 TS_OPT_LINEAR_PATH = 10
 TS_OPT_LINEAR_SHARE = 11
+TS_OPT_LINEAR_LOSE = 12
 TS_MAX_VOCAB_BF16 = 163840
 TS_MAX_VOCAB_F32 = 81920
 TS_NOALLOC_SCRATCH_BYTES = 4194304

@@ -34,6 +34,7 @@ struct ts_sampler {
   int linear_clusters[5][4];  // ts_linear_e4m3: clusters of 1, 2, 4 and 8 CTAs of each kernel
                               // that the GPU holds at once
   int linear_path;    // ts_linear_e4m3: 0 auto, else its kernel (testing)
+  int linear_lose;    // ts_linear_e4m3: 0, else one past the block whose copies get lost (testing)
   int linear_split;   // ts_linear_e4m3: 0 auto, else the CTAs that share a tile (testing)
 };
 

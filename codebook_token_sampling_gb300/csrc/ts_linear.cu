@@ -199,6 +199,8 @@ extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void
   p.out_dim = a->out_dim;
   p.blocks = static_cast<int32_t>(blocks);
   p.status = s->status;
+  p.wait_cycles = s->linear_lose ? 1u << 24 : ts::kWaitCycles;
+  p.lose = s->linear_lose - 1;
   p.wide_scales = aligned(a->x_scale, 16) && (a->n_rows == 1 || a->x_scale_stride % 4 == 0);
   p.wide_out = aligned(a->out, 16) && (a->n_rows == 1 || a->out_stride * es % 16 == 0);
 
@@ -209,6 +211,7 @@ extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void
   const LinearPlan plan = plan_for(s, m, a->out_dim, blocks, {whole_lines(a->x, m, a->x_stride) && whole_lines(a->w, a->out_dim, a->w_stride), p.wide_out != 0});
   const LinearKernel k = kernel_for(plan.kernel);
   const bool few = plan.kernel < 3, pair = plan.kernel == 4;
+  if (pair && s->linear_lose) return TS_ERR_UNSUPPORTED;
   const int64_t tiles_n = ceil_div(a->out_dim, plan.columns), tiles_m = ceil_div(m, plan.rows), tiles = tiles_n * tiles_m;
   if (tiles * plan.split > INT32_MAX / 2) return TS_ERR_UNSUPPORTED;
   p.tiles_n = static_cast<int32_t>(tiles_n);

@@ -22,6 +22,8 @@ struct LinearParams {
   int32_t columns;    // weight rows of a tile
   int32_t wide_out;   // out's rows can be stored in pieces of 16 bytes
   int32_t wide_scales;  // x_scale's rows can be read in such pieces
+  uint32_t wait_cycles;  // of a wait at most
+  int32_t lose;       // tests: the block whose copies the first tile never gets, or -1
   uint32_t *status;
 };
 
@@ -70,6 +72,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t full = smem_addr(bars), empty = full + 8 * NS, summed = empty + 8 * NS, taken = summed + 8 * NB;
   const uint32_t done = taken + 8 * NB;
   const auto stalled = [&]() { return *static_cast<volatile int *>(&gave_up) != 0; };
+  const auto any_stalled = [&]() { return __any_sync(0xFFFFFFFFu, stalled()) != 0; };  // the same in all lanes
 
   const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int tile = static_cast<int>(blockIdx.x) / p.split;
@@ -104,13 +107,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const uint64_t again = l2_evict_normal();
     // weights that no other tile reads leave L2 to the rest
     const uint64_t w_policy = p.n_rows <= TN ? l2_evict_first() : again;
+    const int lose = tile == 0 ? p.lose - b0 : -1;
     int s = 0, issued = 0;
     uint32_t phase = 1;
     for (int i = 0; i < nb; ++i) {
-      mbar_wait(empty + 8 * s, phase, &gave_up);
+      mbar_wait(empty + 8 * s, phase, &gave_up, p.wait_cycles);
       const bool go = !stalled();
       issued += go;
-      if (elected() && go) {
+      if (elected() && go && i != lose) {
         const uint32_t a = smem_addr(ring) + s * (Tile::kStageA + Tile::kStageB), bar = full + 8 * s;
         mbar_expect(bar, Tile::kStageA + Tile::kStageB);
         tensor_load_2d(a, &map_w, (b0 + i) * 128, n0, bar, w_policy);
@@ -119,18 +123,18 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       __syncwarp();
       if (++s == NS) s = 0, phase ^= 1;
     }
-    if (stalled() && elected())
-      for (int j = max(0, issued - NS); j < issued; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
+    if (elected() && stalled())
+      for (int j = max(0, issued - NS); j < issued; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1, p.wait_cycles);
   } else if (warp == 5) {
     constexpr uint32_t kind = e4m3_product(128, TN);
     const uint64_t ring_a = operand_of(smem_addr(ring)), ring_b = operand_of(smem_addr(ring) + Tile::kStageA);
     int s = 0, b = 0;
     uint32_t s_phase = 0, b_phase = 1;
     for (int g = 0; g < nb; g += G) {
-      mbar_wait(taken + 8 * b, b_phase, &gave_up);
+      mbar_wait(taken + 8 * b, b_phase, &gave_up, p.wait_cycles);
       const int count = min(G, nb - g);
       for (int u = 0; u < count; ++u) {
-        mbar_wait(full + 8 * s, s_phase, &gave_up);
+        mbar_wait(full + 8 * s, s_phase, &gave_up, p.wait_cycles);
         tc_fence_after();
         if (elected()) {
           const uint64_t a = ring_a + s * ((Tile::kStageA + Tile::kStageB) >> 4);
@@ -145,9 +149,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       }
       if (++b == NB) b = 0, b_phase ^= 1;
     }
-    if (stalled() && elected()) {
+    if (elected() && stalled()) {
       mma_commit(done);
-      mbar_drain(done, 0);
+      mbar_drain(done, 0, p.wait_cycles);
     }
   } else {
     // four blocks' scales are fetched while the four before them are used
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       for (int g = 0; g < 4; g += G) {
         if (i0 + g >= nb) continue;
         const int group = (i0 + g) / G, b = group % NB;
-        mbar_wait(summed + 8 * b, (group / NB) & 1, &gave_up);
+        mbar_wait(summed + 8 * b, (group / NB) & 1, &gave_up, p.wait_cycles);
         tc_fence_after();
 #pragma unroll
         for (int u = 0; u < G; ++u) {
@@ -309,6 +313,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const uint32_t full = smem_addr(bars), empty = full + 8 * NS, summed = empty + 8 * NS, taken = summed + 8 * NB;
   const uint32_t done = taken + 8 * NB;
   const auto stalled = [&]() { return *static_cast<volatile int *>(&gave_up) != 0; };
+  const auto any_stalled = [&]() { return __any_sync(0xFFFFFFFFu, stalled()) != 0; };  // the same in all lanes
 
   const int shared_by = PAIR ? 2 : p.split;  // CTAs of the cluster
   const int rank = shared_by > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -355,15 +360,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const uint32_t counted = PAIR ? cluster_addr(full, 0) : full;  // the first CTA counts both CTAs' copies
       int s = 0, issued = 0;
       uint32_t phase = 1;
-      for (int tile = first; tile < p.tiles; tile += step) {
+      for (int tile = first; tile < p.tiles && !any_stalled(); tile += step) {
+        const int lose = tile == 0 ? p.lose : -1;
         int32_t m0, n0;
         place(tile, m0, n0);
         const int32_t w0 = n0 + (PAIR ? rank * (p.columns / 2) : 0);
         for (int b = b0; b < b0 + nb; ++b) {
-          mbar_wait(empty + 8 * s, phase, &gave_up);
+          mbar_wait(empty + 8 * s, phase, &gave_up, p.wait_cycles);
           const bool go = !stalled();
           issued += go;
-          if (elected() && go) {
+          if (elected() && go && b != lose) {
             const uint32_t a = smem_addr(ring) + s * kStage;
             if (rank == 0 || !PAIR) mbar_expect(full + 8 * s, bytes);
             if constexpr (PAIR) {
@@ -380,21 +386,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
       // the last arrivals from the pair's other CTA come before this one leaves
       if constexpr (PAIR)
-        for (int j = max(0, issued - NS); j < issued; ++j) mbar_wait(empty + 8 * (j % NS), (j / NS) & 1, &gave_up);
-      if (stalled() && (rank == 0 || !PAIR) && elected())
-        for (int j = max(0, issued - NS); j < issued; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1);
+        for (int j = max(0, issued - NS); j < issued; ++j) mbar_wait(empty + 8 * (j % NS), (j / NS) & 1, &gave_up, p.wait_cycles);
+      if (elected() && (rank == 0 || !PAIR) && stalled())
+        for (int j = max(0, issued - NS); j < issued; ++j) mbar_drain(full + 8 * (j % NS), (j / NS) & 1, p.wait_cycles);
     }
     if (warp == 9 && (rank == 0 || !PAIR)) {
       const uint32_t kind = e4m3_product(PAIR ? 256 : 128, p.columns);
       const uint64_t ring_a = operand_of(smem_addr(ring)), ring_b = operand_of(smem_addr(ring) + Tile::kStageA);
       int s = 0, buf = 0;
       uint32_t s_phase = 0, buf_phase = 1;
-      for (int tile = first; tile < p.tiles; tile += step) {
+      for (int tile = first; tile < p.tiles && !any_stalled(); tile += step) {
         for (int g = 0; g < nb; g += G) {
-          mbar_wait(taken + 8 * buf, buf_phase, &gave_up);
+          mbar_wait(taken + 8 * buf, buf_phase, &gave_up, p.wait_cycles);
           const int count = G == 1 ? 1 : min(G, nb - g);
           for (int u = 0; u < count; ++u) {
-            mbar_wait(full + 8 * s, s_phase, &gave_up);
+            mbar_wait(full + 8 * s, s_phase, &gave_up, p.wait_cycles);
             tc_fence_after();
             if (elected()) {
               const uint32_t d = tmem + (buf * G + u) * Tile::kMaxColumns;
@@ -410,9 +416,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           if (++buf == NB) buf = 0, buf_phase ^= 1;
         }
       }
-      if (stalled() && elected()) {
+      if (elected() && stalled()) {
         mma_commit<PAIR>(done);
-        mbar_drain(done, 0);
+        mbar_drain(done, 0, p.wait_cycles);
       }
     }
   } else {
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               const float f = x_now[u0 + u] * __shfl_sync(0xFFFFFFFFu, w_now, 8 * (u0 + u) + j);
               scale[u][j] = pair_of(f, f);
             }
-          mbar_wait(summed + 8 * buf, (i / NB) & 1, &gave_up);
+          mbar_wait(summed + 8 * buf, (i / NB) & 1, &gave_up, p.wait_cycles);
           ++i;
           tc_fence_after();
           const uint32_t from =
@@ -506,7 +512,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           if constexpr (!PAIR) release(buf);
         }
       }
-      if (stalled()) break;
+      if (any_stalled()) break;
       if constexpr (PAIR) {
         const int32_t m_now = m0, n_now = n0;
         if (tile + step < p.tiles) {

@@ -672,6 +672,7 @@ ts_status ts_create(int device, int max_top_k, ts_sampler **out) {
   s->kv_ctas = 0;
   s->kv_join = 0;
   s->linear_split = 0;
+  s->linear_lose = 0;
   s->linear_path = 0;
   std::memset(s->linear_clusters, 0, sizeof s->linear_clusters);
   ts_status rc = TS_OK;
@@ -972,6 +973,11 @@ ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value) {
   }
   if (option == TS_OPT_LINEAR_SHARE) {
     return value == 0 || value == 1 || value == 2 || value == 4 ? TS_OK : TS_ERR_INVALID_ARG;  // without effect
+  }
+  if (option == TS_OPT_LINEAR_LOSE) {
+    if (value < 0 || value > TS_LINEAR_MAX_DIM / TS_SCALE_BLOCK) return TS_ERR_INVALID_ARG;
+    s->linear_lose = value;
+    return TS_OK;
   }
   if (option == TS_OPT_LINEAR_PATH) {
     if (value < 0 || value > 3) return TS_ERR_INVALID_ARG;

@@ -36,30 +36,38 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase of the given parity to end, kWaitCycles (about two seconds) at
-// most: then, or where another wait of the CTA gave up, *gave_up is set, what comes after
-// works on what there is, and nothing of it is stored.  (No answer: loops whose end
-// depended on one would not count as the same in all lanes, and their products' operands
-// would be moved one by one, 400 cycles a block instead of 100.  No calls: a call would
-// spill what the caller holds in registers.  No %globaltimer, whose reading is slow.)
-constexpr long long kWaitCycles = 4000000000ll;
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+// Waits for the phase of the given parity to end, `limit` cycles at most: then, or where
+// another wait of the CTA gave up, *gave_up is set, what comes after works on what there
+// is, and nothing of it is stored.  (No answer: loops whose end depended on one would not
+// count as the same in all lanes, and their products' operands would be moved one by one,
+// 400 cycles a block instead of 100.  No calls: a call would spill what the caller holds in
+// registers.  No %globaltimer, whose reading is slow.)
+constexpr uint32_t kWaitCycles = 4000000000u;  // about two seconds
+// Cycles that a wait went on since `last`.  Between two looks lie sixteen tries; where more
+// than 2^22 cycles do, the context was switched away, and that is no waiting.
+__device__ __forceinline__ uint32_t waited_since(uint32_t &last) {
+  const uint32_t now = static_cast<uint32_t>(clock()), cycles = min(now - last, 1u << 22);
+  last = now;
+  return cycles;
+}
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, uint32_t limit) {
   if (mbar_try(bar, parity)) return;
-  const long long start = clock64();
+  uint32_t last = static_cast<uint32_t>(clock()), waited = 0;
 #pragma unroll 1
-  for (int i = 1; !mbar_try(bar, parity); ++i) {
-    if ((i & 63) == 0 && (*gave_up || clock64() - start > kWaitCycles)) {
-      *gave_up = 1;
-      break;
+  for (int i = 0; !mbar_try(bar, parity); ++i) {
+    if ((i & 15) == 0) {
+      if (*gave_up) break;
+      if ((waited += waited_since(last)) > limit) *gave_up = 1;
     }
   }
 }
 // The same for copies or products that a CTA waits for after it gave up: they come to
-// their end before it leaves, within kWaitCycles.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-  const long long start = clock64();
-  while (!mbar_try(bar, parity) && clock64() - start < kWaitCycles) {
-  }
+// their end before it leaves, within `limit`.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint32_t limit) {
+  uint32_t last = static_cast<uint32_t>(clock()), waited = 0;
+#pragma unroll 1
+  for (int i = 1; waited <= limit && !mbar_try(bar, parity); ++i)
+    if ((i & 15) == 0) waited += waited_since(last);
 }
 
 // An arrival at a barrier of another CTA of the cluster (its address from cluster_addr).

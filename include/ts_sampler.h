@@ -694,8 +694,9 @@ ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream);
  * an input; TS_ERR_UNSUPPORTED for an in_dim above TS_LINEAR_MAX_DIM, n_rows or
  * out_dim above TS_LINEAR_MAX_ROWS, a stride of 2^40 or more, or where the driver
  * offers no tensor maps.  A copy that does not come
- * within a kernel's waiting limit (which nothing that the call allows brings about)
- * sets TS_ROW_STALLED and leaves a part of out unwritten. */
+ * within a kernel's waiting limit (about two seconds in which the kernel runs; nothing
+ * that the call allows brings it about) sets TS_ROW_STALLED and leaves a part of out
+ * unwritten. */
 #define TS_LINEAR_MAX_DIM 1048576
 #define TS_LINEAR_MAX_ROWS 2147482624
 #define TS_ROW_STALLED 128u
@@ -845,6 +846,11 @@ ts_status ts_read_status(ts_sampler *s, uint32_t *bits, void *stream);
 /* TS_OPT_LINEAR_SHARE: 0, 1, 2 or 4, without effect: it was the number of CTAs that
  * fetched their rows of x together (by multicast loads), and each fetches its own now. */
 #define TS_OPT_LINEAR_SHARE 11
+/* TS_OPT_LINEAR_LOSE (tests only): n > 0 makes ts_linear_e4m3 keep back the copies of
+ * block n - 1 (of 128 along in_dim) of its first tile, and limits its waits to about ten
+ * milliseconds, so that they run out: TS_ROW_STALLED is set and that tile of out is left
+ * as it was.  Calls that take pairs of CTAs are refused (TS_ERR_UNSUPPORTED).  0: none. */
+#define TS_OPT_LINEAR_LOSE 12
 ts_status ts_set_option(ts_sampler *s, int32_t option, int32_t value);
 
 /* Describes the kernel that ts_sample would launch for `b` (path 1 .. 4,

@@ -110,3 +110,47 @@ def test_two_graphs_of_finite_products(ts, sampler):
     torch.cuda.synchronize()
     for _, out, want, _ in runs:
         assert torch.equal(out, want)
+
+
+# --------------------------------------------------------------------------
+# A copy that does not come
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("m,n,k,path,split", [(3, 300, 1100, 1, 1), (30, 300, 1100, 1, 2), (60, 260, 2048, 1, 4), (64, 400, 300, 1, 1),
+                                              (100, 300, 1100, 2, 1), (200, 260, 1500, 2, 2), (300, 700, 130, 2, 1)])
+def test_a_lost_copy_ends_the_waits(ts, sampler, m, n, k, path, split):
+    """The copies of one block never come to the first tile: the kernel's waits run out, the
+    status says so, that tile's outputs stay as they were, the other tiles' are right, and so
+    is the next call."""
+    import torch
+    rng = np.random.default_rng([m, n, k])
+    blocks, wide = -(-k // 128), -(-k // 16) * 16
+    x, w = (put(rng.integers(-8, 9, (r, wide)), "e4m3")[:, :k] for r in (m, n))
+    xs, ws = put(rng.uniform(0.5, 1, (m, blocks))), put(rng.uniform(0.5, 1, (-(-n // 128), blocks)))
+    out = torch.empty((m, n), device="cuda")
+    call = ts.LinearE4m3(x, xs, w, ws, out)
+    sampler.read_status()
+    try:
+        sampler.set_option(ts.TS_OPT_LINEAR_PATH, path)
+        sampler.set_option(ts.TS_OPT_LINEAR_SPLIT, split)
+        ts.ts_linear_e4m3(sampler.handle, call)
+        want = out.clone()
+        assert sampler.read_status() == 0 and not bool((want == 7).any())
+        for block in sorted({0, blocks // 2, blocks - 1}):
+            sampler.set_option(ts.TS_OPT_LINEAR_LOSE, block + 1)
+            out.fill_(7)
+            ts.ts_linear_e4m3(sampler.handle, call)
+            assert sampler.read_status() == ts.TS_ROW_STALLED, block
+            kept = out == 7
+            assert bool(kept[:min(m, 16), :32].all()) and bool((kept | (out == want)).all())
+            assert bool((~kept[:, -1:]).all())  # of the last tile's columns
+            sampler.set_option(ts.TS_OPT_LINEAR_LOSE, 0)
+            ts.ts_linear_e4m3(sampler.handle, call)
+            assert sampler.read_status() == 0 and torch.equal(out, want)
+        sampler.set_option(ts.TS_OPT_LINEAR_PATH, 3)
+        sampler.set_option(ts.TS_OPT_LINEAR_LOSE, 1)
+        with pytest.raises(ts.SamplerError) as e:  # pairs wait for one another
+            ts.ts_linear_e4m3(sampler.handle, call)
+        assert e.value.status == ts.TS_ERR_UNSUPPORTED
+    finally:
+        for option in (ts.TS_OPT_LINEAR_LOSE, ts.TS_OPT_LINEAR_PATH, ts.TS_OPT_LINEAR_SPLIT):
+            sampler.set_option(option, 0)
