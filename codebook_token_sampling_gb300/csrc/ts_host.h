@@ -31,6 +31,7 @@ struct ts_sampler {
   struct ts_kv_state *kv;  // the paged cache's workspace (ts_reserve_kv), or null
   int kv_ctas;        // paged attention: 0 auto, else its number of CTAs (testing)
   int kv_join;        // 0 auto, 1 joins by a launch of their own, 2 by the last CTA (testing)
+  bool linear_ready;  // ts_linear_e4m3: its set-up succeeded
   int linear_clusters[5][4];  // ts_linear_e4m3: clusters of 1, 2, 4 and 8 CTAs of each kernel
                               // that the GPU holds at once
   int linear_path;    // ts_linear_e4m3: 0 auto, else its kernel (testing)
@@ -46,8 +47,9 @@ ts_status cuda_fail(cudaError_t e, const char *what);
 // Frees the paged cache's workspace (the device is current).
 cudaError_t kv_free(ts_sampler *s);
 
-// Once per ts_create, on the current device: what ts_linear_e4m3 needs of it.
-ts_status linear_setup(ts_sampler *s);
+// Once per ts_create, on the current device: what ts_linear_e4m3 needs of it, or that it
+// cannot be had.
+void linear_setup(ts_sampler *s);
 
 // One launch, with programmatic dependent launch if `pdl`.
 cudaError_t launch(const void *fn, dim3 grid, dim3 block, size_t smem, bool pdl, cudaStream_t st, void **args);

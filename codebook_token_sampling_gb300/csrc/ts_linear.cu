@@ -2,6 +2,8 @@
 // choice and launch on the caller's stream.
 #include <algorithm>
 #include <cstring>
+#include <mutex>
+#include <vector>
 
 #include "ts_host.h"
 #include "ts_linear.cuh"
@@ -16,17 +18,6 @@ using ts_host::cuda_fail;
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled g_encode = nullptr;  // set by the first ts_create, the same for all
-
-// Rows of bytes in boxes of 128 columns by `box_rows`, swizzled; what lies outside is 0.
-bool tensor_map(CUtensorMap *m, const void *p, int64_t columns, int64_t rows, int64_t stride, int box_rows) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
-  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, steps[2] = {1, 1};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // The kernels: tokens as the products' columns (16, 32 or 64), as their rows, and the
 // latter by pairs of CTAs.
@@ -45,9 +36,29 @@ LinearKernel rows_kernel() {
           ts::kRowsThreads};
 }
 constexpr int kKernels = 5;
+
+// What is the same for all handles (a handle's calls read g_encode only after its own
+// linear_setup saw it set).
+struct LinearDevice {
+  int device, clusters[kKernels][4];
+};
+std::mutex g_linear_mu;
+std::vector<LinearDevice> g_linear_devices;
+EncodeTiled g_encode = nullptr;
+
 LinearKernel kernel_for(int i) {
   return i == 0 ? few_kernel<16>() : i == 1 ? few_kernel<32>() : i == 2 ? few_kernel<64>()
        : i == 3 ? rows_kernel<2, false>() : rows_kernel<4, true>();
+}
+
+// Rows of bytes in boxes of 128 columns by `box_rows`, swizzled; what lies outside is 0.
+bool tensor_map(CUtensorMap *m, const void *p, int64_t columns, int64_t rows, int64_t stride, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, steps[2] = {1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -120,41 +131,63 @@ LinearPlan plan_for(const ts_sampler *s, int64_t m, int64_t n, int64_t blocks, c
 
 }  // namespace
 
-// Shared-memory limits of the kernels, and the driver's encoder of tensor maps.
-ts_status ts_host::linear_setup(ts_sampler *s) {
+// Shared-memory limits of the kernels, the clusters that the device holds of each (asked for
+// once per device: seventeen queries), and the driver's encoder of tensor maps.  A handle
+// for which one of these fails is without ts_linear_e4m3 only.
+void ts_host::linear_setup(ts_sampler *s) {
+  std::lock_guard<std::mutex> lock(g_linear_mu);
+  s->linear_ready = false;
   for (int i = 0; i < kKernels; ++i) {
     const LinearKernel k = kernel_for(i);
-    const cudaError_t e =
-        cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  }
-  for (int i = 0; i < kKernels; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const LinearKernel k = kernel_for(i);
-      cudaLaunchConfig_t cfg;
-      std::memset(&cfg, 0, sizeof cfg);
-      cfg.gridDim = dim3(static_cast<unsigned>(s->num_sms >> j << j));
-      cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
-      cfg.dynamicSmemBytes = k.smem;
-      cudaLaunchAttribute attr;
-      attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = 1u << j;
-      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      int held = 0;
-      const cudaError_t e = cudaOccupancyMaxActiveClusters(&held, k.fn, &cfg);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
-      s->linear_clusters[i][j] = std::max(held, 1);
+    if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem)) != cudaSuccess) {
+      cudaGetLastError();
+      return;
     }
-  void *fn = nullptr;
-  cudaDriverEntryPointQueryResult found;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) == cudaSuccess &&
-      found == cudaDriverEntryPointSuccess)
+  }
+  LinearDevice *d = nullptr;
+  for (LinearDevice &known : g_linear_devices)
+    if (known.device == s->device) d = &known;
+  if (!d) {
+    LinearDevice now;
+    now.device = s->device;
+    std::memset(now.clusters, 0, sizeof now.clusters);
+    for (int i = 0; i < kKernels; ++i)
+      for (int j = 0; j < 4; ++j) {
+        if (i == 4 && j != 1) continue;  // pairs are clusters of two
+        const LinearKernel k = kernel_for(i);
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof cfg);
+        cfg.gridDim = dim3(static_cast<unsigned>(s->num_sms >> j << j));
+        cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
+        cfg.dynamicSmemBytes = k.smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1u << j;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int held = 0;
+        if (cudaOccupancyMaxActiveClusters(&held, k.fn, &cfg) != cudaSuccess) {
+          cudaGetLastError();
+          return;
+        }
+        now.clusters[i][j] = std::max(held, 1);
+      }
+    g_linear_devices.push_back(now);
+    d = &g_linear_devices.back();
+  }
+  std::memcpy(s->linear_clusters, d->clusters, sizeof s->linear_clusters);
+  if (!g_encode) {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return;
+    }
     g_encode = reinterpret_cast<EncodeTiled>(fn);
-  else
-    cudaGetLastError();  // ts_linear_e4m3 says TS_ERR_UNSUPPORTED
-  return TS_OK;
+  }
+  s->linear_ready = true;
 }
 
 extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void *stream) {
@@ -184,7 +217,7 @@ extern "C" ts_status ts_linear_e4m3(ts_sampler *s, const ts_linear_args *a, void
       out.meets(ts_host::rows_span(a->w, a->out_dim, a->in_dim, a->w_stride, 1)) ||
       out.meets(ts_host::rows_span(a->w_scale, blocks_of(a->out_dim), blocks, a->w_scale_stride, 4)))
     return TS_ERR_INVALID_ARG;
-  if (!g_encode) return TS_ERR_UNSUPPORTED;
+  if (!s->linear_ready) return TS_ERR_UNSUPPORTED;
 
   ts::LinearParams p;
   std::memset(&p, 0, sizeof p);

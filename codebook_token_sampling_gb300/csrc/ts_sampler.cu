@@ -674,6 +674,7 @@ ts_status ts_create(int device, int max_top_k, ts_sampler **out) {
   s->linear_split = 0;
   s->linear_lose = 0;
   s->linear_path = 0;
+  s->linear_ready = false;
   std::memset(s->linear_clusters, 0, sizeof s->linear_clusters);
   ts_status rc = TS_OK;
   e = cudaDeviceGetAttribute(&s->num_sms, cudaDevAttrMultiProcessorCount, device);
@@ -690,7 +691,7 @@ ts_status ts_create(int device, int max_top_k, ts_sampler **out) {
   }
   if (rc == TS_OK) rc = set_attributes(device);
   if (rc == TS_OK) rc = warp_occupancy(s);
-  if (rc == TS_OK) rc = ts_host::linear_setup(s);
+  if (rc == TS_OK) ts_host::linear_setup(s);
   cudaSetDevice(prev);
   if (rc != TS_OK) {
     if (s->status) cudaFree(s->status);

@@ -693,7 +693,7 @@ ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream);
  * stride below its row (x, out and x_scale of one row: any), or an out that overlaps
  * an input; TS_ERR_UNSUPPORTED for an in_dim above TS_LINEAR_MAX_DIM, n_rows or
  * out_dim above TS_LINEAR_MAX_ROWS, a stride of 2^40 or more, or where the driver
- * offers no tensor maps.  A copy that does not come
+ * offers no tensor maps or refuses the kernels.  A copy that does not come
  * within a kernel's waiting limit (about two seconds in which the kernel runs; nothing
  * that the call allows brings it about) sets TS_ROW_STALLED and leaves a part of out
  * unwritten. */

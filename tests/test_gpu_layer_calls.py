@@ -154,3 +154,33 @@ def test_a_lost_copy_ends_the_waits(ts, sampler, m, n, k, path, split):
     finally:
         for option in (ts.TS_OPT_LINEAR_LOSE, ts.TS_OPT_LINEAR_PATH, ts.TS_OPT_LINEAR_SPLIT):
             sampler.set_option(option, 0)
+
+
+def test_handles_made_at_once(ts):
+    """Handles made by several threads, each of which multiplies: the same bits from all."""
+    import threading
+    import torch
+    rng = np.random.default_rng(3)
+    x, w = (put(rng.integers(-8, 9, (r, 256)), "e4m3") for r in (70, 300))
+    xs, ws = put(rng.uniform(0.5, 1, (70, 2))), put(rng.uniform(0.5, 1, (3, 2)))
+    outs, made, failed = [torch.zeros((70, 300), device="cuda") for _ in range(8)], [], []
+    torch.cuda.synchronize()
+
+    def work(out):
+        try:
+            torch.cuda.set_device(0)
+            handle = ts.Sampler(0)
+            made.append(handle)
+            stream = torch.cuda.Stream()
+            ts.ts_linear_e4m3(handle.handle, ts.LinearE4m3(x, xs, w, ws, out), stream)
+            stream.synchronize()
+        except Exception as e:  # the thread's own
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(out,)) for out in outs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for handle in made:
+        handle.close()
+    assert not failed and bool((outs[0] != 0).any()) and all(torch.equal(out, outs[0]) for out in outs)
