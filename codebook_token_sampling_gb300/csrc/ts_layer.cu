@@ -239,12 +239,15 @@ ts_status ts_rms_norm(ts_sampler *s, const ts_norm_args *a, void *stream) {
       (!same(sum, x) && span(sum).meets(span(x))) || (!same(sum, res) && span(sum).meets(span(res))))
     return TS_ERR_INVALID_ARG;
 
-  // Sixteen elements a lane to 8-bit rows where rows are many: a block's scale by fewer lanes
-  // (32,768 x 4096 without a residual bf16 84 us, 125 with eight, fp32 106, 155; bf16 x 1024
-  // with one 37, 43), but not with a residual where DRAM bounds either way (bf16 x 4096 149 us,
-  // 144 with eight; fp32 x 2048 153, 146).
-  const int widest = !a->residual ? 4096 : a->dtype == TS_DTYPE_BF16 ? 2048 : 0;
-  const bool half = e4m3 && dim >= 512 && dim <= widest && n > 4 * s->num_sms;
+  // Sixteen elements a lane to 8-bit rows where rows are many: a block's scale by fewer lanes.
+  // Without a residual at every width (2^27 elements in rows of 512 to 4096: bf16 74 to 107 us,
+  // 116 to 138 with eight; fp32 100 to 124, 141 to 160; 2^22 elements 5 to 6.5, 5.3 to 7.5).
+  // With one, bf16: rows of 512 to 1024 37 to 39 us (43 to 45), of 2560 and 3584 140 and 139
+  // (148 and 150), 8192 of 4096 36.8 (40.0), but not 32,768 of 4096 (149, 144 with eight; of
+  // 1536 and 2048 that many elements take 151, 147 and 143 with eight, fewer 37, 39).  With
+  // one, fp32: eight (2^25 elements 68 to 71 us, 72 to 76 with sixteen; 2^22 up to 13.3, 11.1).
+  const bool wide_block = !a->residual || (a->dtype == TS_DTYPE_BF16 && (dim < 4096 || n * dim < (1 << 26)));
+  const bool half = e4m3 && dim >= 512 && dim <= 4096 && wide_block && n > 4 * s->num_sms;
   const auto fits = [&](int width) {
     bool ok = dim % width == 0 && (!ws || aligned(a->weight, 16));
     for (const Rows &r : {x, res, sum, out}) ok = ok && (!r.p || in_pieces(r, n, width));

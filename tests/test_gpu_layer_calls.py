@@ -3,7 +3,8 @@ once."""
 import numpy as np
 import pytest
 
-from test_gpu_layer import get, kind_of, put, sampler, ts  # noqa: F401  (fixtures among them)
+from oracle import layer as olayer
+from test_gpu_layer import check_rows, close, get, HALF, norm_error, put, run_norm, sampler, TINY, ts  # noqa: F401  (fixtures among them)
 
 pytestmark = pytest.mark.gpu
 
@@ -184,3 +185,40 @@ def test_handles_made_at_once(ts):
     for handle in made:
         handle.close()
     assert not failed and bool((outs[0] != 0).any()) and all(torch.equal(out, outs[0]) for out in outs)
+
+
+# --------------------------------------------------------------------------
+# Norms at the borders of their variants
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,dim", [(609, 2064), (700, 3584), (640, 4080), (611, 4096), (608, 4096), (609, 4112), (700, 512), (700, 504)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_norm_with_residual_to_8_bits_at_the_borders(ts, sampler, rows, dim, kind):
+    """Wide rows with a residual on both sides of 608 rows (four to an SM), of 512 and of
+    4096 elements."""
+    rng = np.random.default_rng([rows, dim])
+    x, w, r = rng.normal(0, 3, (rows, dim)), rng.normal(1, 0.3, dim), rng.normal(0, 5, (rows, dim))
+    got = run_norm(ts, sampler, x, w, r, kind, "e4m3", eps=1e-5)
+    h, y = olayer.rms_norm(got["x"], got["weight"], got["residual"], eps=1e-5)
+    check_rows(got["out"], got["scale"], y, norm_error(dim), 0.0, "e4m3")
+    close(get(got["sum"]), h, (2.0 ** -24 + HALF[kind]) * np.abs(h) + TINY[kind], "sum")
+
+
+def test_norm_of_many_elements_in_rows_of_4096(ts, sampler):
+    """2^26 elements and more take another variant than fewer: the rows of a large call are
+    those of its halves, to a step of the code."""
+    import torch
+    x, r = (torch.randn((16384, 4096), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    out, scale, total = torch.empty(x.shape, device="cuda", dtype=torch.float8_e4m3fn), torch.empty((16384, 32), device="cuda"), torch.empty_like(x)
+    ts.ts_rms_norm(sampler.handle, ts.RmsNorm(x, out, residual=r, residual_out=total, out_scale=scale))
+    for part in (slice(0, 8192), slice(8192, 16384)):
+        o, s, t = torch.empty_like(out[part]), torch.empty_like(scale[part]), torch.empty_like(total[part])
+        ts.ts_rms_norm(sampler.handle, ts.RmsNorm(x[part], o, residual=r[part], residual_out=t, out_scale=s))
+        assert torch.equal(t, total[part])
+        # sums added in another order: a scale some steps of 2^-24 off, a code where it was at a tie
+        assert bool(((s - scale[part]).abs() <= 2 * norm_error(4096) * scale[part]).all())
+        a, b = (q.float().view(8192, 32, 128) * k[..., None] for q, k in ((o, s), (out[part], scale[part])))
+        assert bool(((a - b).abs() <= 2.0 ** -3 * b.abs() * 1.001 + 2.0 ** -9 * s[..., None]).all())
+        # two values that far apart lie on two sides of a tie in as many of a code's steps (2^-4 of
+        # it at least) as they are apart
+        other = (a - b).abs() > 2.0 ** -5 * b.abs() + 2.0 ** -10 * s[..., None]
+        assert float(other.float().mean()) <= 2 * norm_error(4096) / 2.0 ** -4
