@@ -38,7 +38,7 @@ struct LinearParams {
 // of which two fit and three do not.  Bound by latency (launch, tensor maps, the first
 // copies, the cluster's sums: 32 x 4096 x 1024 4.3 us) and, with enough tiles, by what a
 // CTA's chain of copies, products and sums takes for a block, about 250 ns (16 x 11,008 x
-// 4096: 10 us for 45 MB).  Other tiles: 64 or 32 weight rows would read the tokens more
+// 4096: 11 us for 45 MB).  Other tiles: 64 or 32 weight rows would read the tokens more
 // often; eight CTAs a cluster are 1 us slower than four.
 template <int TN>
 struct FewTile {
@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   if (t == 0 && stalled()) atomicOr(p.status, kRowStalled);
 }
 
-// More rows.  8192 x 8192 x 4096: 211 us, 2.6 PFLOP/s by pairs (732 us with tokens as the
+// More rows.  8192 x 8192 x 4096: 210 us, 2.6 PFLOP/s by pairs, 229 us repeated for
+// seconds under the power cap (732 us with tokens as the
 // products' columns, 422 us by single CTAs of 128 columns); bound by the chain from a
 // block's products to the answer that its accumulator is free, of which a tile of 256
 // columns has two.  128 x 11,008 x 4096: 15 us by 115 CTAs, bound by that chain (250 ns a

@@ -683,7 +683,8 @@ ts_status ts_gate(ts_sampler *s, const ts_gate_args *a, void *stream);
  * [in_dim], both E4M3: with b counting blocks of 128 along in_dim,
  *   out[m][n] = sum_b x_scale[m][b] w_scale[n / 128][b] sum_{k in b} x[m][k] w[n][k].
  * A block's products are summed by the tensor cores in fp32, the blocks' sums are
- * scaled and added in fp32, and the result is rounded to out_dtype once.  The order
+ * multiplied by their two scales' product (rounded to fp32, which has to hold it) and
+ * added in fp32, and the result is rounded to out_dtype once.  The order
  * of the blocks' additions depends on the sizes, and is the same in every run.
  *
  * x and w are 16-byte aligned and their strides multiples of 16; in_dim may be any
