@@ -60,27 +60,26 @@ struct Heads {
   // within one another counts as if it did.
   bool meets(const Heads &o) const {
     if (none() || o.none() || from >= o.end() || o.from >= end()) return false;
+    const __int128 most = static_cast<__int128>(1) << 60;
+    if (end() - from > most || o.end() - o.from > most) return true;
     const bool many_rows = rows > 1 && o.rows > 1, many_heads = heads > 1 && o.heads > 1;
-    const int64_t by_row = rows > 1 ? row : o.row, by_head = heads > 1 ? head : o.head;
-    if ((!many_rows || row == o.row) && (!many_heads || head == o.head) && wide == o.wide) {
-      // rows i and heads j apart (of those that there are): nearer than a head's width?
-      const __int128 apart = static_cast<__int128>(o.from) - static_cast<__int128>(from);
-      for (int64_t j = 1 - heads; j < o.heads; ++j) {
-        const __int128 at = apart + static_cast<__int128>(j) * by_head;
-        __int128 i = 0;
-        if ((rows > 1 || o.rows > 1) && by_row > 0)
-          i = std::min<__int128>(std::max<__int128>((at < 0 ? by_row / 2 - at : -by_row / 2 - at) / by_row, 1 - rows), o.rows - 1);
-        const __int128 off = at + i * by_row;
-        if (off < wide && -off < wide) return true;
-      }
-      return false;
+    if (many_rows && row == o.row && row > 0 && !by_row().meets(o.by_row())) return false;
+    if ((many_rows && row != o.row) || (many_heads && head != o.head) || wide != o.wide) return true;
+    // rows i and heads j apart (of those that there are): nearer than a head's width?
+    const int64_t step = rows > 1 ? row : o.rows > 1 ? o.row : 0, head_step = heads > 1 ? head : o.head;
+    const int64_t apart = static_cast<int64_t>(o.from - from);
+    for (int64_t j = 1 - heads; j < o.heads; ++j) {
+      const int64_t at = apart + j * head_step;
+      int64_t i = 0;
+      if (step > 0) i = std::min(std::max((at < 0 ? step / 2 - at : -step / 2 - at) / step, 1 - rows), o.rows - 1);
+      const int64_t off = at + i * step;
+      if (off < wide && -off < wide) return true;
     }
-    if (many_rows && row == o.row && row > 0) {
-      const Span a = {from, static_cast<uintptr_t>(end()), static_cast<uintptr_t>(row), static_cast<uintptr_t>((heads - 1) * head + wide)};
-      const Span b = {o.from, static_cast<uintptr_t>(o.end()), static_cast<uintptr_t>(row), static_cast<uintptr_t>((o.heads - 1) * o.head + o.wide)};
-      return a.meets(b);
-    }
-    return true;
+    return false;
+  }
+  // Its rows, as far as all heads reach.
+  Span by_row() const {
+    return {from, static_cast<uintptr_t>(end()), static_cast<uintptr_t>(row), static_cast<uintptr_t>((heads - 1) * head + wide)};
   }
 };
 
