@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t full = smem_addr(bars), empty = full + 8 * NS, summed = empty + 8 * NS, taken = summed + 8 * NB;
   const uint32_t done = taken + 8 * NB;
   const auto stalled = [&]() { return *static_cast<volatile int *>(&gave_up) != 0; };
-  const auto any_stalled = [&]() { return __any_sync(0xFFFFFFFFu, stalled()) != 0; };  // the same in all lanes
 
   const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int tile = static_cast<int>(blockIdx.x) / p.split;
